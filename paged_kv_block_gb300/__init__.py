@@ -18,6 +18,9 @@ import os
 
 import torch
 
+from . import cache as _cache
+from .cache import *  # noqa: F401,F403
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpagedattn.so")
 
@@ -132,7 +135,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "paged_kv_block_gb300.build.build()")
         h = C.CDLL(LIB_PATH)
-        for name, (res, args) in _EXPORTS.items():
+        for name, (res, args) in {**_EXPORTS, **_cache.EXPORTS}.items():
             f = getattr(h, name)
             f.restype, f.argtypes = res, args
         _LIB = h

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpagedattn.so")
 SOURCES = ["api.cu", "planner.cu", "decode.cu", "attn_tc.cu", "attn256.cu", "qsa.cu", "sage.cu",
-           "decode_static.cu", "probe.cu"]
+           "decode_static.cu", "probe.cu", "rope.cu", "cache.cu"]
 HEADERS = ["common.cuh", "internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -36,8 +36,8 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every translation unit (in parallel) and link the shared library."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include",
-                                                                    "paged_attn.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS]
+    hdrs += [os.path.join(ROOT, "include", h) for h in ("paged_attn.h", "paged_cache.h")]
     jobs = []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
