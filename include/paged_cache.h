@@ -189,7 +189,7 @@ int paged_cache_free_run(const paged_cache_params* params, const int32_t* rows_d
  * page does not hold them.  Item i is served if it needs no page or if the free pages suffice
  * for it and every item listed before it; otherwise its row stays as it is (capacity bit).
  * Rows outside [0, rows), a row listed before, negative tokens and rows that would outgrow C
- * pages are left out (metadata bit). */
+ * pages are left out (metadata bit).  n <= 4096. */
 size_t paged_cache_extend_workspace_size(int n);
 int paged_cache_extend_run(const paged_cache_params* params, const int32_t* rows_dev,
                            const int32_t* new_tokens_dev, int n, int32_t* block_tables_dev,
@@ -202,7 +202,7 @@ int paged_cache_extend_run(const paged_cache_params* params, const int32_t* rows
  * Children are distinct and empty.  Items that break this, rows outside [0, rows), a row that is
  * its own parent and page ids outside the pool are left out (metadata bit); an item for whose
  * fresh page the free pages do not suffice (counted as in extend) leaves its child empty
- * (capacity bit). */
+ * (capacity bit).  n <= 4096. */
 size_t paged_cache_fork_workspace_size(int n);
 int paged_cache_fork_run(const paged_cache_params* params, const paged_cache_pools* pools,
                          const int32_t* parents_dev, const int32_t* children_dev, int n,

@@ -8,6 +8,7 @@ CUDA device and enqueue on the current stream unless `stream` is given.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -76,67 +77,121 @@ EXPORTS = {
 }
 
 
+_I32 = torch.int32
+# The current stream's handle without building a Stream object, where this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+def _device():
+    """Index of the current CUDA device; one that no tensor is on where there is no GPU."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        if torch.cuda.is_available():
+            raise
+        return -2
+
+
 def _lib():
     from . import lib
     return lib()
 
 
+class _Calls:
+    """The library's functions by name, looked up once."""
+
+    def __getattr__(self, name):
+        f = getattr(_lib(), name)
+        setattr(self, name, f)
+        return f
+
+
+_call = _Calls()
+
+
 def _check(code, what):
-    if code != 0:
-        from . import PagedAttnError
-        raise PagedAttnError(code, what)
+    from . import PagedAttnError
+    raise PagedAttnError(code, what)
 
 
-def _stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream().cuda_stream
 
 
-def _on_device(t, name):
+def _on_device(t, dev, name):
     """The current device has to hold `t`: the call runs there."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} is not on the current device")
 
 
-def _ints(t, name, n=None):
-    """Address of a contiguous int32 tensor on the current device (of n elements)."""
-    _on_device(t, name)
-    if t.dtype != torch.int32 or not t.is_contiguous():
+def _ints(t, dev, name):
+    """Address of a contiguous int32 tensor on the current device."""
+    if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+        _on_device(t, dev, name)
         raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
     return t.data_ptr()
 
 
-def _status(t):
+def _ints_of(t, dev, name, n):
+    """The same, of n elements."""
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return _ints(t, dev, name)
+
+
+def _status(t, dev):
     """Address of an optional 4-byte status word (int32 or uint32, any shape)."""
     if t is None:
         return None
-    _on_device(t, "status")
+    _on_device(t, dev, "status")
     if t.element_size() != 4 or t.numel() < 1 or not t.is_contiguous():
         raise ValueError("status must hold a 32-bit word")
     return t.data_ptr()
 
 
-def _table(freqs, name="freqs"):
-    _on_device(freqs, name)
-    if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError(f"{name} must be a table made by rope_frequencies")
+def _empty(t, dtype):
+    """A new contiguous tensor of t's shape (empty_like is the cheaper call)."""
+    if t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
+def _table(freqs, dev):
+    if freqs.dtype is not torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a table made by rope_frequencies")
+    _on_device(freqs, dev, "freqs")
     return freqs.data_ptr()
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, size, n, like, dev):
+    """The caller's workspace, or a new one of size(n) bytes."""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _on_device(workspace, "workspace")
+        return torch.empty(size(n), dtype=torch.uint8, device=like.device)
+    _on_device(workspace, dev, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
 
 
-def _nbytes(t):
-    return t.numel() * t.element_size()
+# Parameter structs depend on the static arguments alone, so equal calls share one (read-only).
+@functools.lru_cache(maxsize=512)
+def _rope_params(*fields):
+    return C.byref(RopeParams(*fields))
+
+
+@functools.lru_cache(maxsize=512)
+def _append_params(*fields):
+    return C.byref(AppendParams(*fields))
+
+
+@functools.lru_cache(maxsize=512)
+def _cache_params(*fields):
+    return C.byref(CacheParams(*fields))
 
 
 # ---------------------------------------------------------------------------------------
@@ -164,35 +219,40 @@ def rope_frequencies(rotary_dim, *, base=10000.0, scaling="none", factor=1.0,
         s = RopeScaling(rotary_dim=rotary_dim, kind=ROPE_SCALING[scaling], base=base,
                         factor=factor, original_max_position=original_max_position, low=low,
                         high=high)
-        _check(_lib().paged_rope_frequencies(C.byref(s), out, C.byref(m)),
-               "paged_rope_frequencies")
+        rc = _call.paged_rope_frequencies(C.byref(s), out, C.byref(m))
+        if rc:
+            _check(rc, "paged_rope_frequencies")
     table = (C.c_uint64 * max(n, 1))()
-    _check(_lib().paged_rope_table(out, n, table), "paged_rope_table")
+    rc = _call.paged_rope_table(out, n, table)
+    if rc:
+        _check(rc, "paged_rope_table")
     host = torch.tensor([v - (1 << 64) if v >= 1 << 63 else v for v in table[:n]],
                         dtype=torch.int64)
     if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+        device = torch.device("cuda", _device())
     return host.to(device), m.value
 
 
-def _rows(t, name):
+def _rows(t, dev, name):
     """(tokens, heads, D, token stride, head stride) of [T, H, D] or [B, S, H, D] rows whose
     columns are contiguous and whose leading dimensions step evenly."""
-    _on_device(t, name)
-    if t.dim() == 4:
-        B, S, H, D = t.shape
-        sb, ts, hs, e = t.stride()
-        if B > 1 and S > 1 and sb != S * ts:
-            raise ValueError(f"{name}: batch and sequence must step evenly")
+    if t.get_device() != dev:
+        _on_device(t, dev, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        T, H, D = shape
+        ts, hs, e = stride
+    elif len(shape) == 4:
+        B, S, H, D = shape
+        sb, ts, hs, e = stride
         if S == 1:
             ts = sb
+        elif B > 1 and sb != S * ts:
+            raise ValueError(f"{name}: batch and sequence must step evenly")
         T = B * S
-    elif t.dim() == 3:
-        T, H, D = t.shape
-        ts, hs, e = t.stride()
     else:
         raise ValueError(f"{name} must be [tokens, heads, D] or [batch, seq, heads, D]")
-    if D > 1 and e != 1:
+    if e != 1 and D > 1:
         raise ValueError(f"{name}: the columns of a head must be contiguous")
     return T, H, D, ts, hs
 
@@ -204,44 +264,45 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
 
     q_out=q rotates in place.  inverse=True turns back by the same angles (times the same
     attention_factor): the gradient of the input from the gradient of the output."""
-    T, Hq, D, qt, qh = _rows(q, "q")
+    dev = _device()
+    T, Hq, D, qt, qh = _rows(q, dev, "q")
     dt = q.dtype
     if dt not in _DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
-    p = RopeParams(num_tokens=T, num_qo_heads=Hq, num_kv_heads=0, head_dim=D,
-                   rotary_dim=2 * freqs.numel(), layout=ROPE_LAYOUT[layout], dtype=_DTYPE[dt],
-                   inverse=int(inverse), attention_factor=attention_factor, q_token_stride=qt,
-                   q_head_stride=qh)
-    pos = _ints(positions, "positions", T)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-        p.q_out_token_stride, p.q_out_head_stride = Hq * D, D
+        q_out = _empty(q, dt)
+        qot, qoh = Hq * D, D
     else:
         if q_out.shape != q.shape or q_out.dtype != dt:
             raise ValueError("q_out must have q's shape and dtype")
-        _, _, _, p.q_out_token_stride, p.q_out_head_stride = _rows(q_out, "q_out")
+        _, _, _, qot, qoh = _rows(q_out, dev, "q_out")
+    Hk = kt = kh = kot = koh = 0
     kp = kop = None
     if k is not None:
-        Tk, Hk, Dk, p.k_token_stride, p.k_head_stride = _rows(k, "k")
+        Tk, Hk, Dk, kt, kh = _rows(k, dev, "k")
         if Tk != T or Dk != D or k.dtype != dt:
             raise ValueError("k must have q's tokens, columns and dtype")
         if Hk < 1:
             raise ValueError("k must have heads")
-        p.num_kv_heads = Hk
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=q.device)
-            p.k_out_token_stride, p.k_out_head_stride = Hk * D, D
+            k_out = _empty(k, dt)
+            kot, koh = Hk * D, D
         else:
             if k_out.shape != k.shape or k_out.dtype != dt:
                 raise ValueError("k_out must have k's shape and dtype")
-            _, _, _, p.k_out_token_stride, p.k_out_head_stride = _rows(k_out, "k_out")
+            _, _, _, kot, koh = _rows(k_out, dev, "k_out")
         kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if T == 0:
-        return q_out if k is None else (q_out, k_out)
-    _check(_lib().paged_rope_run(C.byref(p), q.data_ptr(), kp, pos, _table(freqs),
-                                 q_out.data_ptr(), kop, _stream(stream)), "paged_rope_run")
+    pos = _ints_of(positions, dev, "positions", T)
+    table = _table(freqs, dev)
+    if T:
+        rc = _call.paged_rope_run(
+            _rope_params(T, Hq, Hk, D, 2 * freqs.numel(), ROPE_LAYOUT[layout], _DTYPE[dt],
+                         int(inverse), attention_factor, qt, qh, kt, kh, qot, qoh, kot, koh),
+            q.data_ptr(), kp, pos, table, q_out.data_ptr(), kop, _stream(stream, dev))
+        if rc:
+            _check(rc, "paged_rope_run")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -249,24 +310,26 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
 # Appending to the cache
 # ---------------------------------------------------------------------------------------
 
-def _geometry(cache):
+def _geometry(cache, dev):
     """(K address, V address or None, combined, P, Hkv, page size, D) of a combined cache
     [P, 2, Hkv, ps, D] or a (K, V) pair of pools [P, Hkv, ps, D]; all bf16, contiguous."""
-    pair = isinstance(cache, (tuple, list))
-    k = cache[0] if pair else cache
-    for t in (cache if pair else (cache,)):
-        _on_device(t, "the cache")
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError("the cache must be contiguous bf16")
-    if pair:
-        if len(cache) != 2 or k.dim() != 4 or cache[1].shape != k.shape:
+    if isinstance(cache, (tuple, list)):
+        k, v = cache
+        if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("K and V pools must both be [P, Hkv, page_size, D]")
         P, Hkv, ps, D = k.shape
-        return k.data_ptr(), cache[1].data_ptr(), 0, P, Hkv, ps, D
-    if k.dim() != 5 or k.shape[1] != 2:
+        return _pool(k, dev), _pool(v, dev), 0, P, Hkv, ps, D
+    shape = cache.shape
+    if len(shape) != 5 or shape[1] != 2:
         raise ValueError("a combined cache must be [P, 2, Hkv, page_size, D]")
-    P, _, Hkv, ps, D = k.shape
-    return k.data_ptr(), None, 1, P, Hkv, ps, D
+    return _pool(cache, dev), None, 1, shape[0], shape[2], shape[3], shape[4]
+
+
+def _pool(t, dev):
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or not t.is_contiguous():
+        _on_device(t, dev, "the cache")
+        raise ValueError("the cache must be contiguous bf16")
+    return t.data_ptr()
 
 
 def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=None,
@@ -281,65 +344,67 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     page table is block_tables [B, C] or paged_kv_indptr with paged_kv_indices.  seq_lens_kv
     [B] counts the new tokens in.  freqs (from rope_frequencies) None writes keys as they are.
     status: an int32 word that device-side findings are OR-ed into."""
-    kc, vc, combined, P, Hkv, ps, D = _geometry(paged_kv_cache)
+    dev = _device()
+    kc, vc, combined, P, Hkv, ps, D = _geometry(paged_kv_cache, dev)
     B = seq_lens_kv.numel()
-    T, Hk, Dk, kt, kh = _rows(k, "k")
-    Tv, Hv, Dv, vt, vh = _rows(v, "v")
-    if Hk != Hkv or Dk != D or (Tv, Hv, Dv) != (T, Hk, Dk) or v.dtype != k.dtype:
+    T, Hk, Dk, kt, kh = _rows(k, dev, "k")
+    Tv, Hv, Dv, vt, vh = _rows(v, dev, "v")
+    dt = k.dtype
+    if Hk != Hkv or Dk != D or Tv != T or Hv != Hk or Dv != D or v.dtype is not dt:
         raise ValueError("k and v must have the cache's heads and columns, and the same dtype")
-    if k.dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {k.dtype}")
+    if dt not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
     if (kh != D or vh != D) and Hkv > 1:
         raise ValueError("the heads of k and v must be adjacent")
-    p = AppendParams(batch=B, seq_len_q=0, total_q=0, num_qo_heads=0, num_kv_heads=Hkv,
-                     head_dim=D, page_size=ps, num_pages=P, combined_cache=combined,
-                     max_pages_per_request=0,
-                     rotary_dim=0 if freqs is None else 2 * freqs.numel(),
-                     layout=ROPE_LAYOUT[layout], attention_factor=attention_factor,
-                     in_dtype=_DTYPE[k.dtype], k_token_stride=kt, v_token_stride=vt)
+    total = sq = cols = Hq = qt = 0
+    qo = indptr = qp = qop = table = None
     if qo_indptr is not None:
         if k.dim() != 3:
             raise ValueError("packed k must be [total, heads, D]")
-        qo = _ints(qo_indptr, "qo_indptr", B + 1)
-        p.total_q = T
+        qo = _ints_of(qo_indptr, dev, "qo_indptr", B + 1)
+        total = T
     else:
-        qo = None
         if k.shape[0] != B:
             raise ValueError("k must have one entry per request")
-        p.seq_len_q = T // B if B else 0
+        sq = T // B if B else 0
     if block_tables is not None:
         if paged_kv_indptr is not None or paged_kv_indices is not None:
             raise ValueError("either block_tables or the CSR table")
         if block_tables.dim() != 2 or block_tables.shape[0] != B:
             raise ValueError("block_tables must be [B, C]")
-        indptr, pages = None, _ints(block_tables, "block_tables")
-        p.max_pages_per_request = block_tables.shape[1]
+        pages = _ints(block_tables, dev, "block_tables")
+        cols = block_tables.shape[1]
     else:
         if paged_kv_indptr is None or paged_kv_indices is None:
             raise ValueError("a page table is needed")
-        indptr = _ints(paged_kv_indptr, "paged_kv_indptr", B + 1)
-        pages = _ints(paged_kv_indices, "paged_kv_indices")
-    qp = qop = None
+        indptr = _ints_of(paged_kv_indptr, dev, "paged_kv_indptr", B + 1)
+        pages = _ints(paged_kv_indices, dev, "paged_kv_indices")
     if q is not None:
-        Tq, Hq, Dq, p.q_token_stride, qh = _rows(q, "q")
-        if Tq != T or Dq != D or q.dtype != k.dtype or (qh != D and Hq > 1):
+        Tq, Hq, Dq, qt, qh = _rows(q, dev, "q")
+        if Tq != T or Dq != D or q.dtype is not dt or (qh != D and Hq > 1):
             raise ValueError("q must have k's tokens, columns and dtype, and adjacent heads")
-        p.num_qo_heads = Hq
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
+            q_out = _empty(q, torch.bfloat16)
+        elif (q_out.shape != q.shape or q_out.dtype is not torch.bfloat16
+              or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous bf16 of q's shape")
         else:
-            _on_device(q_out, "q_out")
+            _on_device(q_out, dev, "q_out")
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if T == 0 or B == 0:
-        return q_out
-    _check(_lib().paged_append_run(C.byref(p), qp, k.data_ptr(), v.data_ptr(), qo, indptr, pages,
-                                   _ints(seq_lens_kv, "seq_lens_kv"),
-                                   None if freqs is None else _table(freqs), qop, kc, vc,
-                                   _status(status), _stream(stream)), "paged_append_run")
+    rotary = 0
+    if freqs is not None:
+        table, rotary = _table(freqs, dev), 2 * freqs.numel()
+    lens, status = _ints(seq_lens_kv, dev, "seq_lens_kv"), _status(status, dev)
+    if T:
+        rc = _call.paged_append_run(
+            _append_params(B, sq, total, Hq, Hkv, D, ps, P, combined, cols, rotary,
+                           ROPE_LAYOUT[layout], attention_factor, _DTYPE[dt], qt, kt, vt),
+            qp, k.data_ptr(), v.data_ptr(), qo, indptr, pages, lens, table, qop, kc, vc, status,
+            _stream(stream, dev))
+        if rc:
+            _check(rc, "paged_append_run")
     return q_out
 
 
@@ -355,19 +420,26 @@ class CachePools:
         layers = list(layers)
         if not layers:
             raise ValueError("no layers")
-        got = [_geometry(c) for c in layers]
+        dev = _device()
+        got = [_geometry(c, dev) for c in layers]
         if any(g[2:] != got[0][2:] for g in got):
             raise ValueError("the layers' pools must have the same shape")
         ptrs = [p for g in got for p in g[:2] if p is not None]
         if len(ptrs) > MAX_POOLS:
             raise ValueError(f"more than {MAX_POOLS} pools")
-        self.layers = layers
-        self.device = (layers[0][0] if isinstance(layers[0], (tuple, list)) else layers[0]).device
+        self.layers, self.device_index = layers, dev
         _, _, combined, self.num_pages, Hkv, self.page_size, D = got[0]
         self._ptrs = (C.c_void_p * len(ptrs))(*ptrs)
         self.struct = CachePoolsStruct(num_layers=len(layers), num_pages=self.num_pages,
                                        num_kv_heads=Hkv, page_size=self.page_size, head_dim=D,
                                        combined_cache=combined, pools_host=self._ptrs)
+        self._ref = C.byref(self.struct)
+
+    def ref(self, dev):
+        """The C struct, for a call on the current device."""
+        if self.device_index != dev:
+            raise ValueError("the pools are not on the current device")
+        return self._ref
 
 
 def cache_pools(layers) -> CachePools:
@@ -376,26 +448,29 @@ def cache_pools(layers) -> CachePools:
     return CachePools(layers)
 
 
-def _rows_state(block_tables, seq_lens, page_refs, page_size):
-    if block_tables.dim() != 2:
+def _rows_state(block_tables, seq_lens, page_refs, page_size, dev):
+    """(params, address of the tables, lengths, counts) of the three arrays."""
+    shape = block_tables.shape
+    if len(shape) != 2:
         raise ValueError("block_tables must be [rows, C]")
-    R, cols = block_tables.shape
-    p = CacheParams(rows=R, max_pages_per_request=cols, page_size=page_size,
-                    num_pages=page_refs.numel())
-    return (p, _ints(block_tables, "block_tables"), _ints(seq_lens, "seq_lens", R),
-            _ints(page_refs, "page_refs"))
+    return (_cache_params(shape[0], shape[1], page_size, page_refs.numel()),
+            _ints(block_tables, dev, "block_tables"),
+            _ints_of(seq_lens, dev, "seq_lens", shape[0]), _ints(page_refs, dev, "page_refs"))
 
 
 def free_cache_rows(rows, block_tables, seq_lens, page_refs, page_size, *, status=None,
                     stream=None) -> None:
     """Free the listed rows: their pages' counts go down by one, their lengths to 0."""
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size)
-    _check(_lib().paged_cache_free_run(C.byref(p), _ints(rows, "rows"), rows.numel(), bt, sl, pr,
-                                       _status(status), _stream(stream)), "paged_cache_free_run")
+    dev = _device()
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
+    rc = _call.paged_cache_free_run(p, _ints(rows, dev, "rows"), rows.numel(), bt, sl, pr,
+                                    _status(status, dev), _stream(stream, dev))
+    if rc:
+        _check(rc, "paged_cache_free_run")
 
 
 def extend_cache_workspace_size(n: int) -> int:
-    return int(_lib().paged_cache_extend_workspace_size(int(n)))
+    return int(_call.paged_cache_extend_workspace_size(int(n)))
 
 
 def extend_cache_rows(rows, new_tokens, block_tables, seq_lens, page_refs, page_size, *,
@@ -403,53 +478,63 @@ def extend_cache_rows(rows, new_tokens, block_tables, seq_lens, page_refs, page_
     """Make each listed row longer by new_tokens tokens, with fresh pages (the lowest free ids,
     in the order listed) where needed.  Rows that the free pages do not suffice for stay as
     they are; the workspace's status word says so."""
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size)
+    dev = _device()
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
     n = rows.numel()
-    ws = _workspace(workspace, extend_cache_workspace_size(n), rows.device)
-    _check(_lib().paged_cache_extend_run(C.byref(p), _ints(rows, "rows"),
-                                         _ints(new_tokens, "new_tokens", n), n, bt, sl, pr,
-                                         ws.data_ptr(), _nbytes(ws), _stream(stream)),
-           "paged_cache_extend_run")
+    ws = _workspace(workspace, extend_cache_workspace_size, n, rows, dev)
+    rc = _call.paged_cache_extend_run(p, _ints(rows, dev, "rows"),
+                                      _ints_of(new_tokens, dev, "new_tokens", n), n, bt, sl, pr,
+                                      ws.data_ptr(), ws.nbytes, _stream(stream, dev))
+    if rc:
+        _check(rc, "paged_cache_extend_run")
 
 
 def fork_cache_workspace_size(n: int) -> int:
-    return int(_lib().paged_cache_fork_workspace_size(int(n)))
+    return int(_call.paged_cache_fork_workspace_size(int(n)))
 
 
 def fork_cache_rows(pools, parents, children, block_tables, seq_lens, page_refs, *,
                     workspace=None, stream=None) -> None:
     """Make the (empty) row children[i] a copy of row parents[i]: full pages are shared, the
     live tokens of a partly filled last page are copied into a fresh one, in every layer."""
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size)
+    dev = _device()
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
     n = children.numel()
-    ws = _workspace(workspace, fork_cache_workspace_size(n), children.device)
-    _check(_lib().paged_cache_fork_run(C.byref(p), C.byref(pools.struct),
-                                       _ints(parents, "parents", n),
-                                       _ints(children, "children"), n, bt, sl, pr,
-                                       ws.data_ptr(), _nbytes(ws), _stream(stream)),
-           "paged_cache_fork_run")
+    ws = _workspace(workspace, fork_cache_workspace_size, n, children, dev)
+    rc = _call.paged_cache_fork_run(p, pools.ref(dev), _ints_of(parents, dev, "parents", n),
+                                    _ints(children, dev, "children"), n, bt, sl, pr,
+                                    ws.data_ptr(), ws.nbytes, _stream(stream, dev))
+    if rc:
+        _check(rc, "paged_cache_fork_run")
 
 
 def compact_cache_workspace_size(num_pages: int) -> int:
-    return int(_lib().paged_cache_compact_workspace_size(int(num_pages)))
+    return int(_call.paged_cache_compact_workspace_size(int(num_pages)))
 
 
 def compact_cache(pools, block_tables, seq_lens, page_refs, *, block_tables_out=None,
                   page_refs_out=None, num_live=None, workspace=None, stream=None):
     """Move the live pages to the pools' front, in every layer; returns (block_tables, page_refs,
     num_live [1]) after the move.  In place unless the *_out tensors are given."""
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size)
-    tables = block_tables if block_tables_out is None else block_tables_out
-    refs = page_refs if page_refs_out is None else page_refs_out
+    dev = _device()
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
+    tables, refs, bto, pro = block_tables, page_refs, bt, pr
+    if block_tables_out is not None:
+        tables = block_tables_out
+        if tables.shape != block_tables.shape:
+            raise ValueError("block_tables_out must have block_tables' shape")
+        bto = _ints(tables, dev, "block_tables_out")
+    if page_refs_out is not None:
+        refs = page_refs_out
+        pro = _ints_of(refs, dev, "page_refs_out", page_refs.numel())
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=page_refs.device)
-    ws = _workspace(workspace, compact_cache_workspace_size(p.num_pages), page_refs.device)
-    _check(_lib().paged_cache_compact_run(C.byref(p), C.byref(pools.struct), bt, sl, pr,
-                                          _ints(tables, "block_tables_out", block_tables.numel()),
-                                          _ints(refs, "page_refs_out", page_refs.numel()),
-                                          _ints(num_live, "num_live", 1), ws.data_ptr(),
-                                          _nbytes(ws), _stream(stream)),
-           "paged_cache_compact_run")
+        num_live = torch.empty(1, dtype=_I32, device=page_refs.device)
+    ws = _workspace(workspace, compact_cache_workspace_size, page_refs.numel(), page_refs, dev)
+    rc = _call.paged_cache_compact_run(p, pools.ref(dev), bt, sl, pr, bto, pro,
+                                       _ints_of(num_live, dev, "num_live", 1), ws.data_ptr(),
+                                       ws.nbytes, _stream(stream, dev))
+    if rc:
+        _check(rc, "paged_cache_compact_run")
     return tables, refs, num_live
 
 
@@ -457,12 +542,15 @@ def copy_cache_pages(pools, src_pages, dst_pages, *, dst_pools=None, status=None
                      stream=None) -> None:
     """Copy page src_pages[i] to page dst_pages[i] in every layer, within `pools` or to the same
     layers of `dst_pools`."""
-    dst = pools if dst_pools is None else dst_pools
+    dev = _device()
+    src = pools.ref(dev)
     n = src_pages.numel()
-    _check(_lib().paged_cache_copy_run(C.byref(pools.struct), C.byref(dst.struct),
-                                       _ints(src_pages, "src_pages"),
-                                       _ints(dst_pages, "dst_pages", n), n, _status(status),
-                                       _stream(stream)), "paged_cache_copy_run")
+    rc = _call.paged_cache_copy_run(src, src if dst_pools is None else dst_pools.ref(dev),
+                                    _ints(src_pages, dev, "src_pages"),
+                                    _ints_of(dst_pages, dev, "dst_pages", n), n,
+                                    _status(status, dev), _stream(stream, dev))
+    if rc:
+        _check(rc, "paged_cache_copy_run")
 
 
 __all__ = ["rope_frequencies", "rotary_embedding", "append_paged_kv_cache", "CachePools",

@@ -20,8 +20,13 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;            // portable cluster size
-constexpr int kSmallPages = 8192;          // up to here one CTA plans alone
+constexpr int kStepPages = 4096;           // pages that one CTA counts at a time
 constexpr int kMaxPages = 1 << 24;
+constexpr int kMaxItems = 4096;            // a thread of the planning CTA holds 4 of them
+// Shared memory of a planning kernel at most: items, the hash table of their rows, page counts.
+constexpr int kPlanSmem = (4 * kMaxItems + 4 * kMaxItems +
+                           (kMaxPages / kStepPages / kPlanCluster) * 33 + kMaxPages / kStepPages) * 4;
+static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
 
@@ -29,118 +34,140 @@ struct Pools {
   void* p[PAGED_CACHE_MAX_POOLS];
 };
 
-// ---- scans over the cluster ------------------------------------------------------------------
+// ---- free pages in order, over a cluster -------------------------------------------------------
 // Sums saturate at kManyPages, far above any pool's page count, so that absurd demands cannot
 // wrap around into served ones (summands are at most kMaxPages + 1, so a saturated exclusive
 // prefix is still above every page count).
 constexpr int kManyPages = 1 << 29;
 __device__ __forceinline__ int add_pages(int a, int b) { return min(a + b, kManyPages); }
 
-// Prefix sum over the CTA; returns this thread's exclusive prefix, *total the sum.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
+__device__ __forceinline__ int warp_inclusive(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const int y = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v = add_pages(v, y);
   }
+  return v;
+}
+// Prefix sum over the CTA; returns this thread's exclusive prefix, *total the sum.
+__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = warp_inclusive(x);
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
+  const int w = warp_inclusive(warp_sums[lane]);       // every warp scans the 32 sums itself
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  __syncthreads();
+  return (warp > 0 ? before : 0) + v - x;
+}
+
+// A barrier over the cluster, with its memory; a plain one where the cluster is one CTA.
+__device__ __forceinline__ void sync_cluster(cg::cluster_group& cl) {
+  if (cl.num_blocks() == 1) __syncthreads();
+  else cl.sync();
+}
+
+// The page counts [0, P) are cut into steps of 4096 pages; step g belongs to CTA g % size, and
+// thread t of it holds pages 4 t .. 4 t + 3, so loads coalesce and the order of (step, thread,
+// page) is the order of page ids.  The CTAs interleave so that a demand met by the lowest pages
+// is still handed out by all of them.
+struct FreePages {
+  const int* refs;
+  int P, rank, size, steps, own;     // steps in all, steps of this CTA
+  bool aligned;
+  uint32_t kept;                     // which of the thread's 4 pages are free, first 8 own steps
+  int* warp_before;                  // shared [own, 32]: free pages of the step before a warp
+  int* step_total;                   // shared [own]
+  int* step_before;                  // shared [steps]: free pages before a step
+  int total;                         // free pages
+
+  static __host__ __device__ int steps_of(int P) { return (P + kStepPages - 1) / kStepPages; }
+  static __host__ size_t shared_ints(int P, int size) {
+    const int own = (steps_of(P) + size - 1) / size;
+    return static_cast<size_t>(own) * 33 + steps_of(P);
+  }
+
+  __device__ __forceinline__ int first_page(int j) const {
+    return (j * size + rank) * kStepPages + 4 * static_cast<int>(threadIdx.x);
+  }
+  // Counts of the thread's pages in its j-th step (1, that is not free, past the end).
+  __device__ __forceinline__ int4 load(int j) const {
+    const int p = first_page(j);
+    if (aligned && p + 3 < P) return *reinterpret_cast<const int4*>(refs + p);
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p < P) r.x = refs[p];
+    if (p + 1 < P) r.y = refs[p + 1];
+    if (p + 2 < P) r.z = refs[p + 2];
+    if (p + 3 < P) r.w = refs[p + 3];
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t mask_of(const int4& r) {
+    return (r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) | (r.w == 0 ? 8u : 0u);
+  }
+  // Which of the thread's pages of its j-th step are free (as they were at count()).
+  __device__ __forceinline__ uint32_t mask(int j) const {
+    return j < 8 ? (kept >> (4 * j)) & 15u : mask_of(load(j));
+  }
+
+  // Count the CTA's own steps (before the cluster barrier).
+  __device__ void count(const int* counts, int num_pages, int cta, int ctas, int* shared) {
+    refs = counts;
+    P = num_pages;
+    rank = cta;
+    size = ctas;
+    steps = steps_of(P);
+    own = (steps - rank + size - 1) / size;
+    aligned = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
+    kept = 0;
+    const int room = (steps + size - 1) / size;
+    warp_before = shared;
+    step_total = warp_before + room * 32;
+    step_before = step_total + room;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j0 = 0; j0 < own; j0 += 4) {
+      int4 r[4];
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w = add_pages(w, y);
+      for (int u = 0; u < 4; ++u) r[u] = j0 + u < own ? load(j0 + u) : make_int4(1, 1, 1, 1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + u;
+        if (j >= own) break;
+        const uint32_t m = mask_of(r[u]);
+        if (j < 8) kept |= m << (4 * j);
+        const int n = __reduce_add_sync(0xffffffffu, __popc(m));
+        if (lane == 0) warp_before[j * 32 + warp] = n;
+      }
     }
-    warp_sums[lane] = w;
+    __syncthreads();
+    for (int j = warp; j < own; j += 32) {
+      const int n = warp_before[j * 32 + lane], v = warp_inclusive(n);
+      warp_before[j * 32 + lane] = v - n;
+      if (lane == 31) step_total[j] = v;
+    }
   }
-  __syncthreads();
-  const int before = warp > 0 ? warp_sums[warp - 1] : 0;
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + v - x;
-}
-
-// The page counts [0, P) are split over the CTAs in segments of whole 4096-page steps: thread t
-// of a step holds pages 4 t .. 4 t + 3, so loads coalesce and the order of (step, thread, page)
-// is the order of page ids.
-struct Segment {
-  int first, last, steps;
+  // Put the steps of all CTAs in order (after the cluster barrier).
+  __device__ void order(cg::cluster_group& cl, int* warp_sums) {
+    int carry = 0;
+    for (int g0 = 0; g0 < steps; g0 += kPlanThreads) {
+      const int g = g0 + threadIdx.x;
+      const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
+      int sum;
+      const int before = block_scan(n, warp_sums, &sum);
+      if (g < steps) step_before[g] = carry + before;
+      carry += sum;
+    }
+    total = carry;
+    __syncthreads();
+  }
+  // Free pages before the thread's first page of its j-th step (whole warps).
+  __device__ __forceinline__ int before(int j, uint32_t m) const {
+    const int n = __popc(m);
+    return step_before[j * size + rank] + warp_before[j * 32 + (threadIdx.x >> 5)] +
+           warp_inclusive(n) - n;
+  }
 };
-__device__ __forceinline__ Segment page_segment(int P, int rank, int size) {
-  const int all = (P + 4095) / 4096;
-  const int each = (all + size - 1) / size;
-  Segment s;
-  s.first = min(P, rank * each * 4096);
-  s.last = min(P, (rank + 1) * each * 4096);
-  s.steps = (s.last - s.first + 4095) / 4096;
-  return s;
-}
-// Counts of pages p .. p + 3 (aligned loads; 1, that is not free, past the end).
-__device__ __forceinline__ int4 load_refs(const int* refs, int p, int last, bool aligned) {
-  int4 r = make_int4(1, 1, 1, 1);
-  if (aligned && p + 3 < last) return *reinterpret_cast<const int4*>(refs + p);
-  if (p < last) r.x = refs[p];
-  if (p + 1 < last) r.y = refs[p + 1];
-  if (p + 2 < last) r.z = refs[p + 2];
-  if (p + 3 < last) r.w = refs[p + 3];
-  return r;
-}
-__device__ __forceinline__ int free_of(const int4& r) {
-  return (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-}
-
-// Free pages of the CTA's segment per (step, warp), turned into exclusive prefixes within the
-// segment; returns the segment's total.
-__device__ int scan_segment(const int* refs, const Segment& s, bool aligned, int* step_warp,
-                            int* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = 0; i < s.steps; ++i) {
-    const int4 r = load_refs(refs, s.first + i * 4096 + 4 * threadIdx.x, s.last, aligned);
-    const int n = __reduce_add_sync(0xffffffffu, free_of(r));
-    if (lane == 0) step_warp[i * 32 + warp] = n;
-  }
-  __syncthreads();
-  int carry = 0;
-  for (int i0 = 0; i0 < s.steps * 32; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
-    const int x = i < s.steps * 32 ? step_warp[i] : 0;
-    int total;
-    const int before = block_scan(x, warp_sums, &total);
-    if (i < s.steps * 32) step_warp[i] = carry + before;
-    carry += total;
-  }
-  __syncthreads();
-  return carry;
-}
-// Free pages of this thread's warp before the thread.
-__device__ __forceinline__ int free_before_in_warp(int mine) {
-  const int lane = threadIdx.x & 31;
-  int v = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += y;
-  }
-  return v - mine;
-}
-
-// Sums of one int per CTA over the cluster: the CTAs before this one, and all.
-struct Totals {
-  int before, all;
-};
-__device__ __forceinline__ Totals cluster_totals(cg::cluster_group& cl, int* slot) {
-  Totals t{0, 0};
-  const int rank = cl.block_rank(), size = cl.num_blocks();
-  for (int r = 0; r < size; ++r) {
-    const int x = *cl.map_shared_rank(slot, r);
-    if (r < rank) t.before = add_pages(t.before, x);
-    t.all = add_pages(t.all, x);
-  }
-  return t;
-}
 
 // ---- extend and fork: who gets which fresh page ------------------------------------------------
 struct PlanArgs {
@@ -152,122 +179,160 @@ struct PlanArgs {
   int* lens;
   int* refs;
   int R, C, ps, P;
+  int hash;                // entries of the table of rows seen, a power of two >= 2 n
   uint32_t* status;
-  int* off;                // workspace [n]: first fresh page of the item among all demands
-  int* need;               // workspace [n]: pages; -1: the item is left out
-  int* len;                // workspace [n]: the row's (parent's) length before the call
+  int* need;               // workspace [n], fork: 0, 1 or -1 (left out)
+  int* len;                // workspace [n], fork: the parent's length before the call
   int* page;               // workspace [n], fork: the fresh page of the item, -1 none
 };
+struct Item {
+  int off;                 // first fresh page of the item among all demands
+  int need;                // pages (0: none, or left out)
+  int have;                // pages of the row before the call
+  int row;
+};
 
+// CTA 0 looks after the items, all CTAs after the pages.  Latency bounds this kernel: the chain
+// is rows -> lengths -> scan -> cluster barrier -> tables, with the counts read beside it.
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
-  extern __shared__ int step_warp[];
+  extern __shared__ __align__(16) int shared[];
   __shared__ int warp_sums[32];
-  __shared__ int total_free, total_need;
+  __shared__ int total_need;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
   const int tid = threadIdx.x;
-  if (rank == 0 && tid < 4) a.status[tid] = 0;
-  // this CTA's items, in order
-  const int each = (a.n + size - 1) / size;
-  const int i0 = min(a.n, rank * each), i1 = min(a.n, i0 + each);
+  Item* items = reinterpret_cast<Item*>(shared);
+  int* keys = reinterpret_cast<int*>(items + a.n);             // CTA 0: rows seen, their first item
+  int* offs = keys;                                            // later: a copy of every Item::off
+  int* pages_shared = keys + 2 * a.hash;
+  constexpr int kPer = kMaxItems / kPlanThreads;
+  int L[kPer];                                                 // CTA 0: lengths of its items
   uint32_t bits = 0;
-  for (int i = i0 + tid; i < i1; i += kPlanThreads) {
-    const int row = a.rows[i];
-    int need = -1, L = 0;
-    if (row >= 0 && row < a.R) {
+  FreePages pages;
+  if (rank == 0) {
+    if (tid < 4) a.status[tid] = 0;
+    int* first = keys + a.hash;
+    for (int i = tid; i < a.hash; i += kPlanThreads) {
+      keys[i] = -1;
+      first[i] = a.n;
+    }
+    __syncthreads();
+    int row[kPer], need[kPer], at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kPlanThreads + tid;
+      if (j * kPlanThreads >= a.n) break;
+      row[j] = i < a.n ? a.rows[i] : -1;
+      need[j] = -1;
+      at[j] = L[j] = 0;
+      if (row[j] < 0 || row[j] >= a.R) continue;
       if (kFork) {
         const int parent = a.parents[i];
-        if (parent >= 0 && parent < a.R && parent != row && a.lens[row] == 0) {
-          L = a.lens[parent];
-          if (L >= 0 && (L + a.ps - 1LL) / a.ps <= a.C) need = L % a.ps > 0;
-        }
+        if (parent < 0 || parent >= a.R || parent == row[j]) continue;
+        const int own_len = a.lens[row[j]];
+        L[j] = a.lens[parent];
+        if (own_len == 0 && L[j] >= 0 && (L[j] + a.ps - 1LL) / a.ps <= a.C) need[j] = L[j] % a.ps > 0;
       } else {
-        L = a.lens[row];
         const int more = a.new_tokens[i];
-        if (L >= 0 && more >= 0) {
-          const long long have = (L + a.ps - 1LL) / a.ps;
-          const long long want = (static_cast<long long>(L) + more + a.ps - 1) / a.ps;
-          if (want <= a.C) need = static_cast<int>(want - have);
-        }
+        L[j] = a.lens[row[j]];
+        if (L[j] < 0 || more < 0) continue;
+        const long long have = (L[j] + a.ps - 1LL) / a.ps;
+        const long long want = (static_cast<long long>(L[j]) + more + a.ps - 1) / a.ps;
+        if (want <= a.C) need[j] = static_cast<int>(want - have);
       }
     }
-    if (need < 0) bits |= kErrMetadata;
-    a.need[i] = need;
-    a.len[i] = L;
-    if (kFork) a.page[i] = -1;
-  }
-  // Free pages of the segment, while the items' lengths are on their way.
-  const Segment seg = page_segment(a.P, rank, size);
-  const bool aligned = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
-  const int my_free = scan_segment(a.refs, seg, aligned, step_warp, warp_sums);
-  cl.sync();
-  // A row listed more than once belongs to its first item: the lengths of the listed rows hold
-  // the smallest i - n for a moment (every length has been read).
-  for (int i = i0 + tid; i < i1; i += kPlanThreads)
-    if (a.need[i] >= 0) atomicMin(a.lens + a.rows[i], i - a.n);
-  cl.sync();
-  int carry = 0;
-  for (int b = i0; b < i1; b += kPlanThreads) {
-    const int i = b + tid;
-    int need = i < i1 ? a.need[i] : -1;
-    if (need >= 0 && atomicAdd(a.lens + a.rows[i], 0) != i - a.n) {
-      need = a.need[i] = -1;
-      bits |= kErrMetadata;
-    }
-    int total;
-    const int before = block_scan(min(max(need, 0), kMaxPages + 1), warp_sums, &total);
-    if (i < i1) a.off[i] = add_pages(carry, before);
-    carry = add_pages(carry, total);
-  }
-  if (tid == 0) {
-    total_free = my_free;
-    total_need = carry;
-  }
-  cl.sync();
-  const Totals free = cluster_totals(cl, &total_free), demand = cluster_totals(cl, &total_need);
-  for (int i = i0 + tid; i < i1; i += kPlanThreads) {
-    const int need = a.need[i];
-    const int off = add_pages(a.off[i], demand.before);
-    a.off[i] = off;
-    if (need < 0) continue;
-    const bool served = need == 0 || static_cast<long long>(off) + need <= free.all;
-    const int L = a.len[i];
-    if (!served) {
-      bits |= kErrCapacity;
-      a.need[i] = -1;
-    }
-    a.lens[a.rows[i]] = kFork ? (served ? L : 0) : (served ? L + a.new_tokens[i] : L);
-  }
-  if (bits) report_error(a.status, bits);
-  cl.sync();
-  // The k-th free page goes to the item whose demands [off, off + need) hold k.
-  const int warp = tid >> 5;
-  for (int s = 0; s < seg.steps; ++s) {
-    const int p0 = seg.first + s * 4096 + 4 * tid;
-    const int4 r = load_refs(a.refs, p0, seg.last, aligned);
-    int k = free.before + step_warp[s * 32 + warp] + free_before_in_warp(free_of(r));
-    const int c[4] = {r.x, r.y, r.z, r.w};
+    // A row listed more than once belongs to its first item that is in order.
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (c[j] != 0) continue;
-      const int rank_k = k++;
-      if (rank_k >= demand.all) continue;
-      int lo = 0, hi = a.n;                    // last item with off <= k and a demand
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.off[mid] <= rank_k) lo = mid; else hi = mid;
+    for (int j = 0; j < kPer; ++j) {
+      if (j * kPlanThreads >= a.n) break;
+      if (need[j] < 0) continue;
+      int h = static_cast<int>((static_cast<unsigned>(row[j]) * 2654435769u) >> 8) & (a.hash - 1);
+      while (true) {                                           // ends: at most half the table is used
+        const int key = atomicCAS(keys + h, -1, row[j]);
+        if (key == -1 || key == row[j]) break;
+        h = (h + 1) & (a.hash - 1);
       }
-      // items without a demand share their successor's offset: the last one found owns k
-      const int need = a.need[lo];
-      if (need < 0 || rank_k - a.off[lo] >= need) continue;
-      const int row = a.rows[lo], have = kFork ? a.len[lo] / a.ps : (a.len[lo] + a.ps - 1) / a.ps;
-      a.tables[static_cast<long long>(row) * a.C + have + rank_k - a.off[lo]] = p0 + j;
-      a.refs[p0 + j] = 1;
-      if (kFork) a.page[lo] = p0 + j;
+      atomicMin(first + h, j * kPlanThreads + tid);
+      at[j] = h;
+    }
+    __syncthreads();
+    int carry = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kPlanThreads + tid;
+      if (j * kPlanThreads >= a.n) break;
+      if (need[j] >= 0 && first[at[j]] != i) need[j] = -1;
+      if (need[j] < 0 && i < a.n) bits |= kErrMetadata;
+      const int pages_needed = min(max(need[j], 0), kMaxPages + 1);
+      int sum;
+      const int before = add_pages(carry, block_scan(pages_needed, warp_sums, &sum));
+      carry = add_pages(carry, sum);
+      if (i < a.n)
+        items[i] = {before, pages_needed, kFork ? L[j] / a.ps : static_cast<int>((L[j] + a.ps - 1LL) / a.ps),
+                    need[j] < 0 ? -1 : row[j]};
+    }
+    if (tid == 0) total_need = carry;
+  }
+  pages.count(a.refs, a.P, rank, size, pages_shared);
+  sync_cluster(cl);
+  pages.order(cl, warp_sums);
+  const int demand = *cl.map_shared_rank(&total_need, 0);
+  const Item* from = cl.map_shared_rank(items, 0);
+  if (rank == 0) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kPlanThreads + tid;
+      if (j * kPlanThreads >= a.n) break;
+      if (i >= a.n) continue;
+      const Item it = items[i];
+      const bool served = it.row >= 0 && (it.need == 0 || it.off + it.need <= pages.total);
+      if (it.row >= 0 && !served) bits |= kErrCapacity;
+      if (served) a.lens[it.row] = kFork ? L[j] : L[j] + a.new_tokens[i];
+      if (kFork) {
+        a.need[i] = served ? it.need : -1;
+        a.len[i] = L[j];
+        if (it.need == 0 || !served) a.page[i] = -1;
+      }
+    }
+    if (bits) report_error(a.status, bits);
+  }
+  const int handed = min(demand, pages.total);
+  if (handed > 0) {
+    for (int i = tid; i < a.n; i += kPlanThreads) offs[i] = from[i].off;
+    __syncthreads();
+    // The k-th free page goes to the item whose demands [off, off + need) hold k.
+    Item it{0, 0, 0, -1};
+    int which = -1;
+    for (int j = 0; j < pages.own; ++j) {
+      if (pages.step_before[j * size + rank] >= handed) break;
+      const uint32_t m = pages.mask(j);
+      int k = pages.before(j, m);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (!(m >> b & 1u)) continue;
+        const int mine = k++;
+        if (mine >= handed) continue;
+        if (which < 0 || mine - it.off >= it.need) {
+          // the last item with off <= k: items without a demand share their successor's offset
+          int lo = max(which, 0), hi = a.n;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (offs[mid] <= mine) lo = mid; else hi = mid;
+          }
+          which = lo;
+          it = from[lo];
+        }
+        if (it.row < 0 || it.off + it.need > pages.total) continue;
+        const int p = pages.first_page(j) + b;
+        a.tables[static_cast<long long>(it.row) * a.C + it.have + (mine - it.off)] = p;
+        a.refs[p] = 1;
+        if (kFork) a.page[which] = p;
+      }
     }
   }
   grid_launch_dependents();
+  if (size > 1) cl.sync();                 // the items in CTA 0's shared memory have been read
 }
 
 // ---- copies ----------------------------------------------------------------------------------
@@ -305,7 +370,7 @@ struct CopyArgs {
   int chunks;                // of kCopyChunk bytes per page
   uint32_t* status;
   // compact: table entries to rename
-  const int *tables, *lens, *to;
+  const int *tables, *lens, *to, *num_live;
   int* tables_out;
   int R, C, ps, P;
 };
@@ -320,7 +385,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     const long long w = u / a.chunks;
     const int pool = static_cast<int>(w % a.pools);
     const int i = static_cast<int>(w / a.pools);
-    const int s = a.src_pages[i], d = a.dst_pages[i];
+    const int s = a.src_pages[kCompact ? n - 1 - i : i], d = a.dst_pages[i];
     if (s < 0 || s >= a.src_num_pages || d < 0 || d >= a.dst_num_pages) {
       if (threadIdx.x == 0) report_error(a.status, kErrMetadata);
       continue;
@@ -334,6 +399,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
                bytes / 16);
   }
   if (kCompact) {
+    const int live = *a.num_live;
     const long long entries = static_cast<long long>(a.R) * a.C;
     for (long long e = blockIdx.x * static_cast<long long>(kCopyThreads) + threadIdx.x; e < entries;
          e += static_cast<long long>(gridDim.x) * kCopyThreads) {
@@ -342,8 +408,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       int p = a.tables[e];
       const int old = p;
       if (j < (L + a.ps - 1LL) / a.ps) {
-        if (p >= 0 && p < a.P) p = a.to[p];
-        else report_error(a.status, kErrMetadata);
+        if (p < 0 || p >= a.P) report_error(a.status, kErrMetadata);
+        else if (p >= live) p = a.to[p];
       }
       if (j == 0 && (L + a.ps - 1LL) / a.ps > a.C) report_error(a.status, kErrMetadata);
       if (p != old || a.tables_out != a.tables) a.tables_out[e] = p;
@@ -435,76 +501,57 @@ struct CompactArgs {
   int* refs_out;
   int* num_live;
   int P;
-  int *src, *dst, *to, *moves;   // workspace: move lists, new id of every page, their number
+  int *src, *dst, *to, *moves;   // workspace: move lists, new ids of pages >= live, their number
   uint32_t* status;
 };
 
 __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs a) {
-  extern __shared__ int step_warp[];
+  extern __shared__ __align__(16) int shared[];
   __shared__ int warp_sums[32];
-  __shared__ int total_free, total_holes;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x;
   if (rank == 0 && tid < 4) a.status[tid] = 0;
-  const Segment seg = page_segment(a.P, rank, size);
-  const bool aligned = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
-  const int my_free = scan_segment(a.refs, seg, aligned, step_warp, warp_sums);
-  if (tid == 0) {
-    total_free = my_free;
-    total_holes = 0;
+  FreePages pages;
+  pages.count(a.refs, a.P, rank, size, shared);
+  sync_cluster(cl);
+  pages.order(cl, warp_sums);
+  const int live = a.P - pages.total;
+  if (rank == 0 && tid == 0) {
+    *a.num_live = live;
+    if (live == a.P) *a.moves = 0;
   }
-  cl.sync();
-  const Totals free = cluster_totals(cl, &total_free);
-  const int live = a.P - free.all;
-  // holes of this CTA: free pages below `live`
-  int holes = 0;
-  for (int s = 0; s < seg.steps; ++s) {
-    const int p0 = seg.first + s * 4096 + 4 * tid;
-    const int4 r = load_refs(a.refs, p0, seg.last, aligned);
-    const int c[4] = {r.x, r.y, r.z, r.w};
+  // f free and p - f live pages lie before page p.  The f-th hole is p; of the live pages that
+  // move, live - 1 - (p - f) come after p, which numbers them without knowing how many they are.
+  for (int j = 0; j < pages.own; ++j) {
+    const uint32_t m = pages.mask(j);
+    int f = pages.before(j, m);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) holes += c[j] == 0 && p0 + j < live;
-  }
-  holes = __reduce_add_sync(0xffffffffu, holes);
-  if ((tid & 31) == 0 && holes) atomicAdd(&total_holes, holes);
-  cl.sync();
-  const int H = cluster_totals(cl, &total_holes).all;   // holes below, and live pages above
-  for (int s = 0; s < seg.steps; ++s) {
-    const int p0 = seg.first + s * 4096 + 4 * tid;
-    const int4 r = load_refs(a.refs, p0, seg.last, aligned);
-    int f = free.before + step_warp[s * 32 + warp] + free_before_in_warp(free_of(r));
-    const int c[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p = p0 + j;
-      if (p >= seg.last) continue;
-      if (c[j] == 0) {
+    for (int b = 0; b < 4; ++b) {
+      const int p = pages.first_page(j) + b;
+      if (p >= a.P) break;
+      const bool is_free = m >> b & 1u;
+      if (p == live) *a.moves = f;                  // holes below `live` = live pages from it on
+      if (is_free) {
         if (p < live) a.dst[f] = p;
+        else a.to[p] = p;
         ++f;
       } else if (p >= live) {
-        a.src[p - f - (live - H)] = p;       // p - f live pages lie before p, live - H below `live`
+        a.src[live - 1 - (p - f)] = p;
       }
+      if (a.refs_out != a.refs && is_free == (p >= live)) a.refs_out[p] = is_free ? 0 : a.refs[p];
     }
   }
-  if (rank == 0 && tid == 0) {
-    *a.moves = H;
-    *a.num_live = live;
-  }
-  cl.sync();
-  // new ids and counts (every count has been read)
-  const int i0 = rank * kPlanThreads + tid, stride = size * kPlanThreads;
-  for (int p = i0; p < a.P; p += stride) a.to[p] = p;
-  if (a.refs_out != a.refs)
-    for (int p = i0; p < a.P; p += stride) a.refs_out[p] = a.refs[p];
-  cl.sync();
-  for (int k = i0; k < H; k += stride) {
-    const int s = a.src[k], d = a.dst[k];
+  sync_cluster(cl);
+  const int moves = *a.moves;
+  for (int k = rank * kPlanThreads + tid; k < moves; k += size * kPlanThreads) {
+    const int s = a.src[moves - 1 - k], d = a.dst[k];
     a.to[s] = d;
     a.refs_out[d] = a.refs[s];
     a.refs_out[s] = 0;
   }
   grid_launch_dependents();
+  if (size > 1) cl.sync();                 // the step totals have been read
 }
 
 // ---- host --------------------------------------------------------------------------------------
@@ -519,11 +566,10 @@ struct Take {
 int* at(void* ws, size_t off) { return reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + off); }
 
 struct PlanLayout {
-  size_t status, off, need, len, page, total;
+  size_t status, need, len, page, total;
   explicit PlanLayout(int n) {
     Take t;
     status = t.ints(4);
-    off = t.ints(n);
     need = t.ints(n);
     len = t.ints(n);
     page = t.ints(n);
@@ -577,16 +623,21 @@ bool overlap(const void* a, long long na, const void* b, long long nb) {
 }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA; }
 
-// Launch one of the planning kernels as a single cluster (one CTA for small pools).
+// CTAs that look through P page counts: one per two steps, up to the portable cluster size.
+int plan_ctas(int P) {
+  int size = 1;
+  while (size < kPlanCluster && size * 2 * kStepPages < P) size *= 2;
+  return size;
+}
+
+// Launch one of the planning kernels as a single cluster; `ints` of shared memory besides the
+// page counts'.
 template <typename Args>
-cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, std::atomic<uint64_t>& ready,
-                        cudaStream_t st) {
-  const int size = P <= kSmallPages ? 1 : kPlanCluster;
-  const int each = ceil_div(ceil_div(P, 4096), size);
-  const size_t smem = static_cast<size_t>(each) * 32 * sizeof(int);
-  if (!kernel_smem_ready(kernel, kMaxPages / kPlanCluster / 128 * static_cast<int>(sizeof(int)),
-                         ready))
-    return cudaErrorUnknown;
+cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, size_t ints,
+                        std::atomic<uint64_t>& ready, cudaStream_t st) {
+  const int size = plan_ctas(P);
+  const size_t smem = (FreePages::shared_ints(P, size) + ints) * sizeof(int);
+  if (smem > 48 * 1024 && !kernel_smem_ready(kernel, kPlanSmem, ready)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = size;
   cfg.blockDim = kPlanThreads;
@@ -600,6 +651,14 @@ cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, std::atomic<
   cfg.numAttrs = 1;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool kFork>
+cudaError_t launch_items(PlanArgs a, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  a.hash = 2;
+  while (a.hash < 2 * a.n) a.hash *= 2;
+  return launch_plan(plan_kernel<kFork>, a, a.P, 4 * static_cast<size_t>(a.n) + 2 * a.hash, ready, st);
 }
 
 }  // namespace
@@ -622,8 +681,12 @@ int paged_cache_free_run(const paged_cache_params* p, const int32_t* rows, int n
   return cuda_status(cudaGetLastError());
 }
 
-size_t paged_cache_extend_workspace_size(int n) { return n < 0 ? 0 : PlanLayout(n).total; }
-size_t paged_cache_fork_workspace_size(int n) { return n < 0 ? 0 : PlanLayout(n).total; }
+size_t paged_cache_extend_workspace_size(int n) {
+  return n < 0 || n > kMaxItems ? 0 : PlanLayout(0).total;      // the status word
+}
+size_t paged_cache_fork_workspace_size(int n) {
+  return n < 0 || n > kMaxItems ? 0 : PlanLayout(n).total;
+}
 size_t paged_cache_compact_workspace_size(int num_pages) {
   return num_pages <= 0 || num_pages > kMaxPages ? 0 : CompactLayout(num_pages).total;
 }
@@ -631,10 +694,10 @@ size_t paged_cache_compact_workspace_size(int num_pages) {
 int paged_cache_extend_run(const paged_cache_params* p, const int32_t* rows,
                            const int32_t* new_tokens, int n, int32_t* tables, int32_t* lens,
                            int32_t* refs, void* ws, size_t ws_bytes, void* stream) {
-  if (!cache_params_ok(p) || n < 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!cache_params_ok(p) || n < 0 || n > kMaxItems) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n > 0 && (!rows || !new_tokens || !tables || !lens || !refs))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
-  const PlanLayout l(n);
+  const PlanLayout l(0);
   if (!ws || ws_bytes < l.total) return PAGED_ATTN_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n == 0) return cuda_status(cudaMemsetAsync(ws, 0, 4 * sizeof(uint32_t), st));
@@ -643,15 +706,14 @@ int paged_cache_extend_run(const paged_cache_params* p, const int32_t* rows,
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
-  a.off = at(ws, l.off); a.need = at(ws, l.need); a.len = at(ws, l.len);
-  static std::atomic<uint64_t> ready{0};
-  return cuda_status(launch_plan(plan_kernel<false>, a, a.P, ready, st));
+  return cuda_status(launch_items<false>(a, st));
 }
 
 int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* pools,
                          const int32_t* parents, const int32_t* children, int n, int32_t* tables,
                          int32_t* lens, int32_t* refs, void* ws, size_t ws_bytes, void* stream) {
-  if (!cache_params_ok(p) || !pools_ok(pools) || n < 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!cache_params_ok(p) || !pools_ok(pools) || n < 0 || n > kMaxItems)
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (pools->num_pages != p->num_pages || pools->page_size != p->page_size)
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n > 0 && (!parents || !children || !tables || !lens || !refs))
@@ -665,10 +727,8 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
-  a.off = at(ws, l.off); a.need = at(ws, l.need); a.len = at(ws, l.len); a.page = at(ws, l.page);
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = launch_plan(plan_kernel<true>, a, a.P, ready, st);
-  if (e != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  a.need = at(ws, l.need); a.len = at(ws, l.len); a.page = at(ws, l.page);
+  if (launch_items<true>(a, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
   ForkArgs f{};
   f.npools = pool_count(pools);
   for (int i = 0; i < f.npools; ++i) f.pools.p[i] = pools->pools_host[i];
@@ -712,8 +772,7 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   a.src = at(ws, l.src); a.dst = at(ws, l.dst); a.to = at(ws, l.to); a.moves = at(ws, l.moves);
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = launch_plan(compact_kernel, a, a.P, ready, st);
-  if (e != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  if (launch_plan(compact_kernel, a, a.P, 0, ready, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
   CopyArgs c{};
   c.pools = pool_count(pools);
   for (int i = 0; i < c.pools; ++i) c.src.p[i] = c.dst.p[i] = pools->pools_host[i];
@@ -722,7 +781,7 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   c.page_bytes = page_bytes(pools);
   c.chunks = static_cast<int>(ceil_div_ll(c.page_bytes, kCopyChunk));
   c.status = a.status;
-  c.tables = tables; c.lens = lens; c.to = a.to; c.tables_out = tables_out;
+  c.tables = tables; c.lens = lens; c.to = a.to; c.num_live = num_live; c.tables_out = tables_out;
   c.R = p->rows; c.C = p->max_pages_per_request; c.ps = p->page_size; c.P = p->num_pages;
   const int sms = current_sm_count();
   if (sms <= 0) return PAGED_ATTN_ERR_CUDA;

@@ -24,6 +24,8 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxStaged = 196608;       // bytes of the rows that one CTA stages at most
+constexpr int kStageGoal = 49152;        // four CTAs of them share an SM
 
 struct RopeArgs {
   const void *q, *k, *v;
@@ -33,9 +35,11 @@ struct RopeArgs {
   const int* positions;
   const unsigned long long* table;
   int T, Hq, Hkv, D, n;                  // n = R / 2 column pairs
+  int slots;                             // of a row
   int inverse, q_in_place, k_in_place;
   float m;
   int tile;                              // tokens per CTA
+  int staged_bytes;                      // shared memory of staged rows (a request: may be staged)
   // append
   const int *qo_indptr, *kv_indptr, *pages, *lens;
   int B, SQ, C, ps, num_pages;
@@ -63,16 +67,39 @@ struct alignas(sizeof(T) * V <= 16 ? sizeof(T) * V : 16) Vec {
   T e[V];
 };
 
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& x, float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = to_f(x.e[i]);
+}
+// Rounded to nearest-even; two 16-bit values per conversion.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+  Vec<T, V> x;
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if constexpr (std::is_same<T, __half>::value)
+        *reinterpret_cast<__half2*>(&x.e[i]) = __floats2half2_rn(f[i], f[i + 1]);
+      else
+        *reinterpret_cast<__nv_bfloat162*>(&x.e[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x.e[i] = from_f<T>(f[i]);
+  }
+  return x;
+}
+
 // V elements of TIn, as values of TOut, unchanged where the types agree.
 template <typename TIn, typename TOut, int V>
 __device__ __forceinline__ Vec<TOut, V> convert(const Vec<TIn, V>& x) {
   if constexpr (std::is_same<TIn, TOut>::value) {
     return x;
   } else {
-    Vec<TOut, V> y;
-#pragma unroll
-    for (int i = 0; i < V; ++i) y.e[i] = from_f<TOut>(to_f(x.e[i]));
-    return y;
+    float f[V];
+    unpack(x, f);
+    return pack<TOut>(f);
   }
 }
 
@@ -94,43 +121,72 @@ __device__ __forceinline__ float turned(float a, float c, float b, float s) {
   return __fmaf_rn(a, c, __fmul_rn(b, s));
 }
 
-// One row: slots [0, n / V) (half) or [0, 2 n / V) (interleaved) rotate, the slots after them
-// copy the columns past the rotated ones.  V = 1 in the interleaved layout is one pair read
-// element by element (rows whose alignment allows no wider access).
-template <typename TIn, typename TOut, int V, bool kHalf>
-__device__ __forceinline__ void rotate_slot(const TIn* __restrict__ x, TOut* __restrict__ y,
-                                            const float2* cs, int n, int s) {
-  if constexpr (kHalf) {
-    const Vec<TIn, V> a = *reinterpret_cast<const Vec<TIn, V>*>(x + s * V);
-    const Vec<TIn, V> b = *reinterpret_cast<const Vec<TIn, V>*>(x + n + s * V);
-    Vec<TOut, V> c, d;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 t = cs[s * V + i];
-      const float u = to_f(a.e[i]), w = to_f(b.e[i]);
-      c.e[i] = from_f<TOut>(turned(u, t.x, -w, t.y));
-      d.e[i] = from_f<TOut>(turned(w, t.x, u, t.y));
-    }
-    *reinterpret_cast<Vec<TOut, V>*>(y + s * V) = c;
-    *reinterpret_cast<Vec<TOut, V>*>(y + n + s * V) = d;
-  } else if constexpr (V == 1) {
-    const float2 t = cs[s];
-    const float u = to_f(x[2 * s]), w = to_f(x[2 * s + 1]);
-    y[2 * s] = from_f<TOut>(turned(u, t.x, -w, t.y));
-    y[2 * s + 1] = from_f<TOut>(turned(w, t.x, u, t.y));
-  } else {
-    const Vec<TIn, V> a = *reinterpret_cast<const Vec<TIn, V>*>(x + s * V);
-    Vec<TOut, V> c;
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float2 t = cs[s * (V / 2) + i];
-      const float u = to_f(a.e[2 * i]), w = to_f(a.e[2 * i + 1]);
-      c.e[2 * i] = from_f<TOut>(turned(u, t.x, -w, t.y));
-      c.e[2 * i + 1] = from_f<TOut>(turned(w, t.x, u, t.y));
-    }
-    *reinterpret_cast<Vec<TOut, V>*>(y + s * V) = c;
-  }
+// Bytes (a multiple of 16) from 16-byte aligned global to shared memory, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
+
+// What a thread holds of one slot between its load and its store.  A slot is V columns pairs (half:
+// V of each half) or V columns (interleaved; V = 1 is one pair, element by element, for rows whose
+// alignment allows no wider access); the slots behind the rotated ones copy V columns each.
+template <typename TIn, int V, bool kHalf>
+struct Slot {
+  static constexpr bool kTwo = kHalf || V == 1;
+  Vec<TIn, V> a, b;
+  __device__ __forceinline__ void load(const TIn* x, int n, int s, int rot, int first) {
+    if (s < rot) {
+      a = *reinterpret_cast<const Vec<TIn, V>*>(x + (!kHalf && V == 1 ? 2 * s : s * V));
+      if constexpr (kTwo) b = *reinterpret_cast<const Vec<TIn, V>*>(x + (kHalf ? n + s * V : 2 * s + 1));
+    } else {
+      a = *reinterpret_cast<const Vec<TIn, V>*>(x + first + (s - rot) * V);
+    }
+  }
+  // (cos, sin) of the slot's pairs
+  static constexpr int kPairs = kTwo ? V : V / 2;
+  template <typename TOut>
+  __device__ __forceinline__ void store(TOut* y, const float2 (&cs)[kPairs], int n, int s, int rot,
+                                        int first, bool rotate) const {
+    if (s >= rot) {
+      *reinterpret_cast<Vec<TOut, V>*>(y + first + (s - rot) * V) = convert<TIn, TOut, V>(a);
+      return;
+    }
+    Vec<TOut, V> c, d;
+    if (!rotate) {
+      c = convert<TIn, TOut, V>(a);
+      if constexpr (kTwo) d = convert<TIn, TOut, V>(b);
+    } else {
+      float u[V], y1[V];
+      unpack(a, u);
+      if constexpr (kTwo) {
+        float w[V], y2[V];
+        unpack(b, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          y1[i] = turned(u[i], cs[i].x, -w[i], cs[i].y);
+          y2[i] = turned(w[i], cs[i].x, u[i], cs[i].y);
+        }
+        d = pack<TOut>(y2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          y1[i] = turned(u[i], cs[i / 2].x, -u[i + 1], cs[i / 2].y);
+          y1[i + 1] = turned(u[i + 1], cs[i / 2].x, u[i], cs[i / 2].y);
+        }
+      }
+      c = pack<TOut>(y1);
+    }
+    if constexpr (kTwo) {
+      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? s * V : 2 * s)) = c;
+      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? n + s * V : 2 * s + 1)) = d;
+    } else {
+      *reinterpret_cast<Vec<TOut, V>*>(y + s * V) = c;
+    }
+  }
+};
 
 struct TokenSlot {
   long long off;        // element offset of (page, head 0, slot) in a pool; -1: not written
@@ -138,14 +194,79 @@ struct TokenSlot {
   int position;
 };
 
-template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend>
+// kStaged: the tile's rows are brought to shared memory by bulk copies, which keeps tens of KB in
+// flight per SM whatever the registers allow.  It needs 16-byte aligned tokens with adjacent heads.
+template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, bool kStaged>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  float2* cs = reinterpret_cast<float2*>(smem);                     // [tile, n]
+  using Held = Slot<TIn, V, kHalf>;
+  // Rows in flight per thread: 64 bytes of loads.
+  constexpr int kBytes = V * static_cast<int>(sizeof(TIn)) * (Held::kTwo ? 2 : 1);
+  constexpr int kBatch = kStaged || kBytes >= 64 ? 1 : (64 / kBytes > 8 ? 8 : 64 / kBytes);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t arrived;
+  __shared__ int gave_up;
+  float2* cs = reinterpret_cast<float2*>(smem + a.staged_bytes);    // [tile, n]
   TokenSlot* tok = reinterpret_cast<TokenSlot*>(cs + static_cast<size_t>(a.tile) * a.n);
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * a.tile;
   const int nt = min(a.tile, a.T - t0);
+  const int rot = kHalf ? a.n / V : (V == 1 ? a.n : 2 * a.n / V), first = 2 * a.n;
+  const int heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
+  // A thread keeps one slot of one token, and so its sines, and walks the heads; consecutive
+  // threads hold consecutive slots, then tokens.  `groups` threads share the heads of a slot.
+  const int slots = min(a.slots, kThreads), units = a.tile * slots, groups = kThreads / units;
+  const int group = tid / units, unit = tid - group * units;
+  const int t = unit / slots, s = blockIdx.y * kThreads + unit - t * slots;
+  const bool active = group < groups && t < nt && s < a.slots;
+  const long long token = t0 + t;
+  const int q_row = a.Hq * a.D, k_row = a.Hkv * a.D;                // staged: elements of a token
+  if constexpr (kStaged) {
+    if (tid < 32) {
+      if (tid == 0) {
+        gave_up = 0;
+        mbar_init(&arrived, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&arrived, nt * heads * a.D * static_cast<int>(sizeof(TIn)));
+      }
+      __syncwarp();
+      TIn* to = reinterpret_cast<TIn*>(smem);
+      for (int i = tid; i < nt * (kAppend ? 3 : 2); i += 32) {
+        const int which = i / nt, j = i - which * nt;
+        const long long at = t0 + j;
+        TIn* dst = to + j * heads * a.D;
+        if (which == 0 && a.Hq > 0)
+          bulk_load(dst, static_cast<const TIn*>(a.q) + at * a.q_ts, q_row * sizeof(TIn), &arrived);
+        else if (which == 1 && a.Hkv > 0)
+          bulk_load(dst + q_row, static_cast<const TIn*>(a.k) + at * a.k_ts, k_row * sizeof(TIn),
+                    &arrived);
+        else if (which == 2)
+          bulk_load(dst + q_row + k_row, static_cast<const TIn*>(a.v) + at * a.v_ts,
+                    k_row * sizeof(TIn), &arrived);
+      }
+    }
+  }
+  Held x[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h0 + u * groups;
+      if (h >= heads) break;
+      const TIn* p;
+      if (kStaged)
+        p = reinterpret_cast<const TIn*>(smem) + (t * heads + h) * a.D;
+      else if (h < a.Hq)
+        p = static_cast<const TIn*>(a.q) + token * a.q_ts + h * a.q_hs;
+      else if (!kAppend || h < a.Hq + a.Hkv)
+        p = static_cast<const TIn*>(a.k) + token * a.k_ts + (h - a.Hq) * a.k_hs;
+      else
+        p = static_cast<const TIn*>(a.v) + token * a.v_ts +
+            static_cast<long long>(h - a.Hq - a.Hkv) * a.D;
+      x[u].load(p, a.n, s, rot, first);
+    }
+  };
+  // The first rows are on their way while positions, pages and sines are found.
+  if (!kStaged && active) load(group);
   if constexpr (kAppend) {
     if (a.qo_indptr != nullptr) {
       for (int t = tid; t < nt; t += kThreads) tok[t].request = -1;
@@ -158,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     }
     for (int t = tid; t < nt; t += kThreads) {
       const int b = a.qo_indptr != nullptr ? tok[t].request : (t0 + t) / a.SQ;
-      TokenSlot s{-1, b, 0};
+      TokenSlot found{-1, b, 0};
       if (b >= 0) {
         const int end = a.qo_indptr != nullptr ? a.qo_indptr[b + 1] : (b + 1) * a.SQ;
         const int p = a.lens[b] - (end - (t0 + t));
@@ -168,92 +289,120 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
           first = a.kv_indptr[b];
           count = a.kv_indptr[b + 1] - a.kv_indptr[b];
         }
-        s.position = p;
+        found.position = p;
         const int j = p / a.ps;
         const int page = p >= 0 && j < count ? a.pages[first + j] : -1;
         if (page >= 0 && page < a.num_pages)
-          s.off = page * a.page_elems + static_cast<long long>(p - j * a.ps) * a.D;
+          found.off = page * a.page_elems + static_cast<long long>(p - j * a.ps) * a.D;
         else
           report_error(a.status, kErrMetadata);
       }
-      tok[t] = s;
+      tok[t] = found;
     }
     __syncthreads();
   }
   for (int i = tid; i < nt * a.n; i += kThreads) {
-    const int t = i / a.n, j = i - t * a.n;
-    const int p = kAppend ? tok[t].position : a.positions[t0 + t];
-    cs[i] = turn_of(p, a.table[j], a.m, a.inverse ? -1.f : 1.f);
+    const int j = i / a.n, pair = i - j * a.n;
+    const int p = kAppend ? tok[j].position : a.positions[t0 + j];
+    cs[i] = turn_of(p, a.table[pair], a.m, a.inverse ? -1.f : 1.f);
   }
   __syncthreads();
-
-  // Threads of a row: a power of two that covers its slots (at most the CTA); the others take
-  // further rows.
-  const int rot = kHalf ? a.n / V : (V == 1 ? a.n : 2 * a.n / V);
-  const int pass0 = 2 * a.n;
-  const int heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
-  int tpr = 1;
-  while (tpr < rot + (a.D - pass0) / V && tpr < kThreads) tpr *= 2;
-  const int rows_at_once = kThreads / tpr;
-  const int lane = tid & (tpr - 1);
-  for (int row = tid / tpr; row < nt * heads; row += rows_at_once) {
-    const int t = row / heads;
-    int h = row - t * heads;
-    const float2* c = cs + t * a.n;
-    const long long token = t0 + t;
-    const TIn* x;
-    TOut* y;
-    bool in_place = false, rotate = true;
-    if (h < a.Hq) {
-      if (kAppend && tok[t].request < 0) continue;
-      x = static_cast<const TIn*>(a.q) + token * a.q_ts + h * a.q_hs;
-      y = static_cast<TOut*>(a.qo) + token * a.qo_ts + h * a.qo_hs;
-      in_place = a.q_in_place;
-    } else {
-      h -= a.Hq;
-      if (!kAppend || h < a.Hkv) {
-        x = static_cast<const TIn*>(a.k) + token * a.k_ts + h * a.k_hs;
-      } else {
-        rotate = false;
-        h -= a.Hkv;
-        x = static_cast<const TIn*>(a.v) + token * a.v_ts + static_cast<long long>(h) * a.D;
-      }
-      if (kAppend) {
-        if (tok[t].off < 0) continue;
-        y = static_cast<TOut*>(rotate ? a.ko : a.vo) + tok[t].off +
-            static_cast<long long>(h) * a.ps * a.D;
-      } else {
-        y = static_cast<TOut*>(a.ko) + token * a.ko_ts + h * a.ko_hs;
-        in_place = a.k_in_place;
-      }
-    }
-    const int slots = rotate ? rot : 0, start = rotate ? pass0 : 0;
-    const int all = in_place ? slots : slots + (a.D - start) / V;
-    for (int s = lane; s < all; s += tpr) {
-      if (s < slots) {
-        rotate_slot<TIn, TOut, V, kHalf>(x, y, c, a.n, s);
-      } else {
-        const int at = start + (s - slots) * V;
-        *reinterpret_cast<Vec<TOut, V>*>(y + at) =
-            convert<TIn, TOut, V>(*reinterpret_cast<const Vec<TIn, V>*>(x + at));
-      }
+  if constexpr (kStaged) {
+    if (!mbar_wait(&arrived, 0, a.status, &gave_up)) {
+      drain_wait(&arrived, 0);
+      return;
     }
   }
+  if (!active) return;
+  if constexpr (kStaged) load(group);
+  float2 turn[Held::kPairs];
+#pragma unroll
+  for (int i = 0; i < Held::kPairs; ++i)
+    turn[i] = s < rot ? cs[t * a.n + s * Held::kPairs + i] : make_float2(0.f, 0.f);
+  bool write_q = a.Hq > 0, write_k = true;
+  TOut *q_to, *k_to, *v_to = nullptr;
+  long long k_step;
+  if constexpr (kAppend) {
+    write_q = tok[t].request >= 0;
+    write_k = tok[t].off >= 0;
+    k_to = static_cast<TOut*>(a.ko) + tok[t].off;
+    v_to = static_cast<TOut*>(a.vo) + tok[t].off;
+    k_step = static_cast<long long>(a.ps) * a.D;
+  } else {
+    write_q = !(a.q_in_place && s >= rot);
+    write_k = !(a.k_in_place && s >= rot);
+    k_to = static_cast<TOut*>(a.ko) + token * a.ko_ts;
+    k_step = a.ko_hs;
+  }
+  q_to = static_cast<TOut*>(a.qo) + token * a.qo_ts;
+  for (int h0 = group; h0 < heads;) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h0 + u * groups;
+      if (h >= heads) break;
+      if (h < a.Hq) {
+        if (write_q) x[u].store(q_to + h * a.qo_hs, turn, a.n, s, rot, first, true);
+      } else if (write_k) {
+        const int j = h - a.Hq;
+        if (!kAppend || j < a.Hkv)
+          x[u].store(k_to + j * k_step, turn, a.n, s, rot, first, true);
+        else
+          x[u].store(v_to + (j - a.Hkv) * k_step, turn, a.n, s, rot, first, false);
+      }
+    }
+    h0 += kBatch * groups;
+    load(h0);
+  }
+}
+
+template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend>
+cudaError_t launch_kernel(const RopeArgs& a, dim3 grid, size_t smem, bool staged, cudaStream_t st) {
+  count_launches(1);
+  if constexpr (V * sizeof(TIn) == 16) {
+    if (staged) {
+      static std::atomic<uint64_t> ready{0};
+      const auto kernel = rope_kernel<TIn, TOut, V, kHalf, kAppend, true>;
+      if (!kernel_smem_ready(kernel, kMaxStaged + 16384, ready)) return cudaErrorUnknown;
+      kernel<<<grid, kThreads, smem, st>>>(a);
+      return cudaGetLastError();
+    }
+  }
+  rope_kernel<TIn, TOut, V, kHalf, kAppend, false><<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename TIn, typename TOut, int V, bool kAppend>
 cudaError_t launch_v(RopeArgs a, bool half, cudaStream_t st) {
   const int sms = current_sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  a.tile = a.T >= 16 * sms ? 4 : 1;
-  const size_t smem = static_cast<size_t>(a.tile) * (a.n * sizeof(float2) + sizeof(TokenSlot));
-  const int grid = ceil_div(a.T, a.tile);
-  if (half)
-    rope_kernel<TIn, TOut, V, true, kAppend><<<grid, kThreads, smem, st>>>(a);
-  else
-    rope_kernel<TIn, TOut, V, false, kAppend><<<grid, kThreads, smem, st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  const bool copies = !(a.q_in_place && (a.Hkv == 0 || a.k_in_place));  // columns past the rotated
+  const int rot = half ? a.n / V : (V == 1 ? a.n : 2 * a.n / V);
+  a.slots = rot + (copies ? (a.D - 2 * a.n) / V : 0);
+  const int slots = a.slots < kThreads ? a.slots : kThreads;
+  const long long token_bytes =
+      static_cast<long long>(a.Hq + a.Hkv * (kAppend ? 2 : 1)) * a.D * sizeof(TIn);
+  const bool staged = a.staged_bytes != 0 && V * sizeof(TIn) == 16 && a.T >= 16 * sms &&
+                      (copies || a.D == 2 * a.n) && token_bytes <= kMaxStaged;
+  // Tokens per CTA: one while there are few; else as many as keep most threads busy (the slots of
+  // the tile's tokens, times the groups that share the heads, within the CTA).
+  a.tile = 1;
+  if (a.T >= 16 * sms) {
+    int best = 0;
+    for (int tile = 1; tile <= (staged ? 16 : 4) && tile * slots <= kThreads; tile *= 2) {
+      if (staged && tile > 1 && tile * token_bytes > kStageGoal) break;
+      const int busy = kThreads / (tile * slots) * (tile * slots);
+      if (busy >= best) {
+        best = busy;
+        a.tile = tile;
+      }
+    }
+  }
+  a.staged_bytes = staged ? static_cast<int>(align_up(a.tile * token_bytes, 128)) : 0;
+  const size_t smem = a.staged_bytes +
+                      static_cast<size_t>(a.tile) * (a.n * sizeof(float2) + sizeof(TokenSlot));
+  const dim3 grid(ceil_div(a.T, a.tile), ceil_div(a.slots, kThreads));
+  return half ? launch_kernel<TIn, TOut, V, true, kAppend>(a, grid, smem, staged, st)
+              : launch_kernel<TIn, TOut, V, false, kAppend>(a, grid, smem, staged, st);
 }
 
 template <typename TIn, typename TOut, bool kAppend>
@@ -431,6 +580,8 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
   for (long long s : {a.q_ts, a.q_hs, a.qo_ts, a.qo_hs}) w.stride(s);
   if (has_k)
     for (long long s : {a.k_ts, a.k_hs, a.ko_ts, a.ko_hs}) w.stride(s);
+  a.staged_bytes = aligned_to(q, 16) && aligned_to(k, 16) && a.q_hs == D && a.q_ts * e % 16 == 0 &&
+                   (!has_k || (a.k_hs == D && a.k_ts * e % 16 == 0));
   a.positions = positions;
   a.table = reinterpret_cast<const unsigned long long*>(table);
   a.T = p->num_tokens; a.Hq = p->num_qo_heads; a.Hkv = p->num_kv_heads;
@@ -484,6 +635,8 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
   a.B = p->batch; a.SQ = p->seq_len_q; a.C = p->max_pages_per_request; a.ps = p->page_size;
   a.num_pages = p->num_pages;
   a.status = status;
+  a.staged_bytes = aligned_to(q, 16) && aligned_to(k, 16) && aligned_to(v, 16) &&
+                   a.q_ts * e % 16 == 0 && a.k_ts * e % 16 == 0 && a.v_ts * e % 16 == 0;
   const bool half = p->layout == PAGED_ROPE_HALF;
   Width w(p->rotary_dim, half, e);
   for (const void* t : {q, k, v}) w.pointer(t, e);

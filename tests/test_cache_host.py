@@ -242,6 +242,11 @@ def test_page_call_refusals(lib):
                                           None) == BAD
     assert lib.paged_cache_free_run(C.byref(p), A16, -1, A16, A16, A16, None, None) == BAD
     assert lib.paged_cache_free_run(C.byref(p), None, 0, None, None, None, None, None) == 0
+    for n in (-1, 4097):
+        assert lib.paged_cache_extend_run(C.byref(p), A16, A16, n, A16, A16, A16, A16, big, None) == BAD
+        assert lib.paged_cache_fork_run(C.byref(p), C.byref(_pool_struct()), A16, A16, n, A16, A16,
+                                        A16, A16, big, None) == BAD
+        assert pkb.extend_cache_workspace_size(n) == 0 and pkb.fork_cache_workspace_size(n) == 0
     need = pkb.extend_cache_workspace_size(3)
     for ws, n in ((None, big), (A16, need - 1)):
         assert lib.paged_cache_extend_run(C.byref(p), A16, A16, 3, A16, A16, A16, ws, n,

@@ -144,6 +144,29 @@ def test_without_queries_and_many_requests():
     check(s, None, before, O.frequencies(8)[0])
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv,D,R", [(32, 8, 128, 128), (0, 1, 80, 40), (4, 2, 256, 64), (3, 3, 64, 20),
+                                        (7, 1, 8, 0)])
+def test_long_calls_equal_short_ones(layout, dtype, Hq, Hkv, D, R):
+    """Many tokens in one call give the bits of calls with one request each."""
+    s = problem(D, [1300, 1, 0, 1250], [70, 3, 40, 0], Hq=max(Hq, 1), Hkv=Hkv, D=D, dtype=dtype,
+                combined=True)
+    table = pkb.rope_frequencies(R)[0] if R else None
+    one = s["cache"].clone()
+    q = s["q"] if Hq else None
+    out = pkb.append_paged_kv_cache(s["k"], s["v"], s["cache"], s["lens"], q=q, qo_indptr=s["qo"],
+                                    freqs=table, layout=layout, block_tables=s["tables"])
+    for b, (a, e) in enumerate(zip(s["starts"][:-1], s["starts"][1:])):
+        zero = torch.tensor([0, e - a], dtype=torch.int32, device=DEV)
+        part = pkb.append_paged_kv_cache(s["k"][a:e], s["v"][a:e], one, s["lens"][b:b + 1],
+                                         q=None if q is None else q[a:e], qo_indptr=zero,
+                                         freqs=table, layout=layout,
+                                         block_tables=s["tables"][b:b + 1].contiguous())
+        assert q is None or torch.equal(part, out[a:e])
+    assert torch.equal(one.view(torch.int16), s["cache"].view(torch.int16))
+
+
 @pytest.mark.parametrize("big", [False, True])
 def test_padding_rows_are_left_alone(big):
     """Rows behind the last request: nothing of q_out or of the cache is written for them."""

@@ -37,7 +37,7 @@ class Both:
         self.o = O.State(self.tables.tolist(), self.lens.tolist(), self.refs.tolist(), ps,
                          [self.bits(p) for p in self.pools])
         self.status = torch.zeros(1, dtype=torch.int32, device=DEV)
-        self.ws = torch.full((max(pkb.fork_cache_workspace_size(2000),
+        self.ws = torch.full((max(pkb.fork_cache_workspace_size(4096),
                                   pkb.compact_cache_workspace_size(P)),), 0xAB,
                              dtype=torch.uint8, device=DEV)
 
@@ -146,9 +146,8 @@ def test_lowest_pages_first_in_small_and_large_pools(P):
 
 
 def test_many_rows():
-    """More items than a CTA has threads, in one CTA and in a cluster."""
-    for P in (6000, 9000):
-        R = 1500
+    """More items than a CTA has threads, in one CTA and in clusters of 2 to 8."""
+    for P, R in ((6000, 1500), (9000, 1500), (20000, 4096), (50000, 1500)):
         b = Both(P, R, 4, P, 8, Hkv=1, D=8)
         rng = random.Random(P)
         rows = list(range(R))

@@ -69,6 +69,32 @@ def test_token_counts(T):
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("Hq,Hk,D,R", [(32, 8, 128, 128), (5, 0, 80, 80), (3, 2, 64, 32), (24, 2, 256, 64),
+                                       (1, 1, 8, 8), (2, 1, 64, 20), (70, 9, 512, 512)])
+def test_long_calls_equal_short_ones(layout, dtype, Hq, Hk, D, R):
+    """The launch of a long call (several tokens per CTA, rows staged in shared memory) gives the
+    bits of short calls on its parts; in place too."""
+    gen = torch.Generator(device=DEV).manual_seed(D + R)
+    T = 2600 if D < 512 else 2433
+    fused = torch.randn(T, Hq + Hk, D, generator=gen, device=DEV).to(dtype)
+    q, k = fused[:, :Hq], fused[:, Hq:] if Hk else None
+    pos = torch.randint(-9, 1 << 20, (T,), generator=gen, device=DEV, dtype=torch.int32)
+    table, _ = pkb.rope_frequencies(R)
+
+    def both(x):
+        return x if isinstance(x, tuple) else (x, x[:, :0])
+    got = both(pkb.rotary_embedding(q, pos, table, k=k, layout=layout))
+    for a in range(0, T, 700):
+        part = slice(a, min(T, a + 700))
+        want = both(pkb.rotary_embedding(q[part], pos[part], table, k=None if k is None else k[part],
+                                         layout=layout))
+        assert torch.equal(got[0][part], want[0]) and torch.equal(got[1][part], want[1])
+    pkb.rotary_embedding(q, pos, table, k=k, layout=layout, q_out=q, k_out=k)
+    assert torch.equal(q, got[0]) and (k is None or torch.equal(k, got[1]))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_far_and_negative_positions(layout):
     """Any int32 position: the angle of the last one is as exact as that of the first."""
     gen = torch.Generator().manual_seed(1)
