@@ -147,7 +147,7 @@ class State:
         items, seen = [], set()
         for r, m in zip(rows, new):
             ok = 0 <= r < self.R and m >= 0 and self.lens[r] >= 0
-            ok = ok and self.pages(self.lens[r] + m) <= self.C
+            ok = ok and self.lens[r] + m < 2 ** 31 and self.pages(self.lens[r] + m) <= self.C
             if not ok or r in seen:
                 self.status |= METADATA
                 continue

@@ -7,6 +7,8 @@
 // memory.  The second moves: every SM copies runs of contiguous bytes, as many as the first one
 // listed.  The first is bound by the latency of its dependent steps (a handful of cluster
 // barriers and L2 round trips), the second by HBM.
+#include <climits>
+
 #include <cooperative_groups.h>
 
 #include "../../include/paged_cache.h"
@@ -126,12 +128,12 @@ struct FreePages {
     step_total = warp_before + room * 32;
     step_before = step_total + room;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j0 = 0; j0 < own; j0 += 4) {
-      int4 r[4];
+    for (int j0 = 0; j0 < own; j0 += 8) {
+      int4 r[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) r[u] = j0 + u < own ? load(j0 + u) : make_int4(1, 1, 1, 1);
+      for (int u = 0; u < 8; ++u) r[u] = j0 + u < own ? load(j0 + u) : make_int4(1, 1, 1, 1);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int j = j0 + u;
         if (j >= own) break;
         const uint32_t m = mask_of(r[u]);
@@ -204,43 +206,55 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   const int tid = threadIdx.x;
   Item* items = reinterpret_cast<Item*>(shared);
   int* keys = reinterpret_cast<int*>(items + a.n);             // CTA 0: rows seen, their first item
-  int* offs = keys;                                            // later: a copy of every Item::off
+  Item* mine = reinterpret_cast<Item*>(keys);                  // later: the CTA's copy of the items
   int* pages_shared = keys + 2 * a.hash;
   constexpr int kPer = kMaxItems / kPlanThreads;
-  int L[kPer];                                                 // CTA 0: lengths of its items
+  int row[kPer], L[kPer], other[kPer];     // CTA 0: rows, lengths; new tokens or the child's length
   uint32_t bits = 0;
-  FreePages pages;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (rank == 0) {
     if (tid < 4) a.status[tid] = 0;
-    int* first = keys + a.hash;
     for (int i = tid; i < a.hash; i += kPlanThreads) {
       keys[i] = -1;
-      first[i] = a.n;
+      keys[a.hash + i] = a.n;
     }
-    __syncthreads();
-    int row[kPer], need[kPer], at[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = j * kPlanThreads + tid;
       if (j * kPlanThreads >= a.n) break;
       row[j] = i < a.n ? a.rows[i] : -1;
+      other[j] = i < a.n ? (kFork ? a.parents[i] : a.new_tokens[i]) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (j * kPlanThreads >= a.n) break;
+      const int parent = other[j];
+      const bool known = row[j] >= 0 && row[j] < a.R &&
+                         (!kFork || (parent >= 0 && parent < a.R && parent != row[j]));
+      L[j] = -1;
+      if (!known) continue;
+      L[j] = a.lens[kFork ? parent : row[j]];
+      if (kFork) other[j] = a.lens[row[j]];
+    }
+  }
+  // The counts are read while the lengths are on their way.
+  FreePages pages;
+  pages.count(a.refs, a.P, rank, size, pages_shared);
+  if (rank == 0) {
+    int* first = keys + a.hash;
+    int need[kPer], at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (j * kPlanThreads >= a.n) break;
       need[j] = -1;
-      at[j] = L[j] = 0;
-      if (row[j] < 0 || row[j] >= a.R) continue;
-      if (kFork) {
-        const int parent = a.parents[i];
-        if (parent < 0 || parent >= a.R || parent == row[j]) continue;
-        const int own_len = a.lens[row[j]];
-        L[j] = a.lens[parent];
-        if (own_len == 0 && L[j] >= 0 && (L[j] + a.ps - 1LL) / a.ps <= a.C) need[j] = L[j] % a.ps > 0;
-      } else {
-        const int more = a.new_tokens[i];
-        L[j] = a.lens[row[j]];
-        if (L[j] < 0 || more < 0) continue;
-        const long long have = (L[j] + a.ps - 1LL) / a.ps;
-        const long long want = (static_cast<long long>(L[j]) + more + a.ps - 1) / a.ps;
-        if (want <= a.C) need[j] = static_cast<int>(want - have);
-      }
+      at[j] = 0;
+      if (L[j] < 0 || (kFork ? other[j] != 0 : other[j] < 0)) continue;
+      const long long have = (L[j] + a.ps - 1LL) / a.ps;
+      const long long want =
+          kFork ? have : (static_cast<long long>(L[j]) + other[j] + a.ps - 1) / a.ps;
+      if (!kFork && L[j] > INT_MAX - other[j]) continue;
+      if (want <= a.C) need[j] = kFork ? L[j] % a.ps > 0 : static_cast<int>(want - have);
     }
     // A row listed more than once belongs to its first item that is in order.
 #pragma unroll
@@ -269,12 +283,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int before = add_pages(carry, block_scan(pages_needed, warp_sums, &sum));
       carry = add_pages(carry, sum);
       if (i < a.n)
-        items[i] = {before, pages_needed, kFork ? L[j] / a.ps : static_cast<int>((L[j] + a.ps - 1LL) / a.ps),
+        items[i] = {before, pages_needed,
+                    kFork ? L[j] / a.ps : static_cast<int>((L[j] + a.ps - 1LL) / a.ps),
                     need[j] < 0 ? -1 : row[j]};
     }
     if (tid == 0) total_need = carry;
   }
-  pages.count(a.refs, a.P, rank, size, pages_shared);
   sync_cluster(cl);
   pages.order(cl, warp_sums);
   const int demand = *cl.map_shared_rank(&total_need, 0);
@@ -288,7 +302,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const Item it = items[i];
       const bool served = it.row >= 0 && (it.need == 0 || it.off + it.need <= pages.total);
       if (it.row >= 0 && !served) bits |= kErrCapacity;
-      if (served) a.lens[it.row] = kFork ? L[j] : L[j] + a.new_tokens[i];
+      if (served) a.lens[it.row] = kFork ? L[j] : L[j] + other[j];
       if (kFork) {
         a.need[i] = served ? it.need : -1;
         a.len[i] = L[j];
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   }
   const int handed = min(demand, pages.total);
   if (handed > 0) {
-    for (int i = tid; i < a.n; i += kPlanThreads) offs[i] = from[i].off;
+    for (int i = tid; i < a.n; i += kPlanThreads) mine[i] = from[i];
     __syncthreads();
     // The k-th free page goes to the item whose demands [off, off + need) hold k.
     Item it{0, 0, 0, -1};
@@ -311,27 +325,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         if (!(m >> b & 1u)) continue;
-        const int mine = k++;
-        if (mine >= handed) continue;
-        if (which < 0 || mine - it.off >= it.need) {
+        const int rank_k = k++;
+        if (rank_k >= handed) continue;
+        if (which < 0 || rank_k - it.off >= it.need) {
           // the last item with off <= k: items without a demand share their successor's offset
           int lo = max(which, 0), hi = a.n;
           while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (offs[mid] <= mine) lo = mid; else hi = mid;
+            if (mine[mid].off <= rank_k) lo = mid; else hi = mid;
           }
           which = lo;
-          it = from[lo];
+          it = mine[lo];
         }
         if (it.row < 0 || it.off + it.need > pages.total) continue;
         const int p = pages.first_page(j) + b;
-        a.tables[static_cast<long long>(it.row) * a.C + it.have + (mine - it.off)] = p;
+        a.tables[static_cast<long long>(it.row) * a.C + it.have + (rank_k - it.off)] = p;
         a.refs[p] = 1;
         if (kFork) a.page[which] = p;
       }
     }
   }
-  grid_launch_dependents();
   if (size > 1) cl.sync();                 // the items in CTA 0's shared memory have been read
 }
 
@@ -377,7 +390,8 @@ struct CopyArgs {
 
 template <bool kCompact>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
-  if (kCompact) grid_dependency_wait();
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int n = kCompact ? *a.n_dev : a.n;
   const long long units = static_cast<long long>(n) * a.pools * a.chunks;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -433,6 +447,7 @@ struct ForkArgs {
 
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
   grid_dependency_wait();
+  grid_launch_dependents();
   const int per_item = a.npools + a.table_units;
   const long long units = static_cast<long long>(a.n) * per_item;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -474,6 +489,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 free_kernel(const int* rows, int n, const int* tables, int* lens, int* refs, int R, int C, int ps,
             int P, uint32_t* status) {
   __shared__ int len;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int row = rows[blockIdx.x];
   if (row < 0 || row >= R) {
     if (threadIdx.x == 0) report_error(status, kErrMetadata);
@@ -511,6 +528,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
   const int tid = threadIdx.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (rank == 0 && tid < 4) a.status[tid] = 0;
   FreePages pages;
   pages.count(a.refs, a.P, rank, size, shared);
@@ -550,7 +569,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
     a.refs_out[d] = a.refs[s];
     a.refs_out[s] = 0;
   }
-  grid_launch_dependents();
   if (size > 1) cl.sync();                 // the step totals have been read
 }
 
@@ -643,12 +661,14 @@ cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, size_t ints,
   cfg.blockDim = kPlanThreads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
@@ -674,11 +694,10 @@ int paged_cache_free_run(const paged_cache_params* p, const int32_t* rows, int n
   if (!cache_params_ok(p) || n < 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n == 0) return PAGED_ATTN_OK;
   if (!rows || !tables || !lens || !refs) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
-  free_kernel<<<n, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      rows, n, tables, lens, refs, p->rows, p->max_pages_per_request, p->page_size, p->num_pages,
-      status);
   count_launches(1);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_after_previous(
+      free_kernel, n, kCopyThreads, 0, static_cast<cudaStream_t>(stream), rows, n, tables, lens, refs,
+      p->rows, p->max_pages_per_request, p->page_size, p->num_pages, status));
 }
 
 size_t paged_cache_extend_workspace_size(int n) {
@@ -812,10 +831,10 @@ int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* 
   if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
   const long long units = static_cast<long long>(n) * c.pools * c.chunks;
   const long long most = 8LL * sms;
-  copy_kernel<false><<<static_cast<int>(units < most ? units : most), kCopyThreads, 0,
-                       static_cast<cudaStream_t>(stream)>>>(c);
   count_launches(1);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_after_previous(copy_kernel<false>,
+                                           static_cast<int>(units < most ? units : most),
+                                           kCopyThreads, 0, static_cast<cudaStream_t>(stream), c));
 }
 
 }  // extern "C"

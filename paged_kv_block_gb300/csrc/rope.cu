@@ -23,9 +23,10 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxStaged = 196608;       // bytes of the rows that one CTA stages at most
-constexpr int kStageGoal = 49152;        // four CTAs of them share an SM
+constexpr int kStageGoal = 24576;        // bytes of rows that a CTA stages where it may choose
+constexpr int kStagedCtas = 6;
 
 struct RopeArgs {
   const void *q, *k, *v;
@@ -197,7 +198,7 @@ struct TokenSlot {
 // kStaged: the tile's rows are brought to shared memory by bulk copies, which keeps tens of KB in
 // flight per SM whatever the registers allow.  It needs 16-byte aligned tokens with adjacent heads.
 template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, bool kStaged>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kernel(const RopeArgs a) {
   using Held = Slot<TIn, V, kHalf>;
   // Rows in flight per thread: 64 bytes of loads.
   constexpr int kBytes = V * static_cast<int>(sizeof(TIn)) * (Held::kTwo ? 2 : 1);
@@ -219,6 +220,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   const int t = unit / slots, s = blockIdx.y * kThreads + unit - t * slots;
   const bool active = group < groups && t < nt && s < a.slots;
   const long long token = t0 + t;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int q_row = a.Hq * a.D, k_row = a.Hkv * a.D;                // staged: elements of a token
   if constexpr (kStaged) {
     if (tid < 32) {
@@ -361,14 +364,13 @@ cudaError_t launch_kernel(const RopeArgs& a, dim3 grid, size_t smem, bool staged
   if constexpr (V * sizeof(TIn) == 16) {
     if (staged) {
       static std::atomic<uint64_t> ready{0};
-      const auto kernel = rope_kernel<TIn, TOut, V, kHalf, kAppend, true>;
+      void (*const kernel)(RopeArgs) = rope_kernel<TIn, TOut, V, kHalf, kAppend, true>;
       if (!kernel_smem_ready(kernel, kMaxStaged + 16384, ready)) return cudaErrorUnknown;
-      kernel<<<grid, kThreads, smem, st>>>(a);
-      return cudaGetLastError();
+      return launch_after_previous(kernel, grid, dim3(kThreads), smem, st, a);
     }
   }
-  rope_kernel<TIn, TOut, V, kHalf, kAppend, false><<<grid, kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after_previous(rope_kernel<TIn, TOut, V, kHalf, kAppend, false>, grid,
+                               dim3(kThreads), smem, st, a);
 }
 
 template <typename TIn, typename TOut, int V, bool kAppend>
