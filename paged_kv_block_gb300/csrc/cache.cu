@@ -31,6 +31,8 @@ constexpr int kPlanSmem = (4 * kMaxItems + 4 * kMaxItems +
 static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
+constexpr int kCopyCtas = 24;              // CTAs per SM where they walk the units (see copy_kernel)
+constexpr long long kMaxGrid = 1LL << 30;
 
 struct Pools {
   void* p[PAGED_CACHE_MAX_POOLS];
@@ -388,29 +390,49 @@ struct CopyArgs {
   int R, C, ps, P;
 };
 
+// A unit is up to kCopyChunk bytes of one page of one pool.  Where the host knows the number of
+// pairs there is a CTA per unit; else (compact) four times the CTAs that fit walk the units, each
+// reading the next unit's page ids before it copies the present one.
+// HBM bounds it.  Measured (64 KB pages): copying 1,201 pages of 8 layers, 630 MB, takes 187 us with
+// a CTA per unit, 99% of the rate of a plain copy, and 201 us with 6 resident CTAs per SM that
+// walk the units; moving 1,500 pages of 4 layers 127 us a call with 24 CTAs per SM, 134 with 6, and
+// the same 134 with a ring of bulk copies through shared memory, so there is none.  Units of 8 KB
+// cost 244 us (the CTAs' launches), of 32 KB 190 us.
 template <bool kCompact>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int n = kCompact ? *a.n_dev : a.n;
   const long long units = static_cast<long long>(n) * a.pools * a.chunks;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int chunk = static_cast<int>(u % a.chunks);
-    const long long w = u / a.chunks;
-    const int pool = static_cast<int>(w % a.pools);
-    const int i = static_cast<int>(w / a.pools);
-    const int s = a.src_pages[kCompact ? n - 1 - i : i], d = a.dst_pages[i];
-    if (s < 0 || s >= a.src_num_pages || d < 0 || d >= a.dst_num_pages) {
+  const int per_pair = a.pools * a.chunks;
+  const auto pair_of = [&](long long u) { return static_cast<int>(u / per_pair); };
+  long long u = blockIdx.x;
+  int s = 0, d = 0;
+  if (u < units) {
+    s = a.src_pages[kCompact ? n - 1 - pair_of(u) : pair_of(u)];
+    d = a.dst_pages[pair_of(u)];
+  }
+  for (; u < units; u += gridDim.x) {
+    const int from = s, to = d;
+    const long long next = u + gridDim.x;
+    if (next < units) {
+      s = a.src_pages[kCompact ? n - 1 - pair_of(next) : pair_of(next)];
+      d = a.dst_pages[pair_of(next)];
+    }
+    if (from < 0 || from >= a.src_num_pages || to < 0 || to >= a.dst_num_pages) {
       if (threadIdx.x == 0) report_error(a.status, kErrMetadata);
       continue;
     }
-    if (s == d && a.src.p[pool] == a.dst.p[pool]) continue;
+    const int w = static_cast<int>(u - static_cast<long long>(pair_of(u)) * per_pair);
+    const int pool = w / a.chunks, chunk = w - pool * a.chunks;
+    if (from == to && a.src.p[pool] == a.dst.p[pool]) continue;
     const long long at = static_cast<long long>(chunk) * kCopyChunk;
     const int bytes = static_cast<int>(min(static_cast<long long>(kCopyChunk), a.page_bytes - at));
-    copy_words(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dst.p[pool]) + d * a.page_bytes + at),
-               reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.src.p[pool]) +
-                                              s * a.page_bytes + at),
-               bytes / 16);
+    copy_words(
+        reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dst.p[pool]) + to * a.page_bytes + at),
+        reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.src.p[pool]) +
+                                       from * a.page_bytes + at),
+        bytes / 16);
   }
   if (kCompact) {
     const int live = *a.num_live;
@@ -452,11 +474,11 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constan
   const long long units = static_cast<long long>(a.n) * per_item;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int i = static_cast<int>(u / per_item), w = static_cast<int>(u - static_cast<long long>(i) * per_item);
-    if (a.need[i] < 0) continue;
-    const int L = a.len[i], full = L / a.ps;
-    const long long from = static_cast<long long>(a.parents[i]) * a.C;
+    const int need = a.need[i], L = a.len[i], d = a.page[i], parent = a.parents[i];
+    if (need < 0) continue;
+    const int full = L / a.ps;
+    const long long from = static_cast<long long>(parent) * a.C;
     if (w < a.npools) {
-      const int d = a.page[i];
       if (d < 0) continue;
       const int s = a.tables[from + full];
       if (s < 0 || s >= a.P) {
@@ -761,10 +783,8 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   f.C = a.C; f.ps = a.ps; f.P = a.P;
   f.table_units = ceil_div(a.C, 4 * kCopyThreads);
   f.status = a.status;
-  const int sms = current_sm_count();
-  if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
   const long long units = static_cast<long long>(n) * (f.npools + f.table_units);
-  const long long most = 8LL * sms;
+  const long long most = kMaxGrid;
   count_launches(1);
   return cuda_status(launch_after_previous(fork_kernel, static_cast<int>(units < most ? units : most),
                                            kCopyThreads, 0, st, f));
@@ -804,8 +824,14 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   c.R = p->rows; c.C = p->max_pages_per_request; c.ps = p->page_size; c.P = p->num_pages;
   const int sms = current_sm_count();
   if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
+  // at most half the pages can move; the table's entries want threads too
+  const long long units = (p->num_pages / 2LL) * c.pools * c.chunks;
+  const long long renames = ceil_div_ll(static_cast<long long>(c.R) * c.C, kCopyThreads);
+  long long ctas = units > renames ? units : renames;
+  if (ctas > kCopyCtas * sms) ctas = kCopyCtas * sms;
   count_launches(1);
-  return cuda_status(launch_after_previous(copy_kernel<true>, 8 * sms, kCopyThreads, 0, st, c));
+  return cuda_status(launch_after_previous(copy_kernel<true>, static_cast<int>(ctas > 0 ? ctas : 1),
+                                           kCopyThreads, 0, st, c));
 }
 
 int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* dst,
@@ -827,10 +853,8 @@ int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* 
   c.page_bytes = page_bytes(src);
   c.chunks = static_cast<int>(ceil_div_ll(c.page_bytes, kCopyChunk));
   c.status = status;
-  const int sms = current_sm_count();
-  if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
   const long long units = static_cast<long long>(n) * c.pools * c.chunks;
-  const long long most = 8LL * sms;
+  const long long most = kMaxGrid;
   count_launches(1);
   return cuda_status(launch_after_previous(copy_kernel<false>,
                                            static_cast<int>(units < most ? units : most),
