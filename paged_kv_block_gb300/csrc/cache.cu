@@ -20,14 +20,16 @@ namespace cg = cooperative_groups;
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;         // of a planning CTA, or
+constexpr int kFewThreads = 256;           // where the pool and the list are small
 constexpr int kPlanCluster = 8;            // portable cluster size
-constexpr int kStepPages = 4096;           // pages that one CTA counts at a time
+constexpr int kThreadPages = 8;            // pages that a thread counts at a time
 constexpr int kMaxPages = 1 << 24;
-constexpr int kMaxItems = 4096;            // a thread of the planning CTA holds 4 of them
+constexpr int kPerThread = 4;              // items that a thread of the planning CTA holds
+constexpr int kMaxItems = kPerThread * kPlanThreads;
 // Shared memory of a planning kernel at most: items, the hash table of their rows, page counts.
-constexpr int kPlanSmem = (4 * kMaxItems + 4 * kMaxItems +
-                           (kMaxPages / kStepPages / kPlanCluster) * 33 + kMaxPages / kStepPages) * 4;
+constexpr int kMaxSteps = kMaxPages / (kPlanThreads * kThreadPages);
+constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxSteps) * 4;
 static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
@@ -60,7 +62,8 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   const int v = warp_inclusive(x);
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  const int w = warp_inclusive(warp_sums[lane]);       // every warp scans the 32 sums itself
+  // every warp scans the warps' sums itself
+  const int w = warp_inclusive(lane < static_cast<int>(blockDim.x >> 5) ? warp_sums[lane] : 0);
   const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   *total = __shfl_sync(0xffffffffu, w, 31);
   __syncthreads();
@@ -73,46 +76,61 @@ __device__ __forceinline__ void sync_cluster(cg::cluster_group& cl) {
   else cl.sync();
 }
 
-// The page counts [0, P) are cut into steps of 4096 pages; step g belongs to CTA g % size, and
-// thread t of it holds pages 4 t .. 4 t + 3, so loads coalesce and the order of (step, thread,
+// The page counts [0, P) are cut into steps of 8 pages per thread; step g belongs to CTA g % size,
+// and thread t of it holds pages 8 t .. 8 t + 7, so loads coalesce and the order of (step, thread,
 // page) is the order of page ids.  The CTAs interleave so that a demand met by the lowest pages
 // is still handed out by all of them.
+// What bounds this is instructions, not bytes (every warp of a CTA issues through four schedulers):
+// hence 32-byte loads, one mask per thread and step, and one CTA of 256 threads for small pools.
 struct FreePages {
   const int* refs;
   int P, rank, size, steps, own;     // steps in all, steps of this CTA
   bool aligned;
-  uint32_t kept;                     // which of the thread's 4 pages are free, first 8 own steps
+  uint32_t kept;                     // the thread's masks of its first 4 steps
   int* warp_before;                  // shared [own, 32]: free pages of the step before a warp
   int* step_total;                   // shared [own]
   int* step_before;                  // shared [steps]: free pages before a step
   int total;                         // free pages
 
-  static __host__ __device__ int steps_of(int P) { return (P + kStepPages - 1) / kStepPages; }
-  static __host__ size_t shared_ints(int P, int size) {
-    const int own = (steps_of(P) + size - 1) / size;
-    return static_cast<size_t>(own) * 33 + steps_of(P);
+  static __host__ __device__ int steps_of(int P, int threads) {
+    return (P + threads * kThreadPages - 1) / (threads * kThreadPages);
+  }
+  static __host__ size_t shared_ints(int P, int size, int threads) {
+    const int steps = steps_of(P, threads);
+    return static_cast<size_t>((steps + size - 1) / size) * 33 + steps;
   }
 
   __device__ __forceinline__ int first_page(int j) const {
-    return (j * size + rank) * kStepPages + 4 * static_cast<int>(threadIdx.x);
+    return ((j * size + rank) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) *
+           kThreadPages;
   }
-  // Counts of the thread's pages in its j-th step (1, that is not free, past the end).
-  __device__ __forceinline__ int4 load(int j) const {
+  // Counts of the thread's pages of its j-th step (1, that is not free, past the end).
+  __device__ __forceinline__ void load(int j, uint32_t (&r)[kThreadPages]) const {
     const int p = first_page(j);
-    if (aligned && p + 3 < P) return *reinterpret_cast<const int4*>(refs + p);
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p < P) r.x = refs[p];
-    if (p + 1 < P) r.y = refs[p + 1];
-    if (p + 2 < P) r.z = refs[p + 2];
-    if (p + 3 < P) r.w = refs[p + 3];
-    return r;
+    if (j < own && aligned && p + kThreadPages <= P) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                     "=r"(r[6]), "=r"(r[7])
+                   : "l"(refs + p)
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int b = 0; b < kThreadPages; ++b)
+        r[b] = j < own && p + b < P ? static_cast<uint32_t>(refs[p + b]) : 1u;
+    }
   }
-  static __device__ __forceinline__ uint32_t mask_of(const int4& r) {
-    return (r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) | (r.w == 0 ? 8u : 0u);
+  static __device__ __forceinline__ uint32_t mask_of(const uint32_t (&r)[kThreadPages]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int b = 0; b < kThreadPages; ++b) m |= r[b] == 0 ? 1u << b : 0u;
+    return m;
   }
-  // Which of the thread's pages of its j-th step are free (as they were at count()).
+  // Which of them were free at count().
   __device__ __forceinline__ uint32_t mask(int j) const {
-    return j < 8 ? (kept >> (4 * j)) & 15u : mask_of(load(j));
+    if (j < 4) return (kept >> (8 * j)) & 255u;
+    uint32_t r[kThreadPages];
+    load(j, r);
+    return mask_of(r);
   }
 
   // Count the CTA's own steps (before the cluster barrier).
@@ -121,55 +139,68 @@ struct FreePages {
     P = num_pages;
     rank = cta;
     size = ctas;
-    steps = steps_of(P);
+    steps = steps_of(P, blockDim.x);
     own = (steps - rank + size - 1) / size;
-    aligned = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
+    aligned = (reinterpret_cast<uintptr_t>(refs) & 31) == 0;
     kept = 0;
     const int room = (steps + size - 1) / size;
     warp_before = shared;
     step_total = warp_before + room * 32;
     step_before = step_total + room;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j0 = 0; j0 < own; j0 += 8) {
-      int4 r[8];
+    const int warps = blockDim.x >> 5;
+    for (int j0 = 0; j0 < own; j0 += 4) {
+      uint32_t r[4][kThreadPages];                     // four steps' loads in flight
 #pragma unroll
-      for (int u = 0; u < 8; ++u) r[u] = j0 + u < own ? load(j0 + u) : make_int4(1, 1, 1, 1);
+      for (int u = 0; u < 4; ++u) load(j0 + u, r[u]);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int j = j0 + u;
-        if (j >= own) break;
+      for (int u = 0; u < 4; ++u) {
+        if (j0 + u >= own) break;
         const uint32_t m = mask_of(r[u]);
-        if (j < 8) kept |= m << (4 * j);
+        if (j0 == 0) kept |= m << (8 * u);
         const int n = __reduce_add_sync(0xffffffffu, __popc(m));
-        if (lane == 0) warp_before[j * 32 + warp] = n;
+        if (lane == 0) warp_before[(j0 + u) * 32 + warp] = n;
       }
     }
     __syncthreads();
-    for (int j = warp; j < own; j += 32) {
-      const int n = warp_before[j * 32 + lane], v = warp_inclusive(n);
+    for (int j = warp; j < own; j += warps) {
+      const int n = lane < warps ? warp_before[j * 32 + lane] : 0, v = warp_inclusive(n);
       warp_before[j * 32 + lane] = v - n;
       if (lane == 31) step_total[j] = v;
     }
   }
   // Put the steps of all CTAs in order (after the cluster barrier).
-  __device__ void order(cg::cluster_group& cl, int* warp_sums) {
+  __device__ void order(cg::cluster_group& cl) {
+    const int lane = threadIdx.x & 31;
     int carry = 0;
-    for (int g0 = 0; g0 < steps; g0 += kPlanThreads) {
-      const int g = g0 + threadIdx.x;
+    for (int g0 = 0; g0 < steps; g0 += 32) {           // every warp for itself
+      const int g = g0 + lane;
       const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
-      int sum;
-      const int before = block_scan(n, warp_sums, &sum);
-      if (g < steps) step_before[g] = carry + before;
-      carry += sum;
+      const int v = warp_inclusive(n);
+      if (threadIdx.x < 32 && g < steps) step_before[g] = carry + v - n;
+      carry += __shfl_sync(0xffffffffu, v, 31);
     }
     total = carry;
     __syncthreads();
   }
-  // Free pages before the thread's first page of its j-th step (whole warps).
-  __device__ __forceinline__ int before(int j, uint32_t m) const {
-    const int n = __popc(m);
-    return step_before[j * size + rank] + warp_before[j * 32 + (threadIdx.x >> 5)] +
-           warp_inclusive(n) - n;
+  // Calls f(page, is_free, free pages before it, free pages among the warp's 32) for the pages
+  // of the j-th step with a page per lane: neighbouring lanes hold neighbouring pages and, where
+  // those are free, neighbouring ranks, so that what f stores by either coalesces.  Whole warps.
+  template <typename F>
+  __device__ __forceinline__ void each(int j, const F& f) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t m = mask(j);
+    int before = step_before[j * size + rank] + warp_before[j * 32 + warp];
+    int p = ((j * size + rank) * static_cast<int>(blockDim.x) + warp * 32) * kThreadPages + lane;
+#pragma unroll
+    for (int g = 0; g < kThreadPages; ++g) {           // 32 pages: the masks of 4 lanes
+      const uint32_t theirs = __shfl_sync(0xffffffffu, m, 4 * g + (lane >> 3));
+      const bool is_free = theirs >> (lane & 7) & 1u;
+      const uint32_t all = __ballot_sync(0xffffffffu, is_free);
+      f(p, is_free, before + __popc(all & ((1u << lane) - 1u)), __popc(all));
+      before += __popc(all);
+      p += 32;
+    }
   }
 };
 
@@ -183,6 +214,7 @@ struct PlanArgs {
   int* lens;
   int* refs;
   int R, C, ps, P;
+  unsigned long long by_ps;  // ceil(2^64 / ps)
   int hash;                // entries of the table of rows seen, a power of two >= 2 n
   uint32_t* status;
   int* need;               // workspace [n], fork: 0, 1 or -1 (left out)
@@ -196,6 +228,11 @@ struct Item {
   int row;
 };
 
+// x / page_size, exact for every 32-bit x (x * page_size < 2^64).
+__device__ __forceinline__ int over_page(unsigned x, unsigned long long by_ps) {
+  return static_cast<int>(__umul64hi(x, by_ps));
+}
+
 // CTA 0 looks after the items, all CTAs after the pages.  Latency bounds this kernel: the chain
 // is rows -> lengths -> scan -> cluster barrier -> tables, with the counts read beside it.
 template <bool kFork>
@@ -205,32 +242,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ int total_need;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   Item* items = reinterpret_cast<Item*>(shared);
   int* keys = reinterpret_cast<int*>(items + a.n);             // CTA 0: rows seen, their first item
   Item* mine = reinterpret_cast<Item*>(keys);                  // later: the CTA's copy of the items
-  int* pages_shared = keys + 2 * a.hash;
-  constexpr int kPer = kMaxItems / kPlanThreads;
-  int row[kPer], L[kPer], other[kPer];     // CTA 0: rows, lengths; new tokens or the child's length
+  int* item_of = keys + 2 * a.hash;                            // fork: the item of the k-th demand
+  int* pages_shared = item_of + (kFork ? a.n : 0);
+  int row[kPerThread], L[kPerThread], other[kPerThread];     // CTA 0: rows, lengths; new tokens or the child's length
   uint32_t bits = 0;
   grid_dependency_wait();
   grid_launch_dependents();
   if (rank == 0) {
     if (tid < 4) a.status[tid] = 0;
-    for (int i = tid; i < a.hash; i += kPlanThreads) {
+    for (int i = tid; i < a.hash; i += threads) {
       keys[i] = -1;
       keys[a.hash + i] = a.n;
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = j * kPlanThreads + tid;
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = j * threads + tid;
+      if (j * threads >= a.n) break;
       row[j] = i < a.n ? a.rows[i] : -1;
       other[j] = i < a.n ? (kFork ? a.parents[i] : a.new_tokens[i]) : -1;
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      if (j * threads >= a.n) break;
       const int parent = other[j];
       const bool known = row[j] >= 0 && row[j] < a.R &&
                          (!kFork || (parent >= 0 && parent < a.R && parent != row[j]));
@@ -245,23 +282,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   pages.count(a.refs, a.P, rank, size, pages_shared);
   if (rank == 0) {
     int* first = keys + a.hash;
-    int need[kPer], at[kPer];
+    int need[kPerThread], at[kPerThread], pages_of[kPerThread];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      if (j * threads >= a.n) break;
       need[j] = -1;
-      at[j] = 0;
+      at[j] = pages_of[j] = 0;
       if (L[j] < 0 || (kFork ? other[j] != 0 : other[j] < 0)) continue;
-      const long long have = (L[j] + a.ps - 1LL) / a.ps;
-      const long long want =
-          kFork ? have : (static_cast<long long>(L[j]) + other[j] + a.ps - 1) / a.ps;
       if (!kFork && L[j] > INT_MAX - other[j]) continue;
-      if (want <= a.C) need[j] = kFork ? L[j] % a.ps > 0 : static_cast<int>(want - have);
+      const int full = over_page(L[j], a.by_ps), have = over_page(L[j] + a.ps - 1u, a.by_ps);
+      const int want = kFork ? have : over_page(L[j] + other[j] + a.ps - 1u, a.by_ps);
+      if (want <= a.C) need[j] = kFork ? have - full : want - have;
+      pages_of[j] = kFork ? full : have;
     }
     // A row listed more than once belongs to its first item that is in order.
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      if (j * threads >= a.n) break;
       if (need[j] < 0) continue;
       int h = static_cast<int>((static_cast<unsigned>(row[j]) * 2654435769u) >> 8) & (a.hash - 1);
       while (true) {                                           // ends: at most half the table is used
@@ -269,15 +306,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         if (key == -1 || key == row[j]) break;
         h = (h + 1) & (a.hash - 1);
       }
-      atomicMin(first + h, j * kPlanThreads + tid);
+      atomicMin(first + h, j * threads + tid);
       at[j] = h;
     }
     __syncthreads();
     int carry = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = j * kPlanThreads + tid;
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = j * threads + tid;
+      if (j * threads >= a.n) break;
       if (need[j] >= 0 && first[at[j]] != i) need[j] = -1;
       if (need[j] < 0 && i < a.n) bits |= kErrMetadata;
       const int pages_needed = min(max(need[j], 0), kMaxPages + 1);
@@ -285,21 +322,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int before = add_pages(carry, block_scan(pages_needed, warp_sums, &sum));
       carry = add_pages(carry, sum);
       if (i < a.n)
-        items[i] = {before, pages_needed,
-                    kFork ? L[j] / a.ps : static_cast<int>((L[j] + a.ps - 1LL) / a.ps),
-                    need[j] < 0 ? -1 : row[j]};
+        items[i] = {before, pages_needed, pages_of[j], need[j] < 0 ? -1 : row[j]};
     }
     if (tid == 0) total_need = carry;
   }
   sync_cluster(cl);
-  pages.order(cl, warp_sums);
+  pages.order(cl);
   const int demand = *cl.map_shared_rank(&total_need, 0);
   const Item* from = cl.map_shared_rank(items, 0);
   if (rank == 0) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = j * kPlanThreads + tid;
-      if (j * kPlanThreads >= a.n) break;
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = j * threads + tid;
+      if (j * threads >= a.n) break;
       if (i >= a.n) continue;
       const Item it = items[i];
       const bool served = it.row >= 0 && (it.need == 0 || it.off + it.need <= pages.total);
@@ -313,38 +348,50 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     if (bits) report_error(a.status, bits);
   }
-  const int handed = min(demand, pages.total);
-  if (handed > 0) {
-    for (int i = tid; i < a.n; i += kPlanThreads) mine[i] = from[i];
+  if (demand > 0) {
+    for (int i = tid; i < a.n; i += threads) {
+      const Item x = from[i];
+      mine[i] = x;
+      if (kFork && x.need > 0) item_of[x.off] = i;             // a fork demands one page at most
+    }
     __syncthreads();
-    // The k-th free page goes to the item whose demands [off, off + need) hold k.
-    Item it{0, 0, 0, -1};
-    int which = -1;
+    // The item whose demand holds the k-th fresh page: the last one with off <= k (items without
+    // a demand share their successor's offset).
+    const auto owner = [&](int k, int lo) {
+      int hi = a.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (mine[mid].off <= k) lo = mid; else hi = mid;
+      }
+      return lo;
+    };
+    // Served items come before the first whose demand the free pages do not hold.
+    const int handed = demand <= pages.total ? demand : mine[owner(pages.total, 0)].off;
+    int which = 0;
+    Item it{0, 0, 0, -1};                              // of the warp's last pages
     for (int j = 0; j < pages.own; ++j) {
       if (pages.step_before[j * size + rank] >= handed) break;
-      const uint32_t m = pages.mask(j);
-      int k = pages.before(j, m);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (!(m >> b & 1u)) continue;
-        const int rank_k = k++;
-        if (rank_k >= handed) continue;
-        if (which < 0 || rank_k - it.off >= it.need) {
-          // the last item with off <= k: items without a demand share their successor's offset
-          int lo = max(which, 0), hi = a.n;
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (mine[mid].off <= rank_k) lo = mid; else hi = mid;
-          }
-          which = lo;
-          it = mine[lo];
+      pages.each(j, [&](int p, bool is_free, int k, int count) {
+        const int first = __shfl_sync(0xffffffffu, k, 0), last = min(first + count, handed) - 1;
+        if (last < first) return;
+        int w = which;
+        Item own = it;
+        if (kFork) {
+          w = item_of[min(k, last)];
+          own = mine[w];
+        } else if (first < it.off || last >= it.off + it.need) {
+          // The warp's fresh pages mostly go to the item of its last ones; here each lane looks
+          // for its own.
+          w = owner(min(k, last), which);
+          own = mine[w];
+          which = __shfl_sync(0xffffffffu, w, 31);
+          it = mine[which];
         }
-        if (it.row < 0 || it.off + it.need > pages.total) continue;
-        const int p = pages.first_page(j) + b;
-        a.tables[static_cast<long long>(it.row) * a.C + it.have + (rank_k - it.off)] = p;
+        if (!is_free || k > last) return;
+        a.tables[static_cast<long long>(own.row) * a.C + own.have + (k - own.off)] = p;
         a.refs[p] = 1;
-        if (kFork) a.page[which] = p;
-      }
+        if (kFork) a.page[w] = p;
+      });
     }
   }
   if (size > 1) cl.sync();                 // the items in CTA 0's shared memory have been read
@@ -546,17 +593,29 @@ struct CompactArgs {
 
 __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs a) {
   extern __shared__ __align__(16) int shared[];
-  __shared__ int warp_sums[32];
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   grid_dependency_wait();
   grid_launch_dependents();
   if (rank == 0 && tid < 4) a.status[tid] = 0;
   FreePages pages;
   pages.count(a.refs, a.P, rank, size, shared);
+  if (a.refs_out != a.refs) {              // what moves is set right below, after the barriers
+    constexpr int kBatch = 8;
+    const int stride = size * threads;
+    for (int p0 = rank * threads + tid; p0 < a.P; p0 += kBatch * stride) {
+      int r[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (p0 + u * stride < a.P) r[u] = a.refs[p0 + u * stride];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (p0 + u * stride < a.P) a.refs_out[p0 + u * stride] = r[u];
+    }
+  }
   sync_cluster(cl);
-  pages.order(cl, warp_sums);
+  pages.order(cl);
   const int live = a.P - pages.total;
   if (rank == 0 && tid == 0) {
     *a.num_live = live;
@@ -565,27 +624,20 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
   // f free and p - f live pages lie before page p.  The f-th hole is p; of the live pages that
   // move, live - 1 - (p - f) come after p, which numbers them without knowing how many they are.
   for (int j = 0; j < pages.own; ++j) {
-    const uint32_t m = pages.mask(j);
-    int f = pages.before(j, m);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int p = pages.first_page(j) + b;
-      if (p >= a.P) break;
-      const bool is_free = m >> b & 1u;
+    pages.each(j, [&](int p, bool is_free, int f, int) {
+      if (p >= a.P) return;
       if (p == live) *a.moves = f;                  // holes below `live` = live pages from it on
       if (is_free) {
         if (p < live) a.dst[f] = p;
         else a.to[p] = p;
-        ++f;
       } else if (p >= live) {
         a.src[live - 1 - (p - f)] = p;
       }
-      if (a.refs_out != a.refs && is_free == (p >= live)) a.refs_out[p] = is_free ? 0 : a.refs[p];
-    }
+    });
   }
   sync_cluster(cl);
   const int moves = *a.moves;
-  for (int k = rank * kPlanThreads + tid; k < moves; k += size * kPlanThreads) {
+  for (int k = rank * threads + tid; k < moves; k += size * threads) {
     const int s = a.src[moves - 1 - k], d = a.dst[k];
     a.to[s] = d;
     a.refs_out[d] = a.refs[s];
@@ -663,24 +715,22 @@ bool overlap(const void* a, long long na, const void* b, long long nb) {
 }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA; }
 
-// CTAs that look through P page counts: one per two steps, up to the portable cluster size.
-int plan_ctas(int P) {
-  int size = 1;
-  while (size < kPlanCluster && size * 2 * kStepPages < P) size *= 2;
-  return size;
-}
-
 // Launch one of the planning kernels as a single cluster; `ints` of shared memory besides the
-// page counts'.
+// page counts'.  Small pools and lists: one CTA of 256 threads (its 4 steps of pages stay in
+// registers, an item list fits its threads); else CTAs of 1024, one per step, up to the portable
+// cluster size.
 template <typename Args>
-cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, size_t ints,
+cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_steps, int items, size_t ints,
                         std::atomic<uint64_t>& ready, cudaStream_t st) {
-  const int size = plan_ctas(P);
-  const size_t smem = (FreePages::shared_ints(P, size) + ints) * sizeof(int);
+  const bool few = P <= few_steps * kFewThreads * kThreadPages && items <= kPerThread * kFewThreads;
+  const int threads = few ? kFewThreads : kPlanThreads;
+  int size = 1;
+  while (size < kPlanCluster && size < FreePages::steps_of(P, threads) && !few) size *= 2;
+  const size_t smem = (FreePages::shared_ints(P, size, threads) + ints) * sizeof(int);
   if (smem > 48 * 1024 && !kernel_smem_ready(kernel, kPlanSmem, ready)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = size;
-  cfg.blockDim = kPlanThreads;
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -700,7 +750,9 @@ cudaError_t launch_items(PlanArgs a, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   a.hash = 2;
   while (a.hash < 2 * a.n) a.hash *= 2;
-  return launch_plan(plan_kernel<kFork>, a, a.P, 4 * static_cast<size_t>(a.n) + 2 * a.hash, ready, st);
+  a.by_ps = ~0ull / static_cast<unsigned>(a.ps) + 1;       // ceil(2^64 / ps): ps is even
+  return launch_plan(plan_kernel<kFork>, a, a.P, 4, a.n,
+                     (kFork ? 5 : 4) * static_cast<size_t>(a.n) + 2 * a.hash, ready, st);
 }
 
 }  // namespace
@@ -811,7 +863,7 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   a.src = at(ws, l.src); a.dst = at(ws, l.dst); a.to = at(ws, l.to); a.moves = at(ws, l.moves);
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
   static std::atomic<uint64_t> ready{0};
-  if (launch_plan(compact_kernel, a, a.P, 0, ready, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  if (launch_plan(compact_kernel, a, a.P, 1, 0, 0, ready, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
   CopyArgs c{};
   c.pools = pool_count(pools);
   for (int i = 0; i < c.pools; ++i) c.src.p[i] = c.dst.p[i] = pools->pools_host[i];
