@@ -167,7 +167,7 @@ typedef struct paged_cache_params {
   int num_pages;              /* P <= 2^24                                                 */
 } paged_cache_params;
 
-/* The pools of every layer, all with the same page ids. */
+/* The pools of every layer, all with the same page ids; a page is below 2^31 bytes. */
 #define PAGED_CACHE_MAX_POOLS 256
 typedef struct paged_cache_pools {
   int num_layers;        /* N: N pointers (combined) or 2 N (K, V of each layer in turn), at

@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 struct ForkArgs {
   Pools pools;
   int npools, segs;          // runs of tail bytes per pool: one per head, K and V
-  long long page_bytes, seg_bytes, token_bytes;
+  int page_bytes, seg_bytes, token_bytes;
   const int *children, *parents, *need, *len, *page;
   int n;
   int* tables;
@@ -514,6 +514,10 @@ struct ForkArgs {
   uint32_t* status;
 };
 
+// A CTA copies one item's tail in one pool, after two dependent round trips to L2 (item -> parent's
+// table -> page).  Latency bounds it, so a thread has four 16-byte words in flight: forking 256
+// children in 8 layers takes 28 us a call with its frees, 32 with one word in flight; two pools per
+// CTA changed nothing, half a pool per CTA (more round trips) cost 5 us.
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -532,13 +536,22 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constan
         if (threadIdx.x == 0) report_error(a.status, kErrMetadata);
         continue;
       }
-      const int words = static_cast<int>((L - full * a.ps) * a.token_bytes / 16);
+      const int words = (L - full * a.ps) * a.token_bytes / 16, all = words * a.segs;
       uint8_t* base = static_cast<uint8_t*>(a.pools.p[w]);
-      for (int x = threadIdx.x; x < words * a.segs; x += kCopyThreads) {
-        const int seg = x / words, at = x - seg * words;
-        const long long o = seg * a.seg_bytes + at * 16LL;
-        *reinterpret_cast<uint4*>(base + d * a.page_bytes + o) =
-            ld_stream(reinterpret_cast<const uint4*>(base + s * a.page_bytes + o));
+      const uint8_t* src = base + static_cast<long long>(s) * a.page_bytes;
+      uint8_t* dst = base + static_cast<long long>(d) * a.page_bytes;
+      for (int x0 = threadIdx.x; x0 < all; x0 += 4 * kCopyThreads) {
+        uint4 v[4];
+        int o[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int x = x0 + b * kCopyThreads, seg = x / words;
+          o[b] = seg * a.seg_bytes + (x - seg * words) * 16;
+          if (x < all) v[b] = ld_stream(reinterpret_cast<const uint4*>(src + o[b]));
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (x0 + b * kCopyThreads < all) *reinterpret_cast<uint4*>(dst + o[b]) = v[b];
       }
     } else {
       const long long to = static_cast<long long>(a.children[i]) * a.C;
@@ -686,6 +699,11 @@ bool cache_params_ok(const paged_cache_params* p) {
          p->page_size <= 128 && p->page_size % 8 == 0 && p->num_pages > 0 &&
          p->num_pages <= kMaxPages;
 }
+int pool_count(const paged_cache_pools* p) { return p->num_layers * (p->combined_cache ? 1 : 2); }
+long long seg_bytes(const paged_cache_pools* p) { return 2LL * p->page_size * p->head_dim; }
+long long page_bytes(const paged_cache_pools* p) {
+  return (p->combined_cache ? 2 : 1) * p->num_kv_heads * seg_bytes(p);
+}
 bool pools_ok(const paged_cache_pools* p) {
   if (!p || !p->pools_host || p->num_layers <= 0 || p->num_layers > PAGED_CACHE_MAX_POOLS)
     return false;
@@ -695,14 +713,10 @@ bool pools_ok(const paged_cache_pools* p) {
       p->head_dim % 8)
     return false;
   if (p->page_size < 8 || p->page_size > 128 || p->page_size % 8) return false;
+  if (page_bytes(p) >= 1LL << 31) return false;
   for (int i = 0; i < count; ++i)
     if (!p->pools_host[i] || (reinterpret_cast<uintptr_t>(p->pools_host[i]) & 15)) return false;
   return true;
-}
-int pool_count(const paged_cache_pools* p) { return p->num_layers * (p->combined_cache ? 1 : 2); }
-long long seg_bytes(const paged_cache_pools* p) { return 2LL * p->page_size * p->head_dim; }
-long long page_bytes(const paged_cache_pools* p) {
-  return (p->combined_cache ? 2 : 1) * p->num_kv_heads * seg_bytes(p);
 }
 bool same_geometry(const paged_cache_pools* a, const paged_cache_pools* b) {
   return a->num_layers == b->num_layers && a->num_kv_heads == b->num_kv_heads &&
@@ -826,9 +840,9 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   f.npools = pool_count(pools);
   for (int i = 0; i < f.npools; ++i) f.pools.p[i] = pools->pools_host[i];
   f.segs = (pools->combined_cache ? 2 : 1) * pools->num_kv_heads;
-  f.page_bytes = page_bytes(pools);
-  f.seg_bytes = seg_bytes(pools);
-  f.token_bytes = 2LL * pools->head_dim;
+  f.page_bytes = static_cast<int>(page_bytes(pools));
+  f.seg_bytes = static_cast<int>(seg_bytes(pools));
+  f.token_bytes = 2 * pools->head_dim;
   f.children = children; f.parents = parents; f.need = a.need; f.len = a.len; f.page = a.page;
   f.n = n;
   f.tables = tables; f.refs = refs;

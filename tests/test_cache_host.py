@@ -221,7 +221,8 @@ BAD_STATE = [dict(rows=-1), dict(max_pages_per_request=0), dict(page_size=4), di
              dict(num_pages=0), dict(num_pages=(1 << 24) + 1)]
 BAD_POOLS = [dict(num_layers=0), dict(num_layers=257), dict(num_kv_heads=0), dict(head_dim=4),
              dict(head_dim=520), dict(page_size=12), dict(num_pages=0), dict(ptrs=(None,)),
-             dict(ptrs=(A16 + 8,)), dict(pools_host=None), dict(combined_cache=0, num_layers=129)]
+             dict(ptrs=(A16 + 8,)), dict(pools_host=None), dict(combined_cache=0, num_layers=129),
+             dict(num_kv_heads=16384, page_size=128, head_dim=512)]
 
 
 def test_page_call_refusals(lib):
