@@ -17,9 +17,10 @@
  * Status words.  A call with a workspace clears the status word at the workspace's start and
  * ORs in what it finds (paged_attn_workspace_status reads it); the workspace belongs to one
  * launch in flight at a time.  Calls without a workspace take status_dev, a uint32 word that
- * they OR into and never clear, or NULL to have nothing recorded.  In both,
- * PAGED_ATTN_ERR_METADATA means that an item broke its contract and was left out, and
- * PAGED_ATTN_ERR_CAPACITY that the free pages did not suffice for every item.
+ * they OR into and never clear, or NULL to have nothing recorded (paged_attn_workspace_status
+ * reads such a word too).  In both, PAGED_ATTN_ERR_METADATA means that an item broke its
+ * contract and was left out, PAGED_ATTN_ERR_CAPACITY that the free pages did not suffice for
+ * every item, and PAGED_ATTN_ERR_TIMEOUT that a device wait ran out and rows were not written.
  */
 #ifndef PAGED_CACHE_H
 #define PAGED_CACHE_H
@@ -100,12 +101,12 @@ typedef struct paged_rope_params {
 
 /* Rotate q [T, Hq, D] and k [T, Hkv, D] (NULL with num_kv_heads = 0) at positions_dev [T]
  * (any int32), reading table_dev [R / 2].  Computed in fp32 and rounded once.  An output may
- * be its own input (same pointer and strides: the columns from R on are then not touched);
- * otherwise outputs share no element with any input.  Pointers need the alignment of their
+ * be its own input (same pointer and strides); otherwise outputs share no element with any
+ * input.  Pointers need the alignment of their
  * element; accesses are wide where pointers, strides and R allow 16 bytes. */
 int paged_rope_run(const paged_rope_params* params, const void* q_dev, const void* k_dev,
                    const int32_t* positions_dev, const uint64_t* table_dev, void* q_out_dev,
-                   void* k_out_dev, void* stream);
+                   void* k_out_dev, uint32_t* status_dev, void* stream);
 
 /* ---- appending to the cache ------------------------------------------------------------- */
 typedef struct paged_append_params {

@@ -60,7 +60,7 @@ EXPORTS = {
     "paged_rope_frequencies": (C.c_int, [C.POINTER(RopeScaling), C.POINTER(C.c_double),
                                          C.POINTER(C.c_float)]),
     "paged_rope_table": (C.c_int, [C.POINTER(C.c_double), C.c_int, C.POINTER(C.c_uint64)]),
-    "paged_rope_run": (C.c_int, [C.POINTER(RopeParams)] + [_P] * 7),
+    "paged_rope_run": (C.c_int, [C.POINTER(RopeParams)] + [_P] * 8),
     "paged_append_run": (C.c_int, [C.POINTER(AppendParams)] + [_P] * 13),
     "paged_cache_free_run": (C.c_int, [C.POINTER(CacheParams), _P, C.c_int] + [_P] * 5),
     "paged_cache_extend_workspace_size": (C.c_size_t, [C.c_int]),
@@ -78,6 +78,7 @@ EXPORTS = {
 
 
 _I32 = torch.int32
+_INT_MAX = 2 ** 31 - 1
 # The current stream's handle without building a Stream object, where this torch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -135,6 +136,14 @@ def _ints(t, dev, name):
         _on_device(t, dev, name)
         raise ValueError(f"{name} must be a contiguous int32 tensor")
     return t.data_ptr()
+
+
+def _count(t, name):
+    """Number of elements, as the int that the C call takes."""
+    n = t.numel()
+    if n > _INT_MAX:
+        raise ValueError(f"{name} has more than 2^31 - 1 elements")
+    return n
 
 
 def _ints_of(t, dev, name, n):
@@ -252,18 +261,21 @@ def _rows(t, dev, name):
         T = B * S
     else:
         raise ValueError(f"{name} must be [tokens, heads, D] or [batch, seq, heads, D]")
+    if T > _INT_MAX or H > _INT_MAX:
+        raise ValueError(f"{name} is too large")
     if e != 1 and D > 1:
         raise ValueError(f"{name}: the columns of a head must be contiguous")
     return T, H, D, ts, hs
 
 
 def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_factor=1.0,
-                     inverse=False, q_out=None, k_out=None, stream=None):
+                     inverse=False, q_out=None, k_out=None, status=None, stream=None):
     """Rotate q (and k) [T, heads, D] or [B, S, heads, D] at int32 `positions` (one per token),
     the first 2 * len(freqs) columns of each head; returns q_out, or (q_out, k_out) with k.
 
     q_out=q rotates in place.  inverse=True turns back by the same angles (times the same
-    attention_factor): the gradient of the input from the gradient of the output."""
+    attention_factor): the gradient of the input from the gradient of the output.
+    status: an int32 word that device-side findings are OR-ed into."""
     dev = _device()
     T, Hq, D, qt, qh = _rows(q, dev, "q")
     dt = q.dtype
@@ -295,12 +307,12 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos = _ints_of(positions, dev, "positions", T)
-    table = _table(freqs, dev)
+    table, status = _table(freqs, dev), _status(status, dev)
     if T:
         rc = _call.paged_rope_run(
             _rope_params(T, Hq, Hk, D, 2 * freqs.numel(), ROPE_LAYOUT[layout], _DTYPE[dt],
                          int(inverse), attention_factor, qt, qh, kt, kh, qot, qoh, kot, koh),
-            q.data_ptr(), kp, pos, table, q_out.data_ptr(), kop, _stream(stream, dev))
+            q.data_ptr(), kp, pos, table, q_out.data_ptr(), kop, status, _stream(stream, dev))
         if rc:
             _check(rc, "paged_rope_run")
     return q_out if k is None else (q_out, k_out)
@@ -346,7 +358,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     status: an int32 word that device-side findings are OR-ed into."""
     dev = _device()
     kc, vc, combined, P, Hkv, ps, D = _geometry(paged_kv_cache, dev)
-    B = seq_lens_kv.numel()
+    B = _count(seq_lens_kv, "seq_lens_kv")
     T, Hk, Dk, kt, kh = _rows(k, dev, "k")
     Tv, Hv, Dv, vt, vh = _rows(v, dev, "v")
     dt = k.dtype
@@ -451,9 +463,9 @@ def cache_pools(layers) -> CachePools:
 def _rows_state(block_tables, seq_lens, page_refs, page_size, dev):
     """(params, address of the tables, lengths, counts) of the three arrays."""
     shape = block_tables.shape
-    if len(shape) != 2:
+    if len(shape) != 2 or max(shape) > _INT_MAX:
         raise ValueError("block_tables must be [rows, C]")
-    return (_cache_params(shape[0], shape[1], page_size, page_refs.numel()),
+    return (_cache_params(shape[0], shape[1], page_size, _count(page_refs, "page_refs")),
             _ints(block_tables, dev, "block_tables"),
             _ints_of(seq_lens, dev, "seq_lens", shape[0]), _ints(page_refs, dev, "page_refs"))
 
@@ -463,7 +475,8 @@ def free_cache_rows(rows, block_tables, seq_lens, page_refs, page_size, *, statu
     """Free the listed rows: their pages' counts go down by one, their lengths to 0."""
     dev = _device()
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
-    rc = _call.paged_cache_free_run(p, _ints(rows, dev, "rows"), rows.numel(), bt, sl, pr,
+    rc = _call.paged_cache_free_run(p, _ints(rows, dev, "rows"), _count(rows, "rows"), bt, sl,
+                                    pr,
                                     _status(status, dev), _stream(stream, dev))
     if rc:
         _check(rc, "paged_cache_free_run")
@@ -480,7 +493,7 @@ def extend_cache_rows(rows, new_tokens, block_tables, seq_lens, page_refs, page_
     they are; the workspace's status word says so."""
     dev = _device()
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
-    n = rows.numel()
+    n = _count(rows, "rows")
     ws = _workspace(workspace, extend_cache_workspace_size, n, rows, dev)
     rc = _call.paged_cache_extend_run(p, _ints(rows, dev, "rows"),
                                       _ints_of(new_tokens, dev, "new_tokens", n), n, bt, sl, pr,
@@ -499,7 +512,7 @@ def fork_cache_rows(pools, parents, children, block_tables, seq_lens, page_refs,
     live tokens of a partly filled last page are copied into a fresh one, in every layer."""
     dev = _device()
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
-    n = children.numel()
+    n = _count(children, "children")
     ws = _workspace(workspace, fork_cache_workspace_size, n, children, dev)
     rc = _call.paged_cache_fork_run(p, pools.ref(dev), _ints_of(parents, dev, "parents", n),
                                     _ints(children, dev, "children"), n, bt, sl, pr,
@@ -544,7 +557,7 @@ def copy_cache_pages(pools, src_pages, dst_pages, *, dst_pools=None, status=None
     layers of `dst_pools`."""
     dev = _device()
     src = pools.ref(dev)
-    n = src_pages.numel()
+    n = _count(src_pages, "src_pages")
     rc = _call.paged_cache_copy_run(src, src if dst_pools is None else dst_pools.ref(dev),
                                     _ints(src_pages, dev, "src_pages"),
                                     _ints_of(dst_pages, dev, "dst_pages", n), n,

@@ -741,7 +741,7 @@ cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_step
   int size = 1;
   while (size < kPlanCluster && size < FreePages::steps_of(P, threads) && !few) size *= 2;
   const size_t smem = (FreePages::shared_ints(P, size, threads) + ints) * sizeof(int);
-  if (smem > 48 * 1024 && !kernel_smem_ready(kernel, kPlanSmem, ready)) return cudaErrorUnknown;
+  if (smem > 47 * 1024 && !kernel_smem_ready(kernel, kPlanSmem, ready)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = size;
   cfg.blockDim = threads;

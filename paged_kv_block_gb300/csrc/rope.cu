@@ -23,10 +23,19 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxStaged = 196608;       // bytes of the rows that one CTA stages at most
-constexpr int kStageGoal = 24576;        // bytes of rows that a CTA stages where it may choose
-constexpr int kStagedCtas = 6;
+// Threads of a CTA: 128, but 64 where rows are staged and the slots of its tokens fill no more than
+// half of those (6 heads of 80 columns: 9.5 us with 128 threads, 12.6 with 64, for 12,627 tokens).
+// Small CTAs with one wide token or a few narrow ones keep loads, sines and stores of many tokens
+// overlapped: staging 17,408 tokens of 32 + 8 + 8 bf16 heads (append) takes 68.5 us with 64 threads
+// and 12 KB each, 70 with 128 and 24 KB, 74 with 256 and 48 KB; 16 and more of the 64-thread CTAs
+// per SM (72 us) slow the writes.
+constexpr int kMaxThreads = 128;
+constexpr int kFewThreads = 64;
+constexpr int kStageGoal = 12288;        // bytes of rows that a CTA stages where it may choose
+constexpr int kMaxStaged = 196608;       // and at most
+constexpr int kStagedCtas = 5;           // per SM, of 128 threads: bounds their registers
+constexpr int kTileTokens = 8;           // per SM: from here on a CTA takes several tokens
+constexpr int kStagedTokens = 4;         // per SM: from here on rows are staged
 
 struct RopeArgs {
   const void *q, *k, *v;
@@ -40,7 +49,8 @@ struct RopeArgs {
   int inverse, q_in_place, k_in_place;
   float m;
   int tile;                              // tokens per CTA
-  int staged_bytes;                      // shared memory of staged rows (a request: may be staged)
+  int chunk;                             // heads per CTA
+  int staged_bytes;                      // shared memory of staged rows
   // append
   const int *qo_indptr, *kv_indptr, *pages, *lens;
   int B, SQ, C, ps, num_pages;
@@ -131,13 +141,19 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// What a thread holds of one slot between its load and its store.  A slot is V columns pairs (half:
-// V of each half) or V columns (interleaved; V = 1 is one pair, element by element, for rows whose
-// alignment allows no wider access); the slots behind the rotated ones copy V columns each.
+// What a thread holds of one slot between its load and its store.  A slot is V column pairs (half: V
+// columns of each half) or V columns (interleaved; the last one may hold columns past the rotated
+// ones too.  V = 1 is one pair element by element, for rows whose alignment allows no wider access);
+// the slots from `rot` on copy V columns each, from column `first`.
 template <typename TIn, int V, bool kHalf>
 struct Slot {
   static constexpr bool kTwo = kHalf || V == 1;
+  static constexpr int kPairs = kTwo ? V : V / 2;
   Vec<TIn, V> a, b;
+  static __host__ __device__ int rotated_slots(int n) { return (n + kPairs - 1) / kPairs; }
+  static __host__ __device__ int first_copied(int n) {
+    return kTwo ? 2 * n : rotated_slots(n) * V;
+  }
   __device__ __forceinline__ void load(const TIn* x, int n, int s, int rot, int first) {
     if (s < rot) {
       a = *reinterpret_cast<const Vec<TIn, V>*>(x + (!kHalf && V == 1 ? 2 * s : s * V));
@@ -146,44 +162,53 @@ struct Slot {
       a = *reinterpret_cast<const Vec<TIn, V>*>(x + first + (s - rot) * V);
     }
   }
-  // (cos, sin) of the slot's pairs
-  static constexpr int kPairs = kTwo ? V : V / 2;
+  // cs: (cos, sin) of the slot's pairs; `rotated` columns of the row are kept as they lie in `a`
+  // (already results: mode 2) where TIn is not TOut.
   template <typename TOut>
   __device__ __forceinline__ void store(TOut* y, const float2 (&cs)[kPairs], int n, int s, int rot,
-                                        int first, bool rotate) const {
+                                        int first, bool rotate, int results) const {
     if (s >= rot) {
-      *reinterpret_cast<Vec<TOut, V>*>(y + first + (s - rot) * V) = convert<TIn, TOut, V>(a);
+      const int at = first + (s - rot) * V;
+      Vec<TOut, V> c = convert<TIn, TOut, V>(a);
+      if constexpr (sizeof(TIn) == sizeof(TOut) && !std::is_same<TIn, TOut>::value) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at + i < results) c.e[i] = reinterpret_cast<const TOut*>(&a)[i];
+      }
+      *reinterpret_cast<Vec<TOut, V>*>(y + at) = c;
       return;
     }
-    Vec<TOut, V> c, d;
-    if (!rotate) {
-      c = convert<TIn, TOut, V>(a);
-      if constexpr (kTwo) d = convert<TIn, TOut, V>(b);
-    } else {
-      float u[V], y1[V];
-      unpack(a, u);
-      if constexpr (kTwo) {
-        float w[V], y2[V];
+    Vec<TOut, V> c = convert<TIn, TOut, V>(a), d;
+    if constexpr (kTwo) {
+      d = convert<TIn, TOut, V>(b);
+      if (rotate) {
+        float u[V], w[V], y1[V], y2[V];
+        unpack(a, u);
         unpack(b, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           y1[i] = turned(u[i], cs[i].x, -w[i], cs[i].y);
           y2[i] = turned(w[i], cs[i].x, u[i], cs[i].y);
         }
+        c = pack<TOut>(y1);
         d = pack<TOut>(y2);
-      } else {
+      }
+      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? s * V : 2 * s)) = c;
+      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? n + s * V : 2 * s + 1)) = d;
+    } else {
+      if (rotate) {
+        float u[V], y1[V];
+        unpack(a, u);
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
           y1[i] = turned(u[i], cs[i / 2].x, -u[i + 1], cs[i / 2].y);
           y1[i + 1] = turned(u[i + 1], cs[i / 2].x, u[i], cs[i / 2].y);
         }
+        const Vec<TOut, V> r = pack<TOut>(y1);
+#pragma unroll
+        for (int i = 0; i < V; ++i)                    // a column past the rotated ones keeps its bits
+          if (s * kPairs + i / 2 < n) c.e[i] = r.e[i];
       }
-      c = pack<TOut>(y1);
-    }
-    if constexpr (kTwo) {
-      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? s * V : 2 * s)) = c;
-      *reinterpret_cast<Vec<TOut, V>*>(y + (kHalf ? n + s * V : 2 * s + 1)) = d;
-    } else {
       *reinterpret_cast<Vec<TOut, V>*>(y + s * V) = c;
     }
   }
@@ -195,57 +220,63 @@ struct TokenSlot {
   int position;
 };
 
-// kStaged: the tile's rows are brought to shared memory by bulk copies, which keeps tens of KB in
-// flight per SM whatever the registers allow.  It needs 16-byte aligned tokens with adjacent heads.
-template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, bool kStaged>
-__global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kernel(const RopeArgs a) {
+// How a CTA gets at its rows.
+constexpr int kDirect = 0;    // straight from global memory, a few rows in flight per thread
+constexpr int kStaged = 1;    // brought to shared memory by bulk copies: tens of KB in flight per SM
+                              // whatever the registers allow (16-byte aligned, adjacent heads)
+constexpr int kInShared = 2;  // staged, and rotated there element by element: half layout whose halves
+                              // do not both start on a 16-byte access
+
+template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, int kMode>
+__global__ void __launch_bounds__(kMaxThreads, kMode != kDirect ? kStagedCtas : 1)
+rope_kernel(const RopeArgs a) {
   using Held = Slot<TIn, V, kHalf>;
   // Rows in flight per thread: 64 bytes of loads.
   constexpr int kBytes = V * static_cast<int>(sizeof(TIn)) * (Held::kTwo ? 2 : 1);
-  constexpr int kBatch = kStaged || kBytes >= 64 ? 1 : (64 / kBytes > 8 ? 8 : 64 / kBytes);
+  constexpr int kBatch = kMode != kDirect || kBytes >= 64 ? 1 : (64 / kBytes > 8 ? 8 : 64 / kBytes);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t arrived;
   __shared__ int gave_up;
   float2* cs = reinterpret_cast<float2*>(smem + a.staged_bytes);    // [tile, n]
   TokenSlot* tok = reinterpret_cast<TokenSlot*>(cs + static_cast<size_t>(a.tile) * a.n);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int t0 = blockIdx.x * a.tile;
   const int nt = min(a.tile, a.T - t0);
-  const int rot = kHalf ? a.n / V : (V == 1 ? a.n : 2 * a.n / V), first = 2 * a.n;
+  const int rot = kMode == kInShared ? 0 : Held::rotated_slots(a.n);
+  const int first = kMode == kInShared ? 0 : Held::first_copied(a.n);
   const int heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
+  const int h_begin = blockIdx.y * a.chunk, h_end = min(heads, h_begin + a.chunk);
   // A thread keeps one slot of one token, and so its sines, and walks the heads; consecutive
   // threads hold consecutive slots, then tokens.  `groups` threads share the heads of a slot.
-  const int slots = min(a.slots, kThreads), units = a.tile * slots, groups = kThreads / units;
+  const int slots = min(a.slots, threads), units = a.tile * slots, groups = threads / units;
   const int group = tid / units, unit = tid - group * units;
-  const int t = unit / slots, s = blockIdx.y * kThreads + unit - t * slots;
+  const int t = unit / slots, s = blockIdx.z * threads + unit - t * slots;
   const bool active = group < groups && t < nt && s < a.slots;
   const long long token = t0 + t;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int q_row = a.Hq * a.D, k_row = a.Hkv * a.D;                // staged: elements of a token
-  if constexpr (kStaged) {
+  TIn* const rows = reinterpret_cast<TIn*>(smem);                   // staged [tile, chunk, D]
+  const int row_elems = (h_end - h_begin) * a.D;
+  if constexpr (kMode != kDirect) {
     if (tid < 32) {
       if (tid == 0) {
         gave_up = 0;
         mbar_init(&arrived, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&arrived, nt * heads * a.D * static_cast<int>(sizeof(TIn)));
+        mbar_arrive_expect_tx(&arrived, nt * row_elems * static_cast<int>(sizeof(TIn)));
       }
       __syncwarp();
-      TIn* to = reinterpret_cast<TIn*>(smem);
       for (int i = tid; i < nt * (kAppend ? 3 : 2); i += 32) {
-        const int which = i / nt, j = i - which * nt;
-        const long long at = t0 + j;
-        TIn* dst = to + j * heads * a.D;
-        if (which == 0 && a.Hq > 0)
-          bulk_load(dst, static_cast<const TIn*>(a.q) + at * a.q_ts, q_row * sizeof(TIn), &arrived);
-        else if (which == 1 && a.Hkv > 0)
-          bulk_load(dst + q_row, static_cast<const TIn*>(a.k) + at * a.k_ts, k_row * sizeof(TIn),
-                    &arrived);
-        else if (which == 2)
-          bulk_load(dst + q_row + k_row, static_cast<const TIn*>(a.v) + at * a.v_ts,
-                    k_row * sizeof(TIn), &arrived);
+        const int which = i / nt, j = i - which * nt;               // q, k or v; token
+        const int before = which == 0 ? 0 : a.Hq + (which - 1) * a.Hkv;
+        const int lo = max(h_begin, before);
+        const int hi = min(h_end, before + (which == 0 ? a.Hq : a.Hkv));
+        if (lo >= hi) continue;
+        const TIn* x = static_cast<const TIn*>(which == 0 ? a.q : which == 1 ? a.k : a.v) +
+                       (t0 + j) * (which == 0 ? a.q_ts : which == 1 ? a.k_ts : a.v_ts);
+        bulk_load(rows + j * row_elems + (lo - h_begin) * a.D, x + (lo - before) * a.D,
+                  (hi - lo) * a.D * static_cast<int>(sizeof(TIn)), &arrived);
       }
     }
   }
@@ -254,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kern
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int h = h0 + u * groups;
-      if (h >= heads) break;
+      if (h >= h_end) break;
       const TIn* p;
-      if (kStaged)
-        p = reinterpret_cast<const TIn*>(smem) + (t * heads + h) * a.D;
+      if (kMode != kDirect)
+        p = rows + t * row_elems + (h - h_begin) * a.D;
       else if (h < a.Hq)
         p = static_cast<const TIn*>(a.q) + token * a.q_ts + h * a.q_hs;
       else if (!kAppend || h < a.Hq + a.Hkv)
@@ -269,18 +300,18 @@ __global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kern
     }
   };
   // The first rows are on their way while positions, pages and sines are found.
-  if (!kStaged && active) load(group);
+  if (kMode == kDirect && active) load(h_begin + group);
   if constexpr (kAppend) {
     if (a.qo_indptr != nullptr) {
-      for (int t = tid; t < nt; t += kThreads) tok[t].request = -1;
+      for (int t = tid; t < nt; t += threads) tok[t].request = -1;
       __syncthreads();
-      for (int b = tid; b < a.B; b += kThreads) {
+      for (int b = tid; b < a.B; b += threads) {
         const int lo = max(a.qo_indptr[b], t0), hi = min(a.qo_indptr[b + 1], t0 + nt);
         for (int t = lo; t < hi; ++t) tok[t - t0].request = b;
       }
       __syncthreads();
     }
-    for (int t = tid; t < nt; t += kThreads) {
+    for (int t = tid; t < nt; t += threads) {
       const int b = a.qo_indptr != nullptr ? tok[t].request : (t0 + t) / a.SQ;
       TokenSlot found{-1, b, 0};
       if (b >= 0) {
@@ -304,24 +335,47 @@ __global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kern
     }
     __syncthreads();
   }
-  for (int i = tid; i < nt * a.n; i += kThreads) {
+  for (int i = tid; i < nt * a.n; i += threads) {
     const int j = i / a.n, pair = i - j * a.n;
     const int p = kAppend ? tok[j].position : a.positions[t0 + j];
     cs[i] = turn_of(p, a.table[pair], a.m, a.inverse ? -1.f : 1.f);
   }
   __syncthreads();
-  if constexpr (kStaged) {
-    if (!mbar_wait(&arrived, 0, a.status, &gave_up)) {
-      drain_wait(&arrived, 0);
-      return;
+  if constexpr (kMode != kDirect) {
+    const bool ok = mbar_wait(&arrived, 0, a.status, &gave_up);
+    if (!ok) drain_wait(&arrived, 0);
+    if (kMode == kInShared ? __syncthreads_or(!ok) != 0 : !ok) return;
+  }
+  if constexpr (kMode == kInShared) {
+    // One pair of one token per thread, over the heads to rotate: q and k.
+    const int rotated = min(h_end, a.Hq + a.Hkv) - h_begin;
+    const int pairs = nt * a.n, share = max(1, threads / pairs);
+    for (int i = tid; i < pairs * share; i += threads) {
+      const int g = i / pairs, j = i - g * pairs, at = j / a.n, pair = j - at * a.n;
+      const float2 turn = cs[j];
+      for (int h = g; h < rotated; h += share) {
+        TIn* x = rows + at * row_elems + h * a.D + pair;
+        const float u = to_f(x[0]), w = to_f(x[a.n]);
+        const float y1 = turned(u, turn.x, -w, turn.y), y2 = turned(w, turn.x, u, turn.y);
+        if constexpr (sizeof(TIn) == sizeof(TOut)) {   // the results, rounded once
+          reinterpret_cast<TOut*>(x)[0] = from_f<TOut>(y1);
+          reinterpret_cast<TOut*>(x)[a.n] = from_f<TOut>(y2);
+        } else {                                       // fp32 rows: rounded as they leave
+          x[0] = y1;
+          x[a.n] = y2;
+        }
+      }
     }
+    __syncthreads();
   }
   if (!active) return;
-  if constexpr (kStaged) load(group);
+  if constexpr (kMode != kDirect) load(h_begin + group);
   float2 turn[Held::kPairs];
 #pragma unroll
-  for (int i = 0; i < Held::kPairs; ++i)
-    turn[i] = s < rot ? cs[t * a.n + s * Held::kPairs + i] : make_float2(0.f, 0.f);
+  for (int i = 0; i < Held::kPairs; ++i) {
+    const int pair = s * Held::kPairs + i;
+    turn[i] = s < rot && pair < a.n ? cs[t * a.n + pair] : make_float2(0.f, 0.f);
+  }
   bool write_q = a.Hq > 0, write_k = true;
   TOut *q_to, *k_to, *v_to = nullptr;
   long long k_step;
@@ -332,25 +386,28 @@ __global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kern
     v_to = static_cast<TOut*>(a.vo) + tok[t].off;
     k_step = static_cast<long long>(a.ps) * a.D;
   } else {
-    write_q = !(a.q_in_place && s >= rot);
-    write_k = !(a.k_in_place && s >= rot);
+    // in place, what only copies stays where it is
+    const bool moves = kMode == kInShared ? s * V < 2 * a.n : s < rot;
+    write_q = moves || !a.q_in_place;
+    write_k = moves || !a.k_in_place;
     k_to = static_cast<TOut*>(a.ko) + token * a.ko_ts;
     k_step = a.ko_hs;
   }
   q_to = static_cast<TOut*>(a.qo) + token * a.qo_ts;
-  for (int h0 = group; h0 < heads;) {
+  const int results = kMode == kInShared ? 2 * a.n : 0;
+  for (int h0 = h_begin + group; h0 < h_end;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int h = h0 + u * groups;
-      if (h >= heads) break;
+      if (h >= h_end) break;
       if (h < a.Hq) {
-        if (write_q) x[u].store(q_to + h * a.qo_hs, turn, a.n, s, rot, first, true);
+        if (write_q) x[u].store(q_to + h * a.qo_hs, turn, a.n, s, rot, first, true, results);
       } else if (write_k) {
         const int j = h - a.Hq;
         if (!kAppend || j < a.Hkv)
-          x[u].store(k_to + j * k_step, turn, a.n, s, rot, first, true);
+          x[u].store(k_to + j * k_step, turn, a.n, s, rot, first, true, results);
         else
-          x[u].store(v_to + (j - a.Hkv) * k_step, turn, a.n, s, rot, first, false);
+          x[u].store(v_to + (j - a.Hkv) * k_step, turn, a.n, s, rot, first, false, 0);
       }
     }
     h0 += kBatch * groups;
@@ -358,63 +415,87 @@ __global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 1) rope_kern
   }
 }
 
-template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend>
-cudaError_t launch_kernel(const RopeArgs& a, dim3 grid, size_t smem, bool staged, cudaStream_t st) {
-  count_launches(1);
-  if constexpr (V * sizeof(TIn) == 16) {
-    if (staged) {
-      static std::atomic<uint64_t> ready{0};
-      void (*const kernel)(RopeArgs) = rope_kernel<TIn, TOut, V, kHalf, kAppend, true>;
-      if (!kernel_smem_ready(kernel, kMaxStaged + 16384, ready)) return cudaErrorUnknown;
-      return launch_after_previous(kernel, grid, dim3(kThreads), smem, st, a);
-    }
-  }
-  return launch_after_previous(rope_kernel<TIn, TOut, V, kHalf, kAppend, false>, grid,
-                               dim3(kThreads), smem, st, a);
-}
-
-template <typename TIn, typename TOut, int V, bool kAppend>
-cudaError_t launch_v(RopeArgs a, bool half, cudaStream_t st) {
+template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, int kMode>
+cudaError_t launch_mode(RopeArgs a, cudaStream_t st) {
+  using Held = Slot<TIn, V, kHalf>;
   const int sms = current_sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  const bool copies = !(a.q_in_place && (a.Hkv == 0 || a.k_in_place));  // columns past the rotated
-  const int rot = half ? a.n / V : (V == 1 ? a.n : 2 * a.n / V);
-  a.slots = rot + (copies ? (a.D - 2 * a.n) / V : 0);
-  const int slots = a.slots < kThreads ? a.slots : kThreads;
-  const long long token_bytes =
-      static_cast<long long>(a.Hq + a.Hkv * (kAppend ? 2 : 1)) * a.D * sizeof(TIn);
-  const bool staged = a.staged_bytes != 0 && V * sizeof(TIn) == 16 && a.T >= 16 * sms &&
-                      (copies || a.D == 2 * a.n) && token_bytes <= kMaxStaged;
+  // Slots of a row: those that rotate, and unless every output is its input the ones that copy.
+  const bool copies = !(a.q_in_place && (a.Hkv == 0 || a.k_in_place));
+  if (kMode == kInShared)
+    a.slots = copies ? a.D / V : ceil_div(2 * a.n, V);
+  else
+    a.slots = Held::rotated_slots(a.n) + (copies ? (a.D - Held::first_copied(a.n)) / V : 0);
+  const int heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
+  const long long token_bytes = static_cast<long long>(heads) * a.D * sizeof(TIn);
+  const long long goal = token_bytes < kStageGoal ? kStageGoal / token_bytes : 1;
+  const int threads =
+      kMode == kStaged && goal * a.slots <= kFewThreads / 2 ? kFewThreads : kMaxThreads;
+  const int slots = a.slots < threads ? a.slots : threads;
   // Tokens per CTA: one while there are few; else as many as keep most threads busy (the slots of
   // the tile's tokens, times the groups that share the heads, within the CTA).
   a.tile = 1;
-  if (a.T >= 16 * sms) {
+  if (a.T >= kTileTokens * sms) {
     int best = 0;
-    for (int tile = 1; tile <= (staged ? 16 : 4) && tile * slots <= kThreads; tile *= 2) {
-      if (staged && tile > 1 && tile * token_bytes > kStageGoal) break;
-      const int busy = kThreads / (tile * slots) * (tile * slots);
+    for (int tile = 1; tile <= (kMode != kDirect ? 16 : 4) && tile * slots <= threads; tile *= 2) {
+      if (kMode != kDirect && tile > 1 && tile * token_bytes > kStageGoal) break;
+      const int busy = threads / (tile * slots) * (tile * slots);
       if (busy >= best) {
         best = busy;
         a.tile = tile;
       }
     }
   }
-  a.staged_bytes = staged ? static_cast<int>(align_up(a.tile * token_bytes, 128)) : 0;
+  // Few tokens: their heads are shared out over more CTAs, down to one round of a CTA's groups.
+  const int tiles = ceil_div(a.T, a.tile), groups = threads / (a.tile * slots);
+  int chunks = tiles < 2 * sms ? 2 * sms / tiles : 1;
+  if (chunks > ceil_div(heads, groups)) chunks = ceil_div(heads, groups);
+  a.chunk = ceil_div(heads, chunks);
+  chunks = ceil_div(heads, a.chunk);
+  a.staged_bytes = kMode == kDirect ? 0
+                                    : static_cast<int>(align_up(static_cast<size_t>(a.tile) * a.chunk *
+                                                                    a.D * sizeof(TIn), 128));
   const size_t smem = a.staged_bytes +
                       static_cast<size_t>(a.tile) * (a.n * sizeof(float2) + sizeof(TokenSlot));
-  const dim3 grid(ceil_div(a.T, a.tile), ceil_div(a.slots, kThreads));
-  return half ? launch_kernel<TIn, TOut, V, true, kAppend>(a, grid, smem, staged, st)
-              : launch_kernel<TIn, TOut, V, false, kAppend>(a, grid, smem, staged, st);
+  void (*const kernel)(RopeArgs) = rope_kernel<TIn, TOut, V, kHalf, kAppend, kMode>;
+  if (smem > 47 * 1024) {                  // the default limit holds the static part too
+    static std::atomic<uint64_t> ready{0};
+    if (!kernel_smem_ready(kernel, kMaxStaged + 16384, ready)) return cudaErrorUnknown;
+  }
+  count_launches(1);
+  return launch_after_previous(kernel, dim3(tiles, chunks, ceil_div(a.slots, threads)),
+                               dim3(threads), smem, st, a);
+}
+
+// may_stage: alignment and strides allow bulk copies and 16-byte accesses.
+template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend>
+cudaError_t launch_v(const RopeArgs& a, bool may_stage, cudaStream_t st) {
+  if constexpr (V * sizeof(TIn) == 16) {
+    const int sms = current_sm_count();
+    const bool skips = a.q_in_place && (a.Hkv == 0 || a.k_in_place) && a.D > 2 * a.n;
+    if constexpr (kHalf) {
+      if (a.n % V != 0) return launch_mode<TIn, TOut, V, kHalf, kAppend, kInShared>(a, st);
+    }
+    // In place, direct reads skip the columns that do not rotate; copies would bring them.
+    if (may_stage && !skips && a.T >= kStagedTokens * sms)
+      return launch_mode<TIn, TOut, V, kHalf, kAppend, kStaged>(a, st);
+  }
+  return launch_mode<TIn, TOut, V, kHalf, kAppend, kDirect>(a, st);
 }
 
 template <typename TIn, typename TOut, bool kAppend>
-cudaError_t launch_typed(const RopeArgs& a, int v, bool half, cudaStream_t st) {
+cudaError_t launch_typed(const RopeArgs& a, int v, bool half, bool may_stage, cudaStream_t st) {
+  const auto run = [&](auto width) {
+    constexpr int V = decltype(width)::value;
+    return half ? launch_v<TIn, TOut, V, true, kAppend>(a, may_stage, st)
+                : launch_v<TIn, TOut, V, false, kAppend>(a, may_stage, st);
+  };
   if constexpr (sizeof(TIn) == 2) {
-    if (v >= 8) return launch_v<TIn, TOut, 8, kAppend>(a, half, st);
+    if (v >= 8) return run(std::integral_constant<int, 8>());
   }
-  if (v >= 4) return launch_v<TIn, TOut, 4, kAppend>(a, half, st);
-  if (v >= 2) return launch_v<TIn, TOut, 2, kAppend>(a, half, st);
-  return launch_v<TIn, TOut, 1, kAppend>(a, half, st);
+  if (v >= 4) return run(std::integral_constant<int, 4>());
+  if (v >= 2) return run(std::integral_constant<int, 2>());
+  return run(std::integral_constant<int, 1>());
 }
 
 bool layout_ok(int R, int D, int layout, float m, bool may_be_zero) {
@@ -428,18 +509,21 @@ bool aligned_to(const void* p, size_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
-// The largest power of two of elements per access that the columns, the pointers and the
-// strides allow: in the half layout both halves have to start on an access.
+// The largest power of two of elements per access that the columns, the pointers and the strides
+// allow.  In the half layout both halves have to start on an access, unless the rows are
+// rotated in shared memory.
 struct Width {
   int v;
-  Width(int R, bool half, size_t elem) : v(elem == 4 ? 4 : 8) {
-    while (v > 1 && (half ? (R / 2) % v : R % v) != 0) v /= 2;
-  }
+  explicit Width(size_t elem) : v(elem == 4 ? 4 : 8) {}
   void pointer(const void* p, size_t elem) {
     while (v > 1 && !aligned_to(p, v * elem)) v /= 2;
   }
   void stride(long long s) {
     while (v > 1 && s % v != 0) v /= 2;
+  }
+  void halves(int n, bool in_shared) {
+    if (!in_shared)
+      while (v > 1 && n % v != 0) v /= 2;
   }
 };
 
@@ -549,7 +633,7 @@ int paged_rope_table(const double* freqs, int n, uint64_t* table) {
 
 int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
                    const int32_t* positions, const uint64_t* table, void* q_out, void* k_out,
-                   void* stream) {
+                   uint32_t* status, void* stream) {
   if (!rope_params_ok(p)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const bool has_k = p->num_kv_heads > 0;
   if (!q || !q_out || !positions || !table || has_k != (k != nullptr) ||
@@ -557,6 +641,7 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   RopeArgs a{};
   a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
+  a.status = status;
   const long long D = p->head_dim;
   auto strides = [&](long long ts, long long hs, int heads, long long* to_ts, long long* to_hs) {
     const bool packed = ts == 0 && hs == 0;
@@ -576,28 +661,29 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (p->num_tokens == 0) return PAGED_ATTN_OK;
   const bool half = p->layout == PAGED_ROPE_HALF;
-  Width w(p->rotary_dim, half, e);
+  a.T = p->num_tokens; a.Hq = p->num_qo_heads; a.Hkv = p->num_kv_heads;
+  a.D = p->head_dim; a.n = p->rotary_dim / 2;
+  Width w(e);
   for (const void* t : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     w.pointer(t, e);
   for (long long s : {a.q_ts, a.q_hs, a.qo_ts, a.qo_hs}) w.stride(s);
   if (has_k)
     for (long long s : {a.k_ts, a.k_hs, a.ko_ts, a.ko_hs}) w.stride(s);
-  a.staged_bytes = aligned_to(q, 16) && aligned_to(k, 16) && a.q_hs == D && a.q_ts * e % 16 == 0 &&
-                   (!has_k || (a.k_hs == D && a.k_ts * e % 16 == 0));
+  const bool may_stage = w.v * e == 16 && a.q_hs == D && (!has_k || a.k_hs == D) &&
+                         (a.Hq + a.Hkv) * D * static_cast<long long>(e) <= kMaxStaged;
+  if (half) w.halves(a.n, may_stage);
   a.positions = positions;
   a.table = reinterpret_cast<const unsigned long long*>(table);
-  a.T = p->num_tokens; a.Hq = p->num_qo_heads; a.Hkv = p->num_kv_heads;
-  a.D = p->head_dim; a.n = p->rotary_dim / 2;
   a.inverse = p->inverse != 0;
   a.m = p->attention_factor;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (p->dtype) {
     case PAGED_ATTN_DTYPE_BF16:
-      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, w.v, half, st));
+      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, w.v, half, may_stage, st));
     case PAGED_ATTN_DTYPE_FP16:
-      return cuda_status(launch_typed<__half, __half, false>(a, w.v, half, st));
+      return cuda_status(launch_typed<__half, __half, false>(a, w.v, half, may_stage, st));
     default:
-      return cuda_status(launch_typed<float, float, false>(a, w.v, half, st));
+      return cuda_status(launch_typed<float, float, false>(a, w.v, half, may_stage, st));
   }
 }
 
@@ -637,20 +723,21 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
   a.B = p->batch; a.SQ = p->seq_len_q; a.C = p->max_pages_per_request; a.ps = p->page_size;
   a.num_pages = p->num_pages;
   a.status = status;
-  a.staged_bytes = aligned_to(q, 16) && aligned_to(k, 16) && aligned_to(v, 16) &&
-                   a.q_ts * e % 16 == 0 && a.k_ts * e % 16 == 0 && a.v_ts * e % 16 == 0;
   const bool half = p->layout == PAGED_ROPE_HALF;
-  Width w(p->rotary_dim, half, e);
+  Width w(e);
   for (const void* t : {q, k, v}) w.pointer(t, e);
   for (long long s : {a.q_ts, a.k_ts, a.v_ts}) w.stride(s);
+  const bool may_stage = w.v * e == 16 &&
+                         (a.Hq + 2LL * a.Hkv) * D * static_cast<long long>(e) <= kMaxStaged;
+  if (half) w.halves(a.n, may_stage);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (p->in_dtype) {
     case PAGED_ATTN_DTYPE_BF16:
-      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, w.v, half, st));
+      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
     case PAGED_ATTN_DTYPE_FP16:
-      return cuda_status(launch_typed<__half, __nv_bfloat16, true>(a, w.v, half, st));
+      return cuda_status(launch_typed<__half, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
     default:
-      return cuda_status(launch_typed<float, __nv_bfloat16, true>(a, w.v, half, st));
+      return cuda_status(launch_typed<float, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
   }
 }
 

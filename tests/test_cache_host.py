@@ -157,7 +157,7 @@ def _rope(lib, q=A16, k=A16, pos=A16, table=A16, qo=A16, ko=A16, **kw):
     f = dict(num_tokens=4, num_qo_heads=4, num_kv_heads=2, head_dim=64, rotary_dim=64, layout=0,
              dtype=0, inverse=0, attention_factor=1.0)
     f.update(kw)
-    return lib.paged_rope_run(C.byref(K.RopeParams(**f)), q, k, pos, table, qo, ko, None)
+    return lib.paged_rope_run(C.byref(K.RopeParams(**f)), q, k, pos, table, qo, ko, None, None)
 
 
 def test_rope_refusals(lib):

@@ -145,6 +145,38 @@ def test_lowest_pages_first_in_small_and_large_pools(P):
     b.extend([3, 0], [1, 2])
 
 
+def test_pools_of_many_pages():
+    """More steps of pages than a warp has lanes and than a thread keeps masks for."""
+    P, R = 300001, 40
+    rng = np.random.RandomState(1)
+    b = Both(9, R, 9000, P, 8, Hkv=1, combined=False)
+    used = (rng.rand(P) < 0.9).astype(np.int32)
+    used[:200000] = 1
+    b.set(refs=used.tolist())
+    free = int((used == 0).sum())
+    b.extend(list(range(R)), [rng.randint(0, 2 * 8 * free // R) for _ in range(R)])
+    b.free([3, 5])
+    b.fork([7, 8, 9], [3, 5, 5])
+    b.compact(in_place=False)
+
+
+def test_the_largest_pool():
+    """2^24 pages; one more is refused."""
+    P = 1 << 24
+    refs = torch.ones(P, dtype=torch.int32, device=DEV)
+    free = i32([5, 4_000_000, P - 9, P - 1])
+    refs[free.long()] = 0
+    tables, lens = torch.full((2, 4), -1, dtype=torch.int32, device=DEV), i32([0, 0])
+    ws = torch.empty(pkb.extend_cache_workspace_size(2), dtype=torch.uint8, device=DEV)
+    pkb.extend_cache_rows(i32([1, 0]), i32([24, 17]), tables, lens, refs, 16, workspace=ws)
+    assert tables.tolist() == [[P - 9, P - 1, -1, -1], [5, 4_000_000, -1, -1]]
+    assert lens.tolist() == [17, 24] and refs.eq(1).all()
+    assert pkb.paged_attn_workspace_status(ws)[0] == pkb.OK
+    with pytest.raises(pkb.PagedAttnError):
+        more = torch.ones(P + 1, dtype=torch.int32, device=DEV)
+        pkb.extend_cache_rows(i32([1]), i32([1]), tables, lens, more, 16, workspace=ws)
+
+
 def test_many_rows():
     """More items than a CTA has threads, in one CTA and in clusters of 2 to 8."""
     for P, R in ((6000, 1500), (9000, 1500), (20000, 4096), (50000, 1500)):
