@@ -8,6 +8,7 @@
 // listed.  The first is bound by the latency of its dependent steps (a handful of cluster
 // barriers and L2 round trips), the second by HBM.
 #include <climits>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -34,6 +35,8 @@ static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
 constexpr int kCopyCtas = 24;              // CTAs per SM where they walk the units (see copy_kernel)
+constexpr int kOwnUnits = 16;              // a fork of so little is done by the planning CTA itself:
+constexpr int kOwnBytes = 1 << 17;         // one launch (2.7 us of the host's time) less
 constexpr long long kMaxGrid = 1LL << 30;
 
 struct Pools {
@@ -204,6 +207,86 @@ struct FreePages {
   }
 };
 
+// ---- fork: shared pages and the copied tail ------------------------------------------------------
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+struct ForkArgs {
+  Pools pools;
+  int npools, segs;          // runs of tail bytes per pool: one per head, K and V
+  int page_bytes, seg_bytes, token_bytes;
+  const int *children, *parents;
+  const int* need;           // of the planning kernel: 0, 1 or -1 (left out)
+  const int* len;            // the parent's length before the call
+  const int* page;           // the fresh page of the item, -1 none
+  int n;
+  int* tables;
+  int* refs;
+  int C, ps, P;
+  int table_units;           // CTAs per item for the table row
+  uint32_t* status;
+};
+
+// One unit of a fork, by a whole CTA: the tail of an item in one pool, or part of its table row.  It
+// starts with two dependent round trips to L2 (item -> parent's table -> page), so latency bounds it
+// and a thread has four 16-byte words in flight: forking 256 children in 8 layers takes 28 us a
+// call with its frees, 32 with one word in flight; two pools per CTA changed nothing, half a pool
+// per CTA (more round trips) cost 5 us.
+__device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int per_item = a.npools + a.table_units;
+  const int i = static_cast<int>(u / per_item), w = static_cast<int>(u - static_cast<long long>(i) * per_item);
+  const int need = a.need[i], L = a.len[i], d = a.page[i], parent = a.parents[i];
+  if (need < 0) return;
+  const int full = L / a.ps;
+  const long long from = static_cast<long long>(parent) * a.C;
+  if (w < a.npools) {
+    if (d < 0) return;
+    const int s = a.tables[from + full];
+    if (s < 0 || s >= a.P) {
+      if (tid == 0) report_error(a.status, kErrMetadata);
+      return;
+    }
+    const int words = (L - full * a.ps) * a.token_bytes / 16, all = words * a.segs;
+    uint8_t* base = static_cast<uint8_t*>(a.pools.p[w]);
+    const uint8_t* src = base + static_cast<long long>(s) * a.page_bytes;
+    uint8_t* dst = base + static_cast<long long>(d) * a.page_bytes;
+    for (int x0 = tid; x0 < all; x0 += 4 * threads) {
+      uint4 v[4];
+      int o[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int x = x0 + b * threads, seg = x / words;
+        o[b] = seg * a.seg_bytes + (x - seg * words) * 16;
+        if (x < all) v[b] = ld_stream(reinterpret_cast<const uint4*>(src + o[b]));
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (x0 + b * threads < all) *reinterpret_cast<uint4*>(dst + o[b]) = v[b];
+    }
+  } else {
+    const long long to = static_cast<long long>(a.children[i]) * a.C;
+    for (int j = (w - a.npools) * threads + tid; j < full; j += a.table_units * threads) {
+      const int p = a.tables[from + j];
+      a.tables[to + j] = p;
+      if (p >= 0 && p < a.P) atomicAdd(a.refs + p, 1);
+      else report_error(a.status, kErrMetadata);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const long long units = static_cast<long long>(a.n) * (a.npools + a.table_units);
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) fork_unit(a, u);
+}
+
 // ---- extend and fork: who gets which fresh page ------------------------------------------------
 struct PlanArgs {
   const int* rows;         // extend: rows; fork: children
@@ -221,6 +304,12 @@ struct PlanArgs {
   int* len;                // workspace [n], fork: the parent's length before the call
   int* page;               // workspace [n], fork: the fresh page of the item, -1 none
 };
+struct ForkPlanArgs : PlanArgs {
+  int units;               // units that the (only) CTA does itself; 0: a second kernel does them
+  ForkArgs fork;
+};
+template <bool kFork>
+using PlanArgsOf = std::conditional_t<kFork, ForkPlanArgs, PlanArgs>;
 struct Item {
   int off;                 // first fresh page of the item among all demands
   int need;                // pages (0: none, or left out)
@@ -236,7 +325,7 @@ __device__ __forceinline__ int over_page(unsigned x, unsigned long long by_ps) {
 // CTA 0 looks after the items, all CTAs after the pages.  Latency bounds this kernel: the chain
 // is rows -> lengths -> scan -> cluster barrier -> tables, with the counts read beside it.
 template <bool kFork>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
   extern __shared__ __align__(16) int shared[];
   __shared__ int warp_sums[32];
   __shared__ int total_need;
@@ -394,18 +483,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       });
     }
   }
+  if constexpr (kFork) {
+    if (a.units > 0) {                     // a small fork: no second launch
+      __syncthreads();
+      for (int u = 0; u < a.units; ++u) fork_unit(a.fork, u);
+    }
+  }
   if (size > 1) cl.sync();                 // the items in CTA 0's shared memory have been read
 }
 
 // ---- copies ----------------------------------------------------------------------------------
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 // One CTA copies n16 16-byte words.
 __device__ __forceinline__ void copy_words(uint4* __restrict__ dst, const uint4* __restrict__ src,
                                            int n16) {
@@ -496,72 +583,6 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       }
       if (j == 0 && (L + a.ps - 1LL) / a.ps > a.C) report_error(a.status, kErrMetadata);
       if (p != old || a.tables_out != a.tables) a.tables_out[e] = p;
-    }
-  }
-}
-
-// ---- fork: shared pages and the copied tail ------------------------------------------------------
-struct ForkArgs {
-  Pools pools;
-  int npools, segs;          // runs of tail bytes per pool: one per head, K and V
-  int page_bytes, seg_bytes, token_bytes;
-  const int *children, *parents, *need, *len, *page;
-  int n;
-  int* tables;
-  int* refs;
-  int C, ps, P;
-  int table_units;           // CTAs per item for the table row
-  uint32_t* status;
-};
-
-// A CTA copies one item's tail in one pool, after two dependent round trips to L2 (item -> parent's
-// table -> page).  Latency bounds it, so a thread has four 16-byte words in flight: forking 256
-// children in 8 layers takes 28 us a call with its frees, 32 with one word in flight; two pools per
-// CTA changed nothing, half a pool per CTA (more round trips) cost 5 us.
-__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int per_item = a.npools + a.table_units;
-  const long long units = static_cast<long long>(a.n) * per_item;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = static_cast<int>(u / per_item), w = static_cast<int>(u - static_cast<long long>(i) * per_item);
-    const int need = a.need[i], L = a.len[i], d = a.page[i], parent = a.parents[i];
-    if (need < 0) continue;
-    const int full = L / a.ps;
-    const long long from = static_cast<long long>(parent) * a.C;
-    if (w < a.npools) {
-      if (d < 0) continue;
-      const int s = a.tables[from + full];
-      if (s < 0 || s >= a.P) {
-        if (threadIdx.x == 0) report_error(a.status, kErrMetadata);
-        continue;
-      }
-      const int words = (L - full * a.ps) * a.token_bytes / 16, all = words * a.segs;
-      uint8_t* base = static_cast<uint8_t*>(a.pools.p[w]);
-      const uint8_t* src = base + static_cast<long long>(s) * a.page_bytes;
-      uint8_t* dst = base + static_cast<long long>(d) * a.page_bytes;
-      for (int x0 = threadIdx.x; x0 < all; x0 += 4 * kCopyThreads) {
-        uint4 v[4];
-        int o[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int x = x0 + b * kCopyThreads, seg = x / words;
-          o[b] = seg * a.seg_bytes + (x - seg * words) * 16;
-          if (x < all) v[b] = ld_stream(reinterpret_cast<const uint4*>(src + o[b]));
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (x0 + b * kCopyThreads < all) *reinterpret_cast<uint4*>(dst + o[b]) = v[b];
-      }
-    } else {
-      const long long to = static_cast<long long>(a.children[i]) * a.C;
-      for (int j = (w - a.npools) * kCopyThreads + threadIdx.x; j < full;
-           j += a.table_units * kCopyThreads) {
-        const int p = a.tables[from + j];
-        a.tables[to + j] = p;
-        if (p >= 0 && p < a.P) atomicAdd(a.refs + p, 1);
-        else report_error(a.status, kErrMetadata);
-      }
     }
   }
 }
@@ -733,10 +754,13 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? PAGED_ATTN_OK : PAGED
 // page counts'.  Small pools and lists: one CTA of 256 threads (its 4 steps of pages stay in
 // registers, an item list fits its threads); else CTAs of 1024, one per step, up to the portable
 // cluster size.
+bool plan_is_small(int P, int few_steps, int items) {
+  return P <= few_steps * kFewThreads * kThreadPages && items <= kPerThread * kFewThreads;
+}
 template <typename Args>
 cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_steps, int items, size_t ints,
                         std::atomic<uint64_t>& ready, cudaStream_t st) {
-  const bool few = P <= few_steps * kFewThreads * kThreadPages && items <= kPerThread * kFewThreads;
+  const bool few = plan_is_small(P, few_steps, items);
   const int threads = few ? kFewThreads : kPlanThreads;
   int size = 1;
   while (size < kPlanCluster && size < FreePages::steps_of(P, threads) && !few) size *= 2;
@@ -760,7 +784,7 @@ cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_step
 }
 
 template <bool kFork>
-cudaError_t launch_items(PlanArgs a, cudaStream_t st) {
+cudaError_t launch_items(PlanArgsOf<kFork> a, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   a.hash = 2;
   while (a.hash < 2 * a.n) a.hash *= 2;
@@ -829,14 +853,13 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   if (!ws || ws_bytes < l.total) return PAGED_ATTN_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n == 0) return cuda_status(cudaMemsetAsync(ws, 0, 4 * sizeof(uint32_t), st));
-  PlanArgs a{};
+  ForkPlanArgs a{};
   a.rows = children; a.parents = parents; a.n = n;
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
   a.need = at(ws, l.need); a.len = at(ws, l.len); a.page = at(ws, l.page);
-  if (launch_items<true>(a, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
-  ForkArgs f{};
+  ForkArgs& f = a.fork;
   f.npools = pool_count(pools);
   for (int i = 0; i < f.npools; ++i) f.pools.p[i] = pools->pools_host[i];
   f.segs = (pools->combined_cache ? 2 : 1) * pools->num_kv_heads;
@@ -850,9 +873,14 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   f.table_units = ceil_div(a.C, 4 * kCopyThreads);
   f.status = a.status;
   const long long units = static_cast<long long>(n) * (f.npools + f.table_units);
-  const long long most = kMaxGrid;
+  // A few small pages: the planning CTA copies them itself.
+  if (plan_is_small(a.P, 4, n) && units <= kOwnUnits && units * f.page_bytes <= kOwnBytes)
+    a.units = static_cast<int>(units);
+  if (launch_items<true>(a, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  if (a.units > 0) return PAGED_ATTN_OK;
   count_launches(1);
-  return cuda_status(launch_after_previous(fork_kernel, static_cast<int>(units < most ? units : most),
+  return cuda_status(launch_after_previous(fork_kernel,
+                                           static_cast<int>(units < kMaxGrid ? units : kMaxGrid),
                                            kCopyThreads, 0, st, f));
 }
 
