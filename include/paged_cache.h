@@ -12,7 +12,9 @@
  * memory is the caller's and nothing is allocated; device work goes to `stream` and nothing
  * synchronises the host, so every *_run call can be captured in a CUDA graph; arguments are
  * checked on the host before anything is enqueued; calls work on the current device.  No call
- * here keeps anything between calls but what the caller's arrays hold.
+ * here keeps anything between calls but what the caller's arrays hold, and calls that share
+ * tables, lengths, counts or pages have to be ordered by the caller (one stream, or events).
+ * int32 arrays are 4-byte aligned, workspaces 16-byte, pools and caches 16-byte.
  *
  * Status words.  A call with a workspace clears the status word at the workspace's start and
  * ORs in what it finds (paged_attn_workspace_status reads it); the workspace belongs to one

@@ -749,6 +749,14 @@ bool overlap(const void* a, long long na, const void* b, long long nb) {
   return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA; }
+bool aligned_to(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// int32 arrays at 4-byte addresses (NULL is one).
+template <typename... P>
+bool ints_aligned(const P*... p) {
+  return (... && aligned_to(p, 4));
+}
 
 // Launch one of the planning kernels as a single cluster; `ints` of shared memory besides the
 // page counts'.  Small pools and lists: one CTA of 256 threads (its 4 steps of pages stay in
@@ -805,7 +813,8 @@ int paged_cache_free_run(const paged_cache_params* p, const int32_t* rows, int n
                          void* stream) {
   if (!cache_params_ok(p) || n < 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n == 0) return PAGED_ATTN_OK;
-  if (!rows || !tables || !lens || !refs) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!rows || !tables || !lens || !refs || !ints_aligned(rows, tables, lens, refs, status))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   count_launches(1);
   return cuda_status(launch_after_previous(
       free_kernel, n, kCopyThreads, 0, static_cast<cudaStream_t>(stream), rows, n, tables, lens, refs,
@@ -828,6 +837,8 @@ int paged_cache_extend_run(const paged_cache_params* p, const int32_t* rows,
   if (!cache_params_ok(p) || n < 0 || n > kMaxItems) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n > 0 && (!rows || !new_tokens || !tables || !lens || !refs))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!ints_aligned(rows, new_tokens, tables, lens, refs) || !aligned_to(ws, 16))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const PlanLayout l(0);
   if (!ws || ws_bytes < l.total) return PAGED_ATTN_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -848,6 +859,8 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   if (pools->num_pages != p->num_pages || pools->page_size != p->page_size)
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n > 0 && (!parents || !children || !tables || !lens || !refs))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!ints_aligned(parents, children, tables, lens, refs) || !aligned_to(ws, 16))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const PlanLayout l(n);
   if (!ws || ws_bytes < l.total) return PAGED_ATTN_ERR_WORKSPACE;
@@ -892,6 +905,8 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   if (pools->num_pages != p->num_pages || pools->page_size != p->page_size)
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (!refs || !refs_out || !num_live) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!ints_aligned(tables, lens, refs, tables_out, refs_out, num_live) || !aligned_to(ws, 16))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (p->rows > 0 && (!tables || !tables_out || !lens)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const long long tb = 4LL * p->rows * p->max_pages_per_request, rb = 4LL * p->num_pages;
   if (p->rows > 0 && tables != tables_out && overlap(tables, tb, tables_out, tb))
@@ -934,7 +949,8 @@ int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* 
   if (!pools_ok(src) || !pools_ok(dst) || !same_geometry(src, dst) || n < 0)
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (n == 0) return PAGED_ATTN_OK;
-  if (!src_pages || !dst_pages) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!src_pages || !dst_pages || !ints_aligned(src_pages, dst_pages, status))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   CopyArgs c{};
   c.pools = pool_count(src);
   for (int i = 0; i < c.pools; ++i) {

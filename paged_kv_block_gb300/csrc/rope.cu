@@ -220,6 +220,23 @@ struct TokenSlot {
   int position;
 };
 
+// The request that owns row t of the packed rows (-1: none), by a warp: the last b with
+// offsets[b] <= t, each round trip narrowing the choice to a 32nd.
+__device__ __forceinline__ int request_of(const int* offsets, int B, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;
+  while (true) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned after = __ballot_sync(0xffffffffu, at >= hi || offsets[at] > t);
+    const int c = after == 0 ? 32 : __ffs(after) - 1;       // probes not after t
+    if (c == 0) return -1;
+    lo += (c - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
+  }
+  return t < offsets[lo + 1] ? lo : -1;
+}
+
 // How a CTA gets at its rows.
 constexpr int kDirect = 0;    // straight from global memory, a few rows in flight per thread
 constexpr int kStaged = 1;    // brought to shared memory by bulk copies: tens of KB in flight per SM
@@ -303,11 +320,9 @@ rope_kernel(const RopeArgs a) {
   if (kMode == kDirect && active) load(h_begin + group);
   if constexpr (kAppend) {
     if (a.qo_indptr != nullptr) {
-      for (int t = tid; t < nt; t += threads) tok[t].request = -1;
-      __syncthreads();
-      for (int b = tid; b < a.B; b += threads) {
-        const int lo = max(a.qo_indptr[b], t0), hi = min(a.qo_indptr[b + 1], t0 + nt);
-        for (int t = lo; t < hi; ++t) tok[t - t0].request = b;
+      for (int t = tid >> 5; t < nt; t += threads >> 5) {
+        const int b = request_of(a.qo_indptr, a.B, t0 + t);
+        if ((tid & 31) == 0) tok[t].request = b;
       }
       __syncthreads();
     }
@@ -639,6 +654,8 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
   if (!q || !q_out || !positions || !table || has_k != (k != nullptr) ||
       has_k != (k_out != nullptr))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(positions, 4) || !aligned_to(table, 8) || !aligned_to(status, 4))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   RopeArgs a{};
   a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
   a.status = status;
@@ -698,6 +715,11 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
       has_q != (q_out != nullptr) || (p->combined_cache != 0) == (v_cache != nullptr))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (p->rotary_dim > 0 && !table) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(table, 8)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  for (const void* i : {static_cast<const void*>(qo_indptr), static_cast<const void*>(kv_indptr),
+                        static_cast<const void*>(pages), static_cast<const void*>(lens),
+                        static_cast<const void*>(status)})
+    if (!aligned_to(i, 4)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (!kv_indptr && p->max_pages_per_request <= 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const size_t e = size_of(p->in_dtype);
   if (!aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) || !aligned_to(q_out, 16) ||

@@ -165,7 +165,7 @@ def test_rope_refusals(lib):
                dict(head_dim=60), dict(head_dim=0), dict(head_dim=520), dict(rotary_dim=0),
                dict(rotary_dim=7), dict(rotary_dim=66), dict(layout=2), dict(dtype=3),
                dict(attention_factor=float("nan")), dict(attention_factor=float("inf")),
-               dict(q=None), dict(qo=None), dict(pos=None), dict(table=None), dict(k=None),
+               dict(pos=A16 + 2), dict(table=A16 + 4), dict(q=None), dict(qo=None), dict(pos=None), dict(table=None), dict(k=None),
                dict(ko=None), dict(num_kv_heads=0), dict(q=A16 + 1), dict(ko=A16 + 1),
                dict(dtype=2, q=A16 + 2), dict(q_token_stride=512, q_head_stride=64),
                dict(k_token_stride=512, k_head_stride=64), dict(num_qo_heads=65535)):
@@ -192,7 +192,9 @@ def test_append_refusals(lib):
                dict(q=None), dict(qout=None), dict(pages=None), dict(lens=None), dict(kc=None),
                dict(table=None), dict(vc=A16), dict(combined_cache=0), dict(kc=A16 + 8),
                dict(combined_cache=0, vc=A16 + 8), dict(qout=A16 + 8), dict(k=A16 + 1),
-               dict(attention_factor=float("inf")), dict(num_qo_heads=0),
+               dict(attention_factor=float("inf")), dict(num_qo_heads=0), dict(table=A16 + 4),
+               dict(pages=A16 + 2), dict(lens=A16 + 1), dict(status=A16 + 2), dict(qo=A16 + 2),
+               dict(indptr=A16 + 2),
                dict(batch=1 << 20, seq_len_q=1 << 12), dict(qo=A16, total_q=-1)):
         assert _append(lib, **kw) == BAD, kw
     assert _append(lib, batch=0) == 0
@@ -233,14 +235,17 @@ def test_page_call_refusals(lib):
         assert lib.paged_cache_extend_run(C.byref(p), A16, A16, 1, A16, A16, A16, A16, big, None) == BAD
     p = _params()
     for i in range(4):
-        a = [A16] * 4
-        a[i] = None
-        assert lib.paged_cache_free_run(C.byref(p), a[0], 1, a[1], a[2], a[3], None, None) == BAD
+        for bad in (None, A16 + 2):
+            a = [A16] * 4
+            a[i] = bad
+            assert lib.paged_cache_free_run(C.byref(p), a[0], 1, a[1], a[2], a[3], None, None) == BAD
     for i in range(5):
-        a = [A16] * 5
-        a[i] = None
-        assert lib.paged_cache_extend_run(C.byref(p), a[0], a[1], 1, a[2], a[3], a[4], A16, big,
-                                          None) == BAD
+        for bad in (None, A16 + 2):
+            a = [A16] * 5
+            a[i] = bad
+            assert lib.paged_cache_extend_run(C.byref(p), a[0], a[1], 1, a[2], a[3], a[4], A16, big,
+                                              None) == BAD
+    assert lib.paged_cache_extend_run(C.byref(p), *[A16] * 2, 1, *[A16] * 3, A16 + 4, big, None) == BAD
     assert lib.paged_cache_free_run(C.byref(p), A16, -1, A16, A16, A16, None, None) == BAD
     assert lib.paged_cache_free_run(C.byref(p), None, 0, None, None, None, None, None) == 0
     for n in (-1, 4097):
@@ -275,7 +280,8 @@ def test_page_call_refusals(lib):
         return lib.paged_cache_compact_run(C.byref(p), C.byref(s), bt, ln, rf, bto, rfo, live, ws, n,
                                            None)
     for kw in (dict(bt=None), dict(ln=None), dict(rf=None), dict(bto=None), dict(rfo=None),
-               dict(live=None), dict(bto=A16 + 16), dict(rfo=A16 + 64)):
+               dict(live=None), dict(bto=A16 + 16), dict(rfo=A16 + 64), dict(live=A16 + 2),
+               dict(ws=A16 + 8)):
         assert compact(**kw) == BAD, kw
     for kw in (dict(ws=None), dict(n=pkb.compact_cache_workspace_size(32) - 1)):
         assert compact(**kw) == pkb.ERR_WORKSPACE

@@ -133,9 +133,11 @@ def test_fixed_form(B, SQ):
     check(s, out.reshape(B * SQ, -1, 64), before, f)
 
 
-def test_without_queries_and_many_requests():
-    """K and V alone; more requests than a CTA has threads, most of them with one token."""
-    new = [1] * 700 + [0, 300, 2]
+@pytest.mark.parametrize("many", [31, 32, 33, 700, 1025, 40000])
+def test_without_queries_and_many_requests(many):
+    """K and V alone; up to more requests than a warp finds in three steps, most of them with one
+    token, some with none."""
+    new = [0] + [1] * many + [0, 0, 300, 2, 0]
     s = problem(5, new, [b % 20 for b in range(len(new))], Hq=1, Hkv=1, D=8, ps=8)
     before = s["cache"].clone()
     table, _ = pkb.rope_frequencies(8)

@@ -139,13 +139,14 @@ def test_in_place_touches_the_rotated_columns_only(layout, R):
     assert torch.equal(q2, want[0]) and torch.equal(k2, want[1])
 
 
+@pytest.mark.parametrize("D", [32, 512])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-def test_strides_and_alignment(dtype, layout):
+def test_strides_and_alignment(dtype, layout, D):
     """Slices of a fused projection, head-major storage, rows that start on odd elements, and a
     batch of sequences: all give what contiguous rows give."""
     gen = torch.Generator().manual_seed(6)
-    T, Hq, Hk, D = 9, 4, 2, 32
+    T, Hq, Hk = 9, 4, 2
     table, _ = pkb.rope_frequencies(D)
     pos = torch.randint(0, 9999, (T,), generator=gen, dtype=torch.int32).to(DEV)
     fused = rows(gen, T, Hq + 2 * Hk, D, dtype=dtype)
