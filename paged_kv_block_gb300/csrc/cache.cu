@@ -256,14 +256,22 @@ __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
     uint8_t* base = static_cast<uint8_t*>(a.pools.p[w]);
     const uint8_t* src = base + static_cast<long long>(s) * a.page_bytes;
     uint8_t* dst = base + static_cast<long long>(d) * a.page_bytes;
+    // word x of the tail lies in run x / words; the next one of the thread is `threads` further on
+    const int runs = threads / words, rest = threads - runs * words;
+    int seg = tid / words, at = tid - seg * words;
     for (int x0 = tid; x0 < all; x0 += 4 * threads) {
       uint4 v[4];
       int o[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int x = x0 + b * threads, seg = x / words;
-        o[b] = seg * a.seg_bytes + (x - seg * words) * 16;
-        if (x < all) v[b] = ld_stream(reinterpret_cast<const uint4*>(src + o[b]));
+        o[b] = seg * a.seg_bytes + at * 16;
+        if (x0 + b * threads < all) v[b] = ld_stream(reinterpret_cast<const uint4*>(src + o[b]));
+        seg += runs;
+        at += rest;
+        if (at >= words) {
+          at -= words;
+          ++seg;
+        }
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b)
