@@ -244,6 +244,30 @@ def test_graph_replay_follows_the_lengths():
     check(s, q_out, before, O.frequencies(64)[0])
 
 
+def test_two_streams_at_once():
+    """Long calls on two streams, each into its own cache."""
+    ss = [problem(30 + k, [900, 1, 1200], [3, 50, 0], combined=True) for k in range(2)]
+    table, _ = pkb.rope_frequencies(64)
+    want = []
+    for s in ss:
+        c = s["cache"].clone()
+        q = pkb.append_paged_kv_cache(s["k"], s["v"], c, s["lens"], q=s["q"], qo_indptr=s["qo"],
+                                      freqs=table, block_tables=s["tables"])
+        want.append((q, c))
+    torch.cuda.synchronize()
+    outs = [torch.zeros(s["q"].shape, dtype=torch.bfloat16, device=DEV) for s in ss]
+    streams = [torch.cuda.Stream() for _ in ss]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, st, out in zip(ss, streams, outs):
+            pkb.append_paged_kv_cache(s["k"], s["v"], s["cache"], s["lens"], q=s["q"], q_out=out,
+                                      qo_indptr=s["qo"], freqs=table, block_tables=s["tables"],
+                                      stream=st)
+    torch.cuda.synchronize()
+    for s, out, (q, c) in zip(ss, outs, want):
+        assert torch.equal(out, q) and torch.equal(s["cache"], c)
+
+
 def test_refusals():
     s = problem(14, [2, 3], [0, 0])
     base = dict(k=s["k"], v=s["v"], paged_kv_cache=cache_arg(s), seq_lens_kv=s["lens"],

@@ -357,6 +357,69 @@ def test_graph_and_shared_workspace():
     assert live.item() == n
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turn on one stream, and a call between."""
+    b = Both(6, 6, 8, 60, 16, layers=1)
+    b.extend([0, 1], [50, 70])
+    one, two = (i32([2]), i32([40])), (i32([0]), i32([3]))
+
+    def first():
+        pkb.free_cache_rows(one[0], b.tables, b.lens, b.refs, b.ps)
+        pkb.extend_cache_rows(*one, b.tables, b.lens, b.refs, b.ps, workspace=b.ws)
+
+    def second():
+        pkb.free_cache_rows(two[1], b.tables, b.lens, b.refs, b.ps)
+        pkb.fork_cache_rows(b.handle, *two, b.tables, b.lens, b.refs, workspace=b.ws)
+    first()
+    second()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for graph, call in zip(graphs, (first, second)):
+        with torch.cuda.graph(graph):
+            call()
+    for _ in range(4):
+        graphs[0].replay()
+        graphs[1].replay()
+        pkb.extend_cache_rows(i32([0]), i32([7]), b.tables, b.lens, b.refs, b.ps, workspace=b.ws)
+    b.o.free([2])
+    b.o.extend([2], [40])
+    b.o.free([3])
+    b.o.fork([0], [3])
+    for _ in range(4):
+        b.o.free([2])
+        b.o.extend([2], [40])
+        b.o.free([3])
+        b.o.fork([0], [3])
+        b.o.extend([0], [7])
+    b.same()
+
+
+def test_two_streams_at_once():
+    """Two states with workspaces of their own, driven by interleaved calls on two streams."""
+    both = [Both(20 + k, 8, 9, 9000, 8, Hkv=1, layers=2) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in both]
+    lists = [(i32(list(range(6))), i32([3 + k, 40, 9, 1, 8, 70]), i32([0, 1]), i32([6, 7]))
+             for k in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, st, (rows, new, parents, children) in zip(both, streams, lists):
+            with torch.cuda.stream(st):
+                pkb.free_cache_rows(rows, b.tables, b.lens, b.refs, b.ps)
+                pkb.free_cache_rows(children, b.tables, b.lens, b.refs, b.ps)
+                pkb.extend_cache_rows(rows, new, b.tables, b.lens, b.refs, b.ps, workspace=b.ws)
+                pkb.fork_cache_rows(b.handle, parents, children, b.tables, b.lens, b.refs,
+                                    workspace=b.ws)
+                pkb.compact_cache(b.handle, b.tables, b.lens, b.refs, workspace=b.ws)
+    torch.cuda.synchronize()
+    for k, b in enumerate(both):
+        for _ in range(5):
+            b.o.free(list(range(6)) + [6, 7])
+            b.o.extend(list(range(6)), [3 + k, 40, 9, 1, 8, 70])
+            b.o.fork([0, 1], [6, 7])
+            b.o.compact()
+        b.same()
+
+
 def test_refusals():
     b = Both(5, 3, 4, 10, 16)
     one = i32([0])
