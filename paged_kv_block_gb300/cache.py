@@ -77,15 +77,16 @@ EXPORTS = {
 }
 
 
-_I32 = torch.int32
+_I32, _I64, _BF16 = torch.int32, torch.int64, torch.bfloat16
 _INT_MAX = 2 ** 31 - 1
 # The current stream's handle without building a Stream object, where this torch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 def _device():
     """Index of the current CUDA device; one that no tensor is on where there is no GPU."""
     try:
-        return torch.cuda.current_device()
+        return _current_device()
     except (RuntimeError, AssertionError):
         if torch.cuda.is_available():
             raise
@@ -148,15 +149,16 @@ def _count(t, name):
 
 def _ints_of(t, dev, name, n):
     """The same, of n elements."""
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return _ints(t, dev, name)
+    if (t.numel() != n or t.dtype is not _I32 or t.get_device() != dev
+            or not t.is_contiguous()):
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements")
+        return _ints(t, dev, name)
+    return t.data_ptr()
 
 
 def _status(t, dev):
-    """Address of an optional 4-byte status word (int32 or uint32, any shape)."""
-    if t is None:
-        return None
+    """Address of a 4-byte status word (int32 or uint32, any shape)."""
     _on_device(t, dev, "status")
     if t.element_size() != 4 or t.numel() < 1 or not t.is_contiguous():
         raise ValueError("status must hold a 32-bit word")
@@ -171,9 +173,9 @@ def _empty(t, dtype):
 
 
 def _table(freqs, dev):
-    if freqs.dtype is not torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not _I64 or freqs.get_device() != dev or not freqs.is_contiguous():
+        _on_device(freqs, dev, "freqs")
         raise ValueError("freqs must be a table made by rope_frequencies")
-    _on_device(freqs, dev, "freqs")
     return freqs.data_ptr()
 
 
@@ -307,7 +309,9 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos = _ints_of(positions, dev, "positions", T)
-    table, status = _table(freqs, dev), _status(status, dev)
+    table = _table(freqs, dev)
+    if status is not None:
+        status = _status(status, dev)
     if T:
         rc = _call.paged_rope_run(
             _rope_params(T, Hq, Hk, D, 2 * freqs.numel(), ROPE_LAYOUT[layout], _DTYPE[dt],
@@ -338,7 +342,7 @@ def _geometry(cache, dev):
 
 
 def _pool(t, dev):
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
         _on_device(t, dev, "the cache")
         raise ValueError("the cache must be contiguous bf16")
     return t.data_ptr()
@@ -396,7 +400,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
         if Tq != T or Dq != D or q.dtype is not dt or (qh != D and Hq > 1):
             raise ValueError("q must have k's tokens, columns and dtype, and adjacent heads")
         if q_out is None:
-            q_out = _empty(q, torch.bfloat16)
+            q_out = _empty(q, _BF16)
         elif (q_out.shape != q.shape or q_out.dtype is not torch.bfloat16
               or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous bf16 of q's shape")
@@ -408,7 +412,9 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     rotary = 0
     if freqs is not None:
         table, rotary = _table(freqs, dev), 2 * freqs.numel()
-    lens, status = _ints(seq_lens_kv, dev, "seq_lens_kv"), _status(status, dev)
+    lens = _ints(seq_lens_kv, dev, "seq_lens_kv")
+    if status is not None:
+        status = _status(status, dev)
     if T:
         rc = _call.paged_append_run(
             _append_params(B, sq, total, Hq, Hkv, D, ps, P, combined, cols, rotary,
@@ -477,7 +483,8 @@ def free_cache_rows(rows, block_tables, seq_lens, page_refs, page_size, *, statu
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
     rc = _call.paged_cache_free_run(p, _ints(rows, dev, "rows"), _count(rows, "rows"), bt, sl,
                                     pr,
-                                    _status(status, dev), _stream(stream, dev))
+                                    None if status is None else _status(status, dev),
+                                    _stream(stream, dev))
     if rc:
         _check(rc, "paged_cache_free_run")
 
@@ -561,7 +568,8 @@ def copy_cache_pages(pools, src_pages, dst_pages, *, dst_pools=None, status=None
     rc = _call.paged_cache_copy_run(src, src if dst_pools is None else dst_pools.ref(dev),
                                     _ints(src_pages, dev, "src_pages"),
                                     _ints_of(dst_pages, dev, "dst_pages", n), n,
-                                    _status(status, dev), _stream(stream, dev))
+                                    None if status is None else _status(status, dev),
+                                    _stream(stream, dev))
     if rc:
         _check(rc, "paged_cache_copy_run")
 
