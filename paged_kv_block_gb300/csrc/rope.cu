@@ -34,6 +34,7 @@ constexpr int kFewThreads = 64;
 constexpr int kStageGoal = 12288;        // bytes of rows that a CTA stages where it may choose
 constexpr int kMaxStaged = 196608;       // and at most
 constexpr int kStagedCtas = 5;           // per SM, of 128 threads: bounds their registers
+constexpr int kInSharedCtas = 7;         // the same where the rows are rotated in shared memory
 constexpr int kTileTokens = 8;           // per SM: from here on a CTA takes several tokens
 constexpr int kStagedTokens = 4;         // per SM: from here on rows are staged
 
@@ -241,11 +242,15 @@ __device__ __forceinline__ int request_of(const int* offsets, int B, int t) {
 constexpr int kDirect = 0;    // straight from global memory, a few rows in flight per thread
 constexpr int kStaged = 1;    // brought to shared memory by bulk copies: tens of KB in flight per SM
                               // whatever the registers allow (16-byte aligned, adjacent heads)
-constexpr int kInShared = 2;  // staged, and rotated there element by element: half layout whose halves
+constexpr int kOnePiece = 2;  // the same where the rows of q, k and v and the tokens are one run in memory
+                              // (slices of one projection): one copy per CTA
+constexpr int kInShared = 3;  // staged, and rotated there element by element: half layout whose halves
                               // do not both start on a 16-byte access
 
 template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, int kMode>
-__global__ void __launch_bounds__(kMaxThreads, kMode != kDirect ? kStagedCtas : 1)
+__global__ void __launch_bounds__(kMaxThreads, kMode == kDirect      ? 1
+                                                         : kMode == kInShared ? kInSharedCtas
+                                                                              : kStagedCtas)
 rope_kernel(const RopeArgs a) {
   using Held = Slot<TIn, V, kHalf>;
   // Rows in flight per thread: 64 bytes of loads.
@@ -272,8 +277,27 @@ rope_kernel(const RopeArgs a) {
   const long long token = t0 + t;
   grid_dependency_wait();
   grid_launch_dependents();
-  TIn* const rows = reinterpret_cast<TIn*>(smem);                   // staged [tile, chunk, D]
-  const int row_elems = (h_end - h_begin) * a.D;
+  // Staged rows: [tile, heads, D] in one piece, else tensor by tensor [tile, its heads of the chunk,
+  // D], so that a tensor whose tokens are adjacent comes in one copy too.  (Few large copies: 12
+  // heads of 32,749 tokens take 41 us in one copy per CTA, 44 in three per token.)
+  TIn* const rows = reinterpret_cast<TIn*>(smem);
+  const int k_begin = a.Hq, v_begin = a.Hq + a.Hkv;
+  const int q_rows = max(0, min(h_end, k_begin) - h_begin);
+  const int k_rows = max(0, min(h_end, v_begin) - max(h_begin, k_begin));
+  const int v_rows = h_end - h_begin - q_rows - k_rows;
+  // Where row (t, head h of the chunk) would lie if every tensor were laid out as q, k or v is.
+  struct Staged {
+    TIn *q, *k, *v;
+  };
+  const auto staged = [&](int t) {
+    if constexpr (kMode == kOnePiece) {
+      TIn* const p = rows + t * heads * a.D;
+      return Staged{p, p, p};
+    }
+    return Staged{rows + t * q_rows * a.D,
+                  rows + (a.tile * q_rows + t * k_rows - q_rows) * a.D,
+                  rows + (a.tile * (q_rows + k_rows) + t * v_rows - q_rows - k_rows) * a.D};
+  };
   if constexpr (kMode != kDirect) {
     if (tid < 32) {
       if (tid == 0) {
@@ -281,23 +305,32 @@ rope_kernel(const RopeArgs a) {
         mbar_init(&arrived, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&arrived, nt * row_elems * static_cast<int>(sizeof(TIn)));
+        mbar_arrive_expect_tx(&arrived, nt * (h_end - h_begin) * a.D * static_cast<int>(sizeof(TIn)));
       }
       __syncwarp();
-      for (int i = tid; i < nt * (kAppend ? 3 : 2); i += 32) {
-        const int which = i / nt, j = i - which * nt;               // q, k or v; token
-        const int before = which == 0 ? 0 : a.Hq + (which - 1) * a.Hkv;
-        const int lo = max(h_begin, before);
-        const int hi = min(h_end, before + (which == 0 ? a.Hq : a.Hkv));
-        if (lo >= hi) continue;
-        const TIn* x = static_cast<const TIn*>(which == 0 ? a.q : which == 1 ? a.k : a.v) +
-                       (t0 + j) * (which == 0 ? a.q_ts : which == 1 ? a.k_ts : a.v_ts);
-        bulk_load(rows + j * row_elems + (lo - h_begin) * a.D, x + (lo - before) * a.D,
-                  (hi - lo) * a.D * static_cast<int>(sizeof(TIn)), &arrived);
+      // n rows of one tensor (of `all`, from its head h on) for every token of the tile
+      const auto bring = [&](const void* x, long long ts, int h, int n, int all, TIn* to) {
+        if (n == 0) return;
+        const TIn* from = static_cast<const TIn*>(x) + t0 * ts + static_cast<long long>(h) * a.D;
+        const bool adjacent = n == all && ts == static_cast<long long>(n) * a.D;
+        const int copies = adjacent ? 1 : nt;
+        const int bytes = (adjacent ? nt : 1) * n * a.D * static_cast<int>(sizeof(TIn));
+        for (int i = tid; i < copies; i += 32) bulk_load(to + i * n * a.D, from + i * ts, bytes, &arrived);
+      };
+      if constexpr (kMode == kOnePiece) {
+        bring(a.q, a.q_ts, 0, heads, heads, rows);
+      } else {
+        const int tile = a.tile * a.D;
+        bring(a.q, a.q_ts, h_begin, q_rows, a.Hq, rows);
+        bring(a.k, a.k_ts, max(h_begin, k_begin) - k_begin, k_rows, a.Hkv, rows + tile * q_rows);
+        if (kAppend)
+          bring(a.v, a.v_ts, max(h_begin, v_begin) - v_begin, v_rows, a.Hkv,
+                rows + tile * (q_rows + k_rows));
       }
     }
   }
   Held x[kBatch];
+  const Staged mine = staged(t);
   auto load = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -305,7 +338,7 @@ rope_kernel(const RopeArgs a) {
       if (h >= h_end) break;
       const TIn* p;
       if (kMode != kDirect)
-        p = rows + t * row_elems + (h - h_begin) * a.D;
+        p = (kMode == kOnePiece || h < k_begin ? mine.q : h < v_begin ? mine.k : mine.v) + (h - h_begin) * a.D;
       else if (h < a.Hq)
         p = static_cast<const TIn*>(a.q) + token * a.q_ts + h * a.q_hs;
       else if (!kAppend || h < a.Hq + a.Hkv)
@@ -368,8 +401,9 @@ rope_kernel(const RopeArgs a) {
     for (int i = tid; i < pairs * share; i += threads) {
       const int g = i / pairs, j = i - g * pairs, at = j / a.n, pair = j - at * a.n;
       const float2 turn = cs[j];
+      const Staged of = staged(at);
       for (int h = g; h < rotated; h += share) {
-        TIn* x = rows + at * row_elems + h * a.D + pair;
+        TIn* x = (h_begin + h < k_begin ? of.q : of.k) + h * a.D + pair;
         const float u = to_f(x[0]), w = to_f(x[a.n]);
         const float y1 = turned(u, turn.x, -w, turn.y), y2 = turned(w, turn.x, u, turn.y);
         if constexpr (sizeof(TIn) == sizeof(TOut)) {   // the results, rounded once
@@ -445,16 +479,19 @@ cudaError_t launch_mode(RopeArgs a, cudaStream_t st) {
   const long long token_bytes = static_cast<long long>(heads) * a.D * sizeof(TIn);
   const long long goal = token_bytes < kStageGoal ? kStageGoal / token_bytes : 1;
   const int threads =
-      kMode == kStaged && goal * a.slots <= kFewThreads / 2 ? kFewThreads : kMaxThreads;
+      (kMode == kStaged || kMode == kOnePiece) && goal * a.slots <= kFewThreads / 2 ? kFewThreads : kMaxThreads;
   const int slots = a.slots < threads ? a.slots : threads;
-  // Tokens per CTA: one while there are few; else as many as keep most threads busy (the slots of
-  // the tile's tokens, times the groups that share the heads, within the CTA).
+  // Tokens per CTA: one while there are few; else the most that keep 7 of 8 threads busy (the slots of
+  // the tile's tokens, times the groups that share the heads), or that keep the most busy.  12,627
+  // tokens of 8 + 2 + 2 heads with 32 of 128 columns rotated (14 slots) take 47 us one by one, 20 by
+  // four.
   a.tile = 1;
   if (a.T >= kTileTokens * sms) {
+    const long long most = kMode == kDirect ? 4 : goal < 16 ? goal : 16;
     int best = 0;
-    for (int tile = 1; tile <= (kMode != kDirect ? 16 : 4) && tile * slots <= threads; tile *= 2) {
-      if (kMode != kDirect && tile > 1 && tile * token_bytes > kStageGoal) break;
-      const int busy = threads / (tile * slots) * (tile * slots);
+    for (int tile = 1; tile <= most && tile * slots <= threads; ++tile) {
+      int busy = threads / (tile * slots) * (tile * slots);
+      if (busy * 8 >= threads * 7) busy = threads;
       if (busy >= best) {
         best = busy;
         a.tile = tile;
@@ -463,7 +500,7 @@ cudaError_t launch_mode(RopeArgs a, cudaStream_t st) {
   }
   // Few tokens: their heads are shared out over more CTAs, down to one round of a CTA's groups.
   const int tiles = ceil_div(a.T, a.tile), groups = threads / (a.tile * slots);
-  int chunks = tiles < 2 * sms ? 2 * sms / tiles : 1;
+  int chunks = kMode != kOnePiece && tiles < 2 * sms ? 2 * sms / tiles : 1;
   if (chunks > ceil_div(heads, groups)) chunks = ceil_div(heads, groups);
   a.chunk = ceil_div(heads, chunks);
   chunks = ceil_div(heads, a.chunk);
@@ -492,8 +529,16 @@ cudaError_t launch_v(const RopeArgs& a, bool may_stage, cudaStream_t st) {
       if (a.n % V != 0) return launch_mode<TIn, TOut, V, kHalf, kAppend, kInShared>(a, st);
     }
     // In place, direct reads skip the columns that do not rotate; copies would bring them.
-    if (may_stage && !skips && a.T >= kStagedTokens * sms)
+    if (may_stage && !skips && a.T >= kStagedTokens * sms) {
+      const long long heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
+      const TIn *q = static_cast<const TIn*>(a.q), *k = static_cast<const TIn*>(a.k),
+                *v = static_cast<const TIn*>(a.v);
+      const bool k_follows = a.Hkv == 0 || (k == q + a.Hq * a.D && a.k_ts == a.q_ts);
+      const bool v_follows = !kAppend || (v == k + a.Hkv * a.D && a.v_ts == a.q_ts);
+      if (a.Hq > 0 && a.q_ts == heads * a.D && k_follows && v_follows)
+        return launch_mode<TIn, TOut, V, kHalf, kAppend, kOnePiece>(a, st);
       return launch_mode<TIn, TOut, V, kHalf, kAppend, kStaged>(a, st);
+    }
   }
   return launch_mode<TIn, TOut, V, kHalf, kAppend, kDirect>(a, st);
 }

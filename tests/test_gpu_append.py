@@ -167,6 +167,16 @@ def test_long_calls_equal_short_ones(layout, dtype, Hq, Hkv, D, R):
                                          block_tables=s["tables"][b:b + 1].contiguous())
         assert q is None or torch.equal(part, out[a:e])
     assert torch.equal(one.view(torch.int16), s["cache"].view(torch.int16))
+    # rows that do not lie in one run
+    kc, vc, qc = s["k"].contiguous(), s["v"].contiguous(), None if q is None else q.contiguous()
+    for kk, vv, qq in ((kc, vc, qc), (kc, s["v"], q), (s["k"], vc, qc)):
+        one.fill_(1.0)
+        part = pkb.append_paged_kv_cache(kk, vv, one, s["lens"], q=qq, qo_indptr=s["qo"],
+                                         freqs=table, layout=layout, block_tables=s["tables"])
+        assert q is None or torch.equal(part, out)
+        same = one == s["cache"]
+        assert (same | (one == 1.0)).all()
+    assert same.sum() >= 2 * s["k"].numel()
 
 
 @pytest.mark.parametrize("big", [False, True])

@@ -90,6 +90,11 @@ def test_long_calls_equal_short_ones(layout, dtype, Hq, Hk, D, R):
         want = both(pkb.rotary_embedding(q[part], pos[part], table, k=None if k is None else k[part],
                                          layout=layout))
         assert torch.equal(got[0][part], want[0]) and torch.equal(got[1][part], want[1])
+    # rows that do not lie in one run: tensors of their own, and one of them a slice
+    kc = None if k is None else k.contiguous()
+    for qq, kk in ((q.contiguous(), kc), (q.contiguous(), k), (q, kc)):
+        again = both(pkb.rotary_embedding(qq, pos, table, k=kk, layout=layout))
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
     pkb.rotary_embedding(q, pos, table, k=k, layout=layout, q_out=q, k_out=k)
     assert torch.equal(q, got[0]) and (k is None or torch.equal(k, got[1]))
 
