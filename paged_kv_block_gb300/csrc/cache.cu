@@ -34,9 +34,9 @@ constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxS
 static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
-constexpr int kCopyCtas = 24;              // CTAs per SM where they walk the units (see copy_kernel)
-constexpr int kOwnUnits = 16;              // a fork of so little is done by the planning CTA itself:
-constexpr int kOwnBytes = 1 << 17;         // one launch (2.7 us of the host's time) less
+constexpr int kCopyCtas = 24;              // CTAs per SM where they walk the units (copy_kernel)
+constexpr int kOwnUnits = 16;              // a fork of so little is done by the planning CTA
+constexpr int kOwnBytes = 1 << 17;         // itself: one launch (2.7 us of the host's time) less
 constexpr long long kMaxGrid = 1LL << 30;
 
 struct Pools {
@@ -207,7 +207,7 @@ struct FreePages {
   }
 };
 
-// ---- fork: shared pages and the copied tail ------------------------------------------------------
+// ---- fork: shared pages and the copied tail ---------------------------------------------------
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -232,15 +232,16 @@ struct ForkArgs {
   uint32_t* status;
 };
 
-// One unit of a fork, by a whole CTA: the tail of an item in one pool, or part of its table row.  It
-// starts with two dependent round trips to L2 (item -> parent's table -> page), so latency bounds it
-// and a thread has four 16-byte words in flight: forking 256 children in 8 layers takes 28 us a
-// call with its frees, 32 with one word in flight; two pools per CTA changed nothing, half a pool
-// per CTA (more round trips) cost 5 us.
+// One unit of a fork, by a whole CTA: the tail of an item in one pool, or part of its table row.
+// It starts with two dependent round trips to L2 (item -> parent's table -> page) and then has four
+// 16-byte words per thread in flight: forking 256 children in 8 layers takes 28 us a call with its
+// frees, 32 with one word in flight; two pools per CTA changed nothing, half a pool per CTA (more
+// round trips) cost 5 us, CTAs of 512 threads 3.  The copies then run at 8 to 9 TB/s of L2.
 __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
   const int tid = threadIdx.x, threads = blockDim.x;
   const int per_item = a.npools + a.table_units;
-  const int i = static_cast<int>(u / per_item), w = static_cast<int>(u - static_cast<long long>(i) * per_item);
+  const int i = static_cast<int>(u / per_item);
+  const int w = static_cast<int>(u - static_cast<long long>(i) * per_item);
   const int need = a.need[i], L = a.len[i], d = a.page[i], parent = a.parents[i];
   if (need < 0) return;
   const int full = L / a.ps;
@@ -330,10 +331,15 @@ __device__ __forceinline__ int over_page(unsigned x, unsigned long long by_ps) {
   return static_cast<int>(__umul64hi(x, by_ps));
 }
 
-// CTA 0 looks after the items, all CTAs after the pages.  Latency bounds this kernel: the chain
-// is rows -> lengths -> scan -> cluster barrier -> tables, with the counts read beside it.
+// CTA 0 looks after the items, all CTAs after the pages.  Latency bounds this kernel where there is
+// little to do: the chain is rows -> lengths -> scan -> barrier -> tables, with the counts read
+// beside it (6 us for one item in 1,024 pages; a round trip to L2 alone is half a microsecond);
+// instructions and barriers of eight SMs where there is much: 13 us for 128 items that get 33,000
+// of 262,144 pages, 45 when every page searched for its item and neighbouring lanes stored to
+// distant words.
 template <bool kFork>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
   extern __shared__ __align__(16) int shared[];
   __shared__ int warp_sums[32];
   __shared__ int total_need;
@@ -345,7 +351,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   Item* mine = reinterpret_cast<Item*>(keys);                  // later: the CTA's copy of the items
   int* item_of = keys + 2 * a.hash;                            // fork: the item of the k-th demand
   int* pages_shared = item_of + (kFork ? a.n : 0);
-  int row[kPerThread], L[kPerThread], other[kPerThread];     // CTA 0: rows, lengths; new tokens or the child's length
+  // CTA 0: rows, lengths, and the new tokens or (fork) the child's length
+  int row[kPerThread], L[kPerThread], other[kPerThread];
   uint32_t bits = 0;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (j * threads >= a.n) break;
       if (need[j] < 0) continue;
       int h = static_cast<int>((static_cast<unsigned>(row[j]) * 2654435769u) >> 8) & (a.hash - 1);
-      while (true) {                                           // ends: at most half the table is used
+      while (true) {                           // ends: at most half the table is used
         const int key = atomicCAS(keys + h, -1, row[j]);
         if (key == -1 || key == row[j]) break;
         h = (h + 1) & (a.hash - 1);
@@ -507,7 +514,8 @@ __device__ __forceinline__ void copy_words(uint4* __restrict__ dst, const uint4*
   int i = threadIdx.x;
   for (; i + 3 * kCopyThreads < n16; i += 4 * kCopyThreads) {
     const uint4 a = ld_stream(src + i), b = ld_stream(src + i + kCopyThreads);
-    const uint4 c = ld_stream(src + i + 2 * kCopyThreads), d = ld_stream(src + i + 3 * kCopyThreads);
+    const uint4 c = ld_stream(src + i + 2 * kCopyThreads);
+    const uint4 d = ld_stream(src + i + 3 * kCopyThreads);
     dst[i] = a;
     dst[i + kCopyThreads] = b;
     dst[i + 2 * kCopyThreads] = c;
@@ -535,8 +543,8 @@ struct CopyArgs {
 // A unit is up to kCopyChunk bytes of one page of one pool.  Where the host knows the number of
 // pairs there is a CTA per unit; else (compact) four times the CTAs that fit walk the units, each
 // reading the next unit's page ids before it copies the present one.
-// HBM bounds it.  Measured (64 KB pages): copying 1,201 pages of 8 layers, 630 MB, takes 187 us with
-// a CTA per unit, 99% of the rate of a plain copy, and 201 us with 6 resident CTAs per SM that
+// HBM bounds it.  Measured (64 KB pages): copying 1,201 pages of 8 layers, 630 MB, takes 187 us
+// with a CTA per unit, 99% of the rate of a plain copy, and 201 us with 6 resident CTAs per SM that
 // walk the units; moving 1,500 pages of 4 layers 127 us a call with 24 CTAs per SM, 134 with 6, and
 // the same 134 with a ring of bulk copies through shared memory, so there is none.  Units of 8 KB
 // cost 244 us (the CTAs' launches), of 32 KB 190 us.
@@ -581,7 +589,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     const long long entries = static_cast<long long>(a.R) * a.C;
     for (long long e = blockIdx.x * static_cast<long long>(kCopyThreads) + threadIdx.x; e < entries;
          e += static_cast<long long>(gridDim.x) * kCopyThreads) {
-      const int row = static_cast<int>(e / a.C), j = static_cast<int>(e - static_cast<long long>(row) * a.C);
+      const int row = static_cast<int>(e / a.C);
+      const int j = static_cast<int>(e - static_cast<long long>(row) * a.C);
       const int L = a.lens[row];
       int p = a.tables[e];
       const int old = p;
@@ -596,6 +605,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 }
 
 // ---- free ------------------------------------------------------------------------------------
+// A CTA per row.  The exchange makes a row that is listed twice free once; three dependent round
+// trips to L2 (row, length, pages) and the atomics bound it: 4 us for a row, 5 for 128 rows of 256
+// pages.
 __global__ void __launch_bounds__(kCopyThreads)
 free_kernel(const int* rows, int n, const int* tables, int* lens, int* refs, int R, int C, int ps,
             int P, uint32_t* status) {
@@ -623,7 +635,7 @@ free_kernel(const int* rows, int n, const int* tables, int* lens, int* refs, int
   }
 }
 
-// ---- compact: which page moves where -------------------------------------------------------------
+// ---- compact: which page moves where ----------------------------------------------------------
 struct CompactArgs {
   const int* refs;
   int* refs_out;
@@ -633,6 +645,7 @@ struct CompactArgs {
   uint32_t* status;
 };
 
+// Latency-bound like plan_kernel: 5 us for 256 pages, 8 for 6,007.
 __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs a) {
   extern __shared__ __align__(16) int shared[];
   cg::cluster_group cl = cg::this_cluster();
@@ -774,8 +787,8 @@ bool plan_is_small(int P, int few_steps, int items) {
   return P <= few_steps * kFewThreads * kThreadPages && items <= kPerThread * kFewThreads;
 }
 template <typename Args>
-cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_steps, int items, size_t ints,
-                        std::atomic<uint64_t>& ready, cudaStream_t st) {
+cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int P, int few_steps, int items,
+                        size_t ints, std::atomic<uint64_t>& ready, cudaStream_t st) {
   const bool few = plan_is_small(P, few_steps, items);
   const int threads = few ? kFewThreads : kPlanThreads;
   int size = 1;
@@ -825,8 +838,8 @@ int paged_cache_free_run(const paged_cache_params* p, const int32_t* rows, int n
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   count_launches(1);
   return cuda_status(launch_after_previous(
-      free_kernel, n, kCopyThreads, 0, static_cast<cudaStream_t>(stream), rows, n, tables, lens, refs,
-      p->rows, p->max_pages_per_request, p->page_size, p->num_pages, status));
+      free_kernel, n, kCopyThreads, 0, static_cast<cudaStream_t>(stream), rows, n, tables, lens,
+      refs, p->rows, p->max_pages_per_request, p->page_size, p->num_pages, status));
 }
 
 size_t paged_cache_extend_workspace_size(int n) {
@@ -928,7 +941,8 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   a.src = at(ws, l.src); a.dst = at(ws, l.dst); a.to = at(ws, l.to); a.moves = at(ws, l.moves);
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
   static std::atomic<uint64_t> ready{0};
-  if (launch_plan(compact_kernel, a, a.P, 1, 0, 0, ready, st) != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  if (launch_plan(compact_kernel, a, a.P, 1, 0, 0, ready, st) != cudaSuccess)
+    return PAGED_ATTN_ERR_CUDA;
   CopyArgs c{};
   c.pools = pool_count(pools);
   for (int i = 0; i < c.pools; ++i) c.src.p[i] = c.dst.p[i] = pools->pools_host[i];

@@ -134,18 +134,18 @@ __device__ __forceinline__ float turned(float a, float c, float b, float s) {
 }
 
 // Bytes (a multiple of 16) from 16-byte aligned global to shared memory, counted on an mbarrier.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 
-// What a thread holds of one slot between its load and its store.  A slot is V column pairs (half: V
-// columns of each half) or V columns (interleaved; the last one may hold columns past the rotated
-// ones too.  V = 1 is one pair element by element, for rows whose alignment allows no wider access);
-// the slots from `rot` on copy V columns each, from column `first`.
+// What a thread holds of one slot between its load and its store.  A slot is V column pairs (half:
+// V columns of each half) or V columns (interleaved; the last one may hold columns past the
+// rotated ones too.  V = 1 is one pair element by element, for rows whose alignment allows no
+// wider access); the slots from `rot` on copy V columns each, from column `first`.
 template <typename TIn, int V, bool kHalf>
 struct Slot {
   static constexpr bool kTwo = kHalf || V == 1;
@@ -158,7 +158,8 @@ struct Slot {
   __device__ __forceinline__ void load(const TIn* x, int n, int s, int rot, int first) {
     if (s < rot) {
       a = *reinterpret_cast<const Vec<TIn, V>*>(x + (!kHalf && V == 1 ? 2 * s : s * V));
-      if constexpr (kTwo) b = *reinterpret_cast<const Vec<TIn, V>*>(x + (kHalf ? n + s * V : 2 * s + 1));
+      if constexpr (kTwo)
+        b = *reinterpret_cast<const Vec<TIn, V>*>(x + (kHalf ? n + s * V : 2 * s + 1));
     } else {
       a = *reinterpret_cast<const Vec<TIn, V>*>(x + first + (s - rot) * V);
     }
@@ -207,7 +208,7 @@ struct Slot {
         }
         const Vec<TOut, V> r = pack<TOut>(y1);
 #pragma unroll
-        for (int i = 0; i < V; ++i)                    // a column past the rotated ones keeps its bits
+        for (int i = 0; i < V; ++i)            // a column past the rotated ones keeps its bits
           if (s * kPairs + i / 2 < n) c.e[i] = r.e[i];
       }
       *reinterpret_cast<Vec<TOut, V>*>(y + s * V) = c;
@@ -240,12 +241,12 @@ __device__ __forceinline__ int request_of(const int* offsets, int B, int t) {
 
 // How a CTA gets at its rows.
 constexpr int kDirect = 0;    // straight from global memory, a few rows in flight per thread
-constexpr int kStaged = 1;    // brought to shared memory by bulk copies: tens of KB in flight per SM
-                              // whatever the registers allow (16-byte aligned, adjacent heads)
-constexpr int kOnePiece = 2;  // the same where the rows of q, k and v and the tokens are one run in memory
-                              // (slices of one projection): one copy per CTA
-constexpr int kInShared = 3;  // staged, and rotated there element by element: half layout whose halves
-                              // do not both start on a 16-byte access
+constexpr int kStaged = 1;    // brought to shared memory by bulk copies: tens of KB in flight per
+                              // SM whatever the registers allow (16-byte aligned, adjacent heads)
+constexpr int kOnePiece = 2;  // the same where the rows of q, k and v and the tokens are one run in
+                              // memory (slices of one projection): one copy per CTA
+constexpr int kInShared = 3;  // staged, and rotated there element by element: half layout whose
+                              // halves do not both start on a 16-byte access
 
 template <typename TIn, typename TOut, int V, bool kHalf, bool kAppend, int kMode>
 __global__ void __launch_bounds__(kMaxThreads, kMode == kDirect      ? 1
@@ -277,9 +278,9 @@ rope_kernel(const RopeArgs a) {
   const long long token = t0 + t;
   grid_dependency_wait();
   grid_launch_dependents();
-  // Staged rows: [tile, heads, D] in one piece, else tensor by tensor [tile, its heads of the chunk,
-  // D], so that a tensor whose tokens are adjacent comes in one copy too.  (Few large copies: 12
-  // heads of 32,749 tokens take 41 us in one copy per CTA, 44 in three per token.)
+  // Staged rows: [tile, heads, D] in one piece, else tensor by tensor [tile, its heads of the
+  // chunk, D], so that a tensor whose tokens are adjacent comes in one copy too.  (Few large
+  // copies: 12 heads of 32,749 tokens take 41 us in one copy per CTA, 44 in three per token.)
   TIn* const rows = reinterpret_cast<TIn*>(smem);
   const int k_begin = a.Hq, v_begin = a.Hq + a.Hkv;
   const int q_rows = max(0, min(h_end, k_begin) - h_begin);
@@ -305,7 +306,8 @@ rope_kernel(const RopeArgs a) {
         mbar_init(&arrived, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&arrived, nt * (h_end - h_begin) * a.D * static_cast<int>(sizeof(TIn)));
+        mbar_arrive_expect_tx(&arrived,
+                              nt * (h_end - h_begin) * a.D * static_cast<int>(sizeof(TIn)));
       }
       __syncwarp();
       // n rows of one tensor (of `all`, from its head h on) for every token of the tile
@@ -315,7 +317,8 @@ rope_kernel(const RopeArgs a) {
         const bool adjacent = n == all && ts == static_cast<long long>(n) * a.D;
         const int copies = adjacent ? 1 : nt;
         const int bytes = (adjacent ? nt : 1) * n * a.D * static_cast<int>(sizeof(TIn));
-        for (int i = tid; i < copies; i += 32) bulk_load(to + i * n * a.D, from + i * ts, bytes, &arrived);
+        for (int i = tid; i < copies; i += 32)
+          bulk_load(to + i * n * a.D, from + i * ts, bytes, &arrived);
       };
       if constexpr (kMode == kOnePiece) {
         bring(a.q, a.q_ts, 0, heads, heads, rows);
@@ -338,7 +341,8 @@ rope_kernel(const RopeArgs a) {
       if (h >= h_end) break;
       const TIn* p;
       if (kMode != kDirect)
-        p = (kMode == kOnePiece || h < k_begin ? mine.q : h < v_begin ? mine.k : mine.v) + (h - h_begin) * a.D;
+        p = (kMode == kOnePiece || h < k_begin ? mine.q : h < v_begin ? mine.k : mine.v) +
+            (h - h_begin) * a.D;
       else if (h < a.Hq)
         p = static_cast<const TIn*>(a.q) + token * a.q_ts + h * a.q_hs;
       else if (!kAppend || h < a.Hq + a.Hkv)
@@ -478,13 +482,13 @@ cudaError_t launch_mode(RopeArgs a, cudaStream_t st) {
   const int heads = a.Hq + a.Hkv * (kAppend ? 2 : 1);
   const long long token_bytes = static_cast<long long>(heads) * a.D * sizeof(TIn);
   const long long goal = token_bytes < kStageGoal ? kStageGoal / token_bytes : 1;
-  const int threads =
-      (kMode == kStaged || kMode == kOnePiece) && goal * a.slots <= kFewThreads / 2 ? kFewThreads : kMaxThreads;
+  const bool few = (kMode == kStaged || kMode == kOnePiece) && goal * a.slots <= kFewThreads / 2;
+  const int threads = few ? kFewThreads : kMaxThreads;
   const int slots = a.slots < threads ? a.slots : threads;
-  // Tokens per CTA: one while there are few; else the most that keep 7 of 8 threads busy (the slots of
-  // the tile's tokens, times the groups that share the heads), or that keep the most busy.  12,627
-  // tokens of 8 + 2 + 2 heads with 32 of 128 columns rotated (14 slots) take 47 us one by one, 20 by
-  // four.
+  // Tokens per CTA: one while there are few; else the most that keep 7 of 8 threads busy (the
+  // slots of the tile's tokens, times the groups that share the heads), or that keep the most
+  // busy.  12,627 tokens of 8 + 2 + 2 heads with 32 of 128 columns rotated (14 slots) take 47 us
+  // one by one, 22 by four.
   a.tile = 1;
   if (a.T >= kTileTokens * sms) {
     const long long most = kMode == kDirect ? 4 : goal < 16 ? goal : 16;
@@ -504,9 +508,9 @@ cudaError_t launch_mode(RopeArgs a, cudaStream_t st) {
   if (chunks > ceil_div(heads, groups)) chunks = ceil_div(heads, groups);
   a.chunk = ceil_div(heads, chunks);
   chunks = ceil_div(heads, a.chunk);
-  a.staged_bytes = kMode == kDirect ? 0
-                                    : static_cast<int>(align_up(static_cast<size_t>(a.tile) * a.chunk *
-                                                                    a.D * sizeof(TIn), 128));
+  const size_t rows = static_cast<size_t>(a.tile) * a.chunk;
+  a.staged_bytes =
+      kMode == kDirect ? 0 : static_cast<int>(align_up(rows * a.D * sizeof(TIn), 128));
   const size_t smem = a.staged_bytes +
                       static_cast<size_t>(a.tile) * (a.n * sizeof(float2) + sizeof(TokenSlot));
   void (*const kernel)(RopeArgs) = rope_kernel<TIn, TOut, V, kHalf, kAppend, kMode>;
@@ -716,8 +720,9 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
   strides(p->k_out_token_stride, p->k_out_head_stride, p->num_kv_heads, &a.ko_ts, &a.ko_hs);
   a.q_in_place = q == q_out;
   a.k_in_place = has_k && k == k_out;
-  if (a.q_in_place && (a.q_ts != a.qo_ts || a.q_hs != a.qo_hs)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
-  if (a.k_in_place && (a.k_ts != a.ko_ts || a.k_hs != a.ko_hs)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if ((a.q_in_place && (a.q_ts != a.qo_ts || a.q_hs != a.qo_hs)) ||
+      (a.k_in_place && (a.k_ts != a.ko_ts || a.k_hs != a.ko_hs)))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const size_t e = size_of(p->dtype);
   if (!aligned_to(q, e) || !aligned_to(q_out, e) || !aligned_to(k, e) || !aligned_to(k_out, e))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
@@ -741,7 +746,8 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (p->dtype) {
     case PAGED_ATTN_DTYPE_BF16:
-      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, w.v, half, may_stage, st));
+      return cuda_status(
+          launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, w.v, half, may_stage, st));
     case PAGED_ATTN_DTYPE_FP16:
       return cuda_status(launch_typed<__half, __half, false>(a, w.v, half, may_stage, st));
     default:
@@ -800,7 +806,8 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (p->in_dtype) {
     case PAGED_ATTN_DTYPE_BF16:
-      return cuda_status(launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
+      return cuda_status(
+          launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
     case PAGED_ATTN_DTYPE_FP16:
       return cuda_status(launch_typed<__half, __nv_bfloat16, true>(a, w.v, half, may_stage, st));
     default:
