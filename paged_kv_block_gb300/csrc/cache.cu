@@ -30,7 +30,7 @@ constexpr int kPerThread = 4;              // items that a thread of the plannin
 constexpr int kMaxItems = kPerThread * kPlanThreads;
 // Shared memory of a planning kernel at most: items, the hash table of their rows, page counts.
 constexpr int kMaxSteps = kMaxPages / (kPlanThreads * kThreadPages);
-constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxSteps) * 4;
+constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxSteps + 1) * 4;
 static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
@@ -73,6 +73,13 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   return (warp > 0 ? before : 0) + v - x;
 }
 
+// The two halves of a cluster barrier that orders no memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // A barrier over the cluster, with its memory; a plain one where the cluster is one CTA.
 __device__ __forceinline__ void sync_cluster(cg::cluster_group& cl) {
   if (cl.num_blocks() == 1) __syncthreads();
@@ -92,7 +99,7 @@ struct FreePages {
   uint32_t kept;                     // the thread's masks of its first 4 steps
   int* warp_before;                  // shared [own, 32]: free pages of the step before a warp
   int* step_total;                   // shared [own]
-  int* step_before;                  // shared [steps]: free pages before a step
+  int* step_before;                  // shared [steps + 1]: free pages before a step
   int total;                         // free pages
 
   static __host__ __device__ int steps_of(int P, int threads) {
@@ -100,7 +107,7 @@ struct FreePages {
   }
   static __host__ size_t shared_ints(int P, int size, int threads) {
     const int steps = steps_of(P, threads);
-    return static_cast<size_t>((steps + size - 1) / size) * 33 + steps;
+    return static_cast<size_t>((steps + size - 1) / size) * 33 + steps + 1;
   }
 
   __device__ __forceinline__ int first_page(int j) const {
@@ -174,17 +181,20 @@ struct FreePages {
   }
   // Put the steps of all CTAs in order (after the cluster barrier).
   __device__ void order(cg::cluster_group& cl) {
-    const int lane = threadIdx.x & 31;
-    int carry = 0;
-    for (int g0 = 0; g0 < steps; g0 += 32) {           // every warp for itself
-      const int g = g0 + lane;
-      const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
-      const int v = warp_inclusive(n);
-      if (threadIdx.x < 32 && g < steps) step_before[g] = carry + v - n;
-      carry += __shfl_sync(0xffffffffu, v, 31);
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int carry = 0;
+      for (int g0 = 0; g0 < steps; g0 += 32) {
+        const int g = g0 + lane;
+        const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
+        const int v = warp_inclusive(n);
+        if (g < steps) step_before[g] = carry + v - n;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) step_before[steps] = carry;
     }
-    total = carry;
     __syncthreads();
+    total = step_before[steps];
   }
   // Calls f(page, is_free, free pages before it, free pages among the warp's 32) for the pages
   // of the j-th step with a page per lane: neighbouring lanes hold neighbouring pages and, where
@@ -459,6 +469,10 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
       if (kFork && x.need > 0) item_of[x.off] = i;             // a fork demands one page at most
     }
     __syncthreads();
+  }
+  // From here on no CTA reads another's shared memory; none may end before all have come here.
+  if (size > 1) cluster_arrive();
+  if (demand > 0) {
     // The item whose demand holds the k-th fresh page: the last one with off <= k (items without
     // a demand share their successor's offset).
     const auto owner = [&](int k, int lo) {
@@ -504,7 +518,7 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
       for (int u = 0; u < a.units; ++u) fork_unit(a.fork, u);
     }
   }
-  if (size > 1) cl.sync();                 // the items in CTA 0's shared memory have been read
+  if (size > 1) cluster_wait();
 }
 
 // ---- copies ----------------------------------------------------------------------------------
@@ -690,7 +704,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
       }
     });
   }
-  sync_cluster(cl);
+  sync_cluster(cl);                        // also: every CTA has read the others' step totals
   const int moves = *a.moves;
   for (int k = rank * threads + tid; k < moves; k += size * threads) {
     const int s = a.src[moves - 1 - k], d = a.dst[k];
@@ -698,7 +712,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
     a.refs_out[d] = a.refs[s];
     a.refs_out[s] = 0;
   }
-  if (size > 1) cl.sync();                 // the step totals have been read
 }
 
 // ---- host --------------------------------------------------------------------------------------
