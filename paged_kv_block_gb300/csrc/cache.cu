@@ -30,7 +30,7 @@ constexpr int kPerThread = 4;              // items that a thread of the plannin
 constexpr int kMaxItems = kPerThread * kPlanThreads;
 // Shared memory of a planning kernel at most: items, the hash table of their rows, page counts.
 constexpr int kMaxSteps = kMaxPages / (kPlanThreads * kThreadPages);
-constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxSteps + 1) * 4;
+constexpr int kPlanSmem = (9 * kMaxItems + kMaxSteps / kPlanCluster * 33 + kMaxSteps) * 4;
 static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
@@ -99,7 +99,7 @@ struct FreePages {
   uint32_t kept;                     // the thread's masks of its first 4 steps
   int* warp_before;                  // shared [own, 32]: free pages of the step before a warp
   int* step_total;                   // shared [own]
-  int* step_before;                  // shared [steps + 1]: free pages before a step
+  int* step_before;                  // shared [steps]: free pages before a step
   int total;                         // free pages
 
   static __host__ __device__ int steps_of(int P, int threads) {
@@ -107,7 +107,7 @@ struct FreePages {
   }
   static __host__ size_t shared_ints(int P, int size, int threads) {
     const int steps = steps_of(P, threads);
-    return static_cast<size_t>((steps + size - 1) / size) * 33 + steps + 1;
+    return static_cast<size_t>((steps + size - 1) / size) * 33 + steps;
   }
 
   __device__ __forceinline__ int first_page(int j) const {
@@ -181,20 +181,17 @@ struct FreePages {
   }
   // Put the steps of all CTAs in order (after the cluster barrier).
   __device__ void order(cg::cluster_group& cl) {
-    if (threadIdx.x < 32) {
-      const int lane = threadIdx.x;
-      int carry = 0;
-      for (int g0 = 0; g0 < steps; g0 += 32) {
-        const int g = g0 + lane;
-        const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
-        const int v = warp_inclusive(n);
-        if (g < steps) step_before[g] = carry + v - n;
-        carry += __shfl_sync(0xffffffffu, v, 31);
-      }
-      if (lane == 0) step_before[steps] = carry;
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int g0 = 0; g0 < steps; g0 += 32) {           // every warp for itself
+      const int g = g0 + lane;
+      const int n = g < steps ? *cl.map_shared_rank(step_total + g / size, g % size) : 0;
+      const int v = warp_inclusive(n);
+      if (threadIdx.x < 32 && g < steps) step_before[g] = carry + v - n;
+      carry += __shfl_sync(0xffffffffu, v, 31);
     }
+    total = carry;
     __syncthreads();
-    total = step_before[steps];
   }
   // Calls f(page, is_free, free pages before it, free pages among the warp's 32) for the pages
   // of the j-th step with a page per lane: neighbouring lanes hold neighbouring pages and, where
