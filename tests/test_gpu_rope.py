@@ -264,6 +264,41 @@ def test_other_stream_and_graph():
     assert torch.equal(out, want)
 
 
+def test_graph_between_other_kernels():
+    """Captured between kernels of another library, a memset and a copy, long and short calls: each
+    waits for what precedes it and is waited for."""
+    gen = torch.Generator().manual_seed(10)
+    table, _ = pkb.rope_frequencies(64)
+    for T in (40, 5000):
+        q = rows(gen, T, 6, 64, dtype=torch.bfloat16)
+        pos = torch.arange(T, dtype=torch.int32, device=DEV)
+        buf = {n: torch.zeros_like(q) for n in ("in", "a", "b", "c")}
+
+        def chain():
+            buf["a"].zero_()
+            buf["in"].mul_(2)
+            pkb.rotary_embedding(buf["in"], pos, table, q_out=buf["a"])
+            pkb.rotary_embedding(buf["a"], pos, table, q_out=buf["b"])
+            buf["a"].add_(1)
+            buf["c"].copy_(buf["b"])
+            pkb.rotary_embedding(buf["c"], pos, table, q_out=buf["c"], inverse=True)
+            buf["c"].add_(buf["a"])
+        buf["in"].copy_(q)
+        chain()
+        torch.cuda.synchronize()
+        want = {n: t.clone() for n, t in buf.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+        for t in buf.values():
+            t.fill_(float("nan"))
+        for _ in range(5):
+            buf["in"].copy_(q)
+            graph.replay()
+        for n, t in buf.items():
+            assert torch.equal(t, want[n]), (T, n)
+
+
 def test_refusals():
     table, _ = pkb.rope_frequencies(32)
     q = torch.zeros(4, 2, 32, device=DEV)
