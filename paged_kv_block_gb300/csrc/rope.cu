@@ -24,11 +24,11 @@ namespace pa {
 namespace {
 
 // Threads of a CTA: 128, but 64 where rows are staged and the slots of its tokens fill no more than
-// half of those (6 heads of 80 columns: 9.5 us with 128 threads, 12.6 with 64, for 12,627 tokens).
+// half of those (6 heads of 80 columns: 15.9 us with 128 threads, 17.2 with 64, for 32,749 tokens).
 // Small CTAs with one wide token or a few narrow ones keep loads, sines and stores of many tokens
-// overlapped: staging 17,408 tokens of 32 + 8 + 8 bf16 heads (append) takes 68.5 us with 64 threads
-// and 12 KB each, 70 with 128 and 24 KB, 74 with 256 and 48 KB; 16 and more of the 64-thread CTAs
-// per SM (72 us) slow the writes.
+// overlapped: staging 17,408 tokens of 32 + 8 + 8 bf16 heads (append) takes 65.9 us with 64 threads
+// and 12 KB each, 66.6 with 128 and 24 KB; registers for 16 of the 64-thread CTAs per SM instead of
+// 12 make it 67.2.
 constexpr int kMaxThreads = 128;
 constexpr int kFewThreads = 64;
 constexpr int kStageGoal = 12288;        // bytes of rows that a CTA stages where it may choose
@@ -280,7 +280,7 @@ rope_kernel(const RopeArgs a) {
   grid_launch_dependents();
   // Staged rows: [tile, heads, D] in one piece, else tensor by tensor [tile, its heads of the
   // chunk, D], so that a tensor whose tokens are adjacent comes in one copy too.  (Few large
-  // copies: 12 heads of 32,749 tokens take 41 us in one copy per CTA, 44 in three per token.)
+  // copies: 12 heads of 32,749 tokens take 38.8 us in one copy per CTA, 42.9 in three or more.)
   TIn* const rows = reinterpret_cast<TIn*>(smem);
   const int k_begin = a.Hq, v_begin = a.Hq + a.Hkv;
   const int q_rows = max(0, min(h_end, k_begin) - h_begin);
@@ -355,6 +355,13 @@ rope_kernel(const RopeArgs a) {
   };
   // The first rows are on their way while positions, pages and sines are found.
   if (kMode == kDirect && active) load(h_begin + group);
+  // The chain to the first store of an append is request -> length -> page; what does not depend on
+  // it is fetched beside it: the thread's first table entry before, the page while sines are
+  // taken (17,408 tokens of 48 heads: 67.1 us without either, 65.9 with both; 32,749 of 12:
+  // 41.3 and 38.8).
+  const unsigned long long entry = kAppend && tid < a.tile * a.n ? a.table[tid % a.n] : 0;
+  TokenSlot found{-1, -1, 0};                                       // of token tid (tile <= 16)
+  int page = -1, slot = 0;
   if constexpr (kAppend) {
     if (a.qo_indptr != nullptr) {
       for (int t = tid >> 5; t < nt; t += threads >> 5) {
@@ -363,34 +370,39 @@ rope_kernel(const RopeArgs a) {
       }
       __syncthreads();
     }
-    for (int t = tid; t < nt; t += threads) {
-      const int b = a.qo_indptr != nullptr ? tok[t].request : (t0 + t) / a.SQ;
-      TokenSlot found{-1, b, 0};
+    if (tid < nt) {
+      const int b = a.qo_indptr != nullptr ? tok[tid].request : (t0 + tid) / a.SQ;
+      found.request = b;
       if (b >= 0) {
         const int end = a.qo_indptr != nullptr ? a.qo_indptr[b + 1] : (b + 1) * a.SQ;
-        const int p = a.lens[b] - (end - (t0 + t));
         long long first = static_cast<long long>(b) * a.C;
         int count = a.C;
         if (a.kv_indptr != nullptr) {
           first = a.kv_indptr[b];
           count = a.kv_indptr[b + 1] - a.kv_indptr[b];
         }
+        const int p = a.lens[b] - (end - (t0 + tid)), j = p / a.ps;
         found.position = p;
-        const int j = p / a.ps;
-        const int page = p >= 0 && j < count ? a.pages[first + j] : -1;
-        if (page >= 0 && page < a.num_pages)
-          found.off = page * a.page_elems + static_cast<long long>(p - j * a.ps) * a.D;
-        else
-          report_error(a.status, kErrMetadata);
+        slot = p - j * a.ps;
+        if (p >= 0 && j < count) page = a.pages[first + j];
       }
-      tok[t] = found;
+      tok[tid].position = found.position;
     }
     __syncthreads();
   }
   for (int i = tid; i < nt * a.n; i += threads) {
     const int j = i / a.n, pair = i - j * a.n;
     const int p = kAppend ? tok[j].position : a.positions[t0 + j];
-    cs[i] = turn_of(p, a.table[pair], a.m, a.inverse ? -1.f : 1.f);
+    cs[i] = turn_of(p, kAppend && i == tid ? entry : a.table[pair], a.m, a.inverse ? -1.f : 1.f);
+  }
+  if constexpr (kAppend) {
+    if (tid < nt) {
+      if (page >= 0 && page < a.num_pages)
+        found.off = page * a.page_elems + static_cast<long long>(slot) * a.D;
+      else if (found.request >= 0)
+        report_error(a.status, kErrMetadata);
+      tok[tid] = found;
+    }
   }
   __syncthreads();
   if constexpr (kMode != kDirect) {
