@@ -267,6 +267,12 @@ def _rows(t, dev, name):
         raise ValueError(f"{name} is too large")
     if e != 1 and D > 1:
         raise ValueError(f"{name}: the columns of a head must be contiguous")
+    if H <= 1:                               # the stride of a single head or token says nothing
+        hs = D
+    if T <= 1:
+        ts = H * D
+    elif ts == 0 and hs == 0:                # to the C call that means contiguous rows
+        raise ValueError(f"{name}: all rows are one; repeat it or rotate it once")
     return T, H, D, ts, hs
 
 
@@ -370,8 +376,10 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
         raise ValueError("k and v must have the cache's heads and columns, and the same dtype")
     if dt not in _DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
-    if (kh != D or vh != D) and Hkv > 1:
+    if kh != D or vh != D:
         raise ValueError("the heads of k and v must be adjacent")
+    if kt == 0 or vt == 0:                   # to the C call that means contiguous rows
+        raise ValueError("the tokens of k and v must be rows of their own")
     total = sq = cols = Hq = qt = 0
     qo = indptr = qp = qop = table = None
     if qo_indptr is not None:
@@ -397,8 +405,9 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
         pages = _ints(paged_kv_indices, dev, "paged_kv_indices")
     if q is not None:
         Tq, Hq, Dq, qt, qh = _rows(q, dev, "q")
-        if Tq != T or Dq != D or q.dtype is not dt or (qh != D and Hq > 1):
-            raise ValueError("q must have k's tokens, columns and dtype, and adjacent heads")
+        if Tq != T or Dq != D or q.dtype is not dt or qh != D or (qt == 0 and Hq > 0):
+            raise ValueError("q must have k's tokens, columns and dtype, adjacent heads, and "
+                             "tokens in rows of their own")
         if q_out is None:
             q_out = _empty(q, _BF16)
         elif (q_out.shape != q.shape or q_out.dtype is not torch.bfloat16

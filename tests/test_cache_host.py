@@ -308,3 +308,69 @@ def test_binding_refuses_host_tensors(lib):
         pkb.cache_pools([])
     with pytest.raises(ValueError):
         pkb.free_cache_rows(pos, pos.view(2, 1), pos, pos, 16)
+
+
+# ---- what the binding hands to the C entry points -----------------------------------------------
+
+class _Recorder:
+    """In place of the library: keeps the parameters of the last call."""
+
+    def __init__(self):
+        self.params = None
+
+    def __getattr__(self, name):
+        def call(params, *rest):
+            self.params = params._obj
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """The binding on host tensors (their device index is -1), with the library out of reach."""
+    r = _Recorder()
+    monkeypatch.setattr(K, "_device", lambda: -1)
+    monkeypatch.setattr(K, "_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(K, "_call", r)
+    return r
+
+
+def test_rope_rows_that_step_by_nothing(recorded):
+    pos, table = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)
+
+    def rope(q, **kw):
+        recorded.params = None
+        pkb.rotary_embedding(q, pos[:q.numel() // (q.shape[-1] * q.shape[-2])], table, **kw)
+        return recorded.params
+
+    # two strides of zero mean packed rows to the C call, which would read past a single row
+    one = torch.zeros(8)
+    for shape in ((3, 2, 8), (1, 3, 2, 8)):
+        for kw in (dict(q=one.expand(shape)), dict(q=torch.zeros(shape), k=one.expand(shape)),
+                   dict(q=torch.zeros(shape), q_out=one.expand(shape)),
+                   dict(q=torch.zeros(shape), k=torch.zeros(shape), k_out=one.expand(shape))):
+            with pytest.raises(ValueError):
+                rope(**kw)
+            assert recorded.params is None
+    # a single head or token has no step, whatever its stride says
+    p = rope(torch.as_strided(one, (3, 1, 8), (0, 0, 1)))
+    assert (p.q_token_stride, p.q_head_stride) == (0, 8)
+    p = rope(torch.as_strided(one, (1, 2, 8), (0, 0, 1)))
+    assert (p.q_token_stride, p.q_head_stride) == (16, 0)
+    p = rope(torch.as_strided(torch.zeros(24), (3, 1, 8), (8, 5, 1)))
+    assert (p.q_token_stride, p.q_head_stride) == (8, 8)
+
+
+def test_append_rows_that_step_by_nothing(recorded):
+    cache = torch.zeros(4, 2, 2, 8, 8, dtype=torch.bfloat16)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    lens = torch.ones(3, dtype=torch.int32)
+    row, full = torch.zeros(1, 2, 8), torch.zeros(3, 2, 8)
+    for k, v, q in ((row.expand(3, 2, 8), full, full), (full, row.expand(3, 2, 8), full),
+                    (full, full, row.expand(3, 2, 8))):
+        recorded.params = None
+        with pytest.raises(ValueError):
+            pkb.append_paged_kv_cache(k, v, cache, lens, block_tables=table, q=q)
+        assert recorded.params is None
+    pkb.append_paged_kv_cache(row, row, cache, lens[:1], block_tables=table[:1])
+    assert recorded.params.k_token_stride in (0, 16)
