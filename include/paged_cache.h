@@ -104,8 +104,10 @@ typedef struct paged_rope_params {
 /* Rotate q [T, Hq, D] and k [T, Hkv, D] (NULL with num_kv_heads = 0) at positions_dev [T]
  * (any int32), reading table_dev [R / 2].  Computed in fp32 and rounded once.  An output may
  * be its own input (same pointer and strides); otherwise outputs share no element with any
- * input.  Pointers need the alignment of their
- * element; accesses are wide where pointers, strides and R allow 16 bytes. */
+ * input.  Rows of an input may overlap or be the same (a stride of 0 beside one that is not);
+ * rows of an output lie apart, the tokens within a step of the heads or the heads within a step
+ * of the tokens, or the call is refused.  Pointers need the alignment of their element; accesses
+ * are wide where pointers, strides and R allow 16 bytes. */
 int paged_rope_run(const paged_rope_params* params, const void* q_dev, const void* k_dev,
                    const int32_t* positions_dev, const uint64_t* table_dev, void* q_out_dev,
                    void* k_out_dev, uint32_t* status_dev, void* stream);

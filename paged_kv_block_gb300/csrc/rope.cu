@@ -603,6 +603,15 @@ struct Width {
   }
 };
 
+// Whether T x H rows of D elements lie apart: the rows of one dimension fit in a step of the other.
+bool rows_apart(long long T, long long H, long long D, long long ts, long long hs) {
+  if (ts < 0) ts = -ts;
+  if (hs < 0) hs = -hs;
+  if (H == 1) return T == 1 || ts >= D;
+  if (T == 1) return hs >= D;
+  return (hs >= D && (ts - D) / (H - 1) >= hs) || (ts >= D && (hs - D) / (T - 1) >= ts);
+}
+
 bool dtype_ok(int t) { return t >= PAGED_ATTN_DTYPE_BF16 && t <= PAGED_ATTN_DTYPE_FP32; }
 
 bool rope_params_ok(const paged_rope_params* p) {
@@ -734,6 +743,10 @@ int paged_rope_run(const paged_rope_params* p, const void* q, const void* k,
   a.k_in_place = has_k && k == k_out;
   if ((a.q_in_place && (a.q_ts != a.qo_ts || a.q_hs != a.qo_hs)) ||
       (a.k_in_place && (a.k_ts != a.ko_ts || a.k_hs != a.ko_hs)))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (p->num_tokens > 0 &&
+      (!rows_apart(p->num_tokens, p->num_qo_heads, D, a.qo_ts, a.qo_hs) ||
+       (has_k && !rows_apart(p->num_tokens, p->num_kv_heads, D, a.ko_ts, a.ko_hs))))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const size_t e = size_of(p->dtype);
   if (!aligned_to(q, e) || !aligned_to(q_out, e) || !aligned_to(k, e) || !aligned_to(k_out, e))

@@ -174,6 +174,17 @@ def test_rope_refusals(lib):
     assert _rope(lib, num_tokens=0, num_kv_heads=0, k=None, ko=None) == 0
 
 
+def test_rope_refuses_outputs_whose_rows_overlap(lib):
+    # (token stride, head stride) of 4 tokens of 4 heads (q) or 2 heads (k) of 64 columns
+    for ts, hs in ((256, 0), (0, 64), (64, 64), (192, 64), (256, 63), (63, 256), (64, 255)):
+        assert _rope(lib, qo=2 * A16, q_out_token_stride=ts, q_out_head_stride=hs) == BAD
+        # in place, the input's rows are the output's
+        assert _rope(lib, q_token_stride=ts, q_head_stride=hs, q_out_token_stride=ts,
+                     q_out_head_stride=hs) == BAD
+    for ts, hs in ((128, 0), (0, 64), (64, 64), (127, 64), (64, 255)):
+        assert _rope(lib, ko=2 * A16, k_out_token_stride=ts, k_out_head_stride=hs) == BAD
+
+
 def _append(lib, q=A16, k=A16, v=A16, qo=None, indptr=None, pages=A16, lens=A16, table=A16,
             qout=A16, kc=A16, vc=None, status=None, **kw):
     f = dict(batch=2, seq_len_q=1, total_q=0, num_qo_heads=4, num_kv_heads=2, head_dim=64,

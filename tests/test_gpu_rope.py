@@ -242,6 +242,25 @@ def test_more_elements_than_31_bits():
     assert torch.equal(got, pkb.rotary_embedding(view[-3:].contiguous(), pos[-3:], table))
 
 
+@pytest.mark.parametrize("T", [1, 3, 700])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_broadcast_inputs(T, layout):
+    # one row for all heads, or for all tokens: the same bits as from the repeated rows
+    gen = torch.Generator().manual_seed(15)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    table, _ = pkb.rope_frequencies(64)
+    by_head = rows(gen, T, 1, 64, dtype=torch.bfloat16).expand(T, 6, 64)
+    by_token = rows(gen, 1, 2, 64, dtype=torch.bfloat16).expand(T, 2, 64)
+    got = pkb.rotary_embedding(by_head, pos, table, k=by_token, layout=layout)
+    want = pkb.rotary_embedding(by_head.contiguous(), pos, table, k=by_token.contiguous(),
+                                layout=layout)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    if T > 1:
+        for out in (by_head, torch.zeros(1, 6, 64, device=DEV).bfloat16().expand(T, 6, 64)):
+            with pytest.raises(pkb.PagedAttnError):
+                pkb.rotary_embedding(by_head.contiguous(), pos, table, q_out=out, layout=layout)
+
+
 def test_other_stream_and_graph():
     gen = torch.Generator().manual_seed(9)
     q = rows(gen, 33, 4, 64, dtype=torch.bfloat16)
