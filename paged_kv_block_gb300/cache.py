@@ -3,7 +3,8 @@ to the paged K/V cache, and the pages' ownership.
 
 Argument marshalling only, like the rest of the binding: shapes, types and devices are checked
 here, values on the device by the kernels.  The functions take torch tensors on the current
-CUDA device and enqueue on the current stream unless `stream` is given.
+CUDA device and enqueue on the current stream unless `stream` is given; what they allocate
+belongs to that stream, as under torch.cuda.stream(stream).
 """
 from __future__ import annotations
 
@@ -165,11 +166,20 @@ def _status(t, dev):
     return t.data_ptr()
 
 
-def _empty(t, dtype):
+def _new(shape, dtype, device, stream):
+    """A new tensor from the pool of the stream that the call runs on: from another stream's,
+    the allocator could hand the memory out again while the call's kernels still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(t, dtype, stream):
     """A new contiguous tensor of t's shape (empty_like is the cheaper call)."""
-    if t.dtype is dtype and t.is_contiguous():
+    if stream is None and t.dtype is dtype and t.is_contiguous():
         return torch.empty_like(t)
-    return torch.empty(t.shape, dtype=dtype, device=t.device)
+    return _new(t.shape, dtype, t.device, stream)
 
 
 def _table(freqs, dev):
@@ -179,10 +189,10 @@ def _table(freqs, dev):
     return freqs.data_ptr()
 
 
-def _workspace(workspace, size, n, like, dev):
+def _workspace(workspace, size, n, like, dev, stream):
     """The caller's workspace, or a new one of size(n) bytes."""
     if workspace is None:
-        return torch.empty(size(n), dtype=torch.uint8, device=like.device)
+        return _new(size(n), torch.uint8, like.device, stream)
     _on_device(workspace, dev, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -290,7 +300,7 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
     if dt not in _DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
     if q_out is None:
-        q_out = _empty(q, dt)
+        q_out = _empty(q, dt, stream)
         qot, qoh = Hq * D, D
     else:
         if q_out.shape != q.shape or q_out.dtype != dt:
@@ -305,7 +315,7 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
         if Hk < 1:
             raise ValueError("k must have heads")
         if k_out is None:
-            k_out = _empty(k, dt)
+            k_out = _empty(k, dt, stream)
             kot, koh = Hk * D, D
         else:
             if k_out.shape != k.shape or k_out.dtype != dt:
@@ -409,7 +419,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
             raise ValueError("q must have k's tokens, columns and dtype, adjacent heads, and "
                              "tokens in rows of their own")
         if q_out is None:
-            q_out = _empty(q, _BF16)
+            q_out = _empty(q, _BF16, stream)
         elif (q_out.shape != q.shape or q_out.dtype is not torch.bfloat16
               or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous bf16 of q's shape")
@@ -510,7 +520,7 @@ def extend_cache_rows(rows, new_tokens, block_tables, seq_lens, page_refs, page_
     dev = _device()
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
     n = _count(rows, "rows")
-    ws = _workspace(workspace, extend_cache_workspace_size, n, rows, dev)
+    ws = _workspace(workspace, extend_cache_workspace_size, n, rows, dev, stream)
     rc = _call.paged_cache_extend_run(p, _ints(rows, dev, "rows"),
                                       _ints_of(new_tokens, dev, "new_tokens", n), n, bt, sl, pr,
                                       ws.data_ptr(), ws.nbytes, _stream(stream, dev))
@@ -529,7 +539,7 @@ def fork_cache_rows(pools, parents, children, block_tables, seq_lens, page_refs,
     dev = _device()
     p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
     n = _count(children, "children")
-    ws = _workspace(workspace, fork_cache_workspace_size, n, children, dev)
+    ws = _workspace(workspace, fork_cache_workspace_size, n, children, dev, stream)
     rc = _call.paged_cache_fork_run(p, pools.ref(dev), _ints_of(parents, dev, "parents", n),
                                     _ints(children, dev, "children"), n, bt, sl, pr,
                                     ws.data_ptr(), ws.nbytes, _stream(stream, dev))
@@ -557,8 +567,9 @@ def compact_cache(pools, block_tables, seq_lens, page_refs, *, block_tables_out=
         refs = page_refs_out
         pro = _ints_of(refs, dev, "page_refs_out", page_refs.numel())
     if num_live is None:
-        num_live = torch.empty(1, dtype=_I32, device=page_refs.device)
-    ws = _workspace(workspace, compact_cache_workspace_size, page_refs.numel(), page_refs, dev)
+        num_live = _new(1, _I32, page_refs.device, stream)
+    ws = _workspace(workspace, compact_cache_workspace_size, page_refs.numel(), page_refs, dev,
+                    stream)
     rc = _call.paged_cache_compact_run(p, pools.ref(dev), bt, sl, pr, bto, pro,
                                        _ints_of(num_live, dev, "num_live", 1), ws.data_ptr(),
                                        ws.nbytes, _stream(stream, dev))

@@ -385,3 +385,52 @@ def test_append_rows_that_step_by_nothing(recorded):
         assert recorded.params is None
     pkb.append_paged_kv_cache(row, row, cache, lens[:1], block_tables=table[:1])
     assert recorded.params.k_token_stride in (0, 16)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(recorded, monkeypatch):
+    # A workspace goes back to the allocator when the call returns, while its kernels may still
+    # run: it has to come from the pool of the stream that they run on.
+    current, seen = [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def spy(make):
+        def call(*a, **kw):
+            seen.append(current[-1] if current else None)
+            return make(*a, **kw)
+        return call
+
+    class Sizes(_Recorder):
+        def __getattr__(self, name):
+            return (lambda n: 64) if name.endswith("_size") else super().__getattr__(name)
+
+    cache = torch.zeros(4, 2, 2, 8, 8, dtype=torch.bfloat16)
+    i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32)
+    q, t = torch.zeros(3, 2, 8), torch.zeros(4, dtype=torch.int64)
+    pools = pkb.cache_pools([cache])
+    monkeypatch.setattr(K, "_call", Sizes())
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", spy(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", spy(torch.empty_like))
+    state = (i32(3, 2), i32(3), i32(4))
+    for made, call in (
+            (1, lambda s: pkb.rotary_embedding(q, i32(3), t, stream=s)),
+            (2, lambda s: pkb.rotary_embedding(q, i32(3), t, k=q.transpose(0, 1).contiguous()
+                                               .transpose(0, 1), stream=s)),
+            (1, lambda s: pkb.append_paged_kv_cache(q, q, cache, i32(3), q=q, stream=s,
+                                                    block_tables=i32(3, 2))),
+            (1, lambda s: pkb.extend_cache_rows(i32(2), i32(2), *state, 8, stream=s)),
+            (1, lambda s: pkb.fork_cache_rows(pools, i32(2), i32(2), *state, stream=s)),
+            (2, lambda s: pkb.compact_cache(pools, *state, stream=s))):
+        for stream in (None, "side"):
+            seen.clear()
+            call(stream)
+            assert seen == [stream] * made
