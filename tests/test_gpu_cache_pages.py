@@ -420,6 +420,38 @@ def test_two_streams_at_once():
         b.same()
 
 
+def test_other_stream_without_a_workspace():
+    # the workspaces are freed while their kernels run; what the current stream allocates next
+    # must not be that memory
+    b, side = Both(23, 8, 9, 9000, 8, Hkv=1, layers=2), torch.cuda.Stream()
+    rows, new = i32([0, 1, 2]), i32([30, 5, 60])
+    parents, children = i32([0, 1]), i32([6, 7])
+    refs_out, tables_out = torch.empty_like(b.refs), torch.empty_like(b.tables)
+    torch.cuda.synchronize()
+
+    def churn():
+        for n in (pkb.extend_cache_workspace_size(3), pkb.fork_cache_workspace_size(2),
+                  pkb.compact_cache_workspace_size(9000)):
+            torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+
+    pkb.extend_cache_rows(rows, new, b.tables, b.lens, b.refs, b.ps, stream=side)
+    churn()
+    pkb.fork_cache_rows(b.handle, parents, children, b.tables, b.lens, b.refs, stream=side)
+    churn()
+    pkb.free_cache_rows(rows[:1], b.tables, b.lens, b.refs, b.ps, stream=side)
+    _, _, live = pkb.compact_cache(b.handle, b.tables, b.lens, b.refs, stream=side,
+                                   block_tables_out=tables_out, page_refs_out=refs_out)
+    churn()
+    torch.cuda.synchronize()
+    b.tables.copy_(tables_out)
+    b.refs.copy_(refs_out)
+    b.o.extend([0, 1, 2], [30, 5, 60])
+    b.o.fork([0, 1], [6, 7])
+    b.o.free([0])
+    assert live.item() == b.o.compact()
+    b.same()
+
+
 def test_refusals():
     b = Both(5, 3, 4, 10, 16)
     one = i32([0])
