@@ -204,10 +204,11 @@ int paged_cache_extend_run(const paged_cache_params* params, const int32_t* rows
 /* Make children[i] a copy of parents[i]: the full pages are shared (their counts go up), and a
  * partly filled last page is copied, its live tokens only, into a fresh page, in every layer.
  * A parent may be listed any number of times; parents are read as they are before the call.
- * Children are distinct and empty.  Items that break this, rows outside [0, rows), a row that is
- * its own parent and page ids outside the pool are left out (metadata bit); an item for whose
- * fresh page the free pages do not suffice (counted as in extend) leaves its child empty
- * (capacity bit).  n <= 4096. */
+ * Children are distinct and empty.  Items that break this, that name rows outside [0, rows), a row
+ * as its own parent or a parent whose partly filled page lies outside the pool are left out
+ * (metadata bit); an item for whose fresh page the free pages do not suffice (counted as in extend)
+ * leaves its child empty (capacity bit).  Ids outside the pool among the parent's full pages are
+ * copied as they are and counted nowhere (metadata bit).  n <= 4096. */
 size_t paged_cache_fork_workspace_size(int n);
 int paged_cache_fork_run(const paged_cache_params* params, const paged_cache_pools* pools,
                          const int32_t* parents_dev, const int32_t* children_dev, int n,

@@ -167,11 +167,13 @@ class State:
         for a, c in zip(parents, children):
             ok = 0 <= a < self.R and 0 <= c < self.R and a != c and before[c] == 0
             ok = ok and before[a] >= 0 and self.pages(before[a]) <= self.C
+            full, tail = divmod(before[a], self.ps) if ok else (0, 0)
+            ok = ok and (tail == 0 or 0 <= self.tables[a][full] < self.P)
             if not ok or c in seen:
                 self.status |= METADATA
                 continue
             seen.add(c)
-            items.append((a, c, int(before[a] % self.ps > 0)))
+            items.append((a, c, int(tail > 0)))
         for (a, c, n), pages in zip(items, self._grant([i[2] for i in items])):
             if pages is None:
                 continue
@@ -187,9 +189,6 @@ class State:
                 self.tables[c][full] = p
                 self.refs[p] = 1
                 s = self.tables[a][full]
-                if not 0 <= s < self.P:
-                    self.status |= METADATA
-                    continue
                 for pool in self.pools:
                     pool[p, :, :tail] = pool[s, :, :tail]
             self.lens[c] = before[a]

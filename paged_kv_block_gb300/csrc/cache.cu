@@ -143,8 +143,11 @@ struct FreePages {
     return mask_of(r);
   }
 
-  // Count the CTA's own steps (before the cluster barrier).
-  __device__ void count(const int* counts, int num_pages, int cta, int ctas, int* shared) {
+  // Count the CTA's own steps (before the cluster barrier); `meanwhile` runs while the first loads
+  // are on their way.
+  template <typename F>
+  __device__ void count(const int* counts, int num_pages, int cta, int ctas, int* shared,
+                        const F& meanwhile) {
     refs = counts;
     P = num_pages;
     rank = cta;
@@ -163,6 +166,7 @@ struct FreePages {
       uint32_t r[4][kThreadPages];                     // four steps' loads in flight
 #pragma unroll
       for (int u = 0; u < 4; ++u) load(j0 + u, r[u]);
+      if (j0 == 0) meanwhile();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (j0 + u >= own) break;
@@ -227,9 +231,7 @@ struct ForkArgs {
   Pools pools;
   int npools, segs;          // runs of tail bytes per pool: one per head, K and V
   int page_bytes, seg_bytes, token_bytes;
-  const int *children, *parents;
-  const int* need;           // of the planning kernel: 0, 1 or -1 (left out)
-  const int* len;            // the parent's length before the call
+  const int4* items;         // of the planning kernel (PlanArgs::forks)
   const int* page;           // the fresh page of the item, -1 none
   int n;
   int* tables;
@@ -240,26 +242,23 @@ struct ForkArgs {
 };
 
 // One unit of a fork, by a whole CTA: the tail of an item in one pool, or part of its table row.
-// It starts with two dependent round trips to L2 (item -> parent's table -> page) and then has four
-// 16-byte words per thread in flight: forking 256 children in 8 layers takes 28 us a call with its
-// frees, 32 with one word in flight; two pools per CTA changed nothing, half a pool per CTA (more
-// round trips) cost 5 us, CTAs of 512 threads 3.  The copies then run at 8 to 9 TB/s of L2.
+// It starts with a round trip to L2 for its item and then has four 16-byte words per thread in
+// flight: forking 256 children in 8 layers takes 28.6 us in a graph with its frees (28.0 before
+// plan_kernel looked at the parents' last pages, 0.6 us for one more dependent read); with one word in
+// flight 4 us more; two pools per CTA changed nothing, half a pool per CTA (more round trips) cost 5
+// us, CTAs of 512 threads 3.  The copies then run at 8 to 9 TB/s of L2.
 __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
   const int tid = threadIdx.x, threads = blockDim.x;
   const int per_item = a.npools + a.table_units;
   const int i = static_cast<int>(u / per_item);
   const int w = static_cast<int>(u - static_cast<long long>(i) * per_item);
-  const int need = a.need[i], L = a.len[i], d = a.page[i], parent = a.parents[i];
-  if (need < 0) return;
+  const int4 item = a.items[i];
+  const int L = item.x, s = item.y, d = a.page[i], parent = item.z;
+  if (L < 0) return;
   const int full = L / a.ps;
   const long long from = static_cast<long long>(parent) * a.C;
   if (w < a.npools) {
     if (d < 0) return;
-    const int s = a.tables[from + full];
-    if (s < 0 || s >= a.P) {
-      if (tid == 0) report_error(a.status, kErrMetadata);
-      return;
-    }
     const int words = (L - full * a.ps) * a.token_bytes / 16, all = words * a.segs;
     uint8_t* base = static_cast<uint8_t*>(a.pools.p[w]);
     const uint8_t* src = base + static_cast<long long>(s) * a.page_bytes;
@@ -286,7 +285,7 @@ __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
         if (x0 + b * threads < all) *reinterpret_cast<uint4*>(dst + o[b]) = v[b];
     }
   } else {
-    const long long to = static_cast<long long>(a.children[i]) * a.C;
+    const long long to = static_cast<long long>(item.w) * a.C;
     for (int j = (w - a.npools) * threads + tid; j < full; j += a.table_units * threads) {
       const int p = a.tables[from + j];
       a.tables[to + j] = p;
@@ -316,8 +315,8 @@ struct PlanArgs {
   unsigned long long by_ps;  // ceil(2^64 / ps)
   int hash;                // entries of the table of rows seen, a power of two >= 2 n
   uint32_t* status;
-  int* need;               // workspace [n], fork: 0, 1 or -1 (left out)
-  int* len;                // workspace [n], fork: the parent's length before the call
+  int4* forks;             // workspace [n], fork: the parent's length before the call (-1: left
+                           // out), its partly filled page (in the pool), the parent, the child
   int* page;               // workspace [n], fork: the fresh page of the item, -1 none
 };
 struct ForkPlanArgs : PlanArgs {
@@ -358,7 +357,8 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
   Item* mine = reinterpret_cast<Item*>(keys);                  // later: the CTA's copy of the items
   int* item_of = keys + 2 * a.hash;                            // fork: the item of the k-th demand
   int* pages_shared = item_of + (kFork ? a.n : 0);
-  // CTA 0: rows, lengths, and the new tokens or (fork) the child's length
+  // CTA 0: rows, lengths, and the new tokens or (fork) the child's length, then the parent's last
+  // page if it is partly filled (else 0)
   int row[kPerThread], L[kPerThread], other[kPerThread];
   uint32_t bits = 0;
   grid_dependency_wait();
@@ -388,9 +388,25 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
       if (kFork) other[j] = a.lens[row[j]];
     }
   }
-  // The counts are read while the lengths are on their way.
+  // The counts are read while the lengths are on their way, and the parents' last pages after them.
+  // Before an item gets a page its parent's last one has to lie in the pool: else the child's would
+  // be live without ever having been written.
   FreePages pages;
-  pages.count(a.refs, a.P, rank, size, pages_shared);
+  pages.count(a.refs, a.P, rank, size, pages_shared, [&] {
+    if (!kFork || rank != 0) return;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = j * threads + tid;
+      if (j * threads >= a.n) break;
+      if (L[j] < 0 || other[j] != 0) {                 // left out
+        L[j] = -1;
+        continue;
+      }
+      const int full = over_page(L[j], a.by_ps);
+      if (full < a.C && full * a.ps < L[j])
+        other[j] = a.tables[static_cast<long long>(a.parents[i]) * a.C + full];
+    }
+  });
   if (rank == 0) {
     int* first = keys + a.hash;
     int need[kPerThread], at[kPerThread], pages_of[kPerThread];
@@ -399,7 +415,7 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
       if (j * threads >= a.n) break;
       need[j] = -1;
       at[j] = pages_of[j] = 0;
-      if (L[j] < 0 || (kFork ? other[j] != 0 : other[j] < 0)) continue;
+      if (L[j] < 0 || other[j] < 0 || (kFork && other[j] >= a.P)) continue;
       if (!kFork && L[j] > INT_MAX - other[j]) continue;
       const int full = over_page(L[j], a.by_ps), have = over_page(L[j] + a.ps - 1u, a.by_ps);
       const int want = kFork ? have : over_page(L[j] + other[j] + a.ps - 1u, a.by_ps);
@@ -452,8 +468,7 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
       if (it.row >= 0 && !served) bits |= kErrCapacity;
       if (served) a.lens[it.row] = kFork ? L[j] : L[j] + other[j];
       if (kFork) {
-        a.need[i] = served ? it.need : -1;
-        a.len[i] = L[j];
+        a.forks[i] = make_int4(served ? L[j] : -1, other[j], a.parents[i], row[j]);
         if (it.need == 0 || !served) a.page[i] = -1;
       }
     }
@@ -666,7 +681,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
   grid_launch_dependents();
   if (rank == 0 && tid < 4) a.status[tid] = 0;
   FreePages pages;
-  pages.count(a.refs, a.P, rank, size, shared);
+  pages.count(a.refs, a.P, rank, size, shared, [] {});
   if (a.refs_out != a.refs) {              // what moves is set right below, after the barriers
     constexpr int kBatch = 8;
     const int stride = size * threads;
@@ -723,12 +738,11 @@ struct Take {
 int* at(void* ws, size_t off) { return reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + off); }
 
 struct PlanLayout {
-  size_t status, need, len, page, total;
+  size_t status, forks, page, total;
   explicit PlanLayout(int n) {
     Take t;
     status = t.ints(4);
-    need = t.ints(n);
-    len = t.ints(n);
+    forks = t.ints(4LL * n);
     page = t.ints(n);
     total = t.off;
   }
@@ -902,7 +916,7 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
   a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
-  a.need = at(ws, l.need); a.len = at(ws, l.len); a.page = at(ws, l.page);
+  a.forks = reinterpret_cast<int4*>(at(ws, l.forks)); a.page = at(ws, l.page);
   ForkArgs& f = a.fork;
   f.npools = pool_count(pools);
   for (int i = 0; i < f.npools; ++i) f.pools.p[i] = pools->pools_host[i];
@@ -910,7 +924,7 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   f.page_bytes = static_cast<int>(page_bytes(pools));
   f.seg_bytes = static_cast<int>(seg_bytes(pools));
   f.token_bytes = 2 * pools->head_dim;
-  f.children = children; f.parents = parents; f.need = a.need; f.len = a.len; f.page = a.page;
+  f.items = a.forks; f.page = a.page;
   f.n = n;
   f.tables = tables; f.refs = refs;
   f.C = a.C; f.ps = a.ps; f.P = a.P;
