@@ -18,11 +18,12 @@
  *
  * Status words.  A call with a workspace clears the status word at the workspace's start and
  * ORs in what it finds (paged_attn_workspace_status reads it); the workspace belongs to one
- * launch in flight at a time.  Calls without a workspace take status_dev, a uint32 word that
- * they OR into and never clear, or NULL to have nothing recorded (paged_attn_workspace_status
- * reads such a word too).  In both, PAGED_ATTN_ERR_METADATA means that an item broke its
- * contract and was left out, PAGED_ATTN_ERR_CAPACITY that the free pages did not suffice for
- * every item, and PAGED_ATTN_ERR_TIMEOUT that a device wait ran out and rows were not written.
+ * launch in flight at a time.  Every call takes status_dev too, as an argument or (extend, fork,
+ * compact) in its params: a uint32 word that it ORs into and never clears, or NULL
+ * (paged_attn_workspace_status reads such a word as well).  In both, PAGED_ATTN_ERR_METADATA
+ * means that an item broke its contract and was left out, PAGED_ATTN_ERR_CAPACITY that the free
+ * pages did not suffice for every item, and PAGED_ATTN_ERR_TIMEOUT that a device wait ran out and
+ * rows were not written.
  */
 #ifndef PAGED_CACHE_H
 #define PAGED_CACHE_H
@@ -170,6 +171,7 @@ typedef struct paged_cache_params {
   int max_pages_per_request;  /* C                                                         */
   int page_size;              /* a multiple of 8, at most 128                              */
   int num_pages;              /* P <= 2^24                                                 */
+  uint32_t* status_dev;       /* extend, fork and compact OR their findings in; or NULL    */
 } paged_cache_params;
 
 /* The pools of every layer, all with the same page ids; a page is below 2^31 bytes. */
@@ -192,7 +194,8 @@ int paged_cache_free_run(const paged_cache_params* params, const int32_t* rows_d
 
 /* Make each listed row longer by new_tokens[i] (>= 0) tokens, with fresh pages where its last
  * page does not hold them.  Item i is served if it needs no page or if the free pages suffice
- * for it and every item listed before it; otherwise its row stays as it is (capacity bit).
+ * for it and every item listed before it; otherwise its row stays as it is (capacity bit): its
+ * length does not count the new tokens, so appending them would write over the row's last ones.
  * Rows outside [0, rows), a row listed before, negative tokens and rows that would outgrow C
  * pages are left out (metadata bit).  n <= 4096. */
 size_t paged_cache_extend_workspace_size(int n);

@@ -47,7 +47,7 @@ class AppendParams(C.Structure):
 
 class CacheParams(C.Structure):
     _fields_ = [("rows", C.c_int), ("max_pages_per_request", C.c_int), ("page_size", C.c_int),
-                ("num_pages", C.c_int)]
+                ("num_pages", C.c_int), ("status_dev", C.c_void_p)]
 
 
 class CachePoolsStruct(C.Structure):
@@ -485,12 +485,14 @@ def cache_pools(layers) -> CachePools:
     return CachePools(layers)
 
 
-def _rows_state(block_tables, seq_lens, page_refs, page_size, dev):
+def _rows_state(block_tables, seq_lens, page_refs, page_size, dev, status=None):
     """(params, address of the tables, lengths, counts) of the three arrays."""
     shape = block_tables.shape
     if len(shape) != 2 or max(shape) > _INT_MAX:
         raise ValueError("block_tables must be [rows, C]")
-    return (_cache_params(shape[0], shape[1], page_size, _count(page_refs, "page_refs")),
+    fields = shape[0], shape[1], page_size, _count(page_refs, "page_refs")
+    return (_cache_params(*fields) if status is None else
+            C.byref(CacheParams(*fields, _status(status, dev))),
             _ints(block_tables, dev, "block_tables"),
             _ints_of(seq_lens, dev, "seq_lens", shape[0]), _ints(page_refs, dev, "page_refs"))
 
@@ -513,12 +515,16 @@ def extend_cache_workspace_size(n: int) -> int:
 
 
 def extend_cache_rows(rows, new_tokens, block_tables, seq_lens, page_refs, page_size, *,
-                      workspace=None, stream=None) -> None:
+                      workspace=None, status=None, stream=None) -> None:
     """Make each listed row longer by new_tokens tokens, with fresh pages (the lowest free ids,
-    in the order listed) where needed.  Rows that the free pages do not suffice for stay as
-    they are; the workspace's status word says so."""
+    in the order listed) where needed.
+
+    Rows that the free pages do not suffice for stay as they are, their lengths too: appending
+    to one would write over its last tokens.  `status`, an int32 word that findings are OR-ed
+    into, tells (ERR_CAPACITY's bit 2, for items that broke the contract 4), and so does the
+    workspace's word, which every call clears."""
     dev = _device()
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev)
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, page_size, dev, status)
     n = _count(rows, "rows")
     ws = _workspace(workspace, extend_cache_workspace_size, n, rows, dev, stream)
     rc = _call.paged_cache_extend_run(p, _ints(rows, dev, "rows"),
@@ -533,11 +539,13 @@ def fork_cache_workspace_size(n: int) -> int:
 
 
 def fork_cache_rows(pools, parents, children, block_tables, seq_lens, page_refs, *,
-                    workspace=None, stream=None) -> None:
+                    workspace=None, status=None, stream=None) -> None:
     """Make the (empty) row children[i] a copy of row parents[i]: full pages are shared, the
-    live tokens of a partly filled last page are copied into a fresh one, in every layer."""
+    live tokens of a partly filled last page are copied into a fresh one, in every layer.
+    Children that the free pages do not suffice for stay empty; `status` and the workspace tell,
+    as in extend_cache_rows."""
     dev = _device()
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev, status)
     n = _count(children, "children")
     ws = _workspace(workspace, fork_cache_workspace_size, n, children, dev, stream)
     rc = _call.paged_cache_fork_run(p, pools.ref(dev), _ints_of(parents, dev, "parents", n),
@@ -552,11 +560,12 @@ def compact_cache_workspace_size(num_pages: int) -> int:
 
 
 def compact_cache(pools, block_tables, seq_lens, page_refs, *, block_tables_out=None,
-                  page_refs_out=None, num_live=None, workspace=None, stream=None):
+                  page_refs_out=None, num_live=None, workspace=None, status=None, stream=None):
     """Move the live pages to the pools' front, in every layer; returns (block_tables, page_refs,
-    num_live [1]) after the move.  In place unless the *_out tensors are given."""
+    num_live [1]) after the move.  In place unless the *_out tensors are given.  `status` and the
+    workspace tell of bad table entries, as in extend_cache_rows."""
     dev = _device()
-    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev)
+    p, bt, sl, pr = _rows_state(block_tables, seq_lens, page_refs, pools.page_size, dev, status)
     tables, refs, bto, pro = block_tables, page_refs, bt, pr
     if block_tables_out is not None:
         tables = block_tables_out

@@ -43,6 +43,15 @@ struct Pools {
   void* p[PAGED_CACHE_MAX_POOLS];
 };
 
+// Where a call reports: the word of its workspace and the caller's own (either may be null).
+struct Status {
+  uint32_t *ws, *own;
+};
+__device__ __forceinline__ void report(const Status& s, uint32_t bits) {
+  report_error(s.ws, bits);
+  report_error(s.own, bits);
+}
+
 // ---- free pages in order, over a cluster -------------------------------------------------------
 // Sums saturate at kManyPages, far above any pool's page count, so that absurd demands cannot
 // wrap around into served ones (summands are at most kMaxPages + 1, so a saturated exclusive
@@ -238,15 +247,15 @@ struct ForkArgs {
   int* refs;
   int C, ps, P;
   int table_units;           // CTAs per item for the table row
-  uint32_t* status;
+  Status status;
 };
 
 // One unit of a fork, by a whole CTA: the tail of an item in one pool, or part of its table row.
 // It starts with a round trip to L2 for its item and then has four 16-byte words per thread in
 // flight: forking 256 children in 8 layers takes 28.6 us in a graph with its frees (28.0 before
-// plan_kernel looked at the parents' last pages, 0.6 us for one more dependent read); with one word in
-// flight 4 us more; two pools per CTA changed nothing, half a pool per CTA (more round trips) cost 5
-// us, CTAs of 512 threads 3.  The copies then run at 8 to 9 TB/s of L2.
+// plan_kernel looked at the parents' last pages, 0.6 us for one more dependent read); with one word
+// in flight 4 us more; two pools per CTA changed nothing, half a pool per CTA (more round trips)
+// cost 5 us, CTAs of 512 threads 3.  The copies then run at 8 to 9 TB/s of L2.
 __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
   const int tid = threadIdx.x, threads = blockDim.x;
   const int per_item = a.npools + a.table_units;
@@ -290,7 +299,7 @@ __device__ __forceinline__ void fork_unit(const ForkArgs& a, long long u) {
       const int p = a.tables[from + j];
       a.tables[to + j] = p;
       if (p >= 0 && p < a.P) atomicAdd(a.refs + p, 1);
-      else report_error(a.status, kErrMetadata);
+      else report(a.status, kErrMetadata);
     }
   }
 }
@@ -314,7 +323,7 @@ struct PlanArgs {
   int R, C, ps, P;
   unsigned long long by_ps;  // ceil(2^64 / ps)
   int hash;                // entries of the table of rows seen, a power of two >= 2 n
-  uint32_t* status;
+  Status status;
   int4* forks;             // workspace [n], fork: the parent's length before the call (-1: left
                            // out), its partly filled page (in the pool), the parent, the child
   int* page;               // workspace [n], fork: the fresh page of the item, -1 none
@@ -364,7 +373,7 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (rank == 0) {
-    if (tid < 4) a.status[tid] = 0;
+    if (tid < 4) a.status.ws[tid] = 0;
     for (int i = tid; i < a.hash; i += threads) {
       keys[i] = -1;
       keys[a.hash + i] = a.n;
@@ -472,7 +481,7 @@ plan_kernel(const __grid_constant__ PlanArgsOf<kFork> a) {
         if (it.need == 0 || !served) a.page[i] = -1;
       }
     }
-    if (bits) report_error(a.status, bits);
+    if (bits) report(a.status, bits);
   }
   if (demand > 0) {
     for (int i = tid; i < a.n; i += threads) {
@@ -559,7 +568,7 @@ struct CopyArgs {
   int src_num_pages, dst_num_pages;
   long long page_bytes;
   int chunks;                // of kCopyChunk bytes per page
-  uint32_t* status;
+  Status status;
   // compact: table entries to rename
   const int *tables, *lens, *to, *num_live;
   int* tables_out;
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       d = a.dst_pages[pair_of(next)];
     }
     if (from < 0 || from >= a.src_num_pages || to < 0 || to >= a.dst_num_pages) {
-      if (threadIdx.x == 0) report_error(a.status, kErrMetadata);
+      if (threadIdx.x == 0) report(a.status, kErrMetadata);
       continue;
     }
     const int w = static_cast<int>(u - static_cast<long long>(pair_of(u)) * per_pair);
@@ -621,10 +630,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       int p = a.tables[e];
       const int old = p;
       if (j < (L + a.ps - 1LL) / a.ps) {
-        if (p < 0 || p >= a.P) report_error(a.status, kErrMetadata);
+        if (p < 0 || p >= a.P) report(a.status, kErrMetadata);
         else if (p >= live) p = a.to[p];
       }
-      if (j == 0 && (L + a.ps - 1LL) / a.ps > a.C) report_error(a.status, kErrMetadata);
+      if (j == 0 && (L + a.ps - 1LL) / a.ps > a.C) report(a.status, kErrMetadata);
       if (p != old || a.tables_out != a.tables) a.tables_out[e] = p;
     }
   }
@@ -668,7 +677,7 @@ struct CompactArgs {
   int* num_live;
   int P;
   int *src, *dst, *to, *moves;   // workspace: move lists, new ids of pages >= live, their number
-  uint32_t* status;
+  Status status;
 };
 
 // Latency-bound like plan_kernel: 5 us for 256 pages, 8 for 6,007.
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
   const int tid = threadIdx.x, threads = blockDim.x;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (rank == 0 && tid < 4) a.status[tid] = 0;
+  if (rank == 0 && tid < 4) a.status.ws[tid] = 0;
   FreePages pages;
   pages.count(a.refs, a.P, rank, size, shared, [] {});
   if (a.refs_out != a.refs) {              // what moves is set right below, after the barriers
@@ -763,7 +772,7 @@ struct CompactLayout {
 bool cache_params_ok(const paged_cache_params* p) {
   return p && p->rows >= 0 && p->max_pages_per_request > 0 && p->page_size >= 8 &&
          p->page_size <= 128 && p->page_size % 8 == 0 && p->num_pages > 0 &&
-         p->num_pages <= kMaxPages;
+         p->num_pages <= kMaxPages && (reinterpret_cast<uintptr_t>(p->status_dev) & 3) == 0;
 }
 int pool_count(const paged_cache_pools* p) { return p->num_layers * (p->combined_cache ? 1 : 2); }
 long long seg_bytes(const paged_cache_pools* p) { return 2LL * p->page_size * p->head_dim; }
@@ -892,7 +901,7 @@ int paged_cache_extend_run(const paged_cache_params* p, const int32_t* rows,
   a.rows = rows; a.new_tokens = new_tokens; a.n = n;
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
-  a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
+  a.status = {reinterpret_cast<uint32_t*>(at(ws, l.status)), p->status_dev};
   return cuda_status(launch_items<false>(a, st));
 }
 
@@ -915,7 +924,7 @@ int paged_cache_fork_run(const paged_cache_params* p, const paged_cache_pools* p
   a.rows = children; a.parents = parents; a.n = n;
   a.tables = tables; a.lens = lens; a.refs = refs;
   a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
-  a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
+  a.status = {reinterpret_cast<uint32_t*>(at(ws, l.status)), p->status_dev};
   a.forks = reinterpret_cast<int4*>(at(ws, l.forks)); a.page = at(ws, l.page);
   ForkArgs& f = a.fork;
   f.npools = pool_count(pools);
@@ -963,7 +972,7 @@ int paged_cache_compact_run(const paged_cache_params* p, const paged_cache_pools
   CompactArgs a{};
   a.refs = refs; a.refs_out = refs_out; a.num_live = num_live; a.P = p->num_pages;
   a.src = at(ws, l.src); a.dst = at(ws, l.dst); a.to = at(ws, l.to); a.moves = at(ws, l.moves);
-  a.status = reinterpret_cast<uint32_t*>(at(ws, l.status));
+  a.status = {reinterpret_cast<uint32_t*>(at(ws, l.status)), p->status_dev};
   static std::atomic<uint64_t> ready{0};
   if (launch_plan(compact_kernel, a, a.P, 1, 0, 0, ready, st) != cudaSuccess)
     return PAGED_ATTN_ERR_CUDA;
@@ -1008,7 +1017,7 @@ int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* 
   c.dst_num_pages = dst->num_pages;
   c.page_bytes = page_bytes(src);
   c.chunks = static_cast<int>(ceil_div_ll(c.page_bytes, kCopyChunk));
-  c.status = status;
+  c.status = {nullptr, status};
   const long long units = static_cast<long long>(n) * c.pools * c.chunks;
   const long long most = kMaxGrid;
   count_launches(1);
