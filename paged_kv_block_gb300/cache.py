@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 
 import torch
 
@@ -182,6 +183,11 @@ def _empty(t, dtype, stream):
     return _new(t.shape, dtype, t.device, stream)
 
 
+def _factor(m):
+    """The attention factor as a float; -0.0 as 0.0, its equal."""
+    return float(m) + 0.0
+
+
 def _table(freqs, dev):
     if freqs.dtype is not _I64 or freqs.get_device() != dev or not freqs.is_contiguous():
         _on_device(freqs, dev, "freqs")
@@ -200,6 +206,7 @@ def _workspace(workspace, size, n, like, dev, stream):
 
 
 # Parameter structs depend on the static arguments alone, so equal calls share one (read-only).
+# Every field is a Python number: a tensor would be found again by its identity, changed or not.
 @functools.lru_cache(maxsize=512)
 def _rope_params(*fields):
     return C.byref(RopeParams(*fields))
@@ -331,7 +338,8 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
     if T:
         rc = _call.paged_rope_run(
             _rope_params(T, Hq, Hk, D, 2 * freqs.numel(), ROPE_LAYOUT[layout], _DTYPE[dt],
-                         int(inverse), attention_factor, qt, qh, kt, kh, qot, qoh, kot, koh),
+                         int(inverse), _factor(attention_factor), qt, qh, kt, kh, qot, qoh, kot,
+                         koh),
             q.data_ptr(), kp, pos, table, q_out.data_ptr(), kop, status, _stream(stream, dev))
         if rc:
             _check(rc, "paged_rope_run")
@@ -437,7 +445,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     if T:
         rc = _call.paged_append_run(
             _append_params(B, sq, total, Hq, Hkv, D, ps, P, combined, cols, rotary,
-                           ROPE_LAYOUT[layout], attention_factor, _DTYPE[dt], qt, kt, vt),
+                           ROPE_LAYOUT[layout], _factor(attention_factor), _DTYPE[dt], qt, kt, vt),
             qp, k.data_ptr(), v.data_ptr(), qo, indptr, pages, lens, table, qop, kc, vc, status,
             _stream(stream, dev))
         if rc:
@@ -490,7 +498,7 @@ def _rows_state(block_tables, seq_lens, page_refs, page_size, dev, status=None):
     shape = block_tables.shape
     if len(shape) != 2 or max(shape) > _INT_MAX:
         raise ValueError("block_tables must be [rows, C]")
-    fields = shape[0], shape[1], page_size, _count(page_refs, "page_refs")
+    fields = shape[0], shape[1], operator.index(page_size), _count(page_refs, "page_refs")
     return (_cache_params(*fields) if status is None else
             C.byref(CacheParams(*fields, _status(status, dev))),
             _ints(block_tables, dev, "block_tables"),

@@ -72,3 +72,34 @@ def test_the_c_calls_refuse_a_status_word_off_its_alignment():
     assert lib.paged_cache_fork_run(C.byref(p), C.byref(s), a, a, 1, a, a, a, a, big, None) == bad
     assert lib.paged_cache_compact_run(C.byref(p), C.byref(s), a, a, a, a, a, a, a, big,
                                        None) == bad
+
+
+# ---- parameters are taken by value --------------------------------------------------------------
+
+def test_a_factor_that_changes_in_place_is_read_at_every_call(calls):
+    q, table = torch.zeros(3, 2, 8), torch.zeros(4, dtype=torch.int64)
+    cache, m = torch.zeros(4, 2, 2, 8, 8, dtype=torch.bfloat16), torch.tensor(1.0)
+    for call in (lambda: pkb.rotary_embedding(q, i32(3), table, attention_factor=m),
+                 lambda: pkb.append_paged_kv_cache(q, q, cache, i32(3), freqs=table,
+                                                   block_tables=i32(3, 2), attention_factor=m)):
+        for value in (1.0, 2.0, 0.5, 1.0):
+            m.fill_(value)
+            call()
+            assert calls[-1][1].attention_factor == value
+    # zeros of both signs are equal keys: a call gets the same one whatever came before it
+    for value in (0.0, -0.0, 0.0):
+        pkb.rotary_embedding(q, i32(3), table, attention_factor=value)
+        assert str(calls[-1][1].attention_factor) == "0.0"
+
+
+def test_a_page_size_that_changes_in_place_is_read_at_every_call(calls):
+    state, size = (i32(3, 2), i32(3), i32(4)), torch.tensor(8)
+    for call in (lambda: pkb.free_cache_rows(i32(2), *state, size),
+                 lambda: pkb.extend_cache_rows(i32(2), i32(2), *state, size)):
+        for value in (8, 16, 8):
+            size.fill_(value)
+            call()
+            assert calls[-1][1].page_size == value
+    for bad in (8.0, "8"):                            # also after a call with 8
+        with pytest.raises(TypeError):
+            pkb.free_cache_rows(i32(2), *state, bad)
