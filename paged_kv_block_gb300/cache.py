@@ -83,6 +83,8 @@ _I32, _I64, _BF16 = torch.int32, torch.int64, torch.bfloat16
 _INT_MAX = 2 ** 31 - 1
 # The current stream's handle without building a Stream object, where this torch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_grad_enabled = torch.is_grad_enabled
+_increment_version = torch.autograd.graph.increment_version    # autograd learns of what is written
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 def _device():
@@ -293,6 +295,36 @@ def _rows(t, dev, name):
     return T, H, D, ts, hs
 
 
+class _Rotation(torch.autograd.Function):
+    """rotary_embedding with its gradient, the rotation by the negative angles."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, layout, attention_factor, inverse, status, stream):
+        ctx.save_for_backward(positions, freqs)
+        ctx.how = dict(layout=layout, attention_factor=attention_factor, inverse=not inverse,
+                       status=status)
+        ctx.set_materialize_grads(False)
+        return rotary_embedding(q, positions, freqs, k=k, layout=layout, inverse=inverse,
+                                attention_factor=attention_factor, status=status, stream=stream)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        positions, freqs = ctx.saved_tensors
+        if positions.is_cuda and torch.cuda.is_current_stream_capturing():
+            # An eager graph of the same leaves would tie the captured stream to its own.
+            raise ValueError("the gradient of rotary_embedding is not captured into graphs: call "
+                             "it with inverse=True on the gradient of its output")
+        wanted = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
+        out = [None] * 9
+        if wanted:
+            g = [grads[i].contiguous() for i in wanted]
+            turned = rotary_embedding(g[0], positions, freqs, k=g[1] if len(g) > 1 else None,
+                                      **ctx.how)
+            for i, t in zip(wanted, turned if len(g) > 1 else (turned,)):
+                out[i] = t
+        return tuple(out)
+
+
 def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_factor=1.0,
                      inverse=False, q_out=None, k_out=None, status=None, stream=None):
     """Rotate q (and k) [T, heads, D] or [B, S, heads, D] at int32 `positions` (one per token),
@@ -300,7 +332,19 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
 
     q_out=q rotates in place.  inverse=True turns back by the same angles (times the same
     attention_factor): the gradient of the input from the gradient of the output.
-    status: an int32 word that device-side findings are OR-ed into."""
+    status: an int32 word that device-side findings are OR-ed into.
+
+    Autograd knows the call: q and k may require gradients, then without q_out and k_out.  A
+    gradient is not captured into a CUDA graph; call inverse=True there."""
+    needs = q.requires_grad or (k is not None and k.requires_grad)
+    given = None
+    if q_out is not None or k_out is not None:
+        given = (q_out,) if k_out is None else (k_out,) if q_out is None else (q_out, k_out)
+        if (needs or given[0].requires_grad or given[-1].requires_grad) and _grad_enabled():
+            raise ValueError("q_out and k_out are for tensors that require no gradient")
+    elif needs and _grad_enabled():
+        return _Rotation.apply(q, k, positions, freqs, layout, _factor(attention_factor),
+                               bool(inverse), status, stream)
     dev = _device()
     T, Hq, D, qt, qh = _rows(q, dev, "q")
     dt = q.dtype
@@ -343,6 +387,8 @@ def rotary_embedding(q, positions, freqs, *, k=None, layout="half", attention_fa
             q.data_ptr(), kp, pos, table, q_out.data_ptr(), kop, status, _stream(stream, dev))
         if rc:
             _check(rc, "paged_rope_run")
+        if given is not None:
+            _increment_version(given)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -383,6 +429,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     or [B, SQ, heads, D]; bf16, fp16 or fp32, rows may be slices of a fused projection.  The
     page table is block_tables [B, C] or paged_kv_indptr with paged_kv_indices.  seq_lens_kv
     [B] counts the new tokens in.  freqs (from rope_frequencies) None writes keys as they are.
+    The call has no gradient: what it returns never requires one.
     status: an int32 word that device-side findings are OR-ed into."""
     dev = _device()
     kc, vc, combined, P, Hkv, ps, D = _geometry(paged_kv_cache, dev)
@@ -399,7 +446,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
     if kt == 0 or vt == 0:                   # to the C call that means contiguous rows
         raise ValueError("the tokens of k and v must be rows of their own")
     total = sq = cols = Hq = qt = 0
-    qo = indptr = qp = qop = table = None
+    qo = indptr = qp = qop = table = given = None
     if qo_indptr is not None:
         if k.dim() != 3:
             raise ValueError("packed k must be [total, heads, D]")
@@ -433,6 +480,7 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
             raise ValueError("q_out must be contiguous bf16 of q's shape")
         else:
             _on_device(q_out, dev, "q_out")
+            given = q_out
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -450,6 +498,8 @@ def append_paged_kv_cache(k, v, paged_kv_cache, seq_lens_kv, *, block_tables=Non
             _stream(stream, dev))
         if rc:
             _check(rc, "paged_append_run")
+        if given is not None:
+            _increment_version(given)
     return q_out
 
 

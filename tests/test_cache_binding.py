@@ -103,3 +103,75 @@ def test_a_page_size_that_changes_in_place_is_read_at_every_call(calls):
     for bad in (8.0, "8"):                            # also after a call with 8
         with pytest.raises(TypeError):
             pkb.free_cache_rows(i32(2), *state, bad)
+
+
+# ---- autograd ----------------------------------------------------------------------------------
+
+def test_rotation_is_known_to_autograd(calls):
+    table, pos = torch.zeros(4, dtype=torch.int64), i32(3)
+    q, k = torch.zeros(3, 4, 8, requires_grad=True), torch.zeros(3, 2, 8, requires_grad=True)
+    m = torch.tensor(2.0)
+
+    def shapes(p):
+        return p.num_tokens, p.num_qo_heads, p.num_kv_heads, p.inverse, p.attention_factor
+    qo, ko = pkb.rotary_embedding(q, pos, table, k=k, attention_factor=m)
+    assert qo.requires_grad and ko.requires_grad
+    m.fill_(3.0)                                      # the forward call's factor counts
+    torch.autograd.backward([qo, ko], [torch.ones_like(qo), torch.ones_like(ko)])
+    assert [shapes(c[1]) for c in calls] == [(3, 4, 2, 0, 2.0), (3, 4, 2, 1, 2.0)]
+    assert q.grad.shape == q.shape and k.grad.shape == k.shape
+    # what nobody asks for is not computed
+    calls.clear()
+    qo, ko = pkb.rotary_embedding(q.detach(), pos, table, k=k, inverse=True)
+    assert not qo.requires_grad or qo.grad_fn is ko.grad_fn
+    torch.autograd.grad(ko, k, torch.ones_like(ko))
+    assert [shapes(c[1]) for c in calls] == [(3, 4, 2, 1, 1.0), (3, 2, 0, 0, 1.0)]
+    calls.clear()
+    qo, _ = pkb.rotary_embedding(q, pos, table, k=k)
+    qo.sum().backward()                              # a gradient of step 0: one value for all
+    assert [shapes(c[1]) for c in calls] == [(3, 4, 2, 0, 1.0), (3, 4, 0, 1, 1.0)]
+    assert (calls[1][1].q_token_stride, calls[1][1].q_head_stride) == (32, 8)
+    with torch.no_grad():
+        assert not pkb.rotary_embedding(q, pos, table).requires_grad
+
+
+def test_outputs_that_autograd_cannot_follow_are_refused(calls):
+    table, pos = torch.zeros(4, dtype=torch.int64), i32(3)
+    q, k = torch.zeros(3, 4, 8), torch.zeros(3, 2, 8)
+    leaf_q, leaf_k = (t.clone().requires_grad_() for t in (q, k))
+    for kw in (dict(q=leaf_q, q_out=q), dict(q=leaf_q, q_out=leaf_q), dict(q=q, q_out=leaf_q),
+               dict(q=q, k=leaf_k, k_out=k), dict(q=q, k=k, k_out=leaf_k),
+               dict(q=q, k=leaf_k, q_out=q)):
+        with pytest.raises(ValueError):
+            pkb.rotary_embedding(positions=pos, freqs=table, **kw)
+    assert not calls
+    with torch.no_grad():
+        pkb.rotary_embedding(leaf_q, pos, table, q_out=leaf_q)
+    assert len(calls) == 1
+
+
+def test_given_outputs_count_as_changed(calls):
+    table, pos = torch.zeros(4, dtype=torch.int64), i32(3)
+    q, k = torch.zeros(3, 4, 8), torch.zeros(3, 2, 8)
+    w = torch.ones(8, requires_grad=True)
+    y = (q * w).sum()                                # saves q
+    seen = q._version, k._version
+    pkb.rotary_embedding(q, pos, table, k=k, q_out=q, k_out=k)
+    assert q._version > seen[0] and k._version > seen[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    seen, cache = q._version, torch.zeros(4, 2, 2, 8, 8, dtype=torch.bfloat16)
+    out = torch.zeros(3, 4, 8, dtype=torch.bfloat16)
+    pkb.append_paged_kv_cache(k, k, cache, pos, q=q, q_out=out, block_tables=i32(3, 2))
+    assert out._version > 0 and q._version == seen
+    with torch.inference_mode():                     # such tensors have no version
+        t = torch.zeros(3, 4, 8)
+        pkb.rotary_embedding(t, pos, table, q_out=t)
+
+
+def test_positions_that_change_before_the_gradient_are_noticed(calls):
+    q, pos = torch.zeros(3, 4, 8, requires_grad=True), i32(3)
+    out = pkb.rotary_embedding(q, pos, torch.zeros(4, dtype=torch.int64))
+    pos.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
