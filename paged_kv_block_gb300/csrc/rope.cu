@@ -789,7 +789,8 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
   const bool packed = qo_indptr != nullptr;
   if (!append_params_ok(p, packed)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const bool has_q = p->num_qo_heads > 0;
-  if (!k || !v || !pages || !lens || !k_cache || has_q != (q != nullptr) ||
+  // without requests there are no lengths and no pages, and empty arrays have no address
+  if (!k || !v || (p->batch > 0 && (!pages || !lens)) || !k_cache || has_q != (q != nullptr) ||
       has_q != (q_out != nullptr) || (p->combined_cache != 0) == (v_cache != nullptr))
     return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   if (p->rotary_dim > 0 && !table) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
@@ -798,7 +799,8 @@ int paged_append_run(const paged_append_params* p, const void* q, const void* k,
                         static_cast<const void*>(pages), static_cast<const void*>(lens),
                         static_cast<const void*>(status)})
     if (!aligned_to(i, 4)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
-  if (!kv_indptr && p->max_pages_per_request <= 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (p->batch > 0 && !kv_indptr && p->max_pages_per_request <= 0)
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
   const size_t e = size_of(p->in_dtype);
   if (!aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) || !aligned_to(q_out, 16) ||
       !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16))

@@ -175,3 +175,26 @@ def test_positions_that_change_before_the_gradient_are_noticed(calls):
     pos.add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.sum().backward()
+
+
+# ---- a batch of no request --------------------------------------------------------------------
+
+def test_rows_of_no_request_are_padding():
+    """A packed batch without requests: its rows are padding, and empty arrays have no address."""
+    import ctypes as C
+    B.build()
+    lib = pkb.lib()
+    p = K.AppendParams(batch=0, total_q=5, num_qo_heads=4, num_kv_heads=2, head_dim=64,
+                       page_size=16, num_pages=10, combined_cache=1, max_pages_per_request=4,
+                       rotary_dim=64, attention_factor=1.0)
+
+    def run(p, lens, pages, **kw):
+        a = dict(q=A16, k=A16, v=A16, table=A16, out=A16, kc=A16)
+        a.update(kw)
+        return lib.paged_append_run(C.byref(p), a["q"], a["k"], a["v"], A16, None, pages, lens,
+                                    a["table"], a["out"], a["kc"], None, None, None)
+    assert run(p, None, None) == 0
+    for bad in (dict(k=None), dict(kc=None), dict(out=A16 + 8), dict(q=None), dict(table=None)):
+        assert run(p, None, None, **bad) == pkb.ERR_INVALID_ARGUMENT, bad
+    p.batch = 1                                      # a request's length and pages are needed
+    assert run(p, None, A16) == run(p, A16, None) == pkb.ERR_INVALID_ARGUMENT

@@ -48,3 +48,20 @@ def test_row_layouts_write_the_same_cache(new, combined, layout, dtype, Hq, Hkv,
     odd.copy_(k)
     o, c = run(odd, v, q)
     assert torch.equal(c, cache) and (out is None or torch.equal(o, out))
+
+
+@pytest.mark.parametrize("columns", [0, 3])
+def test_a_batch_of_no_request_writes_nothing(columns):
+    """All rows of the packed tensors are padding."""
+    s = problem(9, [4, 5], [0, 2], Hq=2, Hkv=1, D=16)
+    table, _ = pkb.rope_frequencies(16)
+    before = s["cache"].clone()
+    mark = torch.full(s["q"].shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    q_out, word = mark.clone(), torch.zeros(1, dtype=torch.int32, device=DEV)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    for pages in (dict(block_tables=none.new_zeros(0, columns)),
+                  dict(paged_kv_indptr=none.new_zeros(1), paged_kv_indices=none)):
+        pkb.append_paged_kv_cache(s["k"], s["v"], (s["cache"][0], s["cache"][1]), none, q=s["q"],
+                                  q_out=q_out, qo_indptr=none.new_zeros(1), freqs=table,
+                                  status=word, **pages)
+        assert torch.equal(q_out, mark) and torch.equal(s["cache"], before) and word.item() == 0
