@@ -35,8 +35,19 @@ static_assert(kPlanSmem <= 226 * 1024, "shared memory of the planning kernels");
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;          // bytes of one copy unit
 constexpr int kCopyCtas = 24;              // CTAs per SM where they walk the units (copy_kernel)
-constexpr int kOwnUnits = 16;              // a fork of so little is done by the planning CTA
-constexpr int kOwnBytes = 1 << 17;         // itself: one launch (2.7 us of the host's time) less
+// A fork of so little is done by the planning CTA itself, unit after unit: one launch less.  One
+// child and its free, by the planning CTA / by a second kernel, in a graph and as calls:
+//   2 units (a pool and the table row), 64 KB pages    8.4 /  8.7 us    11.1 / 13.2 us
+//   3 units, 16 KB pages                               8.2    8.2       11.0   12.9
+//   3 units, 32 KB pages                               9.4    8.8       11.1   12.8
+//   3 units, 64 KB pages                              10.4    9.3       11.4   13.5
+//   5 units, 8 KB pages                                9.4    7.8       11.0   13.7
+//   9                                                 11.5    7.3       12.0   13.7
+//   15                                                15.8    8.4       16.4   13.8
+// so it stops where a graph, which saves no launch, would lose more than 0.6 us (units times the
+// page count as bytes).
+constexpr int kOwnUnits = 3;
+constexpr int kOwnBytes = 1 << 17;
 constexpr long long kMaxGrid = 1LL << 30;
 
 struct Pools {
