@@ -1,4 +1,8 @@
 """The rotation under autograd on the GPU: gradients against the transposed map in 64 bits."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,7 @@ from tests.test_gpu_rope import close, rows
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("inverse", [False, True])
@@ -140,3 +145,33 @@ def test_a_captured_forward_and_a_refused_gradient():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(back, want[1])
+
+
+def test_a_captured_gradient_beside_an_eager_graph():
+    """A backward pass under capture while an eager graph of the same leaf lives: refused as an
+    exception, and the process goes on.  In a process of its own."""
+    code = """
+import torch, paged_kv_block_gb300 as pkb
+table, _ = pkb.rope_frequencies(16)
+pos = torch.arange(9, dtype=torch.int32, device="cuda")
+x = torch.randn(9, 2, 16, device="cuda", requires_grad=True)
+eager = pkb.rotary_embedding(x, pos, table).sum()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    loss = pkb.rotary_embedding(x, pos, table).sum()
+    try:
+        loss.backward()
+    except ValueError as e:
+        print("refused:", "inverse=True" in str(e))
+    kept = pkb.rotary_embedding(x.detach(), pos, table)
+graph.replay()
+eager.backward()
+torch.cuda.synchronize()
+want = pkb.rotary_embedding(torch.ones_like(x), pos, table, inverse=True)
+print(torch.equal(x.grad, want), torch.equal(kept, pkb.rotary_embedding(x.detach(), pos, table)))
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    assert run.stdout.split("\n")[:2] == ["refused: True", "True True"], run.stdout
