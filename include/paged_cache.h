@@ -7,6 +7,9 @@
  *     the attention calls read                                  -> paged_append_run
  *   - which row owns which page: giving rows pages for new tokens, forking a row, freeing
  *     rows, compacting the live pages, copying pages            -> paged_cache_*_run
+ *   - keeping rows within a budget of tokens: adding up the attention weight that every token
+ *     receives, selecting the tokens to keep, cutting rows back to them
+ *                              -> paged_weights_run, paged_cache_select_run, paged_cache_evict_run
  *
  * The conventions of paged_attn.h hold: *_dev are device pointers, *_host host pointers; all
  * memory is the caller's and nothing is allocated; device work goes to `stream` and nothing
@@ -19,7 +22,7 @@
  * Status words.  A call with a workspace clears the status word at the workspace's start and
  * ORs in what it finds (paged_attn_workspace_status reads it); the workspace belongs to one
  * launch in flight at a time.  Every call takes status_dev too, as an argument or (extend, fork,
- * compact) in its params: a uint32 word that it ORs into and never clears, or NULL
+ * compact, evict) in its params: a uint32 word that it ORs into and never clears, or NULL
  * (paged_attn_workspace_status reads such a word as well).  In both, PAGED_ATTN_ERR_METADATA
  * means that an item broke its contract and was left out, PAGED_ATTN_ERR_CAPACITY that the free
  * pages did not suffice for every item, and PAGED_ATTN_ERR_TIMEOUT that a device wait ran out and
@@ -171,7 +174,8 @@ typedef struct paged_cache_params {
   int max_pages_per_request;  /* C                                                         */
   int page_size;              /* a multiple of 8, at most 128                              */
   int num_pages;              /* P <= 2^24                                                 */
-  uint32_t* status_dev;       /* extend, fork and compact OR their findings in; or NULL    */
+  uint32_t* status_dev;       /* extend, fork, compact and evict OR their findings in; or
+                                 NULL                                                      */
 } paged_cache_params;
 
 /* The pools of every layer, all with the same page ids; a page is below 2^31 bytes. */
@@ -240,6 +244,97 @@ int paged_cache_compact_run(const paged_cache_params* params, const paged_cache_
 int paged_cache_copy_run(const paged_cache_pools* src, const paged_cache_pools* dst,
                          const int32_t* src_pages_dev, const int32_t* dst_pages_dev, int n,
                          uint32_t* status_dev, void* stream);
+
+/* ---- keeping rows within a budget of tokens ---------------------------------------------------
+ * What the kept tokens of a row are may differ between layers and KV heads, how many there are may
+ * not: each (layer, KV head) keeps a list of its own, and its kept keys and values move to the
+ * row's first slots.  Keys keep the rotation of their old positions. */
+typedef struct paged_weights_params {
+  int batch;             /* B                                                             */
+  int num_qo_heads, num_kv_heads; /* G = Hq / Hkv <= 64                                    */
+  int head_dim;          /* D: 128 or 256                                                 */
+  int page_size;         /* a multiple of 8, at most 128                                  */
+  int num_pages;         /* P                                                             */
+  int combined_cache;    /* 1: [P, 2, Hkv, ps, D]; 0: a K pool [P, Hkv, ps, D]            */
+  int max_pages_per_request; /* C: columns of block_tables (unused with kv_indptr)        */
+  int seq_len_q;         /* fixed form: SQ queries per request                            */
+  int total_q;           /* rows of q and lse                                             */
+  int last_queries;      /* n > 0: only the last n queries of each request count; 0: all  */
+  int mask_type;         /* PAGED_ATTN_MASK_*, as the attention call had it               */
+  int width;             /* W: weights per (request, KV head)                             */
+  float sm_scale;        /* as the attention call had it; <= 0 selects 1 / sqrt(D)        */
+  float decay;           /* factor on the weights before the call                         */
+} paged_weights_params;
+
+/* Add up what the queries of an attention call look at: for each request b, KV head h and key j
+ *     weights[b, h, j] = decay * weights[b, h, j]
+ *                        + sum over counted queries i that see j, and the G query heads of h,
+ *                          of exp(sm_scale q[i, head] . k[j, h] - lse[i, head]),
+ * where the old weight of the tokens that the call's queries stand for, the last nq of a request
+ * with nq queries, is 0: their entries are written without being read, and so is every entry with
+ * decay = 0.  Entries past a request's length are left alone, and so is a request without queries.
+ *   q_dev [total_q, Hq, D] bf16 and lse_dev [total_q, Hq] fp32, natural logarithm: the attention
+ *   call's queries and its LSE (a row with an LSE of -inf sees nothing and adds nothing);
+ *   k_cache_dev: combined cache or K pool;
+ *   qo_indptr_dev [B + 1]: packed form, or NULL: the fixed form;
+ *   kv_indptr_dev [B + 1] with pages_dev (CSR), or NULL: pages_dev is block_tables [B, C];
+ *   weights_dev [B, Hkv, W] fp32.
+ * Scores, exponentials and sums are fp32, each sum in one order whatever the launch, so calls
+ * repeat bit for bit.  Keys past W or past the request's table entries get no weight, a key whose
+ * page id lies outside [0, num_pages) keeps its old one, and a request whose offsets do not lie in
+ * [0, total_q] is left out (metadata bit). */
+int paged_weights_run(const paged_weights_params* params, const void* q_dev, const float* lse_dev,
+                      const void* k_cache_dev, const int32_t* qo_indptr_dev,
+                      const int32_t* kv_indptr_dev, const int32_t* pages_dev,
+                      const int32_t* seq_lens_dev, float* weights_dev, uint32_t* status_dev,
+                      void* stream);
+
+typedef struct paged_cache_select_params {
+  int num_layers;        /* N: layers in weights                                          */
+  int rows;              /* R: rows of weights and seq_lens                               */
+  int num_kv_heads;      /* Hkv                                                           */
+  int width;             /* W: weights per (layer, row, KV head)                          */
+  int keep;              /* K >= 1: tokens to keep of each row                            */
+  int sink;              /* the first `sink` tokens are kept whatever their weight        */
+  int recent;            /* and the last `recent`; sink + recent <= keep                  */
+} paged_cache_select_params;
+
+/* kept_dev [N, n, Hkv, K]: for each layer, listed row and KV head the indices of the tokens to
+ * keep, in ascending order: the first `sink`, the last `recent`, and of the tokens between them
+ * those with the highest weights_dev [N, R, Hkv, W] (fp32), the lower index first among equal
+ * ones (0.0 and -0.0 are equal) and NaN below everything.  A row of at most K tokens keeps them
+ * all: its lists are 0, 1, .. followed by -1.  A row may be listed more than once.  Rows outside
+ * [0, R) and rows with a negative length or more than W tokens are left out: -1 everywhere
+ * (metadata bit).  Weights past a row's length are not read. */
+int paged_cache_select_run(const paged_cache_select_params* params, const int32_t* rows_dev, int n,
+                           const float* weights_dev, const int32_t* seq_lens_dev,
+                           int32_t* kept_dev, uint32_t* status_dev, void* stream);
+
+/* Cut each listed row of more than `keep` tokens back to `keep`: in every layer and KV head slot j
+ * gets token kept[layer, i, head, j] (key and value), and so does weights_dev[layer, row, head, j]
+ * where weights_dev [N, rows, Hkv, weights_width] (fp32) is given.  Rows of at most `keep` tokens
+ * stay as they are, whatever their lists hold.  The lists are ascending, kept_dev [N, n, Hkv,
+ * keep], as paged_cache_select_run writes them for the rows' present lengths.
+ * `sink`: the first `sink` entries of every list are 0, 1, .. sink - 1, so pages that lie wholly
+ * in them do not change and stay shared (0 is always right).  Any other page among the row's first
+ * ceil(keep / page_size) that other rows share is replaced by a fresh one (as in extend: the lowest
+ * free ids, item by item, in the order of the row); pages past them, and replaced ones, lose a
+ * count, and pages whose counts reach 0 this way are free after the call.  What the row's table
+ * holds past its new length, and slots past it in its last page, are kept.
+ * Left out (metadata bit): rows outside [0, rows), a row listed before, rows with ids outside the
+ * pool or more tokens than C pages or weights_width hold, lists whose first entry is negative or
+ * whose last one is not in [keep - 1, length).  A slot whose entry breaks the order (below the
+ * slot's own index, past the length, or another token's inside the `sink` pages) keeps what it
+ * holds (metadata bit); entries that are not ascending otherwise give a mixture of tokens.  A row
+ * for whose fresh pages the free ones do not suffice (counted as in extend) stays as it is
+ * (capacity bit).  n <= 4096. */
+size_t paged_cache_evict_workspace_size(int n, int keep, int page_size);
+int paged_cache_evict_run(const paged_cache_params* params, const paged_cache_pools* pools,
+                          const int32_t* rows_dev, int n, const int32_t* kept_dev, int keep,
+                          int sink, float* weights_dev, int weights_width,
+                          int32_t* block_tables_dev, int32_t* seq_lens_dev,
+                          int32_t* page_refs_dev, void* workspace_dev, size_t workspace_bytes,
+                          void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,582 @@
+// Keeping a row within a budget of tokens (include/paged_cache.h documents the contract): the
+// tokens to keep are selected by the attention weight that they received, and the rows are cut
+// back to them.
+#include "pages.cuh"
+
+namespace pa {
+namespace {
+
+// ---- select ------------------------------------------------------------------------------------
+// A list is the weights of one (layer, row, KV head).  Its tokens get 32-bit keys whose unsigned
+// order is the order of preference; three passes over the keys' digits (11, 11, 10 bits) find the
+// smallest key that is kept, T, and how many of the tokens with that key are; a last pass writes
+// the indices in order, the tokens at T in index order until their number is reached.
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+constexpr uint32_t kMustKeep = 0xffffffffu;
+constexpr int kSelectCluster = 8;
+constexpr int kMaxKeys = 40 * 1024;        // keys that a CTA holds in shared memory
+
+struct SelectArgs {
+  const int* rows;
+  int n, R, N, Hkv, W, K, sink, recent;
+  const float* weights;                    // [N, R, Hkv, W]
+  const int* lens;
+  int* kept;                               // [N, n, Hkv, K]
+  int held;                                // keys that fit into shared memory
+  uint32_t* status;
+};
+
+// Keys order floats, -0.0 as 0.0 and NaN below everything.
+__device__ __forceinline__ uint32_t weight_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ SelectArgs a) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ int hist[kBins];
+  __shared__ int warp_sums[32];
+  __shared__ int found[2];                 // digit of the threshold, tokens above it
+  __shared__ int totals[2];                // of this CTA: tokens above T, tokens at T
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), size = cl.num_blocks();
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int warps = threads >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int list = blockIdx.x / size;      // ((layer, item), head)
+  const int h = list % a.Hkv, li = list / a.Hkv, i = li % a.n, layer = li / a.n;
+  const int row = a.rows[i];
+  int* out = a.kept + static_cast<long long>(list) * a.K;
+  const bool known = row >= 0 && row < a.R;
+  const int L = known ? a.lens[row] : -1;
+  if (L < 0 || L > a.W) {                  // left out: no list
+    if (rank == 0 && tid == 0) report_error(a.status, kErrMetadata);
+    for (int j = rank * threads + tid; j < a.K; j += size * threads) out[j] = -1;
+    return;
+  }
+  if (L <= a.K) {                          // everything is kept
+    for (int j = rank * threads + tid; j < a.K; j += size * threads) out[j] = j < L ? j : -1;
+    return;
+  }
+  // This CTA's tokens [begin, begin + count), a whole number of warps' words in all but the last.
+  const int per = ((L + size - 1) / size + 31) / 32 * 32;
+  const int begin = min(rank * per, L), count = min(per, L - begin);
+  const float* w = a.weights + ((static_cast<long long>(layer) * a.R + row) * a.Hkv + h) * a.W;
+  const auto make_key = [&](int t) {       // of token begin + t
+    const int j = begin + t;
+    return j < a.sink || j >= L - a.recent ? kMustKeep : weight_key(w[j]);
+  };
+  const bool held = count <= a.held;
+  if (held)
+    for (int t = tid; t < count; t += threads) keys[t] = make_key(t);
+  const auto key = [&](int t) { return held ? keys[t] : make_key(t); };
+  uint32_t prefix = 0;                     // digits of T found so far
+  int need = a.K;                          // tokens still wanted among those with that prefix
+  for (int d = 0; d < kDigits; ++d) {
+    const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bits = d == 2 ? 10 : 11;
+    const uint32_t above = d == 0 ? 0u : ~0u << (shift + bits);
+    for (int b = tid; b < kBins; b += threads) hist[b] = 0;
+    __syncthreads();
+    for (int t = tid; t < count; t += threads) {
+      const uint32_t k = key(t);
+      if ((k & above) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
+    }
+    sync_cluster(cl);
+    // Bins from the top, kBins / threads of them per thread (at most 1024 threads, at least 256).
+    const int mine = kBins / threads;
+    int sum = 0, c[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      c[b] = 0;
+      if (b >= mine) break;
+      const int bin = kBins - 1 - (tid * mine + b);
+      for (int r = 0; r < size; ++r) c[b] += *cl.map_shared_rank(hist + bin, r);
+      sum += c[b];
+    }
+    int total;
+    int before = block_scan(sum, warp_sums, &total);
+    if (before < need && before + sum >= need) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b >= mine) break;
+        if (before < need && before + c[b] >= need) {
+          found[0] = kBins - 1 - (tid * mine + b);
+          found[1] = before;
+        }
+        before += c[b];
+      }
+    }
+    sync_cluster(cl);                      // found is set, and every CTA has read the histograms
+    prefix |= static_cast<uint32_t>(found[0]) << shift;
+    need -= found[1];
+    __syncthreads();
+  }
+  // need of the tokens with key T = prefix are kept, the first ones.  Each warp writes a run of its
+  // own: it counts, the counts are summed, it writes.
+  const int run = ((count + warps - 1) / warps + 31) / 32 * 32;
+  const int first = min(warp * run, count), last = min(first + run, count);
+  int gt = 0, eq = 0;
+  for (int t0 = first; t0 < last; t0 += 32) {
+    const uint32_t k = t0 + lane < last ? key(t0 + lane) : 0u;
+    const bool in = t0 + lane < last;
+    gt += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
+  }
+  int all_gt, all_eq;
+  int gt_before = block_scan(lane == 0 ? gt : 0, warp_sums, &all_gt);
+  int eq_before = block_scan(lane == 0 ? eq : 0, warp_sums, &all_eq);
+  gt_before = __shfl_sync(0xffffffffu, gt_before, 0);
+  eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
+  if (size > 1) {
+    if (tid == 0) {
+      totals[0] = all_gt;
+      totals[1] = all_eq;
+    }
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      gt_before += *cl.map_shared_rank(totals, r);
+      eq_before += *cl.map_shared_rank(totals + 1, r);
+    }
+    cluster_arrive();                      // no CTA ends while another reads its totals
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int t0 = first; t0 < last; t0 += 32) {
+    const bool in = t0 + lane < last;
+    const uint32_t k = in ? key(t0 + lane) : 0u;
+    const uint32_t g = __ballot_sync(0xffffffffu, in && k > prefix);
+    const uint32_t e = __ballot_sync(0xffffffffu, in && k == prefix);
+    const int eq_rank = eq_before + __popc(e & below);
+    const bool keep = in && (k > prefix || (k == prefix && eq_rank < need));
+    if (keep) out[gt_before + __popc(g & below) + min(eq_rank, need)] = begin + t0 + lane;
+    gt_before += __popc(g);
+    eq_before += __popc(e);
+  }
+  if (size > 1) cluster_wait();
+}
+
+// ---- evict -------------------------------------------------------------------------------------
+// Three kernels.  The first looks at every item: is it in order, and which of the pages that it
+// will write are shared and so need a fresh one.  The second hands out the fresh pages in order
+// (FreePages) and writes the new tables and lengths.  The third moves the tokens and gives the
+// pages back that the rows no longer name.
+constexpr int kThreads = 256;
+
+struct EvictArgs {
+  Pools pools;
+  int npools, segs;          // runs of tokens per page and pool: one per head, K and V
+  int per_layer;             // pools of a layer
+  long long page_bytes;
+  int seg_bytes, token_bytes;
+  const int* rows;
+  int n;
+  const int* kept;           // [N, n, Hkv, K]
+  int N, Hkv, K;
+  int first_page;            // pages before it keep their contents: sink / ps
+  int need_pages;            // Kp = ceil(K / ps)
+  float* weights;            // [N, R, Hkv, W] or null
+  int W;
+  int* tables;
+  int* lens;
+  int* refs;
+  int R, C, ps, P;
+  unsigned long long by_ps;  // ceil(2^64 / ps)
+  int4* items;               // workspace [n]: row, length (-1: left out), fresh pages needed
+  int* old;                  // workspace [n, Kp]: the row's first pages before the call
+  int* slots;                // workspace [n, Kp]: table columns of the pages to replace
+  int shift, slices;         // move: words of a token per unit (log2), units per token
+  Status status;
+};
+
+__device__ __forceinline__ int page_of(int token, unsigned long long by_ps) {
+  return static_cast<int>(__umul64hi(static_cast<unsigned>(token), by_ps));
+}
+
+__global__ void __launch_bounds__(kThreads) look_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int warp_sums[32];
+  const int tid = threadIdx.x, i = blockIdx.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int row = a.rows[i];
+  int L = row >= 0 && row < a.R ? a.lens[row] : -1;
+  bool bad = L < 0;
+  for (int k = tid; k < i; k += kThreads) bad |= a.rows[k] == row;
+  const int pages = bad ? 0 : static_cast<int>((L + a.ps - 1LL) / a.ps);
+  bad |= pages > a.C;
+  const bool cut = L > a.K;
+  if (cut && !bad) {
+    if (a.weights) bad |= L > a.W;
+    const int lists = a.N * a.Hkv;
+    for (int k = tid; k < lists; k += kThreads) {
+      const int layer = k / a.Hkv, h = k - layer * a.Hkv;
+      const int* list =
+          a.kept + ((static_cast<long long>(layer) * a.n + i) * a.Hkv + h) * a.K;
+      const int last = list[a.K - 1];
+      bad |= list[0] < 0 || last < a.K - 1 || last >= L;
+    }
+    const int* t = a.tables + static_cast<long long>(row) * a.C;
+    if (pages <= a.C)
+      for (int p = tid; p < pages; p += kThreads) bad |= t[p] < 0 || t[p] >= a.P;
+  }
+  bad = __syncthreads_or(bad);
+  int need = 0;
+  if (cut && !bad) {
+    const int* t = a.tables + static_cast<long long>(row) * a.C;
+    const long long at = static_cast<long long>(i) * a.need_pages;
+    for (int p0 = 0; p0 < a.need_pages; p0 += kThreads) {
+      const int p = p0 + tid;
+      bool shared = false;
+      if (p < a.need_pages) {
+        const int page = t[p];
+        a.old[at + p] = page;
+        shared = p >= a.first_page && a.refs[page] > 1;
+      }
+      int sum;
+      const int rank = need + block_scan(shared, warp_sums, &sum);
+      if (shared) a.slots[at + rank] = p;
+      need += sum;
+    }
+  }
+  if (tid == 0) a.items[i] = make_int4(row, bad ? -1 : L, need, 0);
+}
+
+// One cluster.  Every CTA sums the items' demands for itself; without any (rows whose pages are
+// their own) nobody looks at the pages.
+__global__ void __launch_bounds__(kPlanThreads)
+evict_plan_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ __align__(16) int shared[];
+  __shared__ int warp_sums[32];
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), size = cl.num_blocks();
+  const int tid = threadIdx.x, threads = blockDim.x;
+  int* off = shared;                       // [n] first fresh page of the item among all demands
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (rank == 0 && tid < 4) a.status.ws[tid] = 0;
+  int need[kPerThread], before[kPerThread], demand = 0;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = j * threads + tid;
+    if (j * threads >= a.n) break;
+    need[j] = i < a.n ? a.items[i].z : 0;
+    int sum;
+    before[j] = add_pages(demand, block_scan(need[j], warp_sums, &sum));
+    demand = add_pages(demand, sum);
+    if (i < a.n) off[i] = before[j];
+  }
+  FreePages pages;
+  pages.total = 0;
+  if (demand > 0) {
+    pages.count(a.refs, a.P, rank, size, off + a.n, [] {});
+    sync_cluster(cl);
+    pages.order(cl);
+    if (size > 1) cluster_arrive();
+  }
+  uint32_t bits = 0;
+  if (rank == 0) {
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = j * threads + tid;
+      if (j * threads >= a.n) break;
+      if (i >= a.n) continue;
+      const int4 it = a.items[i];
+      if (it.y < 0) bits |= kErrMetadata;
+      if (it.y <= a.K) continue;
+      if (need[j] == 0 || before[j] + need[j] <= pages.total) {
+        a.lens[it.x] = a.K;
+      } else {
+        bits |= kErrCapacity;
+        a.items[i].y = -1;
+      }
+    }
+    __syncthreads();                       // the word is cleared
+    if (bits) report(a.status, bits);
+  }
+  if (demand == 0) return;
+  __syncthreads();
+  const auto owner = [&](int k) {          // the last item with off <= k
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (off[mid] <= k) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  const int handed = demand <= pages.total ? demand : off[owner(pages.total)];
+  for (int j = 0; j < pages.own; ++j) {
+    if (pages.step_before[j * size + rank] >= handed) break;
+    pages.each(j, [&](int p, bool is_free, int k, int) {
+      if (!is_free || k >= handed) return;
+      const int i = owner(k);
+      const int slot = a.slots[static_cast<long long>(i) * a.need_pages + (k - off[i])];
+      a.tables[static_cast<long long>(a.items[i].x) * a.C + slot] = p;
+      a.refs[p] = 1;
+    });
+  }
+  if (size > 1) cluster_wait();
+}
+
+__device__ __forceinline__ uint4 ld_words(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// A unit is the tokens of one (item, pool, head), or a slice of their columns where that makes
+// more CTAs.  Lists are ascending, so token kept[j] lies at or behind slot j: a CTA that goes
+// through the slots in order, loads a tile of tokens, waits for all of its threads and then stores
+// it overwrites nothing that is still to be read.  16 words of 16 bytes per thread are in flight.
+constexpr int kWords = 16;
+__global__ void __launch_bounds__(kThreads, 2) move_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ __align__(16) long long offsets[];       // [2][source, target][tile]
+  const int tid = threadIdx.x;
+  const int tile = (kWords * kThreads) >> a.shift;           // tokens
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int per_pool = a.segs * a.slices, data = a.npools * per_pool;
+  const int lists = a.weights ? a.N * a.Hkv : 0;
+  const int per_item = data + lists + 1;
+  const long long units = static_cast<long long>(a.n) * per_item;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int i = static_cast<int>(u / per_item);
+    const int w = static_cast<int>(u - static_cast<long long>(i) * per_item);
+    const int4 item = a.items[i];
+    const int L = item.y;
+    if (L <= a.K) continue;
+    const int* now = a.tables + static_cast<long long>(item.x) * a.C;
+    const int* old = a.old + static_cast<long long>(i) * a.need_pages;
+    if (w == data + lists) {               // pages that the row no longer names
+      const int pages = static_cast<int>((L + a.ps - 1LL) / a.ps);
+      bool bad = false;
+      for (int p = a.first_page + tid; p < pages; p += kThreads) {
+        int page;
+        if (p < a.need_pages) {
+          page = old[p];
+          if (page == now[p]) continue;
+        } else {
+          page = now[p];
+        }
+        if (atomicSub(a.refs + page, 1) <= 0) {
+          atomicAdd(a.refs + page, 1);
+          bad = true;
+        }
+      }
+      if (bad) report(a.status, kErrMetadata);
+      continue;
+    }
+    if (w >= data) {                       // the weights of one layer and head
+      const int layer = (w - data) / a.Hkv, h = (w - data) - layer * a.Hkv;
+      const int* list = a.kept + ((static_cast<long long>(layer) * a.n + i) * a.Hkv + h) * a.K;
+      float* x = a.weights + ((static_cast<long long>(layer) * a.R + item.x) * a.Hkv + h) * a.W;
+      for (int j0 = 0; j0 < a.K; j0 += kWords * kThreads) {
+        float v[kWords];
+        uint32_t have = 0;
+#pragma unroll
+        for (int b = 0; b < kWords; ++b) {
+          const int j = j0 + b * kThreads + tid;
+          if (j >= a.K) break;
+          const int t = list[j];
+          if (t < j || t >= L) continue;
+          v[b] = x[t];
+          have |= 1u << b;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kWords; ++b)
+          if (have >> b & 1u) x[j0 + b * kThreads + tid] = v[b];
+        __syncthreads();
+      }
+      continue;
+    }
+    const int pool = w / per_pool, seg = (w - pool * per_pool) / a.slices;
+    const int slice = w % a.slices;
+    const int layer = pool / a.per_layer, h = seg % a.Hkv;
+    const int* list = a.kept + ((static_cast<long long>(layer) * a.n + i) * a.Hkv + h) * a.K;
+    uint8_t* base = static_cast<uint8_t*>(a.pools.p[pool]) +
+                    static_cast<long long>(seg) * a.seg_bytes;
+    const int words = a.token_bytes / 16;
+    int buf = 0;
+    bool bad = false;
+    for (int j0 = 0; j0 < a.K; j0 += tile, buf ^= 1) {
+      long long* from = offsets + buf * 2 * tile;
+      long long* to = from + tile;
+      for (int x = tid; x < tile; x += kThreads) {
+        const int j = j0 + x;
+        long long s = -1, d = 0;
+        if (j < a.K) {
+          const int t = list[j], q = page_of(j, a.by_ps);
+          if (t < j || t >= L || (q < a.first_page && t != j)) {
+            bad = true;
+          } else {
+            const int p = page_of(t, a.by_ps);
+            const int source = p < a.need_pages ? old[p] : now[p], target = now[q];
+            s = source * a.page_bytes + static_cast<long long>(t - p * a.ps) * a.token_bytes;
+            d = target * a.page_bytes + static_cast<long long>(j - q * a.ps) * a.token_bytes;
+            if (s == d) s = -1;            // it stays where it is
+          }
+        }
+        from[x] = s;
+        to[x] = d;
+      }
+      __syncthreads();
+      uint4 v[kWords];
+#pragma unroll
+      for (int b = 0; b < kWords; ++b) {
+        const int x = b * kThreads + tid, t = x >> a.shift;
+        const int word = (slice << a.shift) + (x & ((1 << a.shift) - 1));
+        if (word < words && from[t] >= 0) v[b] = ld_words(base + from[t] + word * 16);
+      }
+      __syncthreads();                     // the whole tile is read
+#pragma unroll
+      for (int b = 0; b < kWords; ++b) {
+        const int x = b * kThreads + tid, t = x >> a.shift;
+        const int word = (slice << a.shift) + (x & ((1 << a.shift) - 1));
+        if (word < words && from[t] >= 0)
+          *reinterpret_cast<uint4*>(base + to[t] + word * 16) = v[b];
+      }
+    }
+    if (bad) report(a.status, kErrMetadata);
+    __syncthreads();                       // the next unit writes the offsets anew
+  }
+}
+
+struct EvictLayout {
+  size_t status, items, old, slots, total;
+  EvictLayout(int n, int pages) {
+    Take t;
+    status = t.ints(4);
+    items = t.ints(4LL * n);
+    old = t.ints(static_cast<long long>(n) * pages);
+    slots = t.ints(static_cast<long long>(n) * pages);
+    total = t.off;
+  }
+};
+
+bool page_size_ok(int ps) { return ps >= 8 && ps <= 128 && ps % 8 == 0; }
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int paged_cache_select_run(const paged_cache_select_params* p, const int32_t* rows, int n,
+                           const float* weights, const int32_t* lens, int32_t* kept,
+                           uint32_t* status, void* stream) {
+  if (!p || n < 0 || p->num_layers <= 0 || p->rows < 0 || p->num_kv_heads <= 0 || p->width <= 0 ||
+      p->keep <= 0 || p->sink < 0 || p->recent < 0 || p->recent > p->keep - p->sink)
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (n == 0) return PAGED_ATTN_OK;
+  if (!rows || !weights || !lens || !kept || !ints_aligned(rows, weights, lens, kept, status))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  const long long lists = static_cast<long long>(p->num_layers) * n * p->num_kv_heads;
+  if (lists * kSelectCluster > kMaxGrid) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  const int sms = current_sm_count();
+  if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
+  SelectArgs a{};
+  a.rows = rows; a.n = n; a.R = p->rows; a.N = p->num_layers; a.Hkv = p->num_kv_heads;
+  a.W = p->width; a.K = p->keep; a.sink = p->sink; a.recent = p->recent;
+  a.weights = weights; a.lens = lens; a.kept = kept; a.status = status;
+  int size = 1;
+  while (size < kSelectCluster && lists * size * 2 <= sms && p->width / size > 2048) size *= 2;
+  const int per = (ceil_div(p->width, size) + 31) / 32 * 32;
+  a.held = per < kMaxKeys ? per : kMaxKeys;
+  const int threads = per <= 2048 ? 256 : (per <= 16384 ? 512 : 1024);
+  static std::atomic<uint64_t> ready{0};
+  if (!kernel_smem_ready(select_kernel, kMaxKeys * 4, ready)) return PAGED_ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = static_cast<unsigned>(lists * size);
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = a.held * 4;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  count_launches(1);
+  return cuda_status(cudaLaunchKernelEx(&cfg, select_kernel, a));
+}
+
+size_t paged_cache_evict_workspace_size(int n, int keep, int page_size) {
+  if (n < 0 || n > kMaxItems || keep <= 0 || !page_size_ok(page_size)) return 0;
+  return EvictLayout(n, (keep - 1) / page_size + 1).total;
+}
+
+int paged_cache_evict_run(const paged_cache_params* p, const paged_cache_pools* pools,
+                          const int32_t* rows, int n, const int32_t* kept, int keep, int sink,
+                          float* weights, int weights_width, int32_t* tables, int32_t* lens,
+                          int32_t* refs, void* ws, size_t ws_bytes, void* stream) {
+  if (!cache_params_ok(p) || !pools_ok(pools) || n < 0 || n > kMaxItems || keep <= 0 || sink < 0 ||
+      sink > keep)
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (pools->num_pages != p->num_pages || pools->page_size != p->page_size)
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (n > 0 && (!rows || !kept || !tables || !lens || !refs))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (weights && weights_width <= 0) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!ints_aligned(rows, kept, weights, tables, lens, refs) || !aligned_to(ws, 16))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  EvictArgs a{};
+  a.need_pages = (keep - 1) / p->page_size + 1;
+  const EvictLayout l(n, a.need_pages);
+  if (!ws || ws_bytes < l.total) return PAGED_ATTN_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n == 0) return cuda_status(cudaMemsetAsync(ws, 0, 4 * sizeof(uint32_t), st));
+  const int sms = current_sm_count();
+  if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
+  a.npools = pool_count(pools);
+  for (int i = 0; i < a.npools; ++i) a.pools.p[i] = pools->pools_host[i];
+  a.per_layer = pools->combined_cache ? 1 : 2;
+  a.segs = (pools->combined_cache ? 2 : 1) * pools->num_kv_heads;
+  a.page_bytes = page_bytes(pools);
+  a.seg_bytes = static_cast<int>(seg_bytes(pools));
+  a.token_bytes = 2 * pools->head_dim;
+  a.rows = rows; a.n = n; a.kept = kept;
+  a.N = pools->num_layers; a.Hkv = pools->num_kv_heads; a.K = keep;
+  a.first_page = sink / p->page_size;
+  a.weights = weights; a.W = weights_width;
+  a.tables = tables; a.lens = lens; a.refs = refs;
+  a.R = p->rows; a.C = p->max_pages_per_request; a.ps = p->page_size; a.P = p->num_pages;
+  a.by_ps = ~0ull / static_cast<unsigned>(a.ps) + 1;         // ceil(2^64 / ps): ps is even
+  a.items = reinterpret_cast<int4*>(at(ws, l.items));
+  a.old = at(ws, l.old);
+  a.slots = at(ws, l.slots);
+  a.status = {reinterpret_cast<uint32_t*>(at(ws, l.status)), p->status_dev};
+  // Slices of a token's columns: whole tokens where there are CTAs enough, never under 32 bytes.
+  const int words = pools->head_dim / 8;
+  int shift = 1;
+  while ((1 << shift) < words) ++shift;
+  const long long runs = static_cast<long long>(n) * a.npools * a.segs;
+  while (shift > 1 && runs * ceil_div(words, 1 << shift) < 2LL * sms) --shift;
+  a.shift = shift;
+  a.slices = ceil_div(words, 1 << shift);
+  count_launches(1);
+  cudaError_t e = launch_after_previous(look_kernel, n, kThreads, 0, st, a);
+  if (e != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  e = launch_plan(evict_plan_kernel, a, a.P, 4, n, n, ready, st);
+  if (e != cudaSuccess) return PAGED_ATTN_ERR_CUDA;
+  const long long units =
+      n * (static_cast<long long>(a.npools) * a.segs * a.slices +
+           (weights ? static_cast<long long>(a.N) * a.Hkv : 0) + 1);
+  const int tile = (kWords * kThreads) >> shift;
+  static std::atomic<uint64_t> move_ready{0};
+  if (!kernel_smem_ready(move_kernel, 4 * 8 * ((kWords * kThreads) >> 1), move_ready))
+    return PAGED_ATTN_ERR_CUDA;
+  count_launches(1);
+  return cuda_status(launch_after_previous(move_kernel,
+                                           static_cast<int>(units < kMaxGrid ? units : kMaxGrid),
+                                           kThreads, 4 * 8 * tile, st, a));
+}
+
+}  // extern "C"
