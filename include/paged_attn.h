@@ -8,7 +8,8 @@
  *   - packed-Q dense / causal / sliding-window prefill over separate HND page pools with
  *     a row-strided page table   -> paged_prefill_run
  *   - decode over a CSR-paged cache (one, SQ fixed or packed queries per request) with
- *     split-KV partials and a merge -> paged_decode_run
+ *     split-KV partials and a merge -> paged_decode_run; for requests that share a prefix
+ *     -> paged_decode_shared_run
  *   - block-sparse attention on prequantized inputs (int8 Q/K, FP8 E4M3 V, fp32 scales)
  *     -> paged_sage_run
  * The bitmap form also takes its selection as index rows (PAGED_ATTN_FORM_INDEXED).  The
@@ -267,6 +268,31 @@ int paged_decode_run(const paged_decode_params* params, const void* query_dev,
                      const int32_t* kv_indices_dev, const int32_t* seq_lens_dev,
                      const int32_t* qo_indptr_dev, void* out_dev, float* lse_dev,
                      void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* ---- decode for requests that share a prefix ----------------------------------------------
+ * paged_decode_run for a batch in which groups of consecutive requests start with the same
+ * tokens (samples of one prompt, as paged_cache_fork_run makes them, or questions behind one
+ * system prompt): the prefix's keys and values are read once per group instead of once per
+ * request, as one matrix of all the group's queries.  Same arguments and results as
+ * paged_decode_run, with three differences:
+ *   - the fixed query forms only, G x SQ <= 64, window_left = -1 and split_chunk = 0;
+ *   - group_indptr_dev [num_groups + 1], non-decreasing, in [0, B]: group g is the requests
+ *     group_indptr[g] .. group_indptr[g + 1]; requests in no group share nothing.  Offsets that
+ *     break this set the metadata status bit, and then nothing is shared (the outputs hold);
+ *   - prefix_lens_dev [num_groups]: the first prefix_lens[g] keys and values of group g's
+ *     requests are the same, wherever their pages lie; they are read from the pages of the
+ *     group's first request.  Any length: what some member's queries do not all see (past its
+ *     own length, or under the causal mask past its first query) is left to the requests
+ *     themselves.
+ * A length of 0 is allowed (0 / -inf).  The outputs differ from paged_decode_run's by the
+ * rounding of the fp32 merge and of the probabilities alone. */
+size_t paged_decode_shared_workspace_size(const paged_decode_params* params, int num_groups);
+int paged_decode_shared_run(const paged_decode_params* params, int num_groups,
+                            const void* query_dev, const void* k_dev, const void* v_dev,
+                            const int32_t* kv_indptr_dev, const int32_t* kv_indices_dev,
+                            const int32_t* seq_lens_dev, const int32_t* group_indptr_dev,
+                            const int32_t* prefix_lens_dev, void* out_dev, float* lse_dev,
+                            void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /* ---- [SAGE] prequantized block-sparse attention ---------------------------------------
  * bsa_attn_sm120_blk64_sage_fwd computes block-sparse attention on dequantized inputs:

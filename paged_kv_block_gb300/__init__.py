@@ -111,6 +111,9 @@ _EXPORTS = {
     "paged_decode_split_chunk": (C.c_int, [C.POINTER(DecodeParams)]),
     "paged_decode_run": (C.c_int, [C.POINTER(DecodeParams)] + [C.c_void_p] * 10
                          + [C.c_size_t, C.c_void_p]),
+    "paged_decode_shared_workspace_size": (C.c_size_t, [C.POINTER(DecodeParams), C.c_int]),
+    "paged_decode_shared_run": (C.c_int, [C.POINTER(DecodeParams), C.c_int] + [C.c_void_p] * 11
+                                + [C.c_size_t, C.c_void_p]),
     "paged_attn_plan_layout_of": (C.c_int, [C.POINTER(AttnParams), C.POINTER(PlanLayout)]),
     "paged_prefill_plan_layout_of": (C.c_int, [C.POINTER(PrefillParams), C.POINTER(PlanLayout)]),
     "paged_decode_plan_layout_of": (C.c_int, [C.POINTER(DecodeParams), C.POINTER(PlanLayout)]),
@@ -253,6 +256,24 @@ def paged_decode_run(params: DecodeParams, query, k, v, kv_indptr, kv_indices, s
                                   _dev(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _stream(stream)),
            "paged_decode_run")
+
+
+def paged_decode_shared_workspace_size(params: DecodeParams, num_groups: int) -> int:
+    return int(lib().paged_decode_shared_workspace_size(C.byref(params), int(num_groups)))
+
+
+def paged_decode_shared_run(params: DecodeParams, query, k, v, kv_indptr, kv_indices, seq_lens,
+                            group_indptr, prefix_lens, out, lse, workspace, stream=None) -> None:
+    _check(lib().paged_decode_shared_run(C.byref(params), prefix_lens.numel(), _dev(query, "query"),
+                                         _dev(k, "k"), _dev(v, "v"), _dev(kv_indptr, "kv_indptr"),
+                                         _dev(kv_indices, "kv_indices"),
+                                         _dev(seq_lens, "seq_lens"),
+                                         _dev(group_indptr, "group_indptr"),
+                                         _dev(prefix_lens, "prefix_lens"), _dev(out, "out"),
+                                         _dev(lse, "lse"), _dev(workspace, "workspace"),
+                                         workspace.numel() * workspace.element_size(),
+                                         _stream(stream)),
+           "paged_decode_shared_run")
 
 
 def plan_layout(params) -> PlanLayout:
@@ -481,6 +502,60 @@ def batch_decode_with_paged_kv_cache(query, kv_cache, workspace_buffer, paged_kv
         workspace_buffer = _workspace(paged_decode_workspace_size(params), query.device)
     paged_decode_run(params, query, k, v, paged_kv_indptr, paged_kv_indices, seq_lens, out, lse,
                      workspace_buffer, stream, qo_indptr=qo_indptr)
+    return out, lse
+
+
+def shared_prefix_workspace_size(query, kv_cache, max_seq_len, num_groups, *, seq_len_q=1) -> int:
+    """Workspace bytes of batch_decode_with_shared_prefix."""
+    return paged_decode_shared_workspace_size(
+        decode_params(query, kv_cache, max_seq_len, seq_len_q=seq_len_q), num_groups)
+
+
+def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_indptr,
+                                    paged_kv_indices, seq_lens, max_seq_len, group_indptr,
+                                    prefix_lens, *, seq_len_q=1, bmm1_scale=None, bmm2_scale=1.0,
+                                    out=None, out_dtype=None, lse=None, mask_type="dense",
+                                    kv_layout="HND", stream=None):
+    """batch_decode_with_paged_kv_cache for groups of consecutive requests that start with the
+    same tokens; returns (out, lse).  Group g is the requests group_indptr[g] ..
+    group_indptr[g + 1], whose first prefix_lens[g] keys and values are equal: they are read
+    once, from the pages of the group's first request.  group_indptr [groups + 1] and prefix_lens
+    [groups] are int32; requests outside every group share nothing.  query is [B, Hq, D] or [B, SQ,
+    Hq, D]."""
+    dev = _cache._device()
+    if kv_layout != "HND":
+        raise ValueError("only the HND layout is supported")
+    out_dtype = _out_dtype(out_dtype, out, query)
+    _cache._geometry(kv_cache, dev)
+    k, v, _, _, _, _, D = _pools(kv_cache)
+    B, groups = query.shape[0], _cache._count(prefix_lens, "prefix_lens")
+    if query.dtype != torch.bfloat16 or query.shape[-1] != D:
+        raise ValueError("query must be bf16 with the cache's columns")
+    params = decode_params(query, kv_cache, max_seq_len, bmm1_scale=bmm1_scale,
+                           bmm2_scale=bmm2_scale, mask_type=mask_type, seq_len_q=seq_len_q,
+                           out_dtype=out_dtype)
+    _cache._on_device(query, dev, "query")
+    _cache._ints_of(paged_kv_indptr, dev, "paged_kv_indptr", B + 1)
+    _cache._ints(paged_kv_indices, dev, "paged_kv_indices")
+    _cache._ints_of(seq_lens, dev, "seq_lens", B)
+    _cache._ints_of(group_indptr, dev, "group_indptr", groups + 1)
+    _cache._ints(prefix_lens, dev, "prefix_lens")
+    if out is None:
+        out = _cache._new(query.shape, out_dtype, query.device, stream)
+    elif out.shape != query.shape:
+        raise ValueError("out must have query's shape")
+    _cache._on_device(out, dev, "out")
+    if lse is not None:
+        _cache._on_device(lse, dev, "lse")
+        if lse.shape != query.shape[:-1] or lse.dtype != torch.float32:
+            raise ValueError("lse must be float32, one value per query and head")
+    if workspace_buffer is None:
+        workspace_buffer = _cache._new(
+            max(paged_decode_shared_workspace_size(params, groups), 256), torch.uint8,
+            query.device, stream)
+    _cache._on_device(workspace_buffer, dev, "workspace_buffer")
+    paged_decode_shared_run(params, query, k, v, paged_kv_indptr, paged_kv_indices, seq_lens,
+                            group_indptr, prefix_lens, out, lse, workspace_buffer, stream)
     return out, lse
 
 

@@ -331,6 +331,55 @@ SageLayout sage_layout(const paged_sage_params* p) {
   return g;
 }
 
+// ---- decode with shared prefixes ----------------------------------------------------------
+struct SharedLayout {
+  size_t status, n_tiles, counter, prefix_of, refs, tiles, split_off, items, order;
+  size_t pre_lse, pre_o, tail_lse, tail_o, total;
+  int tile_capacity, item_capacity;
+};
+
+// The decode forms with a fixed number of queries and without a window (most of a long prefix
+// lies outside a window); units of at most kDecodeMaxRows rows.
+bool shared_params_ok(const paged_decode_params* p, int num_groups) {
+  if (!decode_params_ok(p) || decode_packed(p) || p->window_left >= 0 || p->split_chunk != 0)
+    return false;
+  if (num_groups < 0) return false;
+  const int G = p->num_qo_heads / p->num_kv_heads;
+  if (static_cast<long long>(G) * decode_q_per_item(p) > kDecodeMaxRows) return false;
+  // the capacities below stay below 2^31 tiles and items
+  return static_cast<long long>(p->batch) * decode_q_per_item(p) * p->num_kv_heads < (1LL << 27);
+}
+
+// Capacities bound what the plan's rules can give (prefix.cu): the key parts of a group's tiles are
+// as many as its tiles plus its share of one part per SM; a tail's splits one plus its share of 16
+// per SM.
+SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
+  SharedLayout s{};
+  Layout l;
+  const int G = p->num_qo_heads / p->num_kv_heads, SQ = decode_q_per_item(p), B = p->batch;
+  const int sms = num_sms(), pairs = num_groups < B / 2 ? num_groups : B / 2;
+  s.tile_capacity =
+      pairs == 0 ? 0 : sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
+  s.item_capacity = 16 * sms + p->num_kv_heads * B;
+  s.status = l.take(sizeof(uint32_t) * 4);
+  s.n_tiles = l.take(sizeof(int));
+  s.counter = l.take(sizeof(int));
+  s.prefix_of = l.take(sizeof(int) * static_cast<size_t>(B));
+  s.refs = l.take(sizeof(PrefixRef) * static_cast<size_t>(B));
+  s.tiles = l.take(sizeof(TileRec) * static_cast<size_t>(s.tile_capacity));
+  s.split_off = l.take(sizeof(int) * (static_cast<size_t>(B) + 1));
+  s.items = l.take(sizeof(SplitItem) * static_cast<size_t>(s.item_capacity));
+  s.order = l.take(sizeof(int) * static_cast<size_t>(s.item_capacity));
+  const size_t tile_rows = static_cast<size_t>(s.tile_capacity) * 2 * kMTileRows;
+  const size_t tail_rows = static_cast<size_t>(s.item_capacity) * G * SQ;
+  s.pre_lse = l.take(sizeof(float) * tile_rows);
+  s.pre_o = l.take(sizeof(float) * tile_rows * p->head_dim);
+  s.tail_lse = l.take(sizeof(float) * tail_rows);
+  s.tail_o = l.take(sizeof(float) * tail_rows * p->head_dim);
+  s.total = l.off;
+  return s;
+}
+
 // Scales of the prequantized form (see AttnLaunch).
 struct ScaleSet {
   const float* q_scale;
@@ -877,6 +926,150 @@ int paged_decode_run(const paged_decode_params* p, const void* query, const void
   a.window_left = p->window_left;
   a.timer_token = nullptr;
   return launch_decode(a, st) == 0 ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA;
+}
+
+size_t paged_decode_shared_workspace_size(const paged_decode_params* p, int num_groups) {
+  if (!shared_params_ok(p, num_groups)) return 0;
+  return shared_layout(p, num_groups).total;
+}
+
+int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const void* query,
+                            const void* k, const void* v, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, const int32_t* seq_lens,
+                            const int32_t* group_indptr, const int32_t* prefix_lens, void* out,
+                            float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!shared_params_ok(p, num_groups)) return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(query) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(ws))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  const auto misaligned = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 3) != 0; };
+  if (misaligned(kv_indptr) || misaligned(kv_indices) || misaligned(seq_lens) ||
+      misaligned(group_indptr) || misaligned(prefix_lens) || misaligned(lse))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  const SharedLayout s = shared_layout(p, num_groups);
+  if (!ws || ws_bytes < s.total) return PAGED_ATTN_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t* status = at<uint32_t>(ws, s.status);
+  if (p->batch == 0)
+    return cudaMemsetAsync(status, 0, 4 * sizeof(uint32_t), st) == cudaSuccess
+               ? PAGED_ATTN_OK
+               : PAGED_ATTN_ERR_CUDA;
+  if (!query || !k || !kv_indptr || !kv_indices || !seq_lens || !out ||
+      (!p->combined_cache && !v) || (num_groups > 0 && (!group_indptr || !prefix_lens)))
+    return PAGED_ATTN_ERR_INVALID_ARGUMENT;
+  const int Hq = p->num_qo_heads, Hkv = p->num_kv_heads, G = Hq / Hkv, ps = p->page_size;
+  const int D = p->head_dim, SQ = decode_q_per_item(p), q_rows = p->batch * SQ;
+  const void* vp = p->combined_cache ? k : v;
+  const int page_rows = (p->combined_cache ? 2 : 1) * Hkv * ps;
+  const int v_head_off = p->combined_cache ? Hkv * ps : 0;
+  const long long pool_rows = static_cast<long long>(p->num_pages) * page_rows;
+  const float scale =
+      p->bmm1_scale > 0.f ? p->bmm1_scale : 1.0f / std::sqrt(static_cast<float>(D));
+  AttnLaunch t{};
+  CUtensorMap kmap, vmap, qmap;
+  if (!encode_q_map(&t.qmap, query, q_rows, Hq, D, G, sub_tile_tokens(G)) ||
+      !encode_rows_map(&t.kmap, k, pool_rows, D, page_piece_rows(ps, kKvTile)) ||
+      !encode_rows_map(&t.vmap, vp, pool_rows, D, page_piece_rows(ps, kKvTile)) ||
+      !encode_rows_map(&kmap, k, pool_rows, D, page_piece_rows(ps, 64)) ||
+      !encode_rows_map(&vmap, vp, pool_rows, D, page_piece_rows(ps, 64)) ||
+      !encode_q_map(&qmap, query, q_rows, Hq, D, G, SQ))
+    return PAGED_ATTN_ERR_CUDA;
+  SharedLaunch m{};
+  m.lens = seq_lens;
+  m.group_indptr = group_indptr;
+  m.prefix_lens = prefix_lens;
+  m.B = p->batch;
+  m.Hq = Hq;
+  m.Hkv = Hkv;
+  m.G = G;
+  m.SQ = SQ;
+  m.groups = num_groups;
+  m.causal = p->mask_type == PAGED_ATTN_MASK_CAUSAL;
+  m.target = num_sms();
+  m.prefix_of = at<int>(ws, s.prefix_of);
+  m.refs = at<PrefixRef>(ws, s.refs);
+  m.tiles = at<TileRec>(ws, s.tiles);
+  m.n_tiles = at<int>(ws, s.n_tiles);
+  m.tile_capacity = s.tile_capacity;
+  m.split_offset = at<int>(ws, s.split_off);
+  m.items = at<SplitItem>(ws, s.items);
+  m.order = at<int>(ws, s.order);
+  m.item_capacity = s.item_capacity;
+  m.work_counter = at<int>(ws, s.counter);
+  m.status = status;
+  m.pre_o = at<float>(ws, s.pre_o);
+  m.pre_lse = at<float>(ws, s.pre_lse);
+  m.tail_o = at<float>(ws, s.tail_o);
+  m.tail_lse = at<float>(ws, s.tail_lse);
+  m.out = out;
+  m.out_dtype = p->out_dtype;
+  m.lse = lse;
+  m.out_scale = p->bmm2_scale;
+  if (launch_shared_plan(m, st)) return PAGED_ATTN_ERR_CUDA;
+  if (s.tile_capacity > 0) {
+    t.tiles = m.tiles;
+    t.n_tiles = m.n_tiles;
+    t.capacity = s.tile_capacity;
+    t.pt = kv_indices;
+    t.pt_indptr = kv_indptr;
+    t.seq_lens = m.prefix_of;
+    t.q_len = SQ;
+    t.kv_block_size = kKvTile;
+    t.out = at<float>(ws, s.pre_o);
+    t.out_dtype = kOutF32;
+    t.lse = at<float>(ws, s.pre_lse);
+    t.status = status;
+    t.Hq = Hq;
+    t.Hkv = Hkv;
+    t.G = G;
+    t.D = D;
+    t.page_size = ps;
+    t.page_rows = page_rows;
+    t.v_head_off = v_head_off;
+    t.num_pages = p->num_pages;
+    t.window_left = -1;
+    t.scale_log2 = scale * kLog2e;
+    t.out_scale = 1.f;
+    t.parts = 1;
+    void* tok;
+    timer_begin(st, &tok);
+    const int rc = launch_attn(t, st);
+    timer_end(st, tok);
+    if (rc != 0) return PAGED_ATTN_ERR_CUDA;
+  }
+  DecodeLaunch d{};
+  d.kmap = &kmap;
+  d.vmap = &vmap;
+  d.qmap = &qmap;
+  d.work_counter = m.work_counter;
+  d.q_len = SQ;
+  d.q_rows = q_rows;
+  d.rows = G * SQ;
+  d.nrb = d.rows <= 16 ? 1 : (d.rows <= 32 ? 2 : 4);
+  d.causal = m.causal;
+  d.kv_indptr = kv_indptr;
+  d.kv_indices = kv_indices;
+  d.seq_lens = seq_lens;
+  d.split_offset = m.split_offset;
+  d.items = m.items;
+  d.order = m.order;
+  d.part_o = at<float>(ws, s.tail_o);
+  d.part_lse = at<float>(ws, s.tail_lse);
+  d.status = status;
+  d.B = p->batch;
+  d.Hq = Hq;
+  d.Hkv = Hkv;
+  d.D = D;
+  d.page_size = ps;
+  d.page_rows = page_rows;
+  d.v_head_off = v_head_off;
+  d.num_pages = p->num_pages;
+  d.capacity = s.item_capacity;
+  d.scale_log2 = scale * kLog2e;
+  d.out_scale = 1.f;
+  d.window_left = -1;
+  d.parts_only = 1;
+  if (launch_decode(d, st) != 0) return PAGED_ATTN_ERR_CUDA;
+  return launch_shared_merge(m, st) == 0 ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA;
 }
 
 int paged_attn_plan_layout_of(const paged_attn_params* p, paged_attn_plan_layout* o) {

@@ -166,7 +166,9 @@ __device__ __forceinline__ int piece_key(const AttnLaunch& a, const TileInfo<CK>
 
 // SCALED: the prequantized form, whose scores carry a scale per query group and per key
 // block and whose output carries a scale per channel (all positive).
-template <int CK, bool FACTS, bool SCALED>
+// PART: a tile's keys are a part of its rows' keys; row m of sub-tile w goes to row 256 pad + 128 w +
+// m of out and lse, pad being the last field of the tile's record.
+template <int CK, bool FACTS, bool SCALED, bool PART>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, AttnLaunch a) {
@@ -821,7 +823,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       if (has_nx) request_lengths(a, rec_nx.b, L_nx, nq_nx);
       const int head = t.rec.g * G + (m % G);
-      const long long orow = static_cast<long long>(t.rec.q_row0 + w * TM + m / G) * a.Hq + head;
+      const long long orow =
+          PART ? static_cast<long long>(t.rec.pad) * (2 * kMTileRows) + w * kMTileRows + m
+               : static_cast<long long>(t.rec.q_row0 + w * TM + m / G) * a.Hq + head;
       const float inv = l_run > 0.f ? a.out_scale / l_run : 0.f;
       // the whole O row in flight at once; O_w is then free for the next tile's PV
       uint32_t ov[kD];
@@ -890,10 +894,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   }
 }
 
-template <int CK, bool FACTS, bool SCALED = false>
+template <int CK, bool FACTS, bool SCALED = false, bool PART = false>
 int launch_ck(const AttnLaunch& a, cudaStream_t st) {
   static std::atomic<uint64_t> smem_set{0};
-  if (!kernel_smem_ready(attn_tc_kernel<CK, FACTS, SCALED>, kSmemBytes, smem_set)) return -1;
+  constexpr auto kernel = attn_tc_kernel<CK, FACTS, SCALED, PART>;
+  if (!kernel_smem_ready(kernel, kSmemBytes, smem_set)) return -1;
   const int sms = current_sm_count();
   if (sms <= 0) return -1;
   const int grid = a.capacity < sms ? a.capacity : sms;
@@ -902,10 +907,10 @@ int launch_ck(const AttnLaunch& a, cudaStream_t st) {
   // programmatic, the long block-sparse step got 3.6% slower.
   cudaError_t e;
   if constexpr (!FACTS) {
-    e = launch_after_previous(attn_tc_kernel<CK, FACTS, SCALED>, dim3(grid), dim3(kThreads),
-                              kSmemBytes, st, a.qmap, a.kmap, a.vmap, a);
+    e = launch_after_previous(kernel, dim3(grid), dim3(kThreads), kSmemBytes, st, a.qmap, a.kmap,
+                              a.vmap, a);
   } else {
-    attn_tc_kernel<CK, FACTS, SCALED><<<grid, kThreads, kSmemBytes, st>>>(a.qmap, a.kmap, a.vmap, a);
+    kernel<<<grid, kThreads, kSmemBytes, st>>>(a.qmap, a.kmap, a.vmap, a);
     e = cudaSuccess;
   }
   count_launches(1);
@@ -916,6 +921,10 @@ int launch_ck(const AttnLaunch& a, cudaStream_t st) {
 
 int launch_attn(const AttnLaunch& a, cudaStream_t st) {
   if (a.capacity <= 0) return 0;
+  if (a.parts) {                                 // dense tiles over parts of their rows' keys
+    if (a.block_sparse || a.valid_bits || a.k_scale || a.out_dtype != kOutF32) return -2;
+    return launch_ck<128, false, false, true>(a, st);
+  }
   if (a.k_scale) {                               // the prequantized form: 64-key blocks only
     if (!a.block_sparse || attn_sub_chunk(a.kv_block_size, true) != 64 || !a.q_scale ||
         !a.v_scale || a.q_scale_group <= 0)

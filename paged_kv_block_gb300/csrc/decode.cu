@@ -608,7 +608,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         const float on = Lsum > 0.f ? acc / Lsum : 0.f;
         const float lse_nat = Lsum > 0.f ? (Mx + fast_log2(Lsum)) * kLn2 : -INFINITY;
-        if (n_split == 1) {
+        if (n_split == 1 && !a.parts_only) {
           const int qrow = q_row0 + m / G;
           if (qrow < 0 || qrow >= a.q_rows) continue;
           const long long orow = static_cast<long long>(qrow) * a.Hq + g * G + m % G;
@@ -620,7 +620,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
           if (d == 0) a.part_lse[prow] = lse_nat;
         }
       }
-      if (n_split > 1) {
+      if (n_split > 1 && !a.parts_only) {
         // the fence, the split counter and, for the last split of (b, g), the merge run on the
         // merge warp, so the consumers go on to the next item at once
         named_bar(1, kConsumerWarps * 32);         // every partial of this item is written

@@ -187,9 +187,45 @@ struct DecodeLaunch {
   int capacity;              // launched work items
   float scale_log2, out_scale;
   int window_left;
+  int parts_only;            // 1: every item writes its partial and nothing is merged
   void* timer_token;
 };
 int launch_decode(const DecodeLaunch& a, cudaStream_t st);
+
+// ---- shared prefixes (prefix.cu) -----------------------------------------------------------------
+// A request's prefix partials: rows 256 (base + (head * row_tiles + tile) * splits + s) of the
+// tensor-core kernel's partial output, s < splits; its queries are tokens from `token` on among
+// the group's, 256 / G of them to a tile.
+struct PrefixRef {
+  int base, splits, row_tiles, token;
+};
+struct SharedLaunch {
+  const int* lens;
+  const int* group_indptr;   // [groups + 1]
+  const int* prefix_lens;    // [groups]
+  int B, Hq, Hkv, G, SQ, groups, causal, target;
+  // plan
+  int* prefix_of;            // [B] shared keys of the request, 0 none
+  PrefixRef* refs;           // [B]
+  TileRec* tiles;            // tiles of the prefixes, *n_tiles of them
+  int* n_tiles;
+  int tile_capacity;
+  int* split_offset;         // [B + 1] splits of the tails
+  SplitItem* items;
+  int* order;
+  int item_capacity;         // items of all KV heads
+  int* work_counter;
+  uint32_t* status;
+  // merge
+  const float *pre_o, *pre_lse;    // [256 tiles, 128], [256 tiles]
+  const float *tail_o, *tail_lse;  // [items, SQ G, 128], [items, SQ G]
+  void* out;
+  int out_dtype;
+  float* lse;
+  float out_scale;
+};
+int launch_shared_plan(const SharedLaunch& a, cudaStream_t st);
+int launch_shared_merge(const SharedLaunch& a, cudaStream_t st);
 
 // Benchmark hooks (api.cu): count kernel launches; bracket the main kernel with events.
 void count_launches(int n);
@@ -220,6 +256,7 @@ struct AttnLaunch {
   int Hq, Hkv, G, D, page_size, page_rows, k_head_off, v_head_off, num_pages;
   int causal, window_left;
   float scale_log2, out_scale;
+  int parts;                 // 1: fp32 partial outputs by tile (row 256 pad + 128 w + m), not by row
   // Prequantized form (all nullptr otherwise): score scale q_scale[b * q_scale_stride +
   // token / q_scale_group] * k_scale[b * k_scale_stride + key / kv_block_size], output column
   // d scaled by v_scale[b * v_scale_stride + d]; every scale positive.

@@ -1,0 +1,278 @@
+// Decode attention for requests that share a prefix (include/paged_attn.h documents the contract):
+// the plan and the final merge.  The prefix of a group is attended once for all of its rows (query,
+// head) by the tensor-core kernel, its keys split over CTAs; what each request has of its own by
+// the split-KV decode kernel; both leave normalised fp32 partials with their log-sum-exp.
+#include <climits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kD = 128;
+constexpr int kTailSplits = 16;            // tail items aimed at per SM
+
+__device__ __forceinline__ int warp_inclusive(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += y;
+  }
+  return v;
+}
+// Exclusive prefix sum over the CTA of 1024 threads.
+__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = warp_inclusive(x);
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  const int w = warp_inclusive(warp_sums[lane]);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  __syncthreads();
+  return (warp > 0 ? before : 0) + v - x;
+}
+__device__ __forceinline__ long long block_sum(long long x, long long* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  if (lane == 0) warp_sums[warp] = x;
+  __syncthreads();
+  long long s = warp_sums[lane];
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  __syncthreads();
+  return s;
+}
+
+// Keys of request b that all of its queries see, at most.
+__device__ __forceinline__ int visible_to_all(const SharedLaunch& a, int b) {
+  const int L = max(a.lens[b], 0);
+  return a.causal ? max(L - a.SQ + 1, 0) : L;
+}
+__device__ __forceinline__ int tail_base(int prefix) { return prefix / 128 * 128; }
+
+// One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
+// sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts for about
+// `target` CTAs.  Requests: what is left, split as decode splits it.
+__global__ void __launch_bounds__(kThreads)
+shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
+  __shared__ int warp_sums[32];
+  __shared__ long long wide_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (tid < 4) a.status[tid] = 0;
+  if (tid == 0) *a.work_counter = 0;
+  bool bad = false;
+  for (int g = tid; g <= a.groups; g += kThreads) {
+    const int at = a.group_indptr[g];
+    bad |= at < 0 || at > a.B || (g > 0 && a.group_indptr[g - 1] > at);
+  }
+  for (int b = tid; b < a.B; b += kThreads) {
+    a.prefix_of[b] = 0;
+    a.refs[b] = {0, 0, 0, 0};
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) report_error(a.status, kErrMetadata);
+  const int groups = bad ? 0 : a.groups;
+  // a warp per group
+  const int tile_tokens = 2 * (kMTileRows / a.G);
+  for (int g = warp; g < groups; g += kThreads / 32) {
+    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    int n = INT_MAX;
+    for (int b = first + lane; b < last; b += 32) n = min(n, visible_to_all(a, b));
+    n = min(__reduce_min_sync(0xffffffffu, n), a.prefix_lens[g]);
+    if (n <= 0 || last - first < 2) continue;
+    for (int b = first + lane; b < last; b += 32) a.prefix_of[b] = n;
+  }
+  __syncthreads();
+  // steps of 128 keys of all the prefixes' tiles, and of all the tails
+  const auto group_tiles = [&](int g, int& keys) {       // row tiles of group g
+    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    keys = last > first ? (a.prefix_of[first] + kKvTile - 1) / kKvTile : 0;
+    return keys == 0 ? 0 : ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
+  };
+  long long steps = 0, tails = 0;
+  for (int g = tid; g < groups; g += kThreads) {
+    int keys;
+    const int rows = group_tiles(g, keys);
+    steps += static_cast<long long>(rows) * keys;
+  }
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int L = max(a.lens[b], 0), base = tail_base(a.prefix_of[b]);
+    tails += (L - base + kKvTile - 1) / kKvTile;
+  }
+  steps = block_sum(steps, wide_sums) * a.Hkv;
+  tails = block_sum(tails, wide_sums) * a.Hkv;
+  const int part = static_cast<int>(max((steps + a.target - 1) / a.target, 1LL));
+  const long long aim = static_cast<long long>(kTailSplits) * a.target;
+  const long long chunk = max((tails + aim - 1) / aim, 1LL) * kKvTile;
+  // tiles of the prefixes
+  int carry = 0;
+  for (int g0 = 0; g0 < groups; g0 += kThreads) {
+    const int g = g0 + tid;
+    int keys = 0, rows = 0, splits = 0;
+    if (g < groups) rows = group_tiles(g, keys);
+    if (rows > 0) splits = (keys + part - 1) / part;
+    int sum;
+    const int base = carry + block_scan(rows * splits * a.Hkv, warp_sums, &sum);
+    carry += sum;
+    if (rows == 0) continue;
+    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    for (int b = first; b < last; ++b) a.refs[b] = {base, splits, rows, (b - first) * a.SQ};
+  }
+  if (carry > a.tile_capacity) {           // cannot be: the capacity is this sum's bound
+    carry = 0;
+    if (tid == 0) report_error(a.status, kErrCapacity);
+  }
+  if (tid == 0) *a.n_tiles = carry;
+  __syncthreads();
+  for (int g = warp; carry > 0 && g < groups; g += kThreads / 32) {
+    int keys;
+    const int rows = group_tiles(g, keys);
+    if (rows == 0) continue;
+    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    const PrefixRef ref = a.refs[first];
+    const int tokens = (last - first) * a.SQ, count = rows * ref.splits * a.Hkv;
+    for (int k = lane; k < count; k += 32) {
+      const int s = k % ref.splits, r = k / ref.splits % rows, h = k / ref.splits / rows;
+      TileRec t;
+      t.b = first;
+      t.g = h;
+      t.tok0 = r * tile_tokens;
+      t.ntok = min(tile_tokens, tokens - t.tok0);
+      t.kv_begin = static_cast<int>(static_cast<long long>(s) * keys / ref.splits);
+      t.kv_end = static_cast<int>(static_cast<long long>(s + 1) * keys / ref.splits);
+      t.q_row0 = first * a.SQ + t.tok0;
+      t.pad = ref.base + k;
+      a.tiles[ref.base + k] = t;
+    }
+  }
+  // items of the tails, in list order
+  carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.B) {
+      const int L = max(a.lens[b], 0), p = a.prefix_of[b];
+      if (L > p) n = static_cast<int>((L - tail_base(p) + chunk - 1) / chunk);
+    }
+    int sum;
+    const int at = carry + block_scan(n, warp_sums, &sum);
+    if (b < a.B) a.split_offset[b] = at;
+    carry += sum;
+  }
+  if (static_cast<long long>(carry) * a.Hkv > a.item_capacity) {   // cannot be, likewise
+    if (tid == 0) report_error(a.status, kErrCapacity);
+    carry = 0;
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kThreads) a.split_offset[b] = 0;
+  }
+  if (tid == 0) a.split_offset[a.B] = carry;
+  __syncthreads();
+  for (int b = warp; b < a.B; b += kThreads / 32) {
+    const int L = max(a.lens[b], 0), p = a.prefix_of[b];
+    const int at = a.split_offset[b], n = a.split_offset[b + 1] - at;
+    for (int k = lane; k < n * a.Hkv; k += 32) {
+      const int s = k % n;
+      SplitItem it;
+      it.b = b;
+      it.g = k / n;
+      it.kv_begin = s == 0 ? p : static_cast<int>(tail_base(p) + s * chunk);
+      it.kv_end = static_cast<int>(min(tail_base(p) + (s + 1) * chunk, static_cast<long long>(L)));
+      a.items[at * a.Hkv + k] = it;
+      a.order[at * a.Hkv + k] = at * a.Hkv + k;
+    }
+  }
+}
+
+// A warp per (query row, head), a lane per 4 columns: weights of the partials from their
+// log-sum-exps, a lane per partial, then their sum.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads)
+shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
+  const int lane = threadIdx.x & 31;
+  const long long x =
+      static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (x >= static_cast<long long>(a.B) * a.SQ * a.Hq) return;
+  const int row = static_cast<int>(x / a.Hq);
+  const int head = static_cast<int>(x - static_cast<long long>(row) * a.Hq);
+  const int b = row / a.SQ, i = row - b * a.SQ, h = head / a.G, e = head - h * a.G;
+  const PrefixRef ref = a.refs[b];
+  // partial s of the prefix, then of the tail
+  const int TM = kMTileRows / a.G, token = ref.token + i;
+  const int in_tile = token % (2 * TM);
+  const long long pre0 =
+      (ref.base + (static_cast<long long>(h) * ref.row_tiles + token / (2 * TM)) * ref.splits) *
+          (2 * kMTileRows) +
+      in_tile / TM * kMTileRows + in_tile % TM * a.G + e;
+  const int at = a.split_offset[b], tails = a.split_offset[b + 1] - at;
+  const int M = a.SQ * a.G;
+  const long long tail0 =
+      (static_cast<long long>(at) * a.Hkv + static_cast<long long>(h) * tails) * M + i * a.G + e;
+  const int n = ref.splits + tails;
+  const auto row_of = [&](int s) {
+    return s < ref.splits ? pre0 + static_cast<long long>(s) * (2 * kMTileRows)
+                          : tail0 + static_cast<long long>(s - ref.splits) * M;
+  };
+  float top = -INFINITY;
+  for (int s = lane; s < n; s += 32)
+    top = fmaxf(top, __ldcg((s < ref.splits ? a.pre_lse : a.tail_lse) + row_of(s)));
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float shift = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int s = s0 + lane;
+    const float w =
+        s < n ? __expf(__ldcg((s < ref.splits ? a.pre_lse : a.tail_lse) + row_of(s)) - shift) : 0.f;
+    total += w;
+    const int count = min(32, n - s0);
+#pragma unroll 8
+    for (int j = 0; j < count; ++j) {
+      const int t = s0 + j;
+      const float* o = (t < ref.splits ? a.pre_o : a.tail_o) + row_of(t) * kD;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(o) + lane);
+      const float f = __shfl_sync(0xffffffffu, w, j);
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
+  const float sc = total > 0.f ? a.out_scale / total : 0.f;
+  store_out4(a.out, x * kD + lane * 4,
+             make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc), a.out_dtype);
+  if (a.lse && lane == 0) a.lse[x] = total > 0.f ? shift + __logf(total) : -INFINITY;
+}
+
+}  // namespace
+
+int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
+  count_launches(1);
+  return launch_after_previous(shared_plan_kernel, dim3(1), dim3(kThreads), 0, st, a) == cudaSuccess
+             ? 0
+             : -1;
+}
+
+int launch_shared_merge(const SharedLaunch& a, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.B) * a.SQ * a.Hq;
+  const long long ctas = ceil_div_ll(rows, kMergeThreads / 32);
+  if (ctas > INT_MAX) return -1;
+  count_launches(1);
+  return launch_after_previous(shared_merge_kernel, dim3(static_cast<unsigned>(ctas)),
+                               dim3(kMergeThreads), 0, st, a) == cudaSuccess
+             ? 0
+             : -1;
+}
+
+}  // namespace pa
