@@ -188,6 +188,448 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
   }
 }
 
+// ---- many rows: prompts --------------------------------------------------------------------------
+// S^T = K Q^T on the 5th-generation tensor cores: a tile of 128 keys (TMEM lanes) stays in shared
+// memory while the request's queries stream past it, 128 rows (columns of S^T) at a time.  A thread
+// owns a key, so the sum over rows stays inside it.  Persistent, one CTA per SM; a unit is a
+// (request, KV head, key tile), and units come in order of their tiles, so that under the causal
+// mask the CTAs take long ones first, in turns that reverse from round to round.  Roles (384
+// threads):
+//   warps 0-3, 4-7  exponentials and sums of the even and the odd query tiles of a unit
+//   warp  8         TMA producer of K (2 buffers) and Q (a ring of 64-column stages)
+//   warp  9         TMEM owner and MMA issuer
+//   warp  10        the columns' shifts (-lse log2 e) and limits (last key that the row sees)
+//   warp  11        unit descriptions, page ids among them
+// The four score buffers of 128 TMEM columns let the MMAs run ahead of the exponentials.
+constexpr int kWideThreads = 384;
+constexpr int kTile = 128;                 // keys of a unit, rows of a query tile
+constexpr int kBlockBytes = kTile * 128;   // 128 rows of 64 columns
+constexpr int kBuffers = 4;                // score buffers, and query tiles described ahead
+constexpr int kUnits = 4;                  // units described ahead
+__host__ __device__ constexpr int q_stages(int D) { return D == 128 ? 8 : 5; }
+
+struct Unit {
+  int tiles;               // query tiles; -1: no more units
+  int h;
+  int key0, keys;          // first key, live keys of the tile
+  int old;                 // keys below it have an older weight
+  int row0, tokens;        // query rows from row0 on, whole tokens
+  int pos0;                // position of the first one; INT_MAX: every row sees every key
+  long long w;             // offset of the tile's weights
+  int pages[kTile / 8];    // of each piece; -1: outside the pool or past the live keys
+};
+struct alignas(16) Columns {
+  float shift[kTile];
+  int limit[kTile];
+  int masked;              // some row does not see all of the tile's keys
+};
+static_assert(sizeof(Columns) % 16 == 0, "read 16 bytes at a time");
+struct WideCtrl {
+  Unit units[kUnits];
+  Columns columns[kBuffers];
+  float odd[2][kTile];     // sums of the odd tiles
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
+  uint64_t col_full[kBuffers], col_empty[kBuffers];
+  uint64_t s_full[kBuffers], s_empty[kBuffers];
+  uint64_t k_full[2], k_empty[2];
+  uint64_t q_full[8], q_empty[8];
+  uint32_t tmem;
+  int abort_flag;
+};
+template <int D>
+constexpr int wide_smem() {
+  return (2 * (D / 64) + q_stages(D)) * kBlockBytes + static_cast<int>(sizeof(WideCtrl)) + 1024;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+            const __grid_constant__ WeightsArgs a) {
+  constexpr int kBlocks = D / 64, kStages = q_stages(D);
+  extern __shared__ uint8_t raw[];
+  uint8_t* k_s = smem_align<1024>(raw);
+  uint8_t* q_s = k_s + 2 * kBlocks * kBlockBytes;
+  WideCtrl* ctl = reinterpret_cast<WideCtrl*>(q_s + kStages * kBlockBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TM = kTile / a.G;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&ctl->unit_full[i], 1);
+      mbar_init(&ctl->unit_empty[i], 3 + 8);
+    }
+    for (int i = 0; i < kBuffers; ++i) {
+      mbar_init(&ctl->col_full[i], 1);
+      mbar_init(&ctl->col_empty[i], 4);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], 1);
+    }
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  // rows of a query tile that no box writes: zero scores
+  for (int i = threadIdx.x; i < kStages * (kTile - TM * a.G) * 8; i += kWideThreads) {
+    const int per = (kTile - TM * a.G) * 8, s = i / per;
+    reinterpret_cast<uint4*>(q_s + s * kBlockBytes + TM * a.G * 128)[i - s * per] =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  if (warp == 9) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem = ctl->tmem;
+  volatile int* abort_flag = &ctl->abort_flag;
+  // A role's view of the units: entry s of the ring, released by release().
+  const auto next_unit = [&](int s) {
+    return mbar_wait_warp(&ctl->unit_full[s % kUnits], (s / kUnits) & 1, a.status, abort_flag);
+  };
+  const auto release = [&](int s) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->unit_empty[s % kUnits]);
+  };
+
+  if (warp == 11) {
+    // =============================== units ==============================================
+    // 32 candidates at a time, a lane each; those with keys are described one after another.
+    const int pairs = a.B * a.Hkv;
+    const long long total = static_cast<long long>(pairs) * ((a.W + kTile - 1) / kTile);
+    const int R = page_piece_rows(a.ps, kTile), pieces = kTile / R;
+    int s = 0;
+    bool ok = true;
+    for (long long base = 0; ok && base * gridDim.x < total; base += 32) {
+      const long long round = base + lane;
+      const long long u = round * gridDim.x +
+                          (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      Unit x;
+      const int* table = nullptr;
+      bool live = u < total;
+      if (live) {
+        const int c = static_cast<int>(u / pairs);
+        const int bh = static_cast<int>(u - static_cast<long long>(c) * pairs);
+        const int b = bh / a.Hkv;
+        const Request r = request_of(a, b);
+        x.h = bh - b * a.Hkv;
+        if (r.bad && c == 0 && x.h == 0) report_error(a.status, kErrMetadata);
+        x.key0 = c * kTile;
+        x.keys = min(kTile, r.keys - x.key0);
+        live = x.keys > 0;
+        x.old = r.old;
+        // the first token that sees a key of the tile
+        const int t0 = a.causal ? min(max(x.key0 - r.first_pos, 0), r.n) : 0;
+        x.row0 = r.row0 + t0;
+        x.tokens = r.n - t0;
+        x.tiles = (x.tokens + TM - 1) / TM;
+        x.pos0 = a.causal ? r.first_pos + t0 : INT_MAX;
+        x.w = static_cast<long long>(bh) * a.W + x.key0;
+        table = r.pages;
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, live);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int key = __shfl_sync(0xffffffffu, x.key0, src) + lane * R;
+        const int end = __shfl_sync(0xffffffffu, x.key0 + x.keys, src);
+        const int* pages = reinterpret_cast<const int*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(table), src));
+        int page = -1;
+        if (lane < pieces && key < end) {
+          page = __ldg(pages + over(key, a.by_ps));
+          if (page < 0 || page >= a.P) {
+            report_error(a.status, kErrMetadata);
+            page = -1;
+          }
+        }
+        const int slot = s % kUnits;
+        if (s >= kUnits && !mbar_wait_warp(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
+                                           a.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        Unit* out = &ctl->units[slot];
+        if (lane < kTile / 8) out->pages[lane] = page;
+        if (lane == src) {
+          out->tiles = x.tiles;
+          out->h = x.h;
+          out->key0 = x.key0;
+          out->keys = x.keys;
+          out->old = x.old;
+          out->row0 = x.row0;
+          out->tokens = x.tokens;
+          out->pos0 = x.pos0;
+          out->w = x.w;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->unit_full[slot]);
+        ++s;
+      }
+    }
+    const int slot = s % kUnits;
+    if (ok && (s < kUnits || mbar_wait_warp(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
+                                            a.status, abort_flag))) {
+      if (lane == 0) {
+        ctl->units[slot].tiles = -1;
+        mbar_arrive(&ctl->unit_full[slot]);
+      }
+    }
+  } else if (warp == 10) {
+    // =============================== columns ============================================
+    int it = 0;
+    bool ok = true;
+    for (int s = 0; ok && next_unit(s); ++s) {
+      const Unit& x = ctl->units[s % kUnits];
+      const int tiles = x.tiles, h = x.h, last_key = x.key0 + kTile - 1;
+      const int row0 = x.row0, tokens = x.tokens, pos0 = x.pos0;
+      release(s);
+      if (tiles < 0) break;
+      for (int i = 0; i < tiles; ++i, ++it) {
+        const int buf = it % kBuffers;
+        float shift[4];
+        int limit[4];
+        bool masked = (i + 1) * TM > tokens || (pos0 != INT_MAX && pos0 + i * TM < last_key);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int m = lane * 4 + e, t = m / a.G, token = i * TM + t;
+          shift[e] = -INFINITY;
+          limit[e] = -1;
+          if (t < TM && token < tokens) {
+            const float l = __ldg(a.lse + head_row(a, row0 + token, h, m - t * a.G));
+            if (l != -INFINITY) {
+              shift[e] = -l * kLog2e;
+              limit[e] = pos0 == INT_MAX ? INT_MAX : pos0 + token;
+            } else {
+              masked = true;
+            }
+          }
+        }
+        if (it >= kBuffers && !mbar_wait_warp(&ctl->col_empty[buf], ((it / kBuffers) - 1) & 1,
+                                              a.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        Columns* c = &ctl->columns[buf];
+        reinterpret_cast<float4*>(c->shift)[lane] =
+            make_float4(shift[0], shift[1], shift[2], shift[3]);
+        reinterpret_cast<int4*>(c->limit)[lane] =
+            make_int4(limit[0], limit[1], limit[2], limit[3]);
+        masked = __any_sync(0xffffffffu, masked);
+        if (lane == 0) c->masked = masked;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->col_full[buf]);
+      }
+    }
+  } else if (warp == 8) {
+    // =============================== copies =============================================
+    if (lane == 0) {
+      tma_prefetch_desc(&qmap);
+      tma_prefetch_desc(&kmap);
+    }
+    const int R = page_piece_rows(a.ps, kTile), boxes = kTile / R * kBlocks;
+    const uint32_t q_box = static_cast<uint32_t>(TM * a.G) * 128u;
+    int units = 0, qs = 0;                 // K tiles, Q stages
+    bool ok = true;
+    for (int s = 0; ok && next_unit(s); ++s) {
+      const Unit& x = ctl->units[s % kUnits];
+      const int tiles = x.tiles, h = x.h, key0 = x.key0, row0 = x.row0;
+      if (tiles <= 0) {
+        release(s);
+        if (tiles < 0) break;
+        continue;
+      }
+      const int kb = units & 1;
+      if (units >= 2 && !mbar_wait_warp(&ctl->k_empty[kb], ((units >> 1) - 1) & 1, a.status,
+                                        abort_flag))
+        break;
+      uint32_t live = 0;
+      for (int i = lane; i < boxes; i += 32) live += x.pages[i / kBlocks] >= 0;
+      live = __reduce_add_sync(0xffffffffu, live);
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->k_full[kb], live * R * 128u);
+      __syncwarp();
+      for (int i = lane; i < boxes; i += 32) {
+        const int piece = i / kBlocks, col = i % kBlocks, page = x.pages[piece];
+        if (page < 0) continue;
+        const int key = key0 + piece * R;
+        const int row = static_cast<int>(page * a.page_rows) + h * a.ps + key % a.ps;
+        tma_load_2d(k_s + (kb * kBlocks + col) * kBlockBytes + piece * R * 128, &kmap,
+                    &ctl->k_full[kb], col * 64, row);
+      }
+      ++units;
+      release(s);
+      for (int i = 0; ok && i < tiles * kBlocks; ++i, ++qs) {
+        const int stage = qs % kStages;
+        if (qs >= kStages && !mbar_wait_warp(&ctl->q_empty[stage], ((qs / kStages) - 1) & 1,
+                                             a.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl->q_full[stage], q_box);
+          tma_load_3d(q_s + stage * kBlockBytes, &qmap, &ctl->q_full[stage], i % kBlocks * 64,
+                      h * a.G, row0 + i / kBlocks * TM);
+        }
+      }
+    }
+    if (*abort_flag) {                     // no copy may land after the CTA has ended
+      for (int i = max(0, units - 2); i < units; ++i) drain_wait(&ctl->k_full[i & 1], (i >> 1) & 1);
+      for (int i = max(0, qs - kStages); i < qs; ++i)
+        drain_wait(&ctl->q_full[i % kStages], (i / kStages) & 1);
+    }
+  } else if (warp == 9) {
+    // =============================== MMAs ===============================================
+    constexpr uint32_t idesc = idesc_bf16(kTile, kTile, false, false);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(k_s), 16, 1024);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(q_s), 16, 1024);
+    int units = 0, qs = 0, it = 0;
+    bool ok = true;
+    for (int s = 0; ok && next_unit(s); ++s) {
+      const int tiles = ctl->units[s % kUnits].tiles;
+      release(s);
+      if (tiles < 0) break;
+      if (tiles == 0) continue;
+      const int kb = units & 1;
+      if (!mbar_wait_warp(&ctl->k_full[kb], (units >> 1) & 1, a.status, abort_flag)) break;
+      ++units;
+      for (int i = 0; i < tiles; ++i, ++it) {
+        const int buf = it % kBuffers;
+        if (it >= kBuffers && !mbar_wait_warp(&ctl->s_empty[buf], ((it / kBuffers) - 1) & 1,
+                                              a.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        for (int c = 0; c < kBlocks; ++c, ++qs) {
+          const int stage = qs % kStages;
+          if (!mbar_wait_warp(&ctl->q_full[stage], (qs / kStages) & 1, a.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t kd = k_desc + ((kb * kBlocks + c) * kBlockBytes >> 4);
+            const uint64_t qd = q_desc + (stage * kBlockBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + buf * kTile, kd + (k * 32 >> 4), qd + (k * 32 >> 4), idesc,
+                     c > 0 || k > 0);
+            mma_commit(&ctl->q_empty[stage]);
+            if (c == kBlocks - 1) mma_commit(&ctl->s_full[buf]);
+            if (c == kBlocks - 1 && i == tiles - 1) mma_commit(&ctl->k_empty[kb]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    // =============================== exponentials =======================================
+    const int odd = warp >> 2, m = threadIdx.x & 127;        // this thread's key
+    const uint32_t column0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float scale = a.scale_log2;
+    const int R = page_piece_rows(a.ps, kTile);
+    int it = 0;
+    for (int s = 0;; ++s) {
+      bool ok = next_unit(s);
+      const Unit& x = ctl->units[s % kUnits];
+      const int tiles = ok ? x.tiles : 0, key = x.key0 + m;
+      const bool mine = ok && tiles >= 0 && m < x.keys && x.pages[m / R] >= 0;
+      const bool had = mine && key < x.old && a.decay != 0.f;
+      float* w = a.w + x.w + m;
+      if (ok) release(s);
+      // the older weight, on its way during the sums
+      float sum = 0.f, before = 0.f;
+      if (odd == 0 && had) before = *w;
+      for (int i = odd; ok && i < tiles; i += 2) {
+        const int t = it + i, buf = t % kBuffers, parity = (t / kBuffers) & 1;
+        ok = mbar_wait_warp(&ctl->s_full[buf], parity, a.status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[kTile];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tmem_ld32(column0 + buf * kTile + q * 32,
+                    *reinterpret_cast<uint32_t(*)[32]>(&r[q * 32]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->s_empty[buf]);
+        ok = mbar_wait_warp(&ctl->col_full[buf], parity, a.status, abort_flag);
+        if (!ok) break;
+        const Columns& c = ctl->columns[buf];
+        float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;
+        if (!c.masked) {
+#pragma unroll
+          for (int j = 0; j < kTile; j += 4) {
+            const float4 sh = *reinterpret_cast<const float4*>(c.shift + j);
+            float y0, y1, y2, y3;
+            ffma2(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, sh.x, sh.y);
+            ffma2(y2, y3, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]), scale, sh.z, sh.w);
+            fadd2(p0, p1, fast_exp2(y0), fast_exp2(y1));
+            fadd2(p2, p3, fast_exp2(y2), fast_exp2(y3));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTile; j += 4) {
+            const float4 sh = *reinterpret_cast<const float4*>(c.shift + j);
+            const int4 lim = *reinterpret_cast<const int4*>(c.limit + j);
+            float y0, y1, y2, y3;
+            ffma2(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, sh.x, sh.y);
+            ffma2(y2, y3, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]), scale, sh.z, sh.w);
+            y0 = key <= lim.x ? fast_exp2(y0) : 0.f;
+            y1 = key <= lim.y ? fast_exp2(y1) : 0.f;
+            y2 = key <= lim.z ? fast_exp2(y2) : 0.f;
+            y3 = key <= lim.w ? fast_exp2(y3) : 0.f;
+            fadd2(p0, p1, y0, y1);
+            fadd2(p2, p3, y2, y3);
+          }
+        }
+        sum += (p0 + p1) + (p2 + p3);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->col_empty[buf]);
+      }
+      it += tiles;
+      // The odd tiles' sums join the even ones'.  Every warp comes here whatever its waits said and
+      // also after the last unit, so that all of them leave together.
+      if (odd) ctl->odd[s & 1][m] = sum;
+      if (named_bar_or(1, 256, !ok || tiles < 0)) break;
+      if (!odd && mine) *w = (had ? a.decay * before : 0.f) + (sum + ctl->odd[s & 1][m]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int launch_wide(const WeightsArgs& a, cudaStream_t st) {
+  const int sms = current_sm_count();
+  static std::atomic<uint64_t> ready{0};
+  if (sms <= 0 || !kernel_smem_ready(wide_kernel<D>, wide_smem<D>(), ready))
+    return PAGED_ATTN_ERR_CUDA;
+  CUtensorMap qmap, kmap;
+  if (!encode_q_map(&qmap, a.q, a.total, a.Hq, D, a.G, kTile / a.G) ||
+      !encode_rows_map(&kmap, a.k, a.page_rows * a.P, D, page_piece_rows(a.ps, kTile)))
+    return PAGED_ATTN_ERR_CUDA;
+  const long long units = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, kTile);
+  count_launches(1);
+  return cuda_status(launch_after_previous(wide_kernel<D>,
+                                           static_cast<int>(units < sms ? units : sms),
+                                           kWideThreads, wide_smem<D>(), st, qmap, kmap, a));
+}
+
 template <int D, int NT>
 cudaError_t launch_narrow(const WeightsArgs& a, cudaStream_t st) {
   const int sms = current_sm_count();
@@ -257,6 +699,8 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   long long rows = ceil_div(p->total_q, p->batch);         // of a request, on average
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
+  if (rows > 16)
+    return p->head_dim == 128 ? launch_wide<128>(a, st) : launch_wide<256>(a, st);
   if (p->head_dim == 128)
     return cuda_status(rows <= 8 ? launch_narrow<128, 1>(a, st)
                                  : (rows <= 16 ? launch_narrow<128, 2>(a, st)
