@@ -70,7 +70,7 @@ __device__ __forceinline__ int over(int x, unsigned long long by_ps) {
   return static_cast<int>(__umul64hi(static_cast<unsigned>(x), by_ps));
 }
 
-// ---- few rows: decode ----------------------------------------------------------------------------
+// ---- few rows: decode --------------------------------------------------------------------------
 // Bound by reading K.  A warp takes 16 keys at a time as the A operand of warp MMAs, the request's
 // rows (query, head) as the B operand, 8 NT of them.  The contraction runs over columns in any
 // order, so a lane loads 16 bytes of its key's row and takes them as its operands of two MMAs:
@@ -188,26 +188,41 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
   }
 }
 
-// ---- many rows: prompts --------------------------------------------------------------------------
-// S^T = K Q^T on the 5th-generation tensor cores: a tile of 128 keys (TMEM lanes) stays in shared
-// memory while the request's queries stream past it, 128 rows (columns of S^T) at a time.  A thread
-// owns a key, so the sum over rows stays inside it.  Persistent, one CTA per SM; a unit is a
+// ---- many rows: prompts ------------------------------------------------------------------------
+// S = Q K^T on the 5th-generation tensor cores: the keys of a unit stay in shared memory while the
+// request's queries stream past them, 128 rows (TMEM lanes) at a time.  A thread owns a row, whose
+// shift -lse log2 e it keeps in a register, and 128 keys, whose sums over its rows it keeps in 128
+// registers until the unit ends and the lanes are summed.  Persistent, one CTA per SM; a unit is a
 // (request, KV head, key tile), and units come in order of their tiles, so that under the causal
 // mask the CTAs take long ones first, in turns that reverse from round to round.  Roles (384
 // threads):
-//   warps 0-3, 4-7  exponentials and sums of the even and the odd query tiles of a unit
-//   warp  8         TMA producer of K (2 buffers) and Q (a ring of 64-column stages)
+//   warps 0-3, 4-7  exponentials and sums
+//   warp  8         TMA producer of K and of Q (a ring of 64-column stages)
 //   warp  9         TMEM owner and MMA issuer
-//   warp  10        the columns' shifts (-lse log2 e) and limits (last key that the row sees)
 //   warp  11        unit descriptions, page ids among them
-// The four score buffers of 128 TMEM columns let the MMAs run ahead of the exponentials.
+// kPair: tiles of 256 keys; both warpgroups take every query tile, 128 keys each.  Else tiles of
+// 128 keys, and the warpgroups take query tiles in turn.
+// The queries come from L2 once per key tile: 128 keys ask for 64 bytes per cycle and SM, far above
+// what L2 gives all SMs (some 20), so prompts want the 256; tiles of 128 make more and smaller
+// units and leave room for the next unit's K at D = 256.
 constexpr int kWideThreads = 384;
-constexpr int kTile = 128;                 // keys of a unit, rows of a query tile
-constexpr int kBlockBytes = kTile * 128;   // 128 rows of 64 columns
-constexpr int kBuffers = 4;                // score buffers, and query tiles described ahead
+constexpr int kRows = 128;                 // of a query tile
+constexpr int kBlockBytes = kRows * 128;   // 128 rows of 64 columns
 constexpr int kUnits = 4;                  // units described ahead
-__host__ __device__ constexpr int q_stages(int D) { return D == 128 ? 8 : 5; }
+// Registers after set-up (launch: 384 x 168): 2 x 128 x 208 + 128 x 88 = 384 x 168.
+constexpr int kSumRegs = 208;
+constexpr int kControlRegs = 88;
+static_assert(2 * 128 * kSumRegs + 128 * kControlRegs <= kWideThreads * 168, "register split");
 
+template <int D, bool kPair>
+struct Wide {
+  static constexpr int kKeys = kPair ? 256 : 128;
+  static constexpr int kBlocks = D / 64;                        // of 64 columns
+  static constexpr int kKBuffers = D == 256 && kPair ? 1 : 2;
+  static constexpr int kSBuffers = 512 / kKeys;                 // score buffers
+  static constexpr int kQStages = D == 128 && !kPair ? 8 : 5;
+  static constexpr int kKBytes = kKeys * 128;                   // of a block
+};
 struct Unit {
   int tiles;               // query tiles; -1: no more units
   int h;
@@ -216,54 +231,99 @@ struct Unit {
   int row0, tokens;        // query rows from row0 on, whole tokens
   int pos0;                // position of the first one; INT_MAX: every row sees every key
   long long w;             // offset of the tile's weights
-  int pages[kTile / 8];    // of each piece; -1: outside the pool or past the live keys
+  int pages[32];           // of each piece; -1: outside the pool or past the live keys
 };
-struct alignas(16) Columns {
-  float shift[kTile];
-  int limit[kTile];
-  int masked;              // some row does not see all of the tile's keys
-};
-static_assert(sizeof(Columns) % 16 == 0, "read 16 bytes at a time");
 struct WideCtrl {
   Unit units[kUnits];
-  Columns columns[kBuffers];
-  float odd[2][kTile];     // sums of the odd tiles
+  alignas(16) float sums[2][8][kRows];     // by unit parity: each warp's sums of its 128 keys
   uint64_t unit_full[kUnits], unit_empty[kUnits];
-  uint64_t col_full[kBuffers], col_empty[kBuffers];
-  uint64_t s_full[kBuffers], s_empty[kBuffers];
+  uint64_t s_full[4], s_empty[4];
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[8], q_empty[8];
   uint32_t tmem;
   int abort_flag;
 };
-template <int D>
+template <int D, bool kPair>
 constexpr int wide_smem() {
-  return (2 * (D / 64) + q_stages(D)) * kBlockBytes + static_cast<int>(sizeof(WideCtrl)) + 1024;
+  using X = Wide<D, kPair>;
+  return X::kKBuffers * X::kBlocks * X::kKBytes + X::kQStages * kBlockBytes +
+         static_cast<int>(sizeof(WideCtrl)) + 1024;
 }
 
-template <int D>
+// Exponentials of 32 scores, added to the sums of their keys.  kMask: only keys j <= limit count.
+template <bool kMask>
+__device__ __forceinline__ void add_weights(float (&sums)[kRows], const uint32_t (&r)[32], int j0,
+                                            float scale, float shift, int limit) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float y0, y1;
+    ffma2_bcast(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, shift);
+    y0 = fast_exp2(y0);
+    y1 = fast_exp2(y1);
+    if (kMask) {
+      y0 = j0 + j <= limit ? y0 : 0.f;
+      y1 = j0 + j + 1 <= limit ? y1 : 0.f;
+    }
+    fadd2(sums[j0 + j], sums[j0 + j + 1], y0, y1);
+  }
+}
+// The 128 scores of a row; `done` is called when they have left TMEM.
+template <bool kMask, typename F>
+__device__ __forceinline__ void add_row(float (&sums)[kRows], uint32_t column, float scale,
+                                        float shift, int limit, const F& done) {
+  uint32_t r0[32], r1[32];
+  tmem_ld32(column, r0);
+  tmem_ld_wait();
+  tmem_ld32(column + 32, r1);
+  add_weights<kMask>(sums, r0, 0, scale, shift, limit);
+  tmem_ld_wait();
+  tmem_ld32(column + 64, r0);
+  add_weights<kMask>(sums, r1, 32, scale, shift, limit);
+  tmem_ld_wait();
+  tmem_ld32(column + 96, r1);
+  add_weights<kMask>(sums, r0, 64, scale, shift, limit);
+  tmem_ld_wait();
+  done();
+  add_weights<kMask>(sums, r1, 96, scale, shift, limit);
+}
+
+// Sums over a warp's rows: at each step a lane gives away half of its keys, until lane l has those
+// of keys 4 l .. 4 l + 3.
+template <int kHalf, int kLane>
+__device__ __forceinline__ void sum_lanes(float (&sums)[kRows], int lane) {
+  const bool upper = lane & kLane;
+#pragma unroll
+  for (int j = 0; j < kHalf; ++j) {
+    const float give = upper ? sums[j] : sums[j + kHalf];
+    const float keep = upper ? sums[j + kHalf] : sums[j];
+    sums[j] = keep + __shfl_xor_sync(0xffffffffu, give, kLane);
+  }
+  if constexpr (kLane > 1) sum_lanes<kHalf / 2, kLane / 2>(sums, lane);
+}
+
+template <int D, bool kPair>
 __global__ void __launch_bounds__(kWideThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
             const __grid_constant__ WeightsArgs a) {
-  constexpr int kBlocks = D / 64, kStages = q_stages(D);
+  using X = Wide<D, kPair>;
+  constexpr int kKeys = X::kKeys, kBlocks = X::kBlocks, kKBytes = X::kKBytes;
+  constexpr int kKBuffers = X::kKBuffers, kSBuffers = X::kSBuffers, kStages = X::kQStages;
   extern __shared__ uint8_t raw[];
   uint8_t* k_s = smem_align<1024>(raw);
-  uint8_t* q_s = k_s + 2 * kBlocks * kBlockBytes;
+  uint8_t* q_s = k_s + kKBuffers * kBlocks * kKBytes;
   WideCtrl* ctl = reinterpret_cast<WideCtrl*>(q_s + kStages * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int TM = kTile / a.G;
+  const int TM = kRows / a.G;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&ctl->unit_full[i], 1);
-      mbar_init(&ctl->unit_empty[i], 3 + 8);
+      mbar_init(&ctl->unit_empty[i], 2 + 8);
     }
-    for (int i = 0; i < kBuffers; ++i) {
-      mbar_init(&ctl->col_full[i], 1);
-      mbar_init(&ctl->col_empty[i], 4);
+    for (int i = 0; i < kSBuffers; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->s_empty[i], 4);
+      mbar_init(&ctl->s_empty[i], kPair ? 8 : 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kKBuffers; ++i) {
       mbar_init(&ctl->k_full[i], 1);
       mbar_init(&ctl->k_empty[i], 1);
     }
@@ -275,11 +335,10 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     fence_mbar_init();
   }
   // rows of a query tile that no box writes: zero scores
-  for (int i = threadIdx.x; i < kStages * (kTile - TM * a.G) * 8; i += kWideThreads) {
-    const int per = (kTile - TM * a.G) * 8, s = i / per;
-    reinterpret_cast<uint4*>(q_s + s * kBlockBytes + TM * a.G * 128)[i - s * per] =
+  const int spare = (kRows - TM * a.G) * 8;
+  for (int i = threadIdx.x; i < kStages * spare; i += kWideThreads)
+    reinterpret_cast<uint4*>(q_s + i / spare * kBlockBytes + TM * a.G * 128)[i % spare] =
         make_uint4(0u, 0u, 0u, 0u);
-  }
   fence_proxy_async_smem();
   if (warp == 9) {
     tmem_alloc(&ctl->tmem, 512);
@@ -292,21 +351,24 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   grid_launch_dependents();
   const uint32_t tmem = ctl->tmem;
   volatile int* abort_flag = &ctl->abort_flag;
-  // A role's view of the units: entry s of the ring, released by release().
+  // A role's view of the units: entry s of the ring, given back by release().
   const auto next_unit = [&](int s) {
-    return mbar_wait_warp(&ctl->unit_full[s % kUnits], (s / kUnits) & 1, a.status, abort_flag);
+    return mbar_wait_warp<true>(&ctl->unit_full[s % kUnits], (s / kUnits) & 1, a.status,
+                                abort_flag);
   };
   const auto release = [&](int s) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->unit_empty[s % kUnits]);
   };
 
+  if (warp >= 8) {
+  regs_decrease<kControlRegs>();
   if (warp == 11) {
     // =============================== units ==============================================
     // 32 candidates at a time, a lane each; those with keys are described one after another.
     const int pairs = a.B * a.Hkv;
-    const long long total = static_cast<long long>(pairs) * ((a.W + kTile - 1) / kTile);
-    const int R = page_piece_rows(a.ps, kTile), pieces = kTile / R;
+    const long long total = static_cast<long long>(pairs) * ((a.W + kKeys - 1) / kKeys);
+    const int R = page_piece_rows(a.ps, kRows), pieces = kKeys / R;
     int s = 0;
     bool ok = true;
     for (long long base = 0; ok && base * gridDim.x < total; base += 32) {
@@ -323,8 +385,8 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         const Request r = request_of(a, b);
         x.h = bh - b * a.Hkv;
         if (r.bad && c == 0 && x.h == 0) report_error(a.status, kErrMetadata);
-        x.key0 = c * kTile;
-        x.keys = min(kTile, r.keys - x.key0);
+        x.key0 = c * kKeys;
+        x.keys = min(kKeys, r.keys - x.key0);
         live = x.keys > 0;
         x.old = r.old;
         // the first token that sees a key of the tile
@@ -353,13 +415,13 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
           }
         }
         const int slot = s % kUnits;
-        if (s >= kUnits && !mbar_wait_warp(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
-                                           a.status, abort_flag)) {
+        if (s >= kUnits && !mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
+                                                 a.status, abort_flag)) {
           ok = false;
           break;
         }
         Unit* out = &ctl->units[slot];
-        if (lane < kTile / 8) out->pages[lane] = page;
+        out->pages[lane] = page;
         if (lane == src) {
           out->tiles = x.tiles;
           out->h = x.h;
@@ -377,57 +439,11 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       }
     }
     const int slot = s % kUnits;
-    if (ok && (s < kUnits || mbar_wait_warp(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
-                                            a.status, abort_flag))) {
+    if (ok && (s < kUnits || mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
+                                                  a.status, abort_flag))) {
       if (lane == 0) {
         ctl->units[slot].tiles = -1;
         mbar_arrive(&ctl->unit_full[slot]);
-      }
-    }
-  } else if (warp == 10) {
-    // =============================== columns ============================================
-    int it = 0;
-    bool ok = true;
-    for (int s = 0; ok && next_unit(s); ++s) {
-      const Unit& x = ctl->units[s % kUnits];
-      const int tiles = x.tiles, h = x.h, last_key = x.key0 + kTile - 1;
-      const int row0 = x.row0, tokens = x.tokens, pos0 = x.pos0;
-      release(s);
-      if (tiles < 0) break;
-      for (int i = 0; i < tiles; ++i, ++it) {
-        const int buf = it % kBuffers;
-        float shift[4];
-        int limit[4];
-        bool masked = (i + 1) * TM > tokens || (pos0 != INT_MAX && pos0 + i * TM < last_key);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = lane * 4 + e, t = m / a.G, token = i * TM + t;
-          shift[e] = -INFINITY;
-          limit[e] = -1;
-          if (t < TM && token < tokens) {
-            const float l = __ldg(a.lse + head_row(a, row0 + token, h, m - t * a.G));
-            if (l != -INFINITY) {
-              shift[e] = -l * kLog2e;
-              limit[e] = pos0 == INT_MAX ? INT_MAX : pos0 + token;
-            } else {
-              masked = true;
-            }
-          }
-        }
-        if (it >= kBuffers && !mbar_wait_warp(&ctl->col_empty[buf], ((it / kBuffers) - 1) & 1,
-                                              a.status, abort_flag)) {
-          ok = false;
-          break;
-        }
-        Columns* c = &ctl->columns[buf];
-        reinterpret_cast<float4*>(c->shift)[lane] =
-            make_float4(shift[0], shift[1], shift[2], shift[3]);
-        reinterpret_cast<int4*>(c->limit)[lane] =
-            make_int4(limit[0], limit[1], limit[2], limit[3]);
-        masked = __any_sync(0xffffffffu, masked);
-        if (lane == 0) c->masked = masked;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->col_full[buf]);
       }
     }
   } else if (warp == 8) {
@@ -436,7 +452,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       tma_prefetch_desc(&qmap);
       tma_prefetch_desc(&kmap);
     }
-    const int R = page_piece_rows(a.ps, kTile), boxes = kTile / R * kBlocks;
+    const int R = page_piece_rows(a.ps, kRows), boxes = kKeys / R * kBlocks;
     const uint32_t q_box = static_cast<uint32_t>(TM * a.G) * 128u;
     int units = 0, qs = 0;                 // K tiles, Q stages
     bool ok = true;
@@ -448,9 +464,10 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         if (tiles < 0) break;
         continue;
       }
-      const int kb = units & 1;
-      if (units >= 2 && !mbar_wait_warp(&ctl->k_empty[kb], ((units >> 1) - 1) & 1, a.status,
-                                        abort_flag))
+      const int kb = units % kKBuffers;
+      if (units >= kKBuffers && !mbar_wait_warp<true>(&ctl->k_empty[kb],
+                                                      (units / kKBuffers - 1) & 1, a.status,
+                                                      abort_flag))
         break;
       uint32_t live = 0;
       for (int i = lane; i < boxes; i += 32) live += x.pages[i / kBlocks] >= 0;
@@ -462,15 +479,15 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         if (page < 0) continue;
         const int key = key0 + piece * R;
         const int row = static_cast<int>(page * a.page_rows) + h * a.ps + key % a.ps;
-        tma_load_2d(k_s + (kb * kBlocks + col) * kBlockBytes + piece * R * 128, &kmap,
+        tma_load_2d(k_s + (kb * kBlocks + col) * kKBytes + piece * R * 128, &kmap,
                     &ctl->k_full[kb], col * 64, row);
       }
       ++units;
       release(s);
       for (int i = 0; ok && i < tiles * kBlocks; ++i, ++qs) {
         const int stage = qs % kStages;
-        if (qs >= kStages && !mbar_wait_warp(&ctl->q_empty[stage], ((qs / kStages) - 1) & 1,
-                                             a.status, abort_flag)) {
+        if (qs >= kStages && !mbar_wait_fast_warp(&ctl->q_empty[stage], ((qs / kStages) - 1) & 1,
+                                                  a.status, abort_flag)) {
           ok = false;
           break;
         }
@@ -482,45 +499,50 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       }
     }
     if (*abort_flag) {                     // no copy may land after the CTA has ended
-      for (int i = max(0, units - 2); i < units; ++i) drain_wait(&ctl->k_full[i & 1], (i >> 1) & 1);
+      for (int i = max(0, units - kKBuffers); i < units; ++i)
+        drain_wait(&ctl->k_full[i % kKBuffers], (i / kKBuffers) & 1);
       for (int i = max(0, qs - kStages); i < qs; ++i)
         drain_wait(&ctl->q_full[i % kStages], (i / kStages) & 1);
     }
   } else if (warp == 9) {
     // =============================== MMAs ===============================================
-    constexpr uint32_t idesc = idesc_bf16(kTile, kTile, false, false);
+    constexpr uint32_t idesc_all = idesc_bf16(kRows, kKeys, false, false);
+    constexpr uint32_t idesc_half = idesc_bf16(kRows, 128, false, false);
     const uint64_t k_desc = sdesc_sw128(smem_u32(k_s), 16, 1024);
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_s), 16, 1024);
     int units = 0, qs = 0, it = 0;
     bool ok = true;
     for (int s = 0; ok && next_unit(s); ++s) {
-      const int tiles = ctl->units[s % kUnits].tiles;
+      const int tiles = ctl->units[s % kUnits].tiles, keys = ctl->units[s % kUnits].keys;
       release(s);
       if (tiles < 0) break;
       if (tiles == 0) continue;
-      const int kb = units & 1;
-      if (!mbar_wait_warp(&ctl->k_full[kb], (units >> 1) & 1, a.status, abort_flag)) break;
+      const uint32_t idesc = keys > 128 ? idesc_all : idesc_half;
+      const int kb = units % kKBuffers;
+      if (!mbar_wait_fast_warp(&ctl->k_full[kb], (units / kKBuffers) & 1, a.status, abort_flag))
+        break;
       ++units;
-      for (int i = 0; i < tiles; ++i, ++it) {
-        const int buf = it % kBuffers;
-        if (it >= kBuffers && !mbar_wait_warp(&ctl->s_empty[buf], ((it / kBuffers) - 1) & 1,
-                                              a.status, abort_flag)) {
+      for (int i = 0; ok && i < tiles; ++i, ++it) {
+        const int buf = it % kSBuffers;
+        if (it >= kSBuffers && !mbar_wait_fast_warp(&ctl->s_empty[buf], ((it / kSBuffers) - 1) & 1,
+                                                    a.status, abort_flag)) {
           ok = false;
           break;
         }
         for (int c = 0; c < kBlocks; ++c, ++qs) {
           const int stage = qs % kStages;
-          if (!mbar_wait_warp(&ctl->q_full[stage], (qs / kStages) & 1, a.status, abort_flag)) {
+          if (!mbar_wait_fast_warp(&ctl->q_full[stage], (qs / kStages) & 1, a.status,
+                                   abort_flag)) {
             ok = false;
             break;
           }
           if (lane == 0) {
             tc_fence_after();
-            const uint64_t kd = k_desc + ((kb * kBlocks + c) * kBlockBytes >> 4);
+            const uint64_t kd = k_desc + ((kb * kBlocks + c) * kKBytes >> 4);
             const uint64_t qd = q_desc + (stage * kBlockBytes >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + buf * kTile, kd + (k * 32 >> 4), qd + (k * 32 >> 4), idesc,
+              mma_ss(tmem + buf * kKeys, qd + (k * 32 >> 4), kd + (k * 32 >> 4), idesc,
                      c > 0 || k > 0);
             mma_commit(&ctl->q_empty[stage]);
             if (c == kBlocks - 1) mma_commit(&ctl->s_full[buf]);
@@ -528,81 +550,82 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
           }
           __syncwarp();
         }
-        if (!ok) break;
       }
     }
+  }
   } else {
-    // =============================== exponentials =======================================
-    const int odd = warp >> 2, m = threadIdx.x & 127;        // this thread's key
-    const uint32_t column0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    regs_increase<kSumRegs>();
+    // =============================== exponentials and sums ==============================
+    const int group = warp >> 2, m = threadIdx.x & 127;      // this thread's row, later its key
+    const uint32_t column0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                             (kPair ? group * 128 : 0);
     const float scale = a.scale_log2;
-    const int R = page_piece_rows(a.ps, kTile);
+    const int R = page_piece_rows(a.ps, kRows);
+    const int token = m / a.G;                               // of the row, in its tile
+    const long long lse_at = static_cast<long long>(token) * a.Hq + m - token * a.G;
+    const long long lse_step = static_cast<long long>(TM) * a.Hq;
     int it = 0;
     for (int s = 0;; ++s) {
       bool ok = next_unit(s);
       const Unit& x = ctl->units[s % kUnits];
-      const int tiles = ok ? x.tiles : 0, key = x.key0 + m;
-      const bool mine = ok && tiles >= 0 && m < x.keys && x.pages[m / R] >= 0;
-      const bool had = mine && key < x.old && a.decay != 0.f;
-      float* w = a.w + x.w + m;
+      const int tiles = ok ? x.tiles : 0, first = kPair ? group * 128 : 0, k = first + m;
+      const int key0 = x.key0 + first, tokens = x.tokens, pos0 = x.pos0;
+      const bool writes = ok && tiles >= 0 && (kPair || group == 0) && k < x.keys &&
+                          x.pages[k / R] >= 0;
+      const bool had = writes && key0 + m < x.old && a.decay != 0.f;
+      const bool idle = kPair && x.keys <= first;            // no live key of this group
+      float* w = a.w + x.w + k;
+      const float* lse = a.lse + head_row(a, x.row0, x.h, 0) + lse_at;
       if (ok) release(s);
-      // the older weight, on its way during the sums
-      float sum = 0.f, before = 0.f;
-      if (odd == 0 && had) before = *w;
-      for (int i = odd; ok && i < tiles; i += 2) {
-        const int t = it + i, buf = t % kBuffers, parity = (t / kBuffers) & 1;
-        ok = mbar_wait_warp(&ctl->s_full[buf], parity, a.status, abort_flag);
+      const float before = had ? *w : 0.f;                   // on its way during the sums
+      float sums[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) sums[j] = 0.f;
+      const auto load = [&](int i) {
+        return token < TM && i * TM + token < tokens ? __ldg(lse + i * lse_step) : -INFINITY;
+      };
+      constexpr int kStep = kPair ? 1 : 2;
+      const int i0 = kPair ? 0 : group;
+      float next = ok && i0 < tiles ? load(i0) : 0.f;
+      for (int i = i0; ok && i < tiles; i += kStep) {
+        const int t = it + i, buf = t % kSBuffers;
+        const float l = next;
+        if (i + kStep < tiles) next = load(i + kStep);
+        // keys up to `limit` of this thread's 128 count
+        const int limit = l == -INFINITY  ? -1
+                          : pos0 == INT_MAX ? INT_MAX
+                                            : pos0 + i * TM + token - key0;
+        const float shift = -l * kLog2e;
+        ok = mbar_wait_fast_warp(&ctl->s_full[buf], (t / kSBuffers) & 1, a.status, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[kTile];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          tmem_ld32(column0 + buf * kTile + q * 32,
-                    *reinterpret_cast<uint32_t(*)[32]>(&r[q * 32]));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->s_empty[buf]);
-        ok = mbar_wait_warp(&ctl->col_full[buf], parity, a.status, abort_flag);
-        if (!ok) break;
-        const Columns& c = ctl->columns[buf];
-        float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;
-        if (!c.masked) {
-#pragma unroll
-          for (int j = 0; j < kTile; j += 4) {
-            const float4 sh = *reinterpret_cast<const float4*>(c.shift + j);
-            float y0, y1, y2, y3;
-            ffma2(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, sh.x, sh.y);
-            ffma2(y2, y3, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]), scale, sh.z, sh.w);
-            fadd2(p0, p1, fast_exp2(y0), fast_exp2(y1));
-            fadd2(p2, p3, fast_exp2(y2), fast_exp2(y3));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kTile; j += 4) {
-            const float4 sh = *reinterpret_cast<const float4*>(c.shift + j);
-            const int4 lim = *reinterpret_cast<const int4*>(c.limit + j);
-            float y0, y1, y2, y3;
-            ffma2(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, sh.x, sh.y);
-            ffma2(y2, y3, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]), scale, sh.z, sh.w);
-            y0 = key <= lim.x ? fast_exp2(y0) : 0.f;
-            y1 = key <= lim.y ? fast_exp2(y1) : 0.f;
-            y2 = key <= lim.z ? fast_exp2(y2) : 0.f;
-            y3 = key <= lim.w ? fast_exp2(y3) : 0.f;
-            fadd2(p0, p1, y0, y1);
-            fadd2(p2, p3, y2, y3);
-          }
-        }
-        sum += (p0 + p1) + (p2 + p3);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->col_empty[buf]);
+        const uint32_t column = column0 + buf * kKeys;
+        const auto done = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->s_empty[buf]);
+        };
+        if (idle || __all_sync(0xffffffffu, limit < 0)) done();
+        else if (__all_sync(0xffffffffu, limit >= 127))
+          add_row<false>(sums, column, scale, shift, limit, done);
+        else
+          add_row<true>(sums, column, scale, shift, limit, done);
       }
       it += tiles;
-      // The odd tiles' sums join the even ones'.  Every warp comes here whatever its waits said and
-      // also after the last unit, so that all of them leave together.
-      if (odd) ctl->odd[s & 1][m] = sum;
-      if (named_bar_or(1, 256, !ok || tiles < 0)) break;
-      if (!odd && mine) *w = (had ? a.decay * before : 0.f) + (sum + ctl->odd[s & 1][m]);
+      sum_lanes<kRows / 2, 16>(sums, lane);
+      reinterpret_cast<float4*>(ctl->sums[s & 1][warp])[lane] =
+          make_float4(sums[0], sums[1], sums[2], sums[3]);
+      // Every warp comes here whatever its waits said and also after the last unit, so that those
+      // that meet here leave together.
+      const bool leave = !ok || tiles < 0;
+      if (kPair ? named_bar_or(1 + group, 128, leave) : named_bar_or(1, 256, leave)) break;
+      if (writes) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < (kPair ? 4 : 8); ++g)
+          sum += ctl->sums[s & 1][(kPair ? group * 4 : 0) + g][m];
+        *w = (had ? a.decay * before : 0.f) + sum;
+      }
     }
   }
   tc_fence_before();
@@ -613,21 +636,25 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   }
 }
 
-template <int D>
+constexpr int kPairRows = 1024;
+
+template <int D, bool kPair>
 int launch_wide(const WeightsArgs& a, cudaStream_t st) {
+  constexpr int smem = wide_smem<D, kPair>();
+  static_assert(smem <= 227 * 1024, "shared memory");
   const int sms = current_sm_count();
   static std::atomic<uint64_t> ready{0};
-  if (sms <= 0 || !kernel_smem_ready(wide_kernel<D>, wide_smem<D>(), ready))
-    return PAGED_ATTN_ERR_CUDA;
+  constexpr auto kernel = wide_kernel<D, kPair>;
+  if (sms <= 0 || !kernel_smem_ready(kernel, smem, ready)) return PAGED_ATTN_ERR_CUDA;
   CUtensorMap qmap, kmap;
-  if (!encode_q_map(&qmap, a.q, a.total, a.Hq, D, a.G, kTile / a.G) ||
-      !encode_rows_map(&kmap, a.k, a.page_rows * a.P, D, page_piece_rows(a.ps, kTile)))
+  if (!encode_q_map(&qmap, a.q, a.total, a.Hq, D, a.G, kRows / a.G) ||
+      !encode_rows_map(&kmap, a.k, a.page_rows * a.P, D, page_piece_rows(a.ps, kRows)))
     return PAGED_ATTN_ERR_CUDA;
-  const long long units = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, kTile);
+  const long long units =
+      static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, Wide<D, kPair>::kKeys);
   count_launches(1);
-  return cuda_status(launch_after_previous(wide_kernel<D>,
-                                           static_cast<int>(units < sms ? units : sms),
-                                           kWideThreads, wide_smem<D>(), st, qmap, kmap, a));
+  return cuda_status(launch_after_previous(kernel, static_cast<int>(units < sms ? units : sms),
+                                           kWideThreads, smem, st, qmap, kmap, a));
 }
 
 template <int D, int NT>
@@ -699,8 +726,12 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   long long rows = ceil_div(p->total_q, p->batch);         // of a request, on average
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
-  if (rows > 16)
-    return p->head_dim == 128 ? launch_wide<128>(a, st) : launch_wide<256>(a, st);
+  if (rows > 16) {
+    const bool pair = rows >= kPairRows;
+    if (p->head_dim == 128)
+      return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
+    return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
+  }
   if (p->head_dim == 128)
     return cuda_status(rows <= 8 ? launch_narrow<128, 1>(a, st)
                                  : (rows <= 16 ? launch_narrow<128, 2>(a, st)
