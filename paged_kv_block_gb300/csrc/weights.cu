@@ -191,28 +191,29 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
 // ---- many rows: prompts ------------------------------------------------------------------------
 // S = Q K^T on the 5th-generation tensor cores: the keys of a unit stay in shared memory while the
 // request's queries stream past them, 128 rows (TMEM lanes) at a time.  A thread owns a row, whose
-// shift -lse log2 e it keeps in a register, and 128 keys, whose sums over its rows it keeps in 128
+// shift -lse log2 e it keeps in a register, and 64 keys, whose sums over its rows it keeps in 64
 // registers until the unit ends and the lanes are summed.  Persistent, one CTA per SM; a unit is a
-// (request, KV head, key tile), and units come in order of their tiles, so that under the causal
-// mask the CTAs take long ones first, in turns that reverse from round to round.  Roles (384
-// threads):
-//   warps 0-3, 4-7  exponentials and sums
-//   warp  8         TMA producer of K and of Q (a ring of 64-column stages)
-//   warp  9         TMEM owner and MMA issuer
-//   warp  11        unit descriptions, page ids among them
-// kPair: tiles of 256 keys; both warpgroups take every query tile, 128 keys each.  Else tiles of
-// 128 keys, and the warpgroups take query tiles in turn.
+// (request, KV head, key tile).  Roles (640 threads):
+//   warps 0-15  exponentials and sums
+//   warp  16    TMA producer of K and of Q (a ring of 64-column stages)
+//   warp  17    TMEM owner and MMA issuer
+//   warp  19    unit descriptions, page ids among them
+// kPair: tiles of 256 keys; the four warpgroups take every query tile, 64 keys each.  Else tiles of
+// 128 keys, and two pairs of warpgroups take query tiles in turn.
 // The queries come from L2 once per key tile: 128 keys ask for 64 bytes per cycle and SM, far above
 // what L2 gives all SMs (some 20), so prompts want the 256; tiles of 128 make more and smaller
 // units and leave room for the next unit's K at D = 256.
-constexpr int kWideThreads = 384;
+constexpr int kGroups = 4;                 // warpgroups of exponentials
+constexpr int kOwn = 64;                   // keys of a thread
+constexpr int kSumWarps = 4 * kGroups;
+constexpr int kWideThreads = 32 * kSumWarps + 128;
 constexpr int kRows = 128;                 // of a query tile
 constexpr int kBlockBytes = kRows * 128;   // 128 rows of 64 columns
 constexpr int kUnits = 4;                  // units described ahead
-// Registers after set-up (launch: 384 x 168): 2 x 128 x 208 + 128 x 88 = 384 x 168.
-constexpr int kSumRegs = 208;
-constexpr int kControlRegs = 88;
-static_assert(2 * 128 * kSumRegs + 128 * kControlRegs <= kWideThreads * 168, "register split");
+// Registers after set-up (launch: 640 x 96): 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int kSumRegs = 104;
+constexpr int kControlRegs = 64;
+static_assert(32 * kSumWarps * kSumRegs + 128 * kControlRegs <= kWideThreads * 96, "registers");
 
 template <int D, bool kPair>
 struct Wide {
@@ -235,7 +236,7 @@ struct Unit {
 };
 struct WideCtrl {
   Unit units[kUnits];
-  alignas(16) float sums[2][8][kRows];     // by unit parity: each warp's sums of its 128 keys
+  alignas(16) float sums[2][kSumWarps][kOwn];    // by unit parity: each warp's sums of its keys
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t s_full[4], s_empty[4];
   uint64_t k_full[2], k_empty[2];
@@ -250,12 +251,12 @@ constexpr int wide_smem() {
          static_cast<int>(sizeof(WideCtrl)) + 1024;
 }
 
-// Exponentials of 32 scores, added to the sums of their keys.  kMask: only keys j <= limit count.
+// Exponentials of 16 scores, added to the sums of their keys.  kMask: only keys j <= limit count.
 template <bool kMask>
-__device__ __forceinline__ void add_weights(float (&sums)[kRows], const uint32_t (&r)[32], int j0,
+__device__ __forceinline__ void add_weights(float (&sums)[kOwn], const uint32_t (&r)[16], int j0,
                                             float scale, float shift, int limit) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
+  for (int j = 0; j < 16; j += 2) {
     float y0, y1;
     ffma2_bcast(y0, y1, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), scale, shift);
     y0 = fast_exp2(y0);
@@ -267,30 +268,24 @@ __device__ __forceinline__ void add_weights(float (&sums)[kRows], const uint32_t
     fadd2(sums[j0 + j], sums[j0 + j + 1], y0, y1);
   }
 }
-// The 128 scores of a row; `done` is called when they have left TMEM.
+// A thread's scores of a row; `done` is called when they have left TMEM.
 template <bool kMask, typename F>
-__device__ __forceinline__ void add_row(float (&sums)[kRows], uint32_t column, float scale,
+__device__ __forceinline__ void add_row(float (&sums)[kOwn], uint32_t column, float scale,
                                         float shift, int limit, const F& done) {
-  uint32_t r0[32], r1[32];
-  tmem_ld32(column, r0);
-  tmem_ld_wait();
-  tmem_ld32(column + 32, r1);
-  add_weights<kMask>(sums, r0, 0, scale, shift, limit);
-  tmem_ld_wait();
-  tmem_ld32(column + 64, r0);
-  add_weights<kMask>(sums, r1, 32, scale, shift, limit);
-  tmem_ld_wait();
-  tmem_ld32(column + 96, r1);
-  add_weights<kMask>(sums, r0, 64, scale, shift, limit);
-  tmem_ld_wait();
-  done();
-  add_weights<kMask>(sums, r1, 96, scale, shift, limit);
+#pragma unroll
+  for (int q = 0; q < kOwn / 16; ++q) {
+    uint32_t r[16];
+    tmem_ld16(column + q * 16, r);
+    tmem_ld_wait();
+    if (q == kOwn / 16 - 1) done();
+    add_weights<kMask>(sums, r, q * 16, scale, shift, limit);
+  }
 }
 
 // Sums over a warp's rows: at each step a lane gives away half of its keys, until lane l has those
-// of keys 4 l .. 4 l + 3.
+// of keys 2 l and 2 l + 1.
 template <int kHalf, int kLane>
-__device__ __forceinline__ void sum_lanes(float (&sums)[kRows], int lane) {
+__device__ __forceinline__ void sum_lanes(float (&sums)[kOwn], int lane) {
   const bool upper = lane & kLane;
 #pragma unroll
   for (int j = 0; j < kHalf; ++j) {
@@ -317,11 +312,11 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&ctl->unit_full[i], 1);
-      mbar_init(&ctl->unit_empty[i], 2 + 8);
+      mbar_init(&ctl->unit_empty[i], 2 + kSumWarps);
     }
     for (int i = 0; i < kSBuffers; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->s_empty[i], kPair ? 8 : 4);
+      mbar_init(&ctl->s_empty[i], kPair ? kSumWarps : kSumWarps / 2);
     }
     for (int i = 0; i < kKBuffers; ++i) {
       mbar_init(&ctl->k_full[i], 1);
@@ -340,7 +335,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     reinterpret_cast<uint4*>(q_s + i / spare * kBlockBytes + TM * a.G * 128)[i % spare] =
         make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
-  if (warp == 9) {
+  if (warp == kSumWarps + 1) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -361,81 +356,90 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     if (lane == 0) mbar_arrive(&ctl->unit_empty[s % kUnits]);
   };
 
-  if (warp >= 8) {
+  if (warp >= kSumWarps) {
   regs_decrease<kControlRegs>();
-  if (warp == 11) {
+  if (warp == kSumWarps + 3) {
     // =============================== units ==============================================
-    // 32 candidates at a time, a lane each; those with keys are described one after another.
-    const int pairs = a.B * a.Hkv;
-    const long long total = static_cast<long long>(pairs) * ((a.W + kKeys - 1) / kKeys);
-    const int R = page_piece_rows(a.ps, kRows), pieces = kKeys / R;
+    // Units in order of the key tiles left to the request's end: a tile's queries are about as many
+    // under the causal mask, so long units come first whatever the lengths.  The CTAs take them in
+    // turns that reverse from round to round.  (In order of the tiles' indexes, with requests of
+    // 8,192 down to 2,048 tokens, the busiest CTA had 1.25 times the mean, so 1.12.)
+    constexpr int kCached = 4;             // tiles of 32 requests each, a lane each
+    const int R = page_piece_rows(a.ps, kRows), pieces = kKeys / R, grid = gridDim.x;
+    const auto count_tiles = [&](int b) {
+      return b < a.B ? (request_of(a, b).keys + kKeys - 1) / kKeys : 0;
+    };
+    int cached[kCached], most = 0;
+#pragma unroll
+    for (int g = 0; g < kCached; ++g) cached[g] = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane, n = count_tiles(b);
+      if (blockIdx.x == 0 && b < a.B && request_of(a, b).bad) report_error(a.status, kErrMetadata);
+#pragma unroll
+      for (int g = 0; g < kCached; ++g)
+        if (b0 == 32 * g) cached[g] = n;
+      most = max(most, n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
     int s = 0;
+    long long before = 0, round = 0, mine = blockIdx.x;      // units before; this CTA's next one
     bool ok = true;
-    for (long long base = 0; ok && base * gridDim.x < total; base += 32) {
-      const long long round = base + lane;
-      const long long u = round * gridDim.x +
-                          (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      Unit x;
-      const int* table = nullptr;
-      bool live = u < total;
-      if (live) {
-        const int c = static_cast<int>(u / pairs);
-        const int bh = static_cast<int>(u - static_cast<long long>(c) * pairs);
-        const int b = bh / a.Hkv;
-        const Request r = request_of(a, b);
-        x.h = bh - b * a.Hkv;
-        if (r.bad && c == 0 && x.h == 0) report_error(a.status, kErrMetadata);
-        x.key0 = c * kKeys;
-        x.keys = min(kKeys, r.keys - x.key0);
-        live = x.keys > 0;
-        x.old = r.old;
-        // the first token that sees a key of the tile
-        const int t0 = a.causal ? min(max(x.key0 - r.first_pos, 0), r.n) : 0;
-        x.row0 = r.row0 + t0;
-        x.tokens = r.n - t0;
-        x.tiles = (x.tokens + TM - 1) / TM;
-        x.pos0 = a.causal ? r.first_pos + t0 : INT_MAX;
-        x.w = static_cast<long long>(bh) * a.W + x.key0;
-        table = r.pages;
-      }
-      uint32_t todo = __ballot_sync(0xffffffffu, live);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int key = __shfl_sync(0xffffffffu, x.key0, src) + lane * R;
-        const int end = __shfl_sync(0xffffffffu, x.key0 + x.keys, src);
-        const int* pages = reinterpret_cast<const int*>(__shfl_sync(
-            0xffffffffu, reinterpret_cast<unsigned long long>(table), src));
-        int page = -1;
-        if (lane < pieces && key < end) {
-          page = __ldg(pages + over(key, a.by_ps));
-          if (page < 0 || page >= a.P) {
-            report_error(a.status, kErrMetadata);
-            page = -1;
+    for (int left = most; ok && left > 0; --left) {
+      for (int b0 = 0; ok && b0 < a.B; b0 += 32) {
+        int n = 0;
+        if (b0 < 32 * kCached) {
+#pragma unroll
+          for (int g = 0; g < kCached; ++g)
+            if (b0 == 32 * g) n = cached[g];
+        } else {
+          n = count_tiles(b0 + lane);
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, n >= left);
+        const long long after = before + static_cast<long long>(__popc(live)) * a.Hkv;
+        while (mine < after) {
+          const int which = static_cast<int>(mine - before) / a.Hkv;
+          const int h = static_cast<int>(mine - before) - which * a.Hkv;
+          const int at = __fns(live, 0, which + 1), b = b0 + at;
+          const Request r = request_of(a, b);
+          const int key0 = (__shfl_sync(0xffffffffu, n, at) - left) * kKeys;
+          const int keys = min(kKeys, r.keys - key0);
+          int page = -1;
+          const int key = key0 + lane * R;
+          if (lane < pieces && key < key0 + keys) {
+            page = __ldg(r.pages + over(key, a.by_ps));
+            if (page < 0 || page >= a.P) {
+              report_error(a.status, kErrMetadata);
+              page = -1;
+            }
           }
+          const int slot = s % kUnits;
+          if (s >= kUnits && !mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
+                                                   a.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          Unit* out = &ctl->units[slot];
+          out->pages[lane] = page;
+          if (lane == 0) {
+            // from the first token on that sees a key of the tile
+            const int t0 = a.causal ? min(max(key0 - r.first_pos, 0), r.n) : 0;
+            out->tiles = (r.n - t0 + TM - 1) / TM;
+            out->h = h;
+            out->key0 = key0;
+            out->keys = keys;
+            out->old = r.old;
+            out->row0 = r.row0 + t0;
+            out->tokens = r.n - t0;
+            out->pos0 = a.causal ? r.first_pos + t0 : INT_MAX;
+            out->w = (static_cast<long long>(b) * a.Hkv + h) * a.W + key0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->unit_full[slot]);
+          ++s;
+          ++round;
+          mine = round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x);
         }
-        const int slot = s % kUnits;
-        if (s >= kUnits && !mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
-                                                 a.status, abort_flag)) {
-          ok = false;
-          break;
-        }
-        Unit* out = &ctl->units[slot];
-        out->pages[lane] = page;
-        if (lane == src) {
-          out->tiles = x.tiles;
-          out->h = x.h;
-          out->key0 = x.key0;
-          out->keys = x.keys;
-          out->old = x.old;
-          out->row0 = x.row0;
-          out->tokens = x.tokens;
-          out->pos0 = x.pos0;
-          out->w = x.w;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->unit_full[slot]);
-        ++s;
+        before = after;
       }
     }
     const int slot = s % kUnits;
@@ -446,7 +450,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         mbar_arrive(&ctl->unit_full[slot]);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kSumWarps) {
     // =============================== copies =============================================
     if (lane == 0) {
       tma_prefetch_desc(&qmap);
@@ -504,7 +508,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       for (int i = max(0, qs - kStages); i < qs; ++i)
         drain_wait(&ctl->q_full[i % kStages], (i / kStages) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == kSumWarps + 1) {
     // =============================== MMAs ===============================================
     constexpr uint32_t idesc_all = idesc_bf16(kRows, kKeys, false, false);
     constexpr uint32_t idesc_half = idesc_bf16(kRows, 128, false, false);
@@ -556,9 +560,10 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   } else {
     regs_increase<kSumRegs>();
     // =============================== exponentials and sums ==============================
-    const int group = warp >> 2, m = threadIdx.x & 127;      // this thread's row, later its key
-    const uint32_t column0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
-                             (kPair ? group * 128 : 0);
+    const int group = warp >> 2, m = threadIdx.x & 127;      // this thread's row
+    // its group's keys, from `first` on, and which of the query tiles it takes
+    const int first = (kPair ? group : group & 1) * kOwn, turn = kPair ? 0 : group >> 1;
+    const uint32_t column0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + first;
     const float scale = a.scale_log2;
     const int R = page_piece_rows(a.ps, kRows);
     const int token = m / a.G;                               // of the row, in its tile
@@ -568,9 +573,11 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     for (int s = 0;; ++s) {
       bool ok = next_unit(s);
       const Unit& x = ctl->units[s % kUnits];
-      const int tiles = ok ? x.tiles : 0, first = kPair ? group * 128 : 0, k = first + m;
+      const int tiles = ok ? x.tiles : 0;
       const int key0 = x.key0 + first, tokens = x.tokens, pos0 = x.pos0;
-      const bool writes = ok && tiles >= 0 && (kPair || group == 0) && k < x.keys &&
+      // the first half of a group that takes turn 0 writes its keys
+      const int k = first + m;
+      const bool writes = ok && tiles >= 0 && turn == 0 && m < kOwn && k < x.keys &&
                           x.pages[k / R] >= 0;
       const bool had = writes && key0 + m < x.old && a.decay != 0.f;
       const bool idle = kPair && x.keys <= first;            // no live key of this group
@@ -578,20 +585,20 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       const float* lse = a.lse + head_row(a, x.row0, x.h, 0) + lse_at;
       if (ok) release(s);
       const float before = had ? *w : 0.f;                   // on its way during the sums
-      float sums[kRows];
+      float sums[kOwn];
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) sums[j] = 0.f;
+      for (int j = 0; j < kOwn; ++j) sums[j] = 0.f;
       const auto load = [&](int i) {
         return token < TM && i * TM + token < tokens ? __ldg(lse + i * lse_step) : -INFINITY;
       };
       constexpr int kStep = kPair ? 1 : 2;
-      const int i0 = kPair ? 0 : group;
+      const int i0 = turn;
       float next = ok && i0 < tiles ? load(i0) : 0.f;
       for (int i = i0; ok && i < tiles; i += kStep) {
         const int t = it + i, buf = t % kSBuffers;
         const float l = next;
         if (i + kStep < tiles) next = load(i + kStep);
-        // keys up to `limit` of this thread's 128 count
+        // keys up to `limit` of this thread's count
         const int limit = l == -INFINITY  ? -1
                           : pos0 == INT_MAX ? INT_MAX
                                             : pos0 + i * TM + token - key0;
@@ -606,31 +613,32 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
           if (lane == 0) mbar_arrive(&ctl->s_empty[buf]);
         };
         if (idle || __all_sync(0xffffffffu, limit < 0)) done();
-        else if (__all_sync(0xffffffffu, limit >= 127))
+        else if (__all_sync(0xffffffffu, limit >= kOwn - 1))
           add_row<false>(sums, column, scale, shift, limit, done);
         else
           add_row<true>(sums, column, scale, shift, limit, done);
       }
       it += tiles;
-      sum_lanes<kRows / 2, 16>(sums, lane);
-      reinterpret_cast<float4*>(ctl->sums[s & 1][warp])[lane] =
-          make_float4(sums[0], sums[1], sums[2], sums[3]);
+      sum_lanes<kOwn / 2, 16>(sums, lane);
+      reinterpret_cast<float2*>(ctl->sums[s & 1][warp])[lane] = make_float2(sums[0], sums[1]);
       // Every warp comes here whatever its waits said and also after the last unit, so that those
       // that meet here leave together.
       const bool leave = !ok || tiles < 0;
-      if (kPair ? named_bar_or(1 + group, 128, leave) : named_bar_or(1, 256, leave)) break;
+      if (kPair ? named_bar_or(1 + group, 128, leave) : named_bar_or(1 + (group & 1), 256, leave))
+        break;
       if (writes) {
         float sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < (kPair ? 4 : 8); ++g)
-          sum += ctl->sums[s & 1][(kPair ? group * 4 : 0) + g][m];
+        for (int t = 0; t < (kPair ? 1 : 2); ++t)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) sum += ctl->sums[s & 1][(group + 2 * t) * 4 + g][m];
         *w = (had ? a.decay * before : 0.f) + sum;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSumWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -727,7 +735,9 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
   if (rows > 16) {
-    const bool pair = rows >= kPairRows;
+    const bool pair = rows >= kPairRows &&
+                      static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, 256) >=
+                          current_sm_count();
     if (p->head_dim == 128)
       return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);

@@ -141,6 +141,22 @@ def test_longer_prompt():
     p.run(last=1000)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (256, 8, 2), (128, 5, 1), (256, 24, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_wide_tiles(D, Hq, Hkv, causal):
+    """Weights wide enough, by their shape, for key tiles of 256."""
+    p = Problem(D + Hq, [700, 300, 513], [700, 251, 400], Hq, Hkv, D, 24, causal=causal, W=60000)
+    p.run(decay=0.5)
+    p.run(last=300)
+
+
+@pytest.mark.parametrize("B", [31, 33, 140])
+def test_many_prompts(B):
+    """The order in which units are handed out goes over 32 requests at a time."""
+    lens = [1 + (37 * b) % 290 for b in range(B)]
+    Problem(B, lens, [max(1, n // 2) for n in lens], 8, 2, 128, 16).run()
+
+
 def test_more_queries_than_keys():
     """Queries before the first key see nothing."""
     p = Problem(6, [3, 40], [10, 41], 8, 2, 128, 16)
