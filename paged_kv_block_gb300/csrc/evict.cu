@@ -8,14 +8,20 @@ namespace {
 
 // ---- select ------------------------------------------------------------------------------------
 // A list is the weights of one (layer, row, KV head).  Its tokens get 32-bit keys whose unsigned
-// order is the order of preference; three passes over the keys' digits (11, 11, 10 bits) find the
-// smallest key that is kept, T, and how many of the tokens with that key are; a last pass writes
-// the indices in order, the tokens at T in index order until their number is reached.
-constexpr int kDigits = 3;
-constexpr int kBins = 2048;
+// order is the order of preference.  The smallest key that is kept, T, is bracketed between keys of
+// which at least and fewer than the wanted number of tokens follow.  The first bracket comes from a
+// sample of 32 keys of every warp; it is cut at pivots by interpolation between its counts, until
+// exactly the wanted number of tokens follow or few enough keys are left in it to be ranked one by
+// one.  Keys stay in registers, kOwn a thread (32; 8 where there are CTAs to spare and time is
+// latency): a step costs two instructions a key and a barrier.  A last pass writes the indices in
+// order, those of key T until their number is reached.
+// Instructions bound it: for 2,048 lists of 8,192 tokens histograms of the keys' digits took 143
+// us (half of the tokens may have the same weight, and then shared-memory atomics queue up), plain
+// bisection 112 us, interpolation between the least and the greatest key 64 us.
 constexpr uint32_t kMustKeep = 0xffffffffu;
 constexpr int kSelectCluster = 8;
-constexpr int kMaxKeys = 40 * 1024;        // keys that a CTA holds in shared memory
+constexpr int kSelectThreads = 1024;
+constexpr int kFewLeft = 64;               // keys that are ranked one by one
 
 struct SelectArgs {
   const int* rows;
@@ -23,7 +29,6 @@ struct SelectArgs {
   const float* weights;                    // [N, R, Hkv, W]
   const int* lens;
   int* kept;                               // [N, n, Hkv, K]
-  int held;                                // keys that fit into shared memory
   uint32_t* status;
 };
 
@@ -34,16 +39,282 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ SelectArgs a) {
-  extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ int hist[kBins];
-  __shared__ int warp_sums[32];
-  __shared__ int found[2];                 // digit of the threshold, tokens above it
-  __shared__ int totals[2];                // of this CTA: tokens above T, tokens at T
+// What the warps and CTAs of a list exchange, in shared memory; two buffers used in turn, so that a
+// barrier orders each.
+struct SelectShared {
+  uint32_t warps[2][2][32];
+  uint32_t cta[2][2][kSelectCluster];
+  uint32_t left[kFewLeft], lefts, found[3];    // the last keys of the bracket; T, its counts
+};
+
+// The tokens [begin, begin + count) of a list, this CTA's share of it.
+template <bool kHeld, int kOwn>
+__device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& sh, const float* w,
+                                            int L, int begin, int count, int* out) {
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), size = cl.num_blocks();
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int warps = threads >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // Warp v goes through tokens from v * run on, a lane each, 32 at a time.
+  const int run = kHeld ? 32 * kOwn : ((count + warps - 1) / warps + 31) / 32 * 32;
+  const int first = min(warp * run, count), last = min(first + run, count);
+  const int kept_from = L - a.recent;
+  const auto make_key = [&](int t, float x) {
+    const int j = begin + t;
+    return j < a.sink || j >= kept_from ? kMustKeep : weight_key(x);
+  };
+  // few warps have tokens that are kept whatever their weight
+  const bool ends = begin + first < a.sink || begin + last > kept_from;
+  uint32_t held[kOwn];                     // keys past the end are 0, below every pivot
+  if (kHeld) {
+    const float* mine = w + begin + first + lane;
+    const int mine_left = last - first - lane;
+    float x[kOwn];                         // all loads on their way together
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) x[e] = e * 32 < mine_left ? __ldcs(mine + e * 32) : NAN;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) held[e] = weight_key(x[e]);
+    if (ends) {
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e)
+        if (e * 32 < mine_left) held[e] = make_key(first + e * 32 + lane, x[e]);
+    }
+  }
+  const auto load_key = [&](int t) { return t < last ? make_key(t, w[begin + t]) : 0u; };
+  int turn = 0;
+  // Both values over all threads of the list: op(x, y) of two lanes, zero for none.
+  const auto exchange = [&](uint32_t& x, uint32_t& y, const auto& warp_op_x,
+                            const auto& warp_op_y, uint32_t zero_x, uint32_t zero_y) {
+    x = warp_op_x(x);
+    y = warp_op_y(y);
+    if (lane == 0) {
+      sh.warps[turn][0][warp] = x;
+      sh.warps[turn][1][warp] = y;
+    }
+    __syncthreads();
+    x = warp_op_x(lane < warps ? sh.warps[turn][0][lane] : zero_x);
+    y = warp_op_y(lane < warps ? sh.warps[turn][1][lane] : zero_y);
+    if (size > 1) {
+      if (warp == 0 && lane < size) {
+        *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = x;
+        *cl.map_shared_rank(&sh.cta[turn][1][rank], lane) = y;
+      }
+      cl.sync();
+      x = warp_op_x(lane < size ? sh.cta[turn][0][lane] : zero_x);
+      y = warp_op_y(lane < size ? sh.cta[turn][1][lane] : zero_y);
+    }
+    turn ^= 1;
+  };
+  const auto min_of = [](uint32_t v) { return __reduce_min_sync(0xffffffffu, v); };
+  const auto max_of = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
+  const auto sum = [](uint32_t v) { return __reduce_add_sync(0xffffffffu, v); };
+  const auto own_count = [&](uint32_t pivot) {               // of this thread; pivot > 0
+    uint32_t p[4] = {0, 0, 0, 0};
+    if (kHeld) {
+      // key >= pivot is the carry of key + (2^32 - pivot)
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e)
+        asm("{\n\t.reg .u32 t;\n\tadd.cc.u32 t, %1, %2;\n\taddc.u32 %0, %0, 0;\n\t}"
+            : "+r"(p[e & 3])
+            : "r"(held[e]), "r"(0u - pivot));
+    } else {
+      for (int t0 = first; t0 < last; t0 += 32) p[0] += load_key(t0 + lane) >= pivot;
+    }
+    return (p[0] + p[1]) + (p[2] + p[3]);
+  };
+  const auto count_from = [&](uint32_t pivot) {
+    uint32_t c = sum(own_count(pivot));
+    if (lane == 0) sh.warps[turn][0][warp] = c;
+    __syncthreads();
+    c = sum(lane < warps ? sh.warps[turn][0][lane] : 0u);
+    if (size > 1) {
+      if (warp == 0 && lane < size) *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = c;
+      cl.sync();
+      c = sum(lane < size ? sh.cta[turn][0][lane] : 0u);
+    }
+    turn ^= 1;
+    return static_cast<int>(c);
+  };
+  // from_low tokens have keys >= low, at least K; above of them keys >= high, fewer than K (K where
+  // it ends early).
+  uint32_t low = 0u, high = kMustKeep;
+  int from_low = L, above = a.sink + a.recent;
+  bool done = above == a.K;                // nothing else is kept
+  // The sample: every warp with 32 keys, all of them open, takes the one at the wanted place in their
+  // order, and the least and the greatest of those are the first two pivots (one key where many
+  // tokens have it).
+  uint32_t from = kMustKeep, to = 0u;
+  if (threadIdx.x == 0) sh.lefts = 0;      // (the barriers of the exchange order it)
+  if (last - first >= 32 && !ends) {
+    const uint32_t mine = kHeld ? held[0] : load_key(first + lane);
+    uint32_t not_less = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) not_less += __shfl_sync(0xffffffffu, mine, j) >= mine;
+    const uint32_t place = static_cast<uint32_t>(32LL * (a.K - above) / (L - above));
+    from = to = max_of(not_less > place ? mine : 0u);
+  }
+  exchange(from, to, min_of, max_of, kMustKeep, 0u);
+  if (from > to) from = to = 0xbf800000u;  // no sample: some weight
+  from = min(max(from, 1u), kMustKeep - 2);
+  to = min(max(to, from), kMustKeep - 2) + 1;
+  uint32_t leap = max(to - from, 1u << 16);    // past the sample, where T is not inside
+  // Then the root of count - K.  An end that stays while the other one moves twice in a row loses
+  // half of its weight; every fourth pivot is the middle.
+  float f_low = 1.f, f_high = 1.f;
+  int moved = 0;
+  for (int step = 0; !done && high - low > 1; ++step) {
+    if (kHeld && size == 1 && step >= 2 && from_low - above <= kFewLeft) {
+      // The keys in the bracket, ranked by the first warp.
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e)
+        if (held[e] - low < high - low && first + e * 32 + lane < last)
+          sh.left[atomicAdd(&sh.lefts, 1)] = held[e];
+      __syncthreads();
+      if (warp == 0) {
+        const int n = from_low - above, wanted = a.K - above;
+#pragma unroll
+        for (int x0 = 0; x0 < kFewLeft; x0 += 32) {
+          const int x = x0 + lane;
+          if (x >= n) break;
+          const uint32_t mine = sh.left[x];
+          int more = 0, same = 0;
+          for (int j = 0; j < n; ++j) {
+            more += sh.left[j] > mine;
+            same += sh.left[j] == mine;
+          }
+          if (more < wanted && wanted <= more + same) {      // the same for all that are T
+            sh.found[0] = mine;
+            sh.found[1] = more;
+            sh.found[2] = same;
+          }
+        }
+      }
+      __syncthreads();
+      low = sh.found[0];
+      high = low + 1;
+      above += sh.found[1];
+      from_low = above + sh.found[2];
+      break;
+    }
+    uint32_t pivot;
+    if (step < 2) {
+      pivot = step == 0 ? from : to;
+      if (pivot <= low || pivot >= high) continue;
+    } else if (low == 0u || high == kMustKeep) {
+      pivot = low == 0u ? (high > leap ? high - leap : 1u)
+                        : (high - low > leap ? low + leap : high - 1);
+      leap = leap < 1u << 28 ? leap * 8 : 1u << 31;
+    } else {
+      const uint32_t width = high - low;
+      uint32_t d = width / 2;
+      if (step == 6 && low == from) d = 1;     // the key of many tokens?
+      else if ((step & 3) != 3)
+        d = static_cast<uint32_t>(static_cast<float>(width) * __fdividef(f_low, f_low + f_high));
+      pivot = low + min(max(d, 1u), width - 1);
+    }
+    const int c = count_from(pivot);
+    if (c == a.K) {                        // exactly the keys from here on are kept
+      high = pivot;
+      above = c;
+      done = true;
+    } else if (c > a.K) {
+      low = pivot;
+      from_low = c;
+      f_low = static_cast<float>(c - a.K) + 0.5f;
+      if (moved > 0) f_high *= 0.5f;
+      moved = 1;
+    } else {
+      high = pivot;
+      above = c;
+      f_high = static_cast<float>(a.K - c) - 0.5f;
+      if (moved < 0) f_low *= 0.5f;
+      moved = -1;
+    }
+  }
+  // Kept: the keys >= high and, while they last, the first K - above tokens with key low.  Where
+  // there is nothing to choose among those, the keys from one cut on.
+  const int need = a.K - above;
+  const bool choose = need > 0 && need < from_low - above;
+  const uint32_t cut = need > 0 ? low : high;
+  uint32_t gt = 0, eq = 0;                 // tokens from the cut on (choose: above it), and at it
+  const auto tally = [&](uint32_t k, bool live) {
+    if (!live) return;
+    gt += choose ? k > cut : k >= cut;
+    eq += k == cut;
+  };
+  if (kHeld && cut > 0 && !choose) {
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) gt += held[e] >= cut;
+  } else if (kHeld) {
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) tally(held[e], first + e * 32 + lane < last);
+  } else {
+    for (int t0 = first; t0 < last; t0 += 32) tally(load_key(t0 + lane), t0 + lane < last);
+  }
+  gt = sum(gt);
+  eq = sum(eq);
+  if (lane == 0) {
+    sh.warps[turn][0][warp] = gt;
+    sh.warps[turn][1][warp] = eq;
+  }
+  __syncthreads();
+  const int g = lane < warps ? sh.warps[turn][0][lane] : 0;
+  const int q = lane < warps ? sh.warps[turn][1][lane] : 0;
+  const int gs = warp_inclusive(g), qs = warp_inclusive(q);
+  int gt_before = __shfl_sync(0xffffffffu, gs - g, warp);
+  int eq_before = __shfl_sync(0xffffffffu, qs - q, warp);
+  if (size > 1) {
+    const int all_gt = __shfl_sync(0xffffffffu, gs, 31), all_eq = __shfl_sync(0xffffffffu, qs, 31);
+    if (warp == 0 && lane < size) {
+      *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = all_gt;
+      *cl.map_shared_rank(&sh.cta[turn][1][rank], lane) = all_eq;
+    }
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      gt_before += sh.cta[turn][0][r];
+      eq_before += sh.cta[turn][1][r];
+    }
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  if (kHeld && cut > 0 && !choose) {
+    int* to = out + gt_before;
+    const int token = begin + first + lane;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const bool keep = held[e] >= cut;
+      const uint32_t m = __ballot_sync(0xffffffffu, keep);
+      if (keep) to[__popc(m & below)] = token + e * 32;
+      to += __popc(m);
+    }
+    return;
+  }
+  for (int t0 = first, e = 0; t0 < last; t0 += 32, ++e) {
+    uint32_t k;
+    if (kHeld) {
+      k = held[0];
+#pragma unroll
+      for (int x = 1; x < kOwn; ++x) k = e == x ? held[x] : k;
+    } else {
+      k = load_key(t0 + lane);
+    }
+    const bool in = t0 + lane < last;
+    const uint32_t gm = __ballot_sync(0xffffffffu, in && (choose ? k > cut : k >= cut));
+    const uint32_t qm = __ballot_sync(0xffffffffu, choose && in && k == cut);
+    const int rank_eq = choose ? eq_before + __popc(qm & below) : 0;
+    const bool is_eq = choose && k == cut;
+    if (in && (is_eq ? rank_eq < need : k >= cut))
+      out[gt_before + __popc(gm & below) + min(rank_eq, need)] = begin + t0 + lane;
+    gt_before += __popc(gm);
+    eq_before += __popc(qm);
+  }
+}
+
+template <int kOwn>
+__global__ void __launch_bounds__(kSelectThreads)
+select_kernel(const __grid_constant__ SelectArgs a) {
+  __shared__ SelectShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), size = cl.num_blocks();
+  const int tid = threadIdx.x, threads = blockDim.x;
   grid_dependency_wait();
   grid_launch_dependents();
   const int list = blockIdx.x / size;      // ((layer, item), head)
@@ -61,100 +332,12 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
     for (int j = rank * threads + tid; j < a.K; j += size * threads) out[j] = j < L ? j : -1;
     return;
   }
-  // This CTA's tokens [begin, begin + count), a whole number of warps' words in all but the last.
+  if (size > 1) cl.sync();                 // every CTA's shared memory is there
   const int per = ((L + size - 1) / size + 31) / 32 * 32;
   const int begin = min(rank * per, L), count = min(per, L - begin);
   const float* w = a.weights + ((static_cast<long long>(layer) * a.R + row) * a.Hkv + h) * a.W;
-  const auto make_key = [&](int t) {       // of token begin + t
-    const int j = begin + t;
-    return j < a.sink || j >= L - a.recent ? kMustKeep : weight_key(w[j]);
-  };
-  const bool held = count <= a.held;
-  if (held)
-    for (int t = tid; t < count; t += threads) keys[t] = make_key(t);
-  const auto key = [&](int t) { return held ? keys[t] : make_key(t); };
-  uint32_t prefix = 0;                     // digits of T found so far
-  int need = a.K;                          // tokens still wanted among those with that prefix
-  for (int d = 0; d < kDigits; ++d) {
-    const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bits = d == 2 ? 10 : 11;
-    const uint32_t above = d == 0 ? 0u : ~0u << (shift + bits);
-    for (int b = tid; b < kBins; b += threads) hist[b] = 0;
-    __syncthreads();
-    for (int t = tid; t < count; t += threads) {
-      const uint32_t k = key(t);
-      if ((k & above) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
-    }
-    sync_cluster(cl);
-    // Bins from the top, kBins / threads of them per thread (at most 1024 threads, at least 256).
-    const int mine = kBins / threads;
-    int sum = 0, c[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      c[b] = 0;
-      if (b >= mine) break;
-      const int bin = kBins - 1 - (tid * mine + b);
-      for (int r = 0; r < size; ++r) c[b] += *cl.map_shared_rank(hist + bin, r);
-      sum += c[b];
-    }
-    int total;
-    int before = block_scan(sum, warp_sums, &total);
-    if (before < need && before + sum >= need) {
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (b >= mine) break;
-        if (before < need && before + c[b] >= need) {
-          found[0] = kBins - 1 - (tid * mine + b);
-          found[1] = before;
-        }
-        before += c[b];
-      }
-    }
-    sync_cluster(cl);                      // found is set, and every CTA has read the histograms
-    prefix |= static_cast<uint32_t>(found[0]) << shift;
-    need -= found[1];
-    __syncthreads();
-  }
-  // need of the tokens with key T = prefix are kept, the first ones.  Each warp writes a run of its
-  // own: it counts, the counts are summed, it writes.
-  const int run = ((count + warps - 1) / warps + 31) / 32 * 32;
-  const int first = min(warp * run, count), last = min(first + run, count);
-  int gt = 0, eq = 0;
-  for (int t0 = first; t0 < last; t0 += 32) {
-    const uint32_t k = t0 + lane < last ? key(t0 + lane) : 0u;
-    const bool in = t0 + lane < last;
-    gt += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
-  }
-  int all_gt, all_eq;
-  int gt_before = block_scan(lane == 0 ? gt : 0, warp_sums, &all_gt);
-  int eq_before = block_scan(lane == 0 ? eq : 0, warp_sums, &all_eq);
-  gt_before = __shfl_sync(0xffffffffu, gt_before, 0);
-  eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
-  if (size > 1) {
-    if (tid == 0) {
-      totals[0] = all_gt;
-      totals[1] = all_eq;
-    }
-    cl.sync();
-    for (int r = 0; r < rank; ++r) {
-      gt_before += *cl.map_shared_rank(totals, r);
-      eq_before += *cl.map_shared_rank(totals + 1, r);
-    }
-    cluster_arrive();                      // no CTA ends while another reads its totals
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int t0 = first; t0 < last; t0 += 32) {
-    const bool in = t0 + lane < last;
-    const uint32_t k = in ? key(t0 + lane) : 0u;
-    const uint32_t g = __ballot_sync(0xffffffffu, in && k > prefix);
-    const uint32_t e = __ballot_sync(0xffffffffu, in && k == prefix);
-    const int eq_rank = eq_before + __popc(e & below);
-    const bool keep = in && (k > prefix || (k == prefix && eq_rank < need));
-    if (keep) out[gt_before + __popc(g & below) + min(eq_rank, need)] = begin + t0 + lane;
-    gt_before += __popc(g);
-    eq_before += __popc(e);
-  }
-  if (size > 1) cluster_wait();
+  if (per <= threads * kOwn) select_list<true, kOwn>(a, sh, w, L, begin, count, out);
+  else select_list<false, kOwn>(a, sh, w, L, begin, count, out);
 }
 
 // ---- evict -------------------------------------------------------------------------------------
@@ -483,17 +666,16 @@ int paged_cache_select_run(const paged_cache_select_params* p, const int32_t* ro
   a.rows = rows; a.n = n; a.R = p->rows; a.N = p->num_layers; a.Hkv = p->num_kv_heads;
   a.W = p->width; a.K = p->keep; a.sink = p->sink; a.recent = p->recent;
   a.weights = weights; a.lens = lens; a.kept = kept; a.status = status;
+  // A cluster where there are few lists and long ones; threads for all of a list's keys.
   int size = 1;
-  while (size < kSelectCluster && lists * size * 2 <= sms && p->width / size > 2048) size *= 2;
-  const int per = (ceil_div(p->width, size) + 31) / 32 * 32;
-  a.held = per < kMaxKeys ? per : kMaxKeys;
-  const int threads = per <= 2048 ? 256 : (per <= 16384 ? 512 : 1024);
-  static std::atomic<uint64_t> ready{0};
-  if (!kernel_smem_ready(select_kernel, kMaxKeys * 4, ready)) return PAGED_ATTN_ERR_CUDA;
+  while (size < kSelectCluster && lists * size * 2 <= sms && p->width / size > 8192) size *= 2;
+  const int per = ceil_div(p->width, size);
+  const bool few = lists * size <= 2 * sms && per <= 8 * kSelectThreads;
+  int threads = (ceil_div(per, few ? 8 : 32) + 31) / 32 * 32;
+  threads = threads < 64 ? 64 : (threads > kSelectThreads ? kSelectThreads : threads);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = static_cast<unsigned>(lists * size);
   cfg.blockDim = threads;
-  cfg.dynamicSmemBytes = a.held * 4;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -504,7 +686,8 @@ int paged_cache_select_run(const paged_cache_select_params* p, const int32_t* ro
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launches(1);
-  return cuda_status(cudaLaunchKernelEx(&cfg, select_kernel, a));
+  return cuda_status(few ? cudaLaunchKernelEx(&cfg, select_kernel<8>, a)
+                         : cudaLaunchKernelEx(&cfg, select_kernel<32>, a));
 }
 
 size_t paged_cache_evict_workspace_size(int n, int keep, int page_size) {
