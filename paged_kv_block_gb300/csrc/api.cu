@@ -1067,7 +1067,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   d.scale_log2 = scale * kLog2e;
   d.out_scale = 1.f;
   d.window_left = -1;
-  d.parts_only = 1;
+  d.parts_only = s.tile_capacity > 0 ? 2 : 1;
   if (launch_decode(d, st) != 0) return PAGED_ATTN_ERR_CUDA;
   return launch_shared_merge(m, st) == 0 ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA;
 }

@@ -238,6 +238,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   // so that the CTA takes one branch.
   if constexpr (!FACTS) {
     grid_dependency_wait();
+    if constexpr (PART) grid_launch_dependents();   // the tails' kernel reads nothing of this one
     if (threadIdx.x == 0) {
       const int n0 = a.n_tiles ? *a.n_tiles : a.capacity;
       ctl->skip = (static_cast<int>(blockIdx.x) >= n0 || launch_aborted(a.status)) ? 1 : 0;

@@ -207,11 +207,19 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
     tma_prefetch_desc(&qmap);
   }
   // everything below reads the plan, which the launch before this one writes
-  grid_dependency_wait();
+  // (__ldcg: in the second case this kernel has not waited for its writer itself)
+  if (a.parts_only != 2) grid_dependency_wait();
   if (threadIdx.x == 0) sm->skip = launch_aborted(a.status) ? 1 : 0;
   __syncthreads();
-  if (sm->skip) return;
-  const int n_items = a.Hkv * a.split_offset[a.B];
+  if (sm->skip) {
+    if (a.parts_only == 2) grid_dependency_wait();
+    return;
+  }
+  const int n_items = a.Hkv * __ldcg(a.split_offset + a.B);
+  const auto item_of = [&](int item) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(a.items + item));
+    return SplitItem{v.x, v.y, v.z, v.w};
+  };
   volatile int* abort_flag = &sm->abort_flag;
 
   if (warp == kProducerWarp) {
@@ -238,8 +246,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         break;
       }
-      item = __ldg(a.order + item);
-      const SplitItem it = a.items[item];
+      item = __ldcg(a.order + item);
+      const SplitItem it = item_of(item);
       if (lane == 0) {
         sm->item_id[islot] = item;
         uint8_t* qdst = qslots + islot * 2 * qhalf;
@@ -352,7 +360,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         break;
       }
-      const SplitItem it = a.items[item];
+      const SplitItem it = item_of(item);
       const int b = it.b, g = it.g;
       const int kv_begin = it.kv_begin, kv_end = it.kv_end;
       const int first_key = (kv_begin / kStageKeys) * kStageKeys;
@@ -591,7 +599,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       }
       named_bar(1, kConsumerWarps * 32);
       const int d = threadIdx.x;   // 0..127: one output column
-      const int n_split = a.split_offset[b + 1] - a.split_offset[b];
+      const int n_split = __ldcg(a.split_offset + b + 1) - __ldcg(a.split_offset + b);
       const int live_rows = nq <= 0 ? 0 : (nq * G < M ? nq * G : M);
       for (int m = 0; m < live_rows; ++m) {
         float Mx = -INFINITY;
@@ -638,6 +646,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       if (have_stage && lane == 0) mbar_arrive(&sm->empty[last_slot]);
     }
   }
+  if (a.parts_only == 2) grid_dependency_wait();
 }
 
 template <int NRB, bool ROWMASK>

@@ -187,7 +187,9 @@ struct DecodeLaunch {
   int capacity;              // launched work items
   float scale_log2, out_scale;
   int window_left;
-  int parts_only;            // 1: every item writes its partial and nothing is merged
+  int parts_only;            // 1, 2: every item writes its partial and nothing is merged; 2: the
+                             // launch before this one has waited for the plan, so only this one's
+                             // end waits for that launch
   void* timer_token;
 };
 int launch_decode(const DecodeLaunch& a, cudaStream_t st);

@@ -14,55 +14,49 @@ constexpr int kThreads = 1024;
 constexpr int kD = 128;
 constexpr int kTailSplits = 16;            // tail items aimed at per SM
 
-__device__ __forceinline__ int warp_inclusive(int v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += y;
-  }
-  return v;
+// Two sums in one 64-bit word: the upper and the lower half.
+__device__ __forceinline__ long long pack(long long upper, int lower) {
+  return upper << 32 | static_cast<unsigned>(lower);
 }
+__device__ __forceinline__ int upper_of(long long x) { return static_cast<int>(x >> 32); }
+__device__ __forceinline__ int lower_of(long long x) { return static_cast<int>(x); }
 // Exclusive prefix sum over the CTA of 1024 threads.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,
+                                                long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int v = warp_inclusive(x);
+  const auto inclusive = [&](long long v) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += y;
+    }
+    return v;
+  };
+  const long long v = inclusive(x);
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  const int w = warp_inclusive(warp_sums[lane]);
-  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  const long long w = inclusive(warp_sums[lane]);
+  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   *total = __shfl_sync(0xffffffffu, w, 31);
   __syncthreads();
   return (warp > 0 ? before : 0) + v - x;
 }
-__device__ __forceinline__ long long block_sum(long long x, long long* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-  if (lane == 0) warp_sums[warp] = x;
-  __syncthreads();
-  long long s = warp_sums[lane];
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-  __syncthreads();
-  return s;
-}
 
-// Keys of request b that all of its queries see, at most.
-__device__ __forceinline__ int visible_to_all(const SharedLaunch& a, int b) {
-  const int L = max(a.lens[b], 0);
-  return a.causal ? max(L - a.SQ + 1, 0) : L;
-}
 __device__ __forceinline__ int tail_base(int prefix) { return prefix / 128 * 128; }
+__device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1) / kKvTile; }
 
 // One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
 // sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts for about
-// `target` CTAs.  Requests: what is left, split as decode splits it.
+// `target` CTAs.  Requests: what is left, split as decode splits it.  Latency bounds it: the
+// lengths stay in shared memory (up to kHeld requests), tiles and items are counted in one scan.
+constexpr int kHeld = 8192;
 __global__ void __launch_bounds__(kThreads)
 shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
-  __shared__ int warp_sums[32];
-  __shared__ long long wide_sums[32];
+  extern __shared__ int held[];            // [2, B]: lengths, shared keys
+  __shared__ long long sums[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool hold = a.B <= kHeld;
+  int* prefix = hold ? held + a.B : a.prefix_of;
   grid_dependency_wait();
   grid_launch_dependents();
   if (tid < 4) a.status[tid] = 0;
@@ -73,70 +67,115 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     bad |= at < 0 || at > a.B || (g > 0 && a.group_indptr[g - 1] > at);
   }
   for (int b = tid; b < a.B; b += kThreads) {
-    a.prefix_of[b] = 0;
-    a.refs[b] = {0, 0, 0, 0};
+    if (hold) held[b] = max(a.lens[b], 0);
+    prefix[b] = 0;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) report_error(a.status, kErrMetadata);
   const int groups = bad ? 0 : a.groups;
+  const auto length = [&](int b) { return hold ? held[b] : max(a.lens[b], 0); };
   // a warp per group
   const int tile_tokens = 2 * (kMTileRows / a.G);
   for (int g = warp; g < groups; g += kThreads / 32) {
     const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
-    int n = INT_MAX;
-    for (int b = first + lane; b < last; b += 32) n = min(n, visible_to_all(a, b));
-    n = min(__reduce_min_sync(0xffffffffu, n), a.prefix_lens[g]);
-    if (n <= 0 || last - first < 2) continue;
-    for (int b = first + lane; b < last; b += 32) a.prefix_of[b] = n;
+    int n = a.prefix_lens[g];
+    if (last - first < 2) continue;
+    for (int b = first + lane; b < last; b += 32)          // what all queries of b see
+      n = min(n, a.causal ? length(b) - a.SQ + 1 : length(b));
+    n = __reduce_min_sync(0xffffffffu, n);
+    if (n <= 0) continue;
+    for (int b = first + lane; b < last; b += 32) prefix[b] = n;
   }
   __syncthreads();
-  // steps of 128 keys of all the prefixes' tiles, and of all the tails
-  const auto group_tiles = [&](int g, int& keys) {       // row tiles of group g
+  // a thread per group and per request: steps of 128 keys of all tiles, and of all tails
+  const auto row_tiles = [&](int g) {
     const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
-    keys = last > first ? (a.prefix_of[first] + kKvTile - 1) / kKvTile : 0;
-    return keys == 0 ? 0 : ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
+    if (last <= first || prefix[first] == 0) return 0;
+    return ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
   };
   long long steps = 0, tails = 0;
   for (int g = tid; g < groups; g += kThreads) {
-    int keys;
-    const int rows = group_tiles(g, keys);
-    steps += static_cast<long long>(rows) * keys;
+    const int rows = row_tiles(g);
+    if (rows > 0) steps += static_cast<long long>(rows) * ceil_tiles(prefix[a.group_indptr[g]]);
   }
-  for (int b = tid; b < a.B; b += kThreads) {
-    const int L = max(a.lens[b], 0), base = tail_base(a.prefix_of[b]);
-    tails += (L - base + kKvTile - 1) / kKvTile;
+  for (int b = tid; b < a.B; b += kThreads) tails += ceil_tiles(length(b) - tail_base(prefix[b]));
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    steps += __shfl_xor_sync(0xffffffffu, steps, d);
+    tails += __shfl_xor_sync(0xffffffffu, tails, d);
   }
-  steps = block_sum(steps, wide_sums) * a.Hkv;
-  tails = block_sum(tails, wide_sums) * a.Hkv;
+  if (lane == 0) {
+    sums[0][warp] = steps;
+    sums[1][warp] = tails;
+  }
+  __syncthreads();
+  steps = sums[0][lane];
+  tails = sums[1][lane];
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    steps += __shfl_xor_sync(0xffffffffu, steps, d);
+    tails += __shfl_xor_sync(0xffffffffu, tails, d);
+  }
+  steps *= a.Hkv;
+  tails *= a.Hkv;
+  __syncthreads();
   const int part = static_cast<int>(max((steps + a.target - 1) / a.target, 1LL));
   const long long aim = static_cast<long long>(kTailSplits) * a.target;
   const long long chunk = max((tails + aim - 1) / aim, 1LL) * kKvTile;
-  // tiles of the prefixes
-  int carry = 0;
-  for (int g0 = 0; g0 < groups; g0 += kThreads) {
-    const int g = g0 + tid;
-    int keys = 0, rows = 0, splits = 0;
-    if (g < groups) rows = group_tiles(g, keys);
-    if (rows > 0) splits = (keys + part - 1) / part;
-    int sum;
-    const int base = carry + block_scan(rows * splits * a.Hkv, warp_sums, &sum);
-    carry += sum;
-    if (rows == 0) continue;
-    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
-    for (int b = first; b < last; ++b) a.refs[b] = {base, splits, rows, (b - first) * a.SQ};
+  const auto splits_of = [&](int b) {      // of the tail of request b
+    const int left = length(b) - tail_base(prefix[b]);
+    return length(b) > prefix[b] ? static_cast<int>((left + chunk - 1) / chunk) : 0;
+  };
+  // tiles before each group, items before each request
+  int tiles = 0, items = 0;
+  for (int x0 = 0; x0 < max(groups, a.B); x0 += kThreads) {
+    const int x = x0 + tid;
+    int rows = 0, splits = 0, keys = 0;
+    if (x < groups) rows = row_tiles(x);
+    if (rows > 0) {
+      keys = ceil_tiles(prefix[a.group_indptr[x]]);
+      splits = (keys + part - 1) / part;
+    }
+    const int n = x < a.B ? splits_of(x) : 0;
+    long long total;
+    const long long before =
+        block_scan(pack(static_cast<long long>(rows) * splits * a.Hkv, n), sums[0], &total);
+    if (rows > 0)                          // the group's first request keeps it for all of them
+      a.refs[a.group_indptr[x]] = {tiles + upper_of(before), splits, rows, 0};
+    if (x < a.B) a.split_offset[x] = items + lower_of(before);
+    tiles += upper_of(total);
+    items += lower_of(total);
   }
-  if (carry > a.tile_capacity) {           // cannot be: the capacity is this sum's bound
-    carry = 0;
+  // (cannot be: the capacities are these sums' bounds)
+  const bool fits = tiles <= a.tile_capacity &&
+                    static_cast<long long>(items) * a.Hkv <= a.item_capacity;
+  if (!fits) {
+    tiles = items = 0;
     if (tid == 0) report_error(a.status, kErrCapacity);
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kThreads) a.split_offset[b] = 0;
   }
-  if (tid == 0) *a.n_tiles = carry;
+  if (tid == 0) {
+    *a.n_tiles = tiles;
+    a.split_offset[a.B] = items;
+  }
   __syncthreads();
-  for (int g = warp; carry > 0 && g < groups; g += kThreads / 32) {
-    int keys;
-    const int rows = group_tiles(g, keys);
+  if (hold)
+    for (int b = tid; b < a.B; b += kThreads) a.prefix_of[b] = prefix[b];
+  // requests outside every group, or in one that shares nothing
+  for (int b = tid; b < a.B; b += kThreads)
+    if (prefix[b] == 0 || !fits) a.refs[b] = {0, 0, 0, 0};
+  for (int g = warp; fits && g < groups; g += kThreads / 32) {
+    const int rows = row_tiles(g);
     if (rows == 0) continue;
     const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
-    const PrefixRef ref = a.refs[first];
+    const int keys = ceil_tiles(prefix[first]);
+    PrefixRef ref = a.refs[first];
+    __syncwarp();
+    for (int b = first + lane; b < last; b += 32) {
+      ref.token = (b - first) * a.SQ;
+      a.refs[b] = ref;
+    }
     const int tokens = (last - first) * a.SQ, count = rows * ref.splits * a.Hkv;
     for (int k = lane; k < count; k += 32) {
       const int s = k % ref.splits, r = k / ref.splits % rows, h = k / ref.splits / rows;
@@ -152,31 +191,8 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
       a.tiles[ref.base + k] = t;
     }
   }
-  // items of the tails, in list order
-  carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < a.B) {
-      const int L = max(a.lens[b], 0), p = a.prefix_of[b];
-      if (L > p) n = static_cast<int>((L - tail_base(p) + chunk - 1) / chunk);
-    }
-    int sum;
-    const int at = carry + block_scan(n, warp_sums, &sum);
-    if (b < a.B) a.split_offset[b] = at;
-    carry += sum;
-  }
-  if (static_cast<long long>(carry) * a.Hkv > a.item_capacity) {   // cannot be, likewise
-    if (tid == 0) report_error(a.status, kErrCapacity);
-    carry = 0;
-    __syncthreads();
-    for (int b = tid; b < a.B; b += kThreads) a.split_offset[b] = 0;
-  }
-  if (tid == 0) a.split_offset[a.B] = carry;
-  __syncthreads();
-  for (int b = warp; b < a.B; b += kThreads / 32) {
-    const int L = max(a.lens[b], 0), p = a.prefix_of[b];
-    const int at = a.split_offset[b], n = a.split_offset[b + 1] - at;
+  for (int b = warp; items > 0 && b < a.B; b += kThreads / 32) {
+    const int L = length(b), p = prefix[b], at = a.split_offset[b], n = splits_of(b);
     for (int k = lane; k < n * a.Hkv; k += 32) {
       const int s = k % n;
       SplitItem it;
@@ -259,7 +275,11 @@ shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
 
 int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
   count_launches(1);
-  return launch_after_previous(shared_plan_kernel, dim3(1), dim3(kThreads), 0, st, a) == cudaSuccess
+  const size_t smem = a.B <= kHeld ? 2 * sizeof(int) * static_cast<size_t>(a.B) : 0;
+  static std::atomic<uint64_t> ready{0};
+  if (smem > 47 * 1024 && !kernel_smem_ready(shared_plan_kernel, 8 * kHeld, ready)) return -1;
+  return launch_after_previous(shared_plan_kernel, dim3(1), dim3(kThreads), smem, st, a) ==
+                 cudaSuccess
              ? 0
              : -1;
 }
