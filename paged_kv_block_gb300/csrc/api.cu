@@ -351,8 +351,8 @@ bool shared_params_ok(const paged_decode_params* p, int num_groups) {
 }
 
 // Capacities bound what the plan's rules can give (prefix.cu): the key parts of a group's tiles are
-// as many as its tiles plus its share of one part per SM; a tail's splits one plus its share of 16
-// per SM.
+// as many as its tiles plus its share of one part per SM; a tail's splits one plus its share of
+// kTailSplits per SM.
 SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   SharedLayout s{};
   Layout l;
@@ -360,7 +360,7 @@ SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   const int sms = num_sms(), pairs = num_groups < B / 2 ? num_groups : B / 2;
   s.tile_capacity =
       pairs == 0 ? 0 : sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
-  s.item_capacity = 16 * sms + p->num_kv_heads * B;
+  s.item_capacity = kTailSplits * sms + p->num_kv_heads * B;
   s.status = l.take(sizeof(uint32_t) * 4);
   s.n_tiles = l.take(sizeof(int));
   s.counter = l.take(sizeof(int));
@@ -984,7 +984,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   m.SQ = SQ;
   m.groups = num_groups;
   m.causal = p->mask_type == PAGED_ATTN_MASK_CAUSAL;
-  m.target = num_sms();
+  m.sms = num_sms();
   m.prefix_of = at<int>(ws, s.prefix_of);
   m.refs = at<PrefixRef>(ws, s.refs);
   m.tiles = at<TileRec>(ws, s.tiles);

@@ -601,6 +601,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       const int d = threadIdx.x;   // 0..127: one output column
       const int n_split = __ldcg(a.split_offset + b + 1) - __ldcg(a.split_offset + b);
       const int live_rows = nq <= 0 ? 0 : (nq * G < M ? nq * G : M);
+#pragma unroll 4
       for (int m = 0; m < live_rows; ++m) {
         float Mx = -INFINITY;
         float Lsum = 0.f, acc = 0.f;

@@ -195,6 +195,7 @@ struct DecodeLaunch {
 int launch_decode(const DecodeLaunch& a, cudaStream_t st);
 
 // ---- shared prefixes (prefix.cu) -----------------------------------------------------------------
+constexpr int kTailSplits = 8;       // tail items aimed at per SM
 // A request's prefix partials: rows 256 (base + (head * row_tiles + tile) * splits + s) of the
 // tensor-core kernel's partial output, s < splits; its queries are tokens from `token` on among
 // the group's, 256 / G of them to a tile.
@@ -205,7 +206,7 @@ struct SharedLaunch {
   const int* lens;
   const int* group_indptr;   // [groups + 1]
   const int* prefix_lens;    // [groups]
-  int B, Hq, Hkv, G, SQ, groups, causal, target;
+  int B, Hq, Hkv, G, SQ, groups, causal, sms;
   // plan
   int* prefix_of;            // [B] shared keys of the request, 0 none
   PrefixRef* refs;           // [B]

@@ -10,9 +10,12 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;             // of the planning CTA, or
+constexpr int kFewThreads = 256;           // for so many groups and requests
 constexpr int kD = 128;
-constexpr int kTailSplits = 16;            // tail items aimed at per SM
+// SM time in microseconds of a step of 256 rows (128, where a group has no more) and 128 keys, and
+// of 128 keys of a tail, as measured: the SMs are shared out by them.
+constexpr float kStepCost = 2.0f, kHalfStepCost = 1.2f, kTailCost = 1.4f;
 
 // Two sums in one 64-bit word: the upper and the lower half.
 __device__ __forceinline__ long long pack(long long upper, int lower) {
@@ -20,7 +23,7 @@ __device__ __forceinline__ long long pack(long long upper, int lower) {
 }
 __device__ __forceinline__ int upper_of(long long x) { return static_cast<int>(x >> 32); }
 __device__ __forceinline__ int lower_of(long long x) { return static_cast<int>(x); }
-// Exclusive prefix sum over the CTA of 1024 threads.
+// Exclusive prefix sum over the CTA.
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums,
                                                 long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -35,7 +38,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   const long long v = inclusive(x);
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  const long long w = inclusive(warp_sums[lane]);
+  const long long w = inclusive(lane < static_cast<int>(blockDim.x >> 5) ? warp_sums[lane] : 0);
   const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   *total = __shfl_sync(0xffffffffu, w, 31);
   __syncthreads();
@@ -46,15 +49,20 @@ __device__ __forceinline__ int tail_base(int prefix) { return prefix / 128 * 128
 __device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1) / kKvTile; }
 
 // One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
-// sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts for about
-// `target` CTAs.  Requests: what is left, split as decode splits it.  Latency bounds it: the
-// lengths stay in shared memory (up to kHeld requests), tiles and items are counted in one scan.
+// sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts.  Requests:
+// what is left, split as decode splits it.  The kernels of the two run side by side, a prefix CTA or
+// two tail CTAs on an SM, so the prefixes are cut into parts for their share of the SMs: 64
+// requests with tails of some 300 keys behind 8,192 common ones took 64 us with parts for all SMs,
+// one kernel after the other.  Latency bounds this kernel: the lengths stay in shared memory (up to
+// kHeld requests), tiles and items are counted in one scan.
 constexpr int kHeld = 8192;
 __global__ void __launch_bounds__(kThreads)
 shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   extern __shared__ int held[];            // [2, B]: lengths, shared keys
   __shared__ long long sums[2][32];
+  __shared__ float costs[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, warps = threads >> 5;
   const bool hold = a.B <= kHeld;
   int* prefix = hold ? held + a.B : a.prefix_of;
   grid_dependency_wait();
@@ -62,11 +70,11 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   if (tid < 4) a.status[tid] = 0;
   if (tid == 0) *a.work_counter = 0;
   bool bad = false;
-  for (int g = tid; g <= a.groups; g += kThreads) {
+  for (int g = tid; g <= a.groups; g += threads) {
     const int at = a.group_indptr[g];
     bad |= at < 0 || at > a.B || (g > 0 && a.group_indptr[g - 1] > at);
   }
-  for (int b = tid; b < a.B; b += kThreads) {
+  for (int b = tid; b < a.B; b += threads) {
     if (hold) held[b] = max(a.lens[b], 0);
     prefix[b] = 0;
   }
@@ -76,7 +84,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   const auto length = [&](int b) { return hold ? held[b] : max(a.lens[b], 0); };
   // a warp per group
   const int tile_tokens = 2 * (kMTileRows / a.G);
-  for (int g = warp; g < groups; g += kThreads / 32) {
+  for (int g = warp; g < groups; g += warps) {
     const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
     int n = a.prefix_lens[g];
     if (last - first < 2) continue;
@@ -94,33 +102,46 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     return ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
   };
   long long steps = 0, tails = 0;
-  for (int g = tid; g < groups; g += kThreads) {
+  float cost = 0.f;                        // of the steps
+  for (int g = tid; g < groups; g += threads) {
     const int rows = row_tiles(g);
-    if (rows > 0) steps += static_cast<long long>(rows) * ceil_tiles(prefix[a.group_indptr[g]]);
+    if (rows == 0) continue;
+    const int first = a.group_indptr[g];
+    const long long n = static_cast<long long>(rows) * ceil_tiles(prefix[first]);
+    steps += n;
+    cost += n * (2 * (a.group_indptr[g + 1] - first) * a.SQ <= tile_tokens ? kHalfStepCost
+                                                                           : kStepCost);
   }
-  for (int b = tid; b < a.B; b += kThreads) tails += ceil_tiles(length(b) - tail_base(prefix[b]));
+  for (int b = tid; b < a.B; b += threads) tails += ceil_tiles(length(b) - tail_base(prefix[b]));
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     steps += __shfl_xor_sync(0xffffffffu, steps, d);
     tails += __shfl_xor_sync(0xffffffffu, tails, d);
+    cost += __shfl_xor_sync(0xffffffffu, cost, d);
   }
   if (lane == 0) {
     sums[0][warp] = steps;
     sums[1][warp] = tails;
+    costs[warp] = cost;
   }
   __syncthreads();
-  steps = sums[0][lane];
-  tails = sums[1][lane];
+  steps = lane < warps ? sums[0][lane] : 0;
+  tails = lane < warps ? sums[1][lane] : 0;
+  cost = lane < warps ? costs[lane] : 0.f;
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     steps += __shfl_xor_sync(0xffffffffu, steps, d);
     tails += __shfl_xor_sync(0xffffffffu, tails, d);
+    cost += __shfl_xor_sync(0xffffffffu, cost, d);
   }
   steps *= a.Hkv;
   tails *= a.Hkv;
+  cost *= a.Hkv;
   __syncthreads();
-  const int part = static_cast<int>(max((steps + a.target - 1) / a.target, 1LL));
-  const long long aim = static_cast<long long>(kTailSplits) * a.target;
+  const float share = cost / (cost + kTailCost * tails + 1e-6f);
+  const int parts = max(static_cast<int>(a.sms * share + 0.5f), 1);
+  const int part = static_cast<int>(max((steps + parts - 1) / parts, 1LL));
+  const long long aim = static_cast<long long>(kTailSplits) * a.sms;
   const long long chunk = max((tails + aim - 1) / aim, 1LL) * kKvTile;
   const auto splits_of = [&](int b) {      // of the tail of request b
     const int left = length(b) - tail_base(prefix[b]);
@@ -128,7 +149,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   };
   // tiles before each group, items before each request
   int tiles = 0, items = 0;
-  for (int x0 = 0; x0 < max(groups, a.B); x0 += kThreads) {
+  for (int x0 = 0; x0 < max(groups, a.B); x0 += threads) {
     const int x = x0 + tid;
     int rows = 0, splits = 0, keys = 0;
     if (x < groups) rows = row_tiles(x);
@@ -153,7 +174,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     tiles = items = 0;
     if (tid == 0) report_error(a.status, kErrCapacity);
     __syncthreads();
-    for (int b = tid; b < a.B; b += kThreads) a.split_offset[b] = 0;
+    for (int b = tid; b < a.B; b += threads) a.split_offset[b] = 0;
   }
   if (tid == 0) {
     *a.n_tiles = tiles;
@@ -161,11 +182,11 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   }
   __syncthreads();
   if (hold)
-    for (int b = tid; b < a.B; b += kThreads) a.prefix_of[b] = prefix[b];
+    for (int b = tid; b < a.B; b += threads) a.prefix_of[b] = prefix[b];
   // requests outside every group, or in one that shares nothing
-  for (int b = tid; b < a.B; b += kThreads)
+  for (int b = tid; b < a.B; b += threads)
     if (prefix[b] == 0 || !fits) a.refs[b] = {0, 0, 0, 0};
-  for (int g = warp; fits && g < groups; g += kThreads / 32) {
+  for (int g = warp; fits && g < groups; g += warps) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
     const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
@@ -191,7 +212,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
       a.tiles[ref.base + k] = t;
     }
   }
-  for (int b = warp; items > 0 && b < a.B; b += kThreads / 32) {
+  for (int b = warp; items > 0 && b < a.B; b += warps) {
     const int L = length(b), p = prefix[b], at = a.split_offset[b], n = splits_of(b);
     for (int k = lane; k < n * a.Hkv; k += 32) {
       const int s = k % n;
@@ -275,10 +296,11 @@ shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
 
 int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
   count_launches(1);
+  const int threads = a.B <= 2 * kFewThreads && a.groups < kFewThreads ? kFewThreads : kThreads;
   const size_t smem = a.B <= kHeld ? 2 * sizeof(int) * static_cast<size_t>(a.B) : 0;
   static std::atomic<uint64_t> ready{0};
   if (smem > 47 * 1024 && !kernel_smem_ready(shared_plan_kernel, 8 * kHeld, ready)) return -1;
-  return launch_after_previous(shared_plan_kernel, dim3(1), dim3(kThreads), smem, st, a) ==
+  return launch_after_previous(shared_plan_kernel, dim3(1), dim3(threads), smem, st, a) ==
                  cudaSuccess
              ? 0
              : -1;
