@@ -333,7 +333,7 @@ SageLayout sage_layout(const paged_sage_params* p) {
 
 // ---- decode with shared prefixes ----------------------------------------------------------
 struct SharedLayout {
-  size_t status, n_tiles, counter, prefix_of, refs, tiles, split_off, items, order;
+  size_t status, n_tiles, max_ctas, counter, prefix_of, refs, tiles, split_off, items;
   size_t pre_lse, pre_o, tail_lse, tail_o, total;
   int tile_capacity, item_capacity;
 };
@@ -350,16 +350,15 @@ bool shared_params_ok(const paged_decode_params* p, int num_groups) {
   return static_cast<long long>(p->batch) * decode_q_per_item(p) * p->num_kv_heads < (1LL << 27);
 }
 
-// Capacities bound what the plan's rules can give (prefix.cu): the key parts of a group's tiles are
-// as many as its tiles plus its share of one part per SM; a tail's splits one plus its share of
-// kTailSplits per SM.
+// Capacities: one part per tile of a prefix and two more per SM (the plan chooses parts that fit,
+// prefix.cu); a tail's splits are one plus its share of kTailSplits per SM.
 SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   SharedLayout s{};
   Layout l;
   const int G = p->num_qo_heads / p->num_kv_heads, SQ = decode_q_per_item(p), B = p->batch;
   const int sms = num_sms(), pairs = num_groups < B / 2 ? num_groups : B / 2;
   s.tile_capacity =
-      pairs == 0 ? 0 : sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
+      pairs == 0 ? 0 : 2 * sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
   s.item_capacity = kTailSplits * sms + p->num_kv_heads * B;
   s.status = l.take(sizeof(uint32_t) * 4);
   s.n_tiles = l.take(sizeof(int));
@@ -369,7 +368,7 @@ SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   s.tiles = l.take(sizeof(TileRec) * static_cast<size_t>(s.tile_capacity));
   s.split_off = l.take(sizeof(int) * (static_cast<size_t>(B) + 1));
   s.items = l.take(sizeof(SplitItem) * static_cast<size_t>(s.item_capacity));
-  s.order = l.take(sizeof(int) * static_cast<size_t>(s.item_capacity));
+  s.max_ctas = l.take(sizeof(int));
   const size_t tile_rows = static_cast<size_t>(s.tile_capacity) * 2 * kMTileRows;
   const size_t tail_rows = static_cast<size_t>(s.item_capacity) * G * SQ;
   s.pre_lse = l.take(sizeof(float) * tile_rows);
@@ -992,7 +991,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   m.tile_capacity = s.tile_capacity;
   m.split_offset = at<int>(ws, s.split_off);
   m.items = at<SplitItem>(ws, s.items);
-  m.order = at<int>(ws, s.order);
+  m.max_ctas = at<int>(ws, s.max_ctas);
   m.item_capacity = s.item_capacity;
   m.work_counter = at<int>(ws, s.counter);
   m.status = status;
@@ -1030,6 +1029,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
     t.scale_log2 = scale * kLog2e;
     t.out_scale = 1.f;
     t.parts = 1;
+    t.max_ctas = m.max_ctas;
     void* tok;
     timer_begin(st, &tok);
     const int rc = launch_attn(t, st);
@@ -1051,7 +1051,6 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   d.seq_lens = seq_lens;
   d.split_offset = m.split_offset;
   d.items = m.items;
-  d.order = m.order;
   d.part_o = at<float>(ws, s.tail_o);
   d.part_lse = at<float>(ws, s.tail_lse);
   d.status = status;

@@ -241,7 +241,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     if constexpr (PART) grid_launch_dependents();   // the tails' kernel reads nothing of this one
     if (threadIdx.x == 0) {
       const int n0 = a.n_tiles ? *a.n_tiles : a.capacity;
-      ctl->skip = (static_cast<int>(blockIdx.x) >= n0 || launch_aborted(a.status)) ? 1 : 0;
+      const int ctas0 = PART ? min(static_cast<int>(gridDim.x), *a.max_ctas) : n0;
+      ctl->skip = (static_cast<int>(blockIdx.x) >= min(n0, ctas0) || launch_aborted(a.status)) ? 1
+                                                                                               : 0;
     }
   }
   tc_fence_before();
@@ -251,12 +253,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   if constexpr (!FACTS) {
     if (ctl->skip) {
       if (warp == 9) tmem_dealloc(tmem, 512);
-      if (threadIdx.x == 0 && static_cast<int>(gridDim.x) < (a.n_tiles ? *a.n_tiles : a.capacity))
+      if (threadIdx.x == 0 && (PART ? min(static_cast<int>(gridDim.x), *a.max_ctas)
+                                    : static_cast<int>(gridDim.x)) <
+                                  (a.n_tiles ? *a.n_tiles : a.capacity))
         claims_done(a.status);
       return;
     }
   }
   const int n_live = a.n_tiles ? *a.n_tiles : a.capacity;
+  // CTAs that take tiles: tile c is CTA c's first one, the others are claimed
+  const int ctas =
+      PART ? min(static_cast<int>(gridDim.x), *a.max_ctas) : static_cast<int>(gridDim.x);
   volatile int* abort_flag = &ctl->abort_flag;
   // The tile of claim sequence s >= 1 (sequence 0 is tile blockIdx.x, never in the ring; the
   // ring holds sequence s as entry s - 1), read by one warp (all lanes) or by one thread
@@ -283,9 +290,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     int v = n_live;
     if (lane == 0) {
       // nothing to claim when every tile is some CTA's first (small plans): no round trip
-      if (free && static_cast<int>(gridDim.x) < n_live)
-        v = min(n_live, static_cast<int>(gridDim.x) +
-                            static_cast<int>(atomicAdd(a.status + 2, 1u)));
+      if (free && ctas < n_live)
+        v = min(n_live, ctas + static_cast<int>(atomicAdd(a.status + 2, 1u)));
       ctl->tidx[slot] = v;
       mbar_arrive(&ctl->t_full[slot]);
     }
@@ -887,7 +893,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && static_cast<int>(gridDim.x) < n_live) claims_done(a.status);
+  if (threadIdx.x == 0 && ctas < n_live) claims_done(a.status);
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();

@@ -246,7 +246,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         break;
       }
-      item = __ldcg(a.order + item);
+      if (a.order) item = __ldcg(a.order + item);
       const SplitItem it = item_of(item);
       if (lane == 0) {
         sm->item_id[islot] = item;
@@ -601,32 +601,46 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       const int d = threadIdx.x;   // 0..127: one output column
       const int n_split = __ldcg(a.split_offset + b + 1) - __ldcg(a.split_offset + b);
       const int live_rows = nq <= 0 ? 0 : (nq * G < M ? nq * G : M);
-#pragma unroll 4
-      for (int m = 0; m < live_rows; ++m) {
-        float Mx = -INFINITY;
-        float Lsum = 0.f, acc = 0.f;
+      const bool direct = n_split == 1 && !a.parts_only;
+      // Thread m: the weights of row m's slices (in the place of their maxima), its sum (in the
+      // place of its first) and its LSE, once for all columns.
+      if (d < live_rows) {
+        float Mx = -INFINITY, Lsum = 0.f;
         if (have_stage) {
-          for (int w = 0; w < kg; ++w) Mx = fmaxf(Mx, sm->red_m[w * M + m]);
+          for (int w = 0; w < kg; ++w) Mx = fmaxf(Mx, sm->red_m[w * M + d]);
           const float Mu = Mx == -INFINITY ? 0.f : Mx;
           for (int w = 0; w < kg; ++w) {
-            const float f = fast_exp2(sm->red_m[w * M + m] - Mu);
-            Lsum += f * sm->red_l[w * M + m];
-            acc += f * red_o[(w * M + m) * kD + d];
+            const float f = fast_exp2(sm->red_m[w * M + d] - Mu);
+            Lsum += f * sm->red_l[w * M + d];
+            sm->red_m[w * M + d] = f;
           }
           Mx = Mu;
         }
-        const float on = Lsum > 0.f ? acc / Lsum : 0.f;
+        sm->red_l[d] = Lsum;
         const float lse_nat = Lsum > 0.f ? (Mx + fast_log2(Lsum)) * kLn2 : -INFINITY;
-        if (n_split == 1 && !a.parts_only) {
+        const int qrow = q_row0 + d / G;
+        if (!direct)
+          a.part_lse[static_cast<long long>(item) * M + d] = lse_nat;
+        else if (a.lse && qrow >= 0 && qrow < a.q_rows)
+          a.lse[static_cast<long long>(qrow) * a.Hq + g * G + d % G] = lse_nat;
+      }
+      named_bar(1, kConsumerWarps * 32);
+#pragma unroll 4
+      for (int m = 0; m < live_rows; ++m) {
+        float acc = 0.f;
+        if (have_stage) {
+#pragma unroll
+          for (int w = 0; w < kg; ++w) acc += sm->red_m[w * M + m] * red_o[(w * M + m) * kD + d];
+        }
+        const float Lsum = sm->red_l[m];
+        const float on = Lsum > 0.f ? acc / Lsum : 0.f;
+        if (direct) {
           const int qrow = q_row0 + m / G;
           if (qrow < 0 || qrow >= a.q_rows) continue;
           const long long orow = static_cast<long long>(qrow) * a.Hq + g * G + m % G;
           store_out1(a.out, orow * kD + d, on * a.out_scale, a.out_dtype);
-          if (a.lse && d == 0) a.lse[orow] = lse_nat;
         } else {
-          const long long prow = static_cast<long long>(item) * M + m;
-          a.part_o[prow * kD + d] = on;
-          if (d == 0) a.part_lse[prow] = lse_nat;
+          a.part_o[(static_cast<long long>(item) * M + m) * kD + d] = on;
         }
       }
       if (n_split > 1 && !a.parts_only) {

@@ -176,7 +176,7 @@ struct DecodeLaunch {
   const int* seq_lens;
   const int* split_offset;
   const SplitItem* items;
-  const int* order;          // claim order: the k-th claimed item is items[order[k]]
+  const int* order;          // claim order: the k-th claimed item is items[order[k]]; or nullptr
   float* part_o;             // [items, M, D]
   float* part_lse;           // [items, M]
   void* out;                 // [q_rows, Hq, D] of out_dtype
@@ -213,9 +213,9 @@ struct SharedLaunch {
   TileRec* tiles;            // tiles of the prefixes, *n_tiles of them
   int* n_tiles;
   int tile_capacity;
+  int* max_ctas;             // CTAs that the prefixes get
   int* split_offset;         // [B + 1] splits of the tails
   SplitItem* items;
-  int* order;
   int item_capacity;         // items of all KV heads
   int* work_counter;
   uint32_t* status;
@@ -260,6 +260,7 @@ struct AttnLaunch {
   int causal, window_left;
   float scale_log2, out_scale;
   int parts;                 // 1: fp32 partial outputs by tile (row 256 pad + 128 w + m), not by row
+  const int* max_ctas;       // parts: device count of the CTAs that take tiles, the others end
   // Prequantized form (all nullptr otherwise): score scale q_scale[b * q_scale_stride +
   // token / q_scale_group] * k_scale[b * k_scale_stride + key / kv_block_size], output column
   // d scaled by v_scale[b * v_scale_stride + d]; every scale positive.

@@ -16,6 +16,9 @@ constexpr int kD = 128;
 // SM time in microseconds of a step of 256 rows (128, where a group has no more) and 128 keys, and
 // of 128 keys of a tail, as measured: the SMs are shared out by them.
 constexpr float kStepCost = 2.0f, kHalfStepCost = 1.2f, kTailCost = 1.4f;
+constexpr float kTileCost = 6.0f;          // of a part of a prefix besides its steps
+constexpr int kPartChoices = 32;           // lengths of parts that are weighed up, one per lane
+constexpr int kOrdered = 1024;             // groups that are ordered by the lengths of their parts
 
 // Two sums in one 64-bit word: the upper and the lower half.
 __device__ __forceinline__ long long pack(long long upper, int lower) {
@@ -50,17 +53,19 @@ __device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1
 
 // One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
 // sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts.  Requests:
-// what is left, split as decode splits it.  The kernels of the two run side by side, a prefix CTA or
-// two tail CTAs on an SM, so the prefixes are cut into parts for their share of the SMs: 64
+// what is left, split as decode splits it.  The kernels of the two run side by side, a prefix CTA
+// or two tail CTAs on an SM, so the prefixes are cut into parts for their share of the SMs: 64
 // requests with tails of some 300 keys behind 8,192 common ones took 64 us with parts for all SMs,
-// one kernel after the other.  Latency bounds this kernel: the lengths stay in shared memory (up to
-// kHeld requests), tiles and items are counted in one scan.
+// one kernel after the other.  Latency bounds this kernel: the lengths stay in shared memory (up
+// to kHeld requests), tiles and items are counted in one scan.
 constexpr int kHeld = 8192;
 __global__ void __launch_bounds__(kThreads)
 shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   extern __shared__ int held[];            // [2, B]: lengths, shared keys
-  __shared__ long long sums[2][32];
-  __shared__ float costs[32];
+  __shared__ long long sums[32];
+  __shared__ float costs[3][32];
+  __shared__ float items_at[kPartChoices];
+  __shared__ int chosen[2], sizes[kOrdered], order[kOrdered];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, warps = threads >> 5;
   const bool hold = a.B <= kHeld;
@@ -101,68 +106,109 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     if (last <= first || prefix[first] == 0) return 0;
     return ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
   };
-  long long steps = 0, tails = 0;
-  float cost = 0.f;                        // of the steps
+  const auto step_cost = [&](int g) {
+    const int tokens = (a.group_indptr[g + 1] - a.group_indptr[g]) * a.SQ;
+    return 2 * tokens <= tile_tokens ? kHalfStepCost : kStepCost;
+  };
+  float steps = 0.f, cost = 0.f;           // of the tiles
+  int tails = 0;
   for (int g = tid; g < groups; g += threads) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
-    const int first = a.group_indptr[g];
-    const long long n = static_cast<long long>(rows) * ceil_tiles(prefix[first]);
+    const float n = static_cast<float>(rows) * ceil_tiles(prefix[a.group_indptr[g]]);
     steps += n;
-    cost += n * (2 * (a.group_indptr[g + 1] - first) * a.SQ <= tile_tokens ? kHalfStepCost
-                                                                           : kStepCost);
+    cost += n * step_cost(g);
   }
   for (int b = tid; b < a.B; b += threads) tails += ceil_tiles(length(b) - tail_base(prefix[b]));
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     steps += __shfl_xor_sync(0xffffffffu, steps, d);
-    tails += __shfl_xor_sync(0xffffffffu, tails, d);
     cost += __shfl_xor_sync(0xffffffffu, cost, d);
   }
+  tails = __reduce_add_sync(0xffffffffu, tails);
   if (lane == 0) {
-    sums[0][warp] = steps;
-    sums[1][warp] = tails;
-    costs[warp] = cost;
+    costs[0][warp] = steps;
+    costs[1][warp] = cost;
+    costs[2][warp] = static_cast<float>(tails);
+  }
+  if (tid < kPartChoices) items_at[tid] = 0.f;
+  __syncthreads();
+  // Keys (in tiles) of a part: a choice per lane.  Few long parts leave CTAs idle at the end, many
+  // short ones pay kTileCost more often and write more partials.
+  const int choice = 1 << (lane / 2) | (lane & 1 ? 1 << (lane / 2) >> 1 : 0);   // 1 1 2 3 4 6 8 ..
+  for (int g = warp; g < groups; g += warps) {
+    const int rows = row_tiles(g);
+    if (rows > 0)
+      atomicAdd(&items_at[lane], static_cast<float>(rows) *    // (exact below 2^24)
+                                     ((ceil_tiles(prefix[a.group_indptr[g]]) + choice - 1) / choice));
   }
   __syncthreads();
-  steps = lane < warps ? sums[0][lane] : 0;
-  tails = lane < warps ? sums[1][lane] : 0;
-  cost = lane < warps ? costs[lane] : 0.f;
+  if (warp == 0) {
+    float x = lane < warps ? costs[0][lane] : 0.f, y = lane < warps ? costs[1][lane] : 0.f;
+    float z = lane < warps ? costs[2][lane] : 0.f;
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
-    steps += __shfl_xor_sync(0xffffffffu, steps, d);
-    tails += __shfl_xor_sync(0xffffffffu, tails, d);
-    cost += __shfl_xor_sync(0xffffffffu, cost, d);
+    for (int d = 16; d > 0; d /= 2) {
+      x += __shfl_xor_sync(0xffffffffu, x, d);
+      y += __shfl_xor_sync(0xffffffffu, y, d);
+      z += __shfl_xor_sync(0xffffffffu, z, d);
+    }
+    x *= a.Hkv;
+    y *= a.Hkv;
+    z *= a.Hkv;
+    // the prefixes' share of the SMs, and the time that a choice takes on it
+    const float each = x > 0.f ? y / x : 0.f, count = items_at[lane] * a.Hkv;
+    const float work = y + count * kTileCost;
+    const float share = work / (work + kTailCost * z + 1e-6f);
+    const int ctas = max(static_cast<int>(a.sms * share + 0.5f), 1);
+    const float longest = choice * each + kTileCost;
+    float time = count <= ctas ? longest : work / ctas + 0.5f * longest;
+    if (count > a.tile_capacity) time = 3.4e38f;
+    const uint32_t best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));
+    const int pick = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(time) == best)) - 1;
+    if (lane == pick) {
+      chosen[0] = count > a.tile_capacity ? 1 << 30 : choice;
+      *a.max_ctas = ctas;
+    }
+    const float aim = static_cast<float>(kTailSplits * a.sms);
+    if (lane == 0) chosen[1] = max(static_cast<int>(ceilf(z / aim)), 1);
   }
-  steps *= a.Hkv;
-  tails *= a.Hkv;
-  cost *= a.Hkv;
   __syncthreads();
-  const float share = cost / (cost + kTailCost * tails + 1e-6f);
-  const int parts = max(static_cast<int>(a.sms * share + 0.5f), 1);
-  const int part = static_cast<int>(max((steps + parts - 1) / parts, 1LL));
-  const long long aim = static_cast<long long>(kTailSplits) * a.sms;
-  const long long chunk = max((tails + aim - 1) / aim, 1LL) * kKvTile;
+  const int part = chosen[0], chunk = chosen[1];             // in tiles of 128 keys
   const auto splits_of = [&](int b) {      // of the tail of request b
-    const int left = length(b) - tail_base(prefix[b]);
-    return length(b) > prefix[b] ? static_cast<int>((left + chunk - 1) / chunk) : 0;
+    const int L = length(b), p = prefix[b];
+    return L > p ? (ceil_tiles(L - tail_base(p)) + chunk - 1) / chunk : 0;
   };
+  // Groups with the longest parts first, where they are few enough to be ordered by counting.
+  const bool ordered = groups <= threads && groups <= kOrdered;
+  if (ordered) {
+    const auto size_of = [&](int g) {
+      if (row_tiles(g) == 0) return 0;
+      const int keys = ceil_tiles(prefix[a.group_indptr[g]]), n = (keys + part - 1) / part;
+      return (keys + n - 1) / n;
+    };
+    if (tid < groups) sizes[tid] = size_of(tid);
+    __syncthreads();
+    if (tid < groups) {
+      int rank = 0;
+      const int mine = sizes[tid];
+      for (int g = 0; g < groups; ++g) rank += sizes[g] > mine || (sizes[g] == mine && g < tid);
+      order[rank] = tid;
+    }
+    __syncthreads();
+  }
   // tiles before each group, items before each request
   int tiles = 0, items = 0;
   for (int x0 = 0; x0 < max(groups, a.B); x0 += threads) {
-    const int x = x0 + tid;
-    int rows = 0, splits = 0, keys = 0;
-    if (x < groups) rows = row_tiles(x);
-    if (rows > 0) {
-      keys = ceil_tiles(prefix[a.group_indptr[x]]);
-      splits = (keys + part - 1) / part;
-    }
+    const int x = x0 + tid, g = x < groups && ordered ? order[x] : x;
+    int rows = 0, splits = 0;
+    if (x < groups) rows = row_tiles(g);
+    if (rows > 0) splits = (ceil_tiles(prefix[a.group_indptr[g]]) + part - 1) / part;
     const int n = x < a.B ? splits_of(x) : 0;
     long long total;
     const long long before =
-        block_scan(pack(static_cast<long long>(rows) * splits * a.Hkv, n), sums[0], &total);
+        block_scan(pack(static_cast<long long>(rows) * splits * a.Hkv, n), sums, &total);
     if (rows > 0)                          // the group's first request keeps it for all of them
-      a.refs[a.group_indptr[x]] = {tiles + upper_of(before), splits, rows, 0};
+      a.refs[a.group_indptr[g]] = {tiles + upper_of(before), splits, rows, 0};
     if (x < a.B) a.split_offset[x] = items + lower_of(before);
     tiles += upper_of(total);
     items += lower_of(total);
@@ -181,11 +227,11 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     a.split_offset[a.B] = items;
   }
   __syncthreads();
-  if (hold)
-    for (int b = tid; b < a.B; b += threads) a.prefix_of[b] = prefix[b];
-  // requests outside every group, or in one that shares nothing
-  for (int b = tid; b < a.B; b += threads)
+  for (int b = tid; b < a.B; b += threads) {
+    if (hold) a.prefix_of[b] = prefix[b];
+    // requests outside every group, or in one that shares nothing
     if (prefix[b] == 0 || !fits) a.refs[b] = {0, 0, 0, 0};
+  }
   for (int g = warp; fits && g < groups; g += warps) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
@@ -212,17 +258,18 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
       a.tiles[ref.base + k] = t;
     }
   }
-  for (int b = warp; items > 0 && b < a.B; b += warps) {
-    const int L = length(b), p = prefix[b], at = a.split_offset[b], n = splits_of(b);
-    for (int k = lane; k < n * a.Hkv; k += 32) {
-      const int s = k % n;
+  // a thread per request and KV head
+  for (int x = tid; items > 0 && x < a.B * a.Hkv; x += threads) {
+    const int b = x / a.Hkv, h = x - b * a.Hkv, n = splits_of(b);
+    const int L = length(b), p = prefix[b];
+    SplitItem* to = a.items + static_cast<long long>(a.split_offset[b]) * a.Hkv + h * n;
+    for (int s = 0; s < n; ++s) {
       SplitItem it;
       it.b = b;
-      it.g = k / n;
-      it.kv_begin = s == 0 ? p : static_cast<int>(tail_base(p) + s * chunk);
-      it.kv_end = static_cast<int>(min(tail_base(p) + (s + 1) * chunk, static_cast<long long>(L)));
-      a.items[at * a.Hkv + k] = it;
-      a.order[at * a.Hkv + k] = at * a.Hkv + k;
+      it.g = h;
+      it.kv_begin = s == 0 ? p : tail_base(p) + s * chunk * kKvTile;
+      it.kv_end = s == n - 1 ? L : tail_base(p) + (s + 1) * chunk * kKvTile;
+      to[s] = it;
     }
   }
 }
@@ -253,35 +300,60 @@ shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
   const int M = a.SQ * a.G;
   const long long tail0 =
       (static_cast<long long>(at) * a.Hkv + static_cast<long long>(h) * tails) * M + i * a.G + e;
-  const int n = ref.splits + tails;
-  const auto row_of = [&](int s) {
-    return s < ref.splits ? pre0 + static_cast<long long>(s) * (2 * kMTileRows)
-                          : tail0 + static_cast<long long>(s - ref.splits) * M;
-  };
-  float top = -INFINITY;
-  for (int s = lane; s < n; s += 32)
-    top = fmaxf(top, __ldcg((s < ref.splits ? a.pre_lse : a.tail_lse) + row_of(s)));
+  // Two runs of partials, each at a stride of its own.
+  const long long step[2] = {2 * kMTileRows, M};
+  const long long row0[2] = {pre0, tail0};
+  const int count[2] = {ref.splits, tails};
+  const float* lses[2] = {a.pre_lse + row0[0], a.tail_lse + row0[1]};
+  const float4* outs[2] = {reinterpret_cast<const float4*>(a.pre_o + row0[0] * kD) + lane,
+                           reinterpret_cast<const float4*>(a.tail_o + row0[1] * kD) + lane};
+  float top = -INFINITY, first[2];         // first: of the first 32 partials, a lane each
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    first[r] = lane < count[r] ? __ldcg(lses[r] + lane * step[r]) : -INFINITY;
+    top = fmaxf(top, first[r]);
+    for (int s = lane + 32; s < count[r]; s += 32) top = fmaxf(top, __ldcg(lses[r] + s * step[r]));
+  }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float shift = top == -INFINITY ? 0.f : top;
   float total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const int s = s0 + lane;
-    const float w =
-        s < n ? __expf(__ldcg((s < ref.splits ? a.pre_lse : a.tail_lse) + row_of(s)) - shift) : 0.f;
-    total += w;
-    const int count = min(32, n - s0);
-#pragma unroll 8
-    for (int j = 0; j < count; ++j) {
-      const int t = s0 + j;
-      const float* o = (t < ref.splits ? a.pre_o : a.tail_o) + row_of(t) * kD;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(o) + lane);
-      const float f = __shfl_sync(0xffffffffu, w, j);
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float4* o = outs[r];
+    const long long stride = step[r] * (kD / 4);
+    for (int s0 = 0; s0 < count[r]; s0 += 32) {
+      const int s = s0 + lane;
+      const float l = s0 == 0        ? first[r]
+                      : s < count[r] ? __ldcg(lses[r] + s * step[r])
+                                     : -INFINITY;
+      const float w = __expf(l - shift);
+      total += w;
+      const int n = min(32, count[r] - s0);
+      int j = 0;
+      for (; j + 4 <= n; j += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __ldcg(o + e * stride);
+        o += 4 * stride;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = __shfl_sync(0xffffffffu, w, j + e);
+          acc.x += f * v[e].x;
+          acc.y += f * v[e].y;
+          acc.z += f * v[e].z;
+          acc.w += f * v[e].w;
+        }
+      }
+      for (; j < n; ++j, o += stride) {
+        const float4 v = __ldcg(o);
+        const float f = __shfl_sync(0xffffffffu, w, j);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
     }
   }
 #pragma unroll
@@ -296,7 +368,9 @@ shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
 
 int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
   count_launches(1);
-  const int threads = a.B <= 2 * kFewThreads && a.groups < kFewThreads ? kFewThreads : kThreads;
+  const int threads = a.B * a.Hkv <= 2 * kFewThreads && a.groups < kFewThreads
+                          ? kFewThreads
+                          : kThreads;
   const size_t smem = a.B <= kHeld ? 2 * sizeof(int) * static_cast<size_t>(a.B) : 0;
   static std::atomic<uint64_t> ready{0};
   if (smem > 47 * 1024 && !kernel_smem_ready(shared_plan_kernel, 8 * kHeld, ready)) return -1;
