@@ -47,6 +47,8 @@ struct DecodeSmem {
   uint64_t item_full[kItemSlots];
   uint64_t item_empty[kItemSlots];
   int item_id[kItemSlots];
+  SplitItem item_rec[kItemSlots];
+  int4 item_of[kItemSlots];      // its request's length, splits, queries and first query row
   uint64_t merge_full[kMergeSlots];
   uint64_t merge_empty[kMergeSlots];
   int4 merge_job[kMergeSlots];   // (request, KV head, item, splits); request -1 ends the queue
@@ -248,16 +250,21 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       }
       if (a.order) item = __ldcg(a.order + item);
       const SplitItem it = item_of(item);
+      const int L = a.seq_lens[it.b];
       if (lane == 0) {
         sm->item_id[islot] = item;
         uint8_t* qdst = qslots + islot * 2 * qhalf;
         // box: 64 columns x G heads x (M / G) queries; rows past the tensor read as zero
         const int q_row0 = a.qo_indptr ? __ldg(a.qo_indptr + it.b) : it.b * a.q_len;
+        // what the consumers need, so that they start without round trips of their own
+        const int splits = __ldcg(a.split_offset + it.b + 1) - __ldcg(a.split_offset + it.b);
+        sm->item_rec[islot] = it;
+        sm->item_of[islot] = make_int4(
+            L, splits, a.qo_indptr ? __ldg(a.qo_indptr + it.b + 1) - q_row0 : a.q_len, q_row0);
         mbar_arrive_expect_tx(&sm->item_full[islot], 2u * M * 128u);
         tma_load_3d(qdst, &qmap, &sm->item_full[islot], 0, it.g * G, q_row0);
         tma_load_3d(qdst + qhalf, &qmap, &sm->item_full[islot], 64, it.g * G, q_row0);
       }
-      const int L = a.seq_lens[it.b];
       const int first_key = (it.kv_begin / kStageKeys) * kStageKeys;
       const int n_stages =
           it.kv_end > first_key ? (it.kv_end - first_key + kStageKeys - 1) / kStageKeys : 0;
@@ -360,15 +367,14 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         break;
       }
-      const SplitItem it = item_of(item);
+      const SplitItem it = sm->item_rec[islot];
+      const int4 of = sm->item_of[islot];
       const int b = it.b, g = it.g;
       const int kv_begin = it.kv_begin, kv_end = it.kv_end;
       const int first_key = (kv_begin / kStageKeys) * kStageKeys;
       const int n_stages =
           kv_end > first_key ? (kv_end - first_key + kStageKeys - 1) / kStageKeys : 0;
-      const int nq = a.qo_indptr ? a.qo_indptr[b + 1] - a.qo_indptr[b] : a.q_len;
-      const int q_row0 = a.qo_indptr ? a.qo_indptr[b] : b * a.q_len;
-      const int L = a.seq_lens[b];
+      const int L = of.x, n_split = of.y, nq = of.z, q_row0 = of.w;
       // keys [klo, khi) of the split that each of this lane's two rows sees: query i sits at
       // L - nq + i; rows past the item's queries keep the split range (never written)
       int klo[2], khi[2];
@@ -560,7 +566,9 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
 
       // ---- combine the key slices of each row ---------------------------------------------
       // red_o [kg][M][128] fp32 in the item's last stage, which no warp reads any more once
-      // all have passed the first barrier; the stage is released after the last one.
+      // all have passed the first barrier; the stage is released after the last one.  Runs of 8
+      // columns are swapped by row, so that the rows of a store fall into different banks (all in
+      // one, the combine of 16 rows took 8,000 cycles, half of an item of 170 keys).
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
@@ -574,17 +582,13 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         const int r0 = rb * 16 + gr;
 #pragma unroll
         for (int j = 0; j < kD / 8; ++j) {
-          const int col = j * 8 + tq * 2;
-          if (r0 < M) {
-            float* p0 = red_o + (kq * M + r0) * kD + col;
-            p0[0] = o[j][0];
-            p0[1] = o[j][1];
-          }
-          if (r0 + 8 < M) {
-            float* p1 = red_o + (kq * M + r0 + 8) * kD + col;
-            p1[0] = o[j][2];
-            p1[1] = o[j][3];
-          }
+          const int col = (j * 8 + tq * 2) ^ ((r0 & 3) << 3);
+          if (r0 < M)
+            *reinterpret_cast<float2*>(red_o + (kq * M + r0) * kD + col) =
+                make_float2(o[j][0], o[j][1]);
+          if (r0 + 8 < M)
+            *reinterpret_cast<float2*>(red_o + (kq * M + r0 + 8) * kD + col) =
+                make_float2(o[j][2], o[j][3]);
         }
         if (tq == 0) {
           if (r0 < M) {
@@ -598,8 +602,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
       }
       named_bar(1, kConsumerWarps * 32);
-      const int d = threadIdx.x;   // 0..127: one output column
-      const int n_split = __ldcg(a.split_offset + b + 1) - __ldcg(a.split_offset + b);
+      const int d = threadIdx.x;   // 0..127
       const int live_rows = nq <= 0 ? 0 : (nq * G < M ? nq * G : M);
       const bool direct = n_split == 1 && !a.parts_only;
       // Thread m: the weights of row m's slices (in the place of their maxima), its sum (in the
@@ -625,22 +628,36 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
           a.lse[static_cast<long long>(qrow) * a.Hq + g * G + d % G] = lse_nat;
       }
       named_bar(1, kConsumerWarps * 32);
-#pragma unroll 4
-      for (int m = 0; m < live_rows; ++m) {
-        float acc = 0.f;
+      // a warp per row, a lane per 4 columns
+      for (int m = warp; m < live_rows; m += kConsumerWarps) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (have_stage) {
 #pragma unroll
-          for (int w = 0; w < kg; ++w) acc += sm->red_m[w * M + m] * red_o[(w * M + m) * kD + d];
+          for (int w = 0; w < kg; ++w) {
+            const float f = sm->red_m[w * M + m];
+            const float4 v = *reinterpret_cast<const float4*>(
+                red_o + (w * M + m) * kD + ((lane * 4) ^ ((m & 3) << 3)));
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
         }
         const float Lsum = sm->red_l[m];
-        const float on = Lsum > 0.f ? acc / Lsum : 0.f;
+        const float4 on = Lsum > 0.f ? make_float4(acc.x / Lsum, acc.y / Lsum, acc.z / Lsum,
+                                                   acc.w / Lsum)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
         if (direct) {
           const int qrow = q_row0 + m / G;
           if (qrow < 0 || qrow >= a.q_rows) continue;
           const long long orow = static_cast<long long>(qrow) * a.Hq + g * G + m % G;
-          store_out1(a.out, orow * kD + d, on * a.out_scale, a.out_dtype);
+          store_out4(a.out, orow * kD + lane * 4,
+                     make_float4(on.x * a.out_scale, on.y * a.out_scale, on.z * a.out_scale,
+                                 on.w * a.out_scale),
+                     a.out_dtype);
         } else {
-          a.part_o[(static_cast<long long>(item) * M + m) * kD + d] = on;
+          const long long prow = static_cast<long long>(item) * M + m;
+          reinterpret_cast<float4*>(a.part_o + prow * kD)[lane] = on;
         }
       }
       if (n_split > 1 && !a.parts_only) {

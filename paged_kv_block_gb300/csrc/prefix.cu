@@ -139,8 +139,9 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   for (int g = warp; g < groups; g += warps) {
     const int rows = row_tiles(g);
     if (rows > 0)
-      atomicAdd(&items_at[lane], static_cast<float>(rows) *    // (exact below 2^24)
-                                     ((ceil_tiles(prefix[a.group_indptr[g]]) + choice - 1) / choice));
+      atomicAdd(&items_at[lane],           // (exact below 2^24)
+                static_cast<float>(rows) *
+                    ((ceil_tiles(prefix[a.group_indptr[g]]) + choice - 1) / choice));
   }
   __syncthreads();
   if (warp == 0) {
