@@ -351,7 +351,7 @@ bool shared_params_ok(const paged_decode_params* p, int num_groups) {
 }
 
 // Capacities: one part per tile of a prefix and two more per SM (the plan chooses parts that fit,
-// prefix.cu); a tail's splits are one plus its share of kTailSplits per SM.
+// prefix.cu); a tail's splits are one plus its share of kTailWarps or kTailSplits per SM.
 SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   SharedLayout s{};
   Layout l;
@@ -359,7 +359,7 @@ SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   const int sms = num_sms(), pairs = num_groups < B / 2 ? num_groups : B / 2;
   s.tile_capacity =
       pairs == 0 ? 0 : 2 * sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
-  s.item_capacity = kTailSplits * sms + p->num_kv_heads * B;
+  s.item_capacity = (G * SQ <= kTailRows ? kTailWarps : kTailSplits) * sms + p->num_kv_heads * B;
   s.status = l.take(sizeof(uint32_t) * 4);
   s.n_tiles = l.take(sizeof(int));
   s.counter = l.take(sizeof(int));
@@ -967,10 +967,13 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   CUtensorMap kmap, vmap, qmap;
   if (!encode_q_map(&t.qmap, query, q_rows, Hq, D, G, sub_tile_tokens(G)) ||
       !encode_rows_map(&t.kmap, k, pool_rows, D, page_piece_rows(ps, kKvTile)) ||
-      !encode_rows_map(&t.vmap, vp, pool_rows, D, page_piece_rows(ps, kKvTile)) ||
-      !encode_rows_map(&kmap, k, pool_rows, D, page_piece_rows(ps, 64)) ||
-      !encode_rows_map(&vmap, vp, pool_rows, D, page_piece_rows(ps, 64)) ||
-      !encode_q_map(&qmap, query, q_rows, Hq, D, G, SQ))
+      !encode_rows_map(&t.vmap, vp, pool_rows, D, page_piece_rows(ps, kKvTile)))
+    return PAGED_ATTN_ERR_CUDA;
+  const bool narrow = G * SQ <= kTailRows;
+  const int step = narrow ? 16 : 64;       // keys of a step of the tails' kernel
+  if (!encode_rows_map(&kmap, k, pool_rows, D, page_piece_rows(ps, step)) ||
+      !encode_rows_map(&vmap, vp, pool_rows, D, page_piece_rows(ps, step)) ||
+      (!narrow && !encode_q_map(&qmap, query, q_rows, Hq, D, G, SQ)))
     return PAGED_ATTN_ERR_CUDA;
   SharedLaunch m{};
   m.lens = seq_lens;
@@ -984,6 +987,17 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   m.groups = num_groups;
   m.causal = p->mask_type == PAGED_ATTN_MASK_CAUSAL;
   m.sms = num_sms();
+  m.item_unit = narrow ? 16 : kKvTile;
+  m.items_per_sm = narrow ? kTailWarps : kTailSplits;
+  m.q = static_cast<const __nv_bfloat16*>(query);
+  m.kv_indptr = kv_indptr;
+  m.kv_indices = kv_indices;
+  m.ps = ps;
+  m.num_pages = p->num_pages;
+  m.page_rows = page_rows;
+  m.v_head_off = v_head_off;
+  m.scale_log2 = scale * kLog2e;
+  m.behind_prefix = s.tile_capacity > 0;
   m.prefix_of = at<int>(ws, s.prefix_of);
   m.refs = at<PrefixRef>(ws, s.refs);
   m.tiles = at<TileRec>(ws, s.tiles);
@@ -1035,6 +1049,10 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
     const int rc = launch_attn(t, st);
     timer_end(st, tok);
     if (rc != 0) return PAGED_ATTN_ERR_CUDA;
+  }
+  if (narrow) {
+    if (launch_shared_tail(kmap, vmap, m, st) != 0) return PAGED_ATTN_ERR_CUDA;
+    return launch_shared_merge(m, st) == 0 ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA;
   }
   DecodeLaunch d{};
   d.kmap = &kmap;

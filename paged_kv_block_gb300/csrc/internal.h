@@ -195,7 +195,10 @@ struct DecodeLaunch {
 int launch_decode(const DecodeLaunch& a, cudaStream_t st);
 
 // ---- shared prefixes (prefix.cu) -----------------------------------------------------------------
-constexpr int kTailSplits = 8;       // tail items aimed at per SM
+// Tails of up to kTailRows rows (query, head) run on a kernel of their own, in items of a multiple of
+// 16 keys, a warp each; longer ones on the decode kernel, in items of a multiple of 128.
+constexpr int kTailRows = 16;
+constexpr int kTailWarps = 12, kTailSplits = 8;      // items aimed at per SM, by kind
 // A request's prefix partials: rows 256 (base + (head * row_tiles + tile) * splits + s) of the
 // tensor-core kernel's partial output, s < splits; its queries are tokens from `token` on among
 // the group's, 256 / G of them to a tile.
@@ -217,16 +220,25 @@ struct SharedLaunch {
   int* split_offset;         // [B + 1] splits of the tails
   SplitItem* items;
   int item_capacity;         // items of all KV heads
+  int item_unit, items_per_sm;   // 16, kTailWarps or 128, kTailSplits
   int* work_counter;
   uint32_t* status;
   // merge
   const float *pre_o, *pre_lse;    // [256 tiles, 128], [256 tiles]
-  const float *tail_o, *tail_lse;  // [items, SQ G, 128], [items, SQ G]
+  float *tail_o, *tail_lse;        // [items, SQ G, 128], [items, SQ G]
   void* out;
   int out_dtype;
   float* lse;
   float out_scale;
+  // tails of up to kTailRows rows
+  const __nv_bfloat16* q;
+  const int *kv_indptr, *kv_indices;
+  int ps, num_pages, page_rows, v_head_off;
+  float scale_log2;
+  int behind_prefix;         // the launch before this one is the prefixes'
 };
+int launch_shared_tail(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedLaunch& a,
+                       cudaStream_t st);
 int launch_shared_plan(const SharedLaunch& a, cudaStream_t st);
 int launch_shared_merge(const SharedLaunch& a, cudaStream_t st);
 

@@ -1,7 +1,8 @@
 // Decode attention for requests that share a prefix (include/paged_attn.h documents the contract):
 // the plan and the final merge.  The prefix of a group is attended once for all of its rows (query,
 // head) by the tensor-core kernel, its keys split over CTAs; what each request has of its own by
-// the split-KV decode kernel; both leave normalised fp32 partials with their log-sum-exp.
+// tail_kernel, or the split-KV decode kernel where it has many rows; all leave normalised fp32
+// partials with their log-sum-exp.
 #include <climits>
 
 #include "common.cuh"
@@ -13,6 +14,7 @@ namespace {
 constexpr int kThreads = 1024;             // of the planning CTA, or
 constexpr int kFewThreads = 256;           // for so many groups and requests
 constexpr int kD = 128;
+constexpr float kLn2 = 0.6931471805599453f;
 // SM time in microseconds of a step of 256 rows (128, where a group has no more) and 128 keys, and
 // of 128 keys of a tail, as measured: the SMs are shared out by them.
 constexpr float kStepCost = 2.0f, kHalfStepCost = 1.2f, kTailCost = 1.4f;
@@ -48,7 +50,6 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   return (warp > 0 ? before : 0) + v - x;
 }
 
-__device__ __forceinline__ int tail_base(int prefix) { return prefix / 128 * 128; }
 __device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1) / kKvTile; }
 
 // One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
@@ -87,6 +88,11 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   if (bad && tid == 0) report_error(a.status, kErrMetadata);
   const int groups = bad ? 0 : a.groups;
   const auto length = [&](int b) { return hold ? held[b] : max(a.lens[b], 0); };
+  // the first item of a tail starts at the prefix, the others at multiples of their unit from here
+  const auto tail_base = [&](int p) { return p / a.item_unit * a.item_unit; };
+  const auto tail_units = [&](int b) {
+    return (length(b) - tail_base(prefix[b]) + a.item_unit - 1) / a.item_unit;
+  };
   // a warp per group
   const int tile_tokens = 2 * (kMTileRows / a.G);
   for (int g = warp; g < groups; g += warps) {
@@ -119,7 +125,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     steps += n;
     cost += n * step_cost(g);
   }
-  for (int b = tid; b < a.B; b += threads) tails += ceil_tiles(length(b) - tail_base(prefix[b]));
+  for (int b = tid; b < a.B; b += threads) tails += tail_units(b);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     steps += __shfl_xor_sync(0xffffffffu, steps, d);
@@ -159,7 +165,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     // the prefixes' share of the SMs, and the time that a choice takes on it
     const float each = x > 0.f ? y / x : 0.f, count = items_at[lane] * a.Hkv;
     const float work = y + count * kTileCost;
-    const float share = work / (work + kTailCost * z + 1e-6f);
+    const float share = work / (work + kTailCost * z * a.item_unit / kKvTile + 1e-6f);
     const int ctas = max(static_cast<int>(a.sms * share + 0.5f), 1);
     const float longest = choice * each + kTileCost;
     float time = count <= ctas ? longest : work / ctas + 0.5f * longest;
@@ -170,14 +176,13 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
       chosen[0] = count > a.tile_capacity ? 1 << 30 : choice;
       *a.max_ctas = ctas;
     }
-    const float aim = static_cast<float>(kTailSplits * a.sms);
+    const float aim = static_cast<float>(a.items_per_sm * a.sms);
     if (lane == 0) chosen[1] = max(static_cast<int>(ceilf(z / aim)), 1);
   }
   __syncthreads();
-  const int part = chosen[0], chunk = chosen[1];             // in tiles of 128 keys
+  const int part = chosen[0], chunk = chosen[1];   // in tiles of 128 keys, in units of the tails
   const auto splits_of = [&](int b) {      // of the tail of request b
-    const int L = length(b), p = prefix[b];
-    return L > p ? (ceil_tiles(L - tail_base(p)) + chunk - 1) / chunk : 0;
+    return length(b) > prefix[b] ? (tail_units(b) + chunk - 1) / chunk : 0;
   };
   // Groups with the longest parts first, where they are few enough to be ordered by counting.
   const bool ordered = groups <= threads && groups <= kOrdered;
@@ -268,11 +273,266 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
       SplitItem it;
       it.b = b;
       it.g = h;
-      it.kv_begin = s == 0 ? p : tail_base(p) + s * chunk * kKvTile;
-      it.kv_end = s == n - 1 ? L : tail_base(p) + (s + 1) * chunk * kKvTile;
+      it.kv_begin = s == 0 ? p : tail_base(p) + s * chunk * a.item_unit;
+      it.kv_end = s == n - 1 ? L : tail_base(p) + (s + 1) * chunk * a.item_unit;
       to[s] = it;
     }
   }
+}
+
+// What a request has of its own, for up to 16 rows (query, head) of a KV head: a warp per item, 16
+// keys at a time through warp MMAs, S = Q K^T and O += P V.  Tails are short, so what CTA barriers
+// and a combine of warps cost per item counts (16,000 cycles for an item of 170 keys on the decode
+// kernel, a third of them its keys); here every warp has a ring of its own, three steps deep, that
+// its lanes fill by TMA, and the warps of an SM (eight) share nothing.  Operands come from shared
+// memory 16 bytes a lane:
+//   K   the contraction runs over columns in any order, so a lane takes 16 bytes of its key's row
+//       as its operands of two MMAs;
+//   V   a lane takes 16 bytes, columns 8 g .. 8 g + 7, of the four keys of its operand; a register
+//       pairs two keys at one column, and column 8 n + j is column n of output tile j.
+// (Loads from HBM straight into the operands, without shared memory, kept too few bytes in flight:
+// 66 us where this takes 58 less ..., 160 MB of tails.)
+constexpr int kTailThreads = 128, kTailStages = 3;
+constexpr int kStepKeys = 16, kStepHalf = kStepKeys * 128, kStepBytes = 4 * kStepHalf;
+struct TailCtrl {
+  uint64_t full[kTailThreads / 32][kTailStages];
+  int abort_flag;
+};
+constexpr int kTailSmem =
+    kTailThreads / 32 * kTailStages * kStepBytes + static_cast<int>(sizeof(TailCtrl)) + 1024;
+
+template <bool kRowMask>
+__global__ void __launch_bounds__(kTailThreads, 2)
+tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+            const __grid_constant__ SharedLaunch a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = smem_align<1024>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, tq = lane & 3;
+  uint8_t* ring = base + warp * kTailStages * kStepBytes;
+  TailCtrl* ctl = reinterpret_cast<TailCtrl*>(base + kTailThreads / 32 * kTailStages * kStepBytes);
+  uint64_t* full = ctl->full[warp];
+  if (lane == 0) {
+    for (int s = 0; s < kTailStages; ++s) mbar_init(&full[s], 1);
+    if (warp == 0) ctl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  __syncthreads();
+  volatile int* abort_flag = &ctl->abort_flag;
+  // (__ldcg: behind the prefixes, whose kernel has waited for the plan, this one has not)
+  if (!a.behind_prefix) grid_dependency_wait();
+  const int items = launch_aborted(a.status) ? 0 : a.Hkv * __ldcg(a.split_offset + a.B);
+  const auto claim = [&] {
+    int x = 0;
+    if (lane == 0) x = atomicAdd(a.work_counter, 1);
+    return __shfl_sync(0xffffffffu, x, 0);
+  };
+  const int M = a.SQ * a.G, ps = a.ps;
+  const int R = page_piece_rows(ps, kStepKeys), boxes = 4 * (kStepKeys / R);
+  // box `lane` of a step: piece, K or V, 64-column half
+  const int piece = lane >> 2, is_v = lane >> 1 & 1, half = lane & 1;
+  int issued = 0, used = 0;                // steps, over all items
+  int item = claim();
+  int4 it = make_int4(0, 0, 0, 0);
+  if (item < items) it = __ldcg(reinterpret_cast<const int4*>(a.items + item));
+  bool ok = true;
+  while (ok && item < items) {
+    const int b = it.x, h = it.y, begin = it.z, end = it.w;
+    const int* pages = a.kv_indices + a.kv_indptr[b];
+    const int L = kRowMask ? a.lens[b] : 0;
+    const int first = begin / kStepKeys * kStepKeys;
+    const int steps = (end - first + kStepKeys - 1) / kStepKeys;
+    const auto page_of = [&](int step) {   // of this lane's piece; -1: none
+      const int key = first + step * kStepKeys + piece * R;
+      if (lane >= boxes || step >= steps || key >= end) return -1;
+      const int page = __ldg(pages + key / ps);
+      return page < 0 ? INT_MAX : page;    // no page of the pool
+    };
+    const auto issue = [&](int step, int page) {
+      const int slot = issued % kTailStages;
+      const bool in = page >= 0 && page < a.num_pages;
+      if (page >= a.num_pages) report_error(a.status, kErrMetadata);
+      const uint32_t live = __popc(__ballot_sync(0xffffffffu, in));
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], live * R * 128u);
+      __syncwarp();
+      if (in) {
+        const int key = first + step * kStepKeys + piece * R;
+        const int row = page * a.page_rows + h * ps + key % ps + (is_v ? a.v_head_off : 0);
+        tma_load_2d(ring + slot * kStepBytes + (2 * is_v + half) * kStepHalf + piece * R * 128,
+                    is_v ? &vmap : &kmap, &full[slot], half * 64, row);
+      }
+      ++issued;
+    };
+    // the first steps' pages together, then their copies
+    int page[kTailStages];
+#pragma unroll
+    for (int s = 0; s < kTailStages; ++s) page[s] = page_of(s);
+#pragma unroll
+    for (int s = 0; s < kTailStages; ++s)
+      if (s < steps) issue(s, page[s]);
+    int ahead = page_of(kTailStages);
+    const int next = claim();
+    int4 next_it = make_int4(0, 0, 0, 0);
+    // rows gr and gr + 8 of Q, and how far they see
+    uint4 qa[4], qb[4];
+    int high[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int m = gr + 8 * r, i = m / a.G;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<long long>(b) * a.SQ + i) * a.Hq + h * a.G + m - i * a.G) * kD +
+          tq * 8);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint4 v = m < M ? __ldg(src + x * 4) : make_uint4(0u, 0u, 0u, 0u);
+        if (r == 0) qa[x] = v; else qb[x] = v;
+      }
+      high[r] = kRowMask && m < M ? min(end, L - a.SQ + i + 1) : end;
+    }
+    float o[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    for (int step = 0; step < steps; ++step, ++used) {
+      const int slot = used % kTailStages;
+      ok = mbar_wait_fast_warp(&full[slot], (used / kTailStages) & 1, a.status, abort_flag);
+      if (!ok) break;
+      if (step == 0 && next < items)
+        next_it = __ldcg(reinterpret_cast<const int4*>(a.items + next));
+      const uint8_t* st = ring + slot * kStepBytes;
+      const int key0 = first + step * kStepKeys;
+      // scores of rows gr, gr + 8 and keys 8 n + 2 tq, + 1
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // key gr + 8 n, columns 32 i + 8 tq ..
+          const uint4 k = *reinterpret_cast<const uint4*>(
+              st + (i >> 1) * kStepHalf + (gr + 8 * n) * 128 + ((((i & 1) * 4 + tq) ^ gr) << 4));
+          const uint32_t a0[4] = {qa[i].x, qb[i].x, qa[i].y, qb[i].y};
+          const uint32_t a1[4] = {qa[i].z, qb[i].z, qa[i].w, qb[i].w};
+          mma_16816(s[n], a0, k.x, k.y);
+          mma_16816(s[n], a1, k.z, k.w);
+        }
+      }
+      float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, key = key0 + 8 * n + 2 * tq + (e & 1);
+          s[n][e] = key >= begin && key < high[r] ? s[n][e] * a.scale_log2 : -INFINITY;
+          best[r] = fmaxf(best[r], s[n][e]);
+        }
+      // The maximum in use moves only when it is exceeded by more than 8 (powers of two), so O is
+      // rarely rescaled; the quotient at the end does not depend on it.
+      float fade[2] = {1.f, 1.f};
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+        if (best[r] > top[r] + 8.f) {
+          fade[r] = top[r] == -INFINITY ? 0.f : fast_exp2(top[r] - best[r]);
+          top[r] = best[r];
+          moved = true;
+        }
+      }
+      const float shift[2] = {top[0] == -INFINITY ? 0.f : top[0],
+                              top[1] == -INFINITY ? 0.f : top[1]};
+      // P in bf16, as everywhere in this library: its rounding (2^-9 of each probability) is
+      // averaged over the keys; the sums are of the unrounded ones
+      uint32_t p[4];
+      float add[2] = {0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = fast_exp2(s[n][2 * r] - shift[r]);
+          const float p1 = fast_exp2(s[n][2 * r + 1] - shift[r]);
+          add[r] += p0 + p1;
+          p[2 * n + r] = pack_bf16(p0, p1);
+        }
+      sum[0] = sum[0] * fade[0] + add[0];
+      sum[1] = sum[1] * fade[1] + add[1];
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          o[j][0] *= fade[0];
+          o[j][1] *= fade[0];
+          o[j][2] *= fade[1];
+          o[j][3] *= fade[1];
+        }
+      }
+      // what is no key of the item may be anything: zeroed, key by key of a pair
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+      if (key0 < begin || key0 + kStepKeys > end) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = key0 + 8 * n + 2 * tq;
+          keep[n] = (key >= begin && key < end ? 0x0000ffffu : 0u) |
+                    (key + 1 >= begin && key + 1 < end ? 0xffff0000u : 0u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4 v[4];                        // keys 2 tq, + 1, + 8, + 9; columns 64 i + 8 gr ..
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int row = 2 * tq + (n & 1) + (n & 2) * 4;
+          v[n] = *reinterpret_cast<const uint4*>(st + (2 + i) * kStepHalf + row * 128 +
+                                                 ((gr ^ (row & 7)) << 4));
+        }
+        const auto word = [](const uint4& x, int w) {
+          return w == 0 ? x.x : (w == 1 ? x.y : (w == 2 ? x.z : x.w));
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int sel = j & 1 ? 0x7632 : 0x5410;
+          mma_16816(o[8 * i + j], p,
+                    __byte_perm(word(v[0], j / 2), word(v[1], j / 2), sel) & keep[0],
+                    __byte_perm(word(v[2], j / 2), word(v[3], j / 2), sel) & keep[1]);
+        }
+      }
+      __syncwarp();                        // every lane has read the step
+      if (step + kTailStages < steps) {
+        issue(step + kTailStages, ahead);
+        ahead = page_of(step + kTailStages + 1);
+      }
+    }
+    if (!ok) break;
+    // this lane's columns 64 i + 16 tq .. + 15 of rows gr and gr + 8
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      const int m = gr + 8 * r;
+      if (m >= M) continue;
+      const long long to = static_cast<long long>(item) * M + m;
+      const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+      float* out = a.tail_o + to * kD + tq * 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 8; j += 4)
+            *reinterpret_cast<float4*>(out + i * 64 + e * 8 + j) = make_float4(
+                o[8 * i + j][2 * r + e] * inv, o[8 * i + j + 1][2 * r + e] * inv,
+                o[8 * i + j + 2][2 * r + e] * inv, o[8 * i + j + 3][2 * r + e] * inv);
+      if (tq == 0)
+        a.tail_lse[to] = sum[r] > 0.f ? (top[r] + fast_log2(sum[r])) * kLn2 : -INFINITY;
+    }
+    item = next;
+    it = next_it;
+  }
+  if (!ok)                                 // no copy may land after the CTA has ended
+    for (int s = used; s < issued; ++s) drain_wait(&full[s % kTailStages], (s / kTailStages) & 1);
+  __syncthreads();
+  if (a.behind_prefix) grid_dependency_wait();
 }
 
 // A warp per (query row, head), a lane per 4 columns: weights of the partials from their
@@ -377,6 +637,21 @@ int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
   if (smem > 47 * 1024 && !kernel_smem_ready(shared_plan_kernel, 8 * kHeld, ready)) return -1;
   return launch_after_previous(shared_plan_kernel, dim3(1), dim3(threads), smem, st, a) ==
                  cudaSuccess
+             ? 0
+             : -1;
+}
+
+int launch_shared_tail(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedLaunch& a,
+                       cudaStream_t st) {
+  const bool rowmask = a.causal && a.SQ > 1;
+  const auto kernel = rowmask ? tail_kernel<true> : tail_kernel<false>;
+  static std::atomic<uint64_t> ready[2];
+  const int sms = current_sm_count();
+  if (sms <= 0 || !kernel_smem_ready(kernel, kTailSmem, ready[rowmask])) return -1;
+  const int most = ceil_div(a.item_capacity, kTailThreads / 32);
+  count_launches(1);
+  return launch_after_previous(kernel, dim3(most < 2 * sms ? most : 2 * sms), dim3(kTailThreads),
+                               kTailSmem, st, kmap, vmap, a) == cudaSuccess
              ? 0
              : -1;
 }
