@@ -13,7 +13,9 @@ without it, but any call raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
+import operator
 import os
 
 import torch
@@ -505,6 +507,11 @@ def batch_decode_with_paged_kv_cache(query, kv_cache, workspace_buffer, paged_kv
     return out, lse
 
 
+@functools.lru_cache(maxsize=512)
+def _shared_params(*fields):
+    return C.byref(DecodeParams(*fields))
+
+
 def shared_prefix_workspace_size(query, kv_cache, max_seq_len, num_groups, *, seq_len_q=1) -> int:
     """Workspace bytes of batch_decode_with_shared_prefix."""
     return paged_decode_shared_workspace_size(
@@ -525,37 +532,45 @@ def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_
     dev = _cache._device()
     if kv_layout != "HND":
         raise ValueError("only the HND layout is supported")
+    kc, vc, combined, P, Hkv, ps, D = _cache._geometry(kv_cache, dev)
+    shape, groups = query.shape, _cache._count(prefix_lens, "prefix_lens")
+    if seq_len_q == 1 and len(shape) == 3:
+        B, Hq, Dq = shape
+    elif len(shape) == 4 and shape[1] == seq_len_q:
+        B, _, Hq, Dq = shape
+    else:
+        raise ValueError("query must be [B, Hq, D] or [B, seq_len_q, Hq, D]")
+    if Dq != D:
+        raise ValueError("query must have the cache's columns")
     out_dtype = _out_dtype(out_dtype, out, query)
-    _cache._geometry(kv_cache, dev)
-    k, v, _, _, _, _, D = _pools(kv_cache)
-    B, groups = query.shape[0], _cache._count(prefix_lens, "prefix_lens")
-    if query.dtype != torch.bfloat16 or query.shape[-1] != D:
-        raise ValueError("query must be bf16 with the cache's columns")
-    params = decode_params(query, kv_cache, max_seq_len, bmm1_scale=bmm1_scale,
-                           bmm2_scale=bmm2_scale, mask_type=mask_type, seq_len_q=seq_len_q,
-                           out_dtype=out_dtype)
-    _cache._on_device(query, dev, "query")
-    _cache._ints_of(paged_kv_indptr, dev, "paged_kv_indptr", B + 1)
-    _cache._ints(paged_kv_indices, dev, "paged_kv_indices")
-    _cache._ints_of(seq_lens, dev, "seq_lens", B)
-    _cache._ints_of(group_indptr, dev, "group_indptr", groups + 1)
-    _cache._ints(prefix_lens, dev, "prefix_lens")
+    qp = _eviction._plain(query, torch.bfloat16, dev, "query", shape)
+    indptr = _cache._ints_of(paged_kv_indptr, dev, "paged_kv_indptr", B + 1)
+    indices = _cache._ints(paged_kv_indices, dev, "paged_kv_indices")
+    lens = _cache._ints_of(seq_lens, dev, "seq_lens", B)
+    first = _cache._ints_of(group_indptr, dev, "group_indptr", groups + 1)
+    prefix = _cache._ints(prefix_lens, dev, "prefix_lens")
+    params = _shared_params(B, Hq, Hkv, D, ps, P, combined, operator.index(max_seq_len),
+                            MASK[mask_type], -1, float(bmm1_scale or 0.0), float(bmm2_scale) + 0.0,
+                            0, seq_len_q, 0, 0, DTYPE[out_dtype])
+    given = out
     if out is None:
-        out = _cache._new(query.shape, out_dtype, query.device, stream)
-    elif out.shape != query.shape:
-        raise ValueError("out must have query's shape")
-    _cache._on_device(out, dev, "out")
-    if lse is not None:
-        _cache._on_device(lse, dev, "lse")
-        if lse.shape != query.shape[:-1] or lse.dtype != torch.float32:
-            raise ValueError("lse must be float32, one value per query and head")
+        out = _cache._new(shape, out_dtype, query.device, stream)
+    op = _eviction._plain(out, out_dtype, dev, "out", shape)
+    lp = None if lse is None else _eviction._plain(lse, torch.float32, dev, "lse", shape[:-1])
     if workspace_buffer is None:
-        workspace_buffer = _cache._new(
-            max(paged_decode_shared_workspace_size(params, groups), 256), torch.uint8,
-            query.device, stream)
-    _cache._on_device(workspace_buffer, dev, "workspace_buffer")
-    paged_decode_shared_run(params, query, k, v, paged_kv_indptr, paged_kv_indices, seq_lens,
-                            group_indptr, prefix_lens, out, lse, workspace_buffer, stream)
+        need = _cache._call.paged_decode_shared_workspace_size(params, groups)
+        workspace_buffer = _cache._new(max(need, 256), torch.uint8, query.device, stream)
+    else:
+        _cache._on_device(workspace_buffer, dev, "workspace_buffer")
+        if not workspace_buffer.is_contiguous():
+            raise ValueError("workspace_buffer must be contiguous")
+    rc = _cache._call.paged_decode_shared_run(
+        params, groups, qp, kc, vc, indptr, indices, lens, first, prefix, op, lp,
+        workspace_buffer.data_ptr(), workspace_buffer.nbytes, _cache._stream(stream, dev))
+    if rc:
+        raise PagedAttnError(rc, "paged_decode_shared_run")
+    if given is not None or lse is not None:
+        _cache._increment_version([t for t in (given, lse) if t is not None])
     return out, lse
 
 

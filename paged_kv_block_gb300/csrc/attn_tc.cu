@@ -284,9 +284,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   // reader; a claim past the list is the end marker.
   auto claim = [&](int s) -> int {
     const int e = s - 1, slot = e % kTileRing;
-    const bool free = e < kTileRing ||
-                      mbar_wait_warp<true>(&ctl->t_empty[slot], ((e / kTileRing) - 1) & 1,
-                                           a.status, abort_flag);
+    // (parts: only once everyone has taken the claim before; few long tiles have to go where there
+    // is time for them)
+    constexpr int kDepth = PART ? 1 : kTileRing;
+    const int o = e - kDepth;
+    const bool free = o < 0 || mbar_wait_warp<true>(&ctl->t_empty[o % kTileRing],
+                                                    (o / kTileRing) & 1, a.status, abort_flag);
     int v = n_live;
     if (lane == 0) {
       // nothing to claim when every tile is some CTA's first (small plans): no round trip

@@ -17,8 +17,8 @@ constexpr int kD = 128;
 constexpr float kLn2 = 0.6931471805599453f;
 // SM time in microseconds of a step of 256 rows (128, where a group has no more) and 128 keys, and
 // of 128 keys of a tail, as measured: the SMs are shared out by them.
-constexpr float kStepCost = 2.0f, kHalfStepCost = 1.2f, kTailCost = 1.4f;
-constexpr float kTileCost = 6.0f;          // of a part of a prefix besides its steps
+constexpr float kStepCost = 2.0f, kHalfStepCost = 1.2f, kTailCost = 2.1f;
+constexpr float kTileCost = 4.0f;          // of a part of a prefix besides its steps
 constexpr int kPartChoices = 32;           // lengths of parts that are weighed up, one per lane
 constexpr int kOrdered = 1024;             // groups that are ordered by the lengths of their parts
 
@@ -62,15 +62,19 @@ __device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1
 constexpr int kHeld = 8192;
 __global__ void __launch_bounds__(kThreads)
 shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
-  extern __shared__ int held[];            // [2, B]: lengths, shared keys
+  // Shared memory: lengths, shared keys and first splits of the requests, and the groups' offsets,
+  // or, where those are too many, the arrays in global memory.
+  extern __shared__ int held[];
   __shared__ long long sums[32];
   __shared__ float costs[3][32];
   __shared__ float items_at[kPartChoices];
   __shared__ int chosen[2], sizes[kOrdered], order[kOrdered];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, warps = threads >> 5;
-  const bool hold = a.B <= kHeld;
+  const bool hold = a.B <= kHeld, hold_groups = a.groups <= kOrdered;
   int* prefix = hold ? held + a.B : a.prefix_of;
+  int* split_at = hold ? held + 2 * a.B : a.split_offset;
+  int* first_of = held + (hold ? 3 * a.B + 1 : 0);
   grid_dependency_wait();
   grid_launch_dependents();
   if (tid < 4) a.status[tid] = 0;
@@ -79,6 +83,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   for (int g = tid; g <= a.groups; g += threads) {
     const int at = a.group_indptr[g];
     bad |= at < 0 || at > a.B || (g > 0 && a.group_indptr[g - 1] > at);
+    if (hold_groups) first_of[g] = at;
   }
   for (int b = tid; b < a.B; b += threads) {
     if (hold) held[b] = max(a.lens[b], 0);
@@ -87,6 +92,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) report_error(a.status, kErrMetadata);
   const int groups = bad ? 0 : a.groups;
+  const auto start = [&](int g) { return hold_groups ? first_of[g] : a.group_indptr[g]; };
   const auto length = [&](int b) { return hold ? held[b] : max(a.lens[b], 0); };
   // the first item of a tail starts at the prefix, the others at multiples of their unit from here
   const auto tail_base = [&](int p) { return p / a.item_unit * a.item_unit; };
@@ -96,7 +102,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   // a warp per group
   const int tile_tokens = 2 * (kMTileRows / a.G);
   for (int g = warp; g < groups; g += warps) {
-    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    const int first = start(g), last = start(g + 1);
     int n = a.prefix_lens[g];
     if (last - first < 2) continue;
     for (int b = first + lane; b < last; b += 32)          // what all queries of b see
@@ -108,12 +114,12 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   __syncthreads();
   // a thread per group and per request: steps of 128 keys of all tiles, and of all tails
   const auto row_tiles = [&](int g) {
-    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    const int first = start(g), last = start(g + 1);
     if (last <= first || prefix[first] == 0) return 0;
     return ((last - first) * a.SQ + tile_tokens - 1) / tile_tokens;
   };
   const auto step_cost = [&](int g) {
-    const int tokens = (a.group_indptr[g + 1] - a.group_indptr[g]) * a.SQ;
+    const int tokens = (start(g + 1) - start(g)) * a.SQ;
     return 2 * tokens <= tile_tokens ? kHalfStepCost : kStepCost;
   };
   float steps = 0.f, cost = 0.f;           // of the tiles
@@ -121,7 +127,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   for (int g = tid; g < groups; g += threads) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
-    const float n = static_cast<float>(rows) * ceil_tiles(prefix[a.group_indptr[g]]);
+    const float n = static_cast<float>(rows) * ceil_tiles(prefix[start(g)]);
     steps += n;
     cost += n * step_cost(g);
   }
@@ -147,7 +153,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     if (rows > 0)
       atomicAdd(&items_at[lane],           // (exact below 2^24)
                 static_cast<float>(rows) *
-                    ((ceil_tiles(prefix[a.group_indptr[g]]) + choice - 1) / choice));
+                    ((ceil_tiles(prefix[start(g)]) + choice - 1) / choice));
   }
   __syncthreads();
   if (warp == 0) {
@@ -189,7 +195,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   if (ordered) {
     const auto size_of = [&](int g) {
       if (row_tiles(g) == 0) return 0;
-      const int keys = ceil_tiles(prefix[a.group_indptr[g]]), n = (keys + part - 1) / part;
+      const int keys = ceil_tiles(prefix[start(g)]), n = (keys + part - 1) / part;
       return (keys + n - 1) / n;
     };
     if (tid < groups) sizes[tid] = size_of(tid);
@@ -208,14 +214,14 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     const int x = x0 + tid, g = x < groups && ordered ? order[x] : x;
     int rows = 0, splits = 0;
     if (x < groups) rows = row_tiles(g);
-    if (rows > 0) splits = (ceil_tiles(prefix[a.group_indptr[g]]) + part - 1) / part;
+    if (rows > 0) splits = (ceil_tiles(prefix[start(g)]) + part - 1) / part;
     const int n = x < a.B ? splits_of(x) : 0;
     long long total;
     const long long before =
         block_scan(pack(static_cast<long long>(rows) * splits * a.Hkv, n), sums, &total);
     if (rows > 0)                          // the group's first request keeps it for all of them
-      a.refs[a.group_indptr[g]] = {tiles + upper_of(before), splits, rows, 0};
-    if (x < a.B) a.split_offset[x] = items + lower_of(before);
+      a.refs[start(g)] = {tiles + upper_of(before), splits, rows, 0};
+    if (x < a.B) split_at[x] = items + lower_of(before);
     tiles += upper_of(total);
     items += lower_of(total);
   }
@@ -226,7 +232,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     tiles = items = 0;
     if (tid == 0) report_error(a.status, kErrCapacity);
     __syncthreads();
-    for (int b = tid; b < a.B; b += threads) a.split_offset[b] = 0;
+    for (int b = tid; b < a.B; b += threads) split_at[b] = 0;
   }
   if (tid == 0) {
     *a.n_tiles = tiles;
@@ -234,14 +240,17 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   }
   __syncthreads();
   for (int b = tid; b < a.B; b += threads) {
-    if (hold) a.prefix_of[b] = prefix[b];
+    if (hold) {
+      a.prefix_of[b] = prefix[b];
+      a.split_offset[b] = split_at[b];
+    }
     // requests outside every group, or in one that shares nothing
     if (prefix[b] == 0 || !fits) a.refs[b] = {0, 0, 0, 0};
   }
   for (int g = warp; fits && g < groups; g += warps) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
-    const int first = a.group_indptr[g], last = a.group_indptr[g + 1];
+    const int first = start(g), last = start(g + 1);
     const int keys = ceil_tiles(prefix[first]);
     PrefixRef ref = a.refs[first];
     __syncwarp();
@@ -268,7 +277,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   for (int x = tid; items > 0 && x < a.B * a.Hkv; x += threads) {
     const int b = x / a.Hkv, h = x - b * a.Hkv, n = splits_of(b);
     const int L = length(b), p = prefix[b];
-    SplitItem* to = a.items + static_cast<long long>(a.split_offset[b]) * a.Hkv + h * n;
+    SplitItem* to = a.items + static_cast<long long>(split_at[b]) * a.Hkv + h * n;
     for (int s = 0; s < n; ++s) {
       SplitItem it;
       it.b = b;
@@ -284,14 +293,14 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
 // keys at a time through warp MMAs, S = Q K^T and O += P V.  Tails are short, so what CTA barriers
 // and a combine of warps cost per item counts (16,000 cycles for an item of 170 keys on the decode
 // kernel, a third of them its keys); here every warp has a ring of its own, three steps deep, that
-// its lanes fill by TMA, and the warps of an SM (eight) share nothing.  Operands come from shared
-// memory 16 bytes a lane:
+// its lanes fill by TMA, into the next item where there is one, and the warps of an SM (eight)
+// share nothing.  Operands come from shared memory 16 bytes a lane:
 //   K   the contraction runs over columns in any order, so a lane takes 16 bytes of its key's row
 //       as its operands of two MMAs;
 //   V   a lane takes 16 bytes, columns 8 g .. 8 g + 7, of the four keys of its operand; a register
 //       pairs two keys at one column, and column 8 n + j is column n of output tile j.
-// (Loads from HBM straight into the operands, without shared memory, kept too few bytes in flight:
-// 66 us where this takes 58 less ..., 160 MB of tails.)
+// 160 MB of tails of 170 keys, 16 rows: 42 us before the ring went on into the next item, 58 us on
+// the decode kernel, 66 us with loads from HBM straight into the operands (too few in flight).
 constexpr int kTailThreads = 128, kTailStages = 3;
 constexpr int kStepKeys = 16, kStepHalf = kStepKeys * 128, kStepBytes = 4 * kStepHalf;
 struct TailCtrl {
@@ -333,47 +342,60 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
   // box `lane` of a step: piece, K or V, 64-column half
   const int piece = lane >> 2, is_v = lane >> 1 & 1, half = lane & 1;
   int issued = 0, used = 0;                // steps, over all items
+  // The item whose steps are being issued, which may be the one after the one that is computed: its
+  // id is claimed, its record and the place of its pages are read in the steps before, so that no
+  // item starts with those round trips (5 us).
+  int to_h = 0, to_first = 0, to_end = 0, to_step = 0, to_steps = 0, ahead = -1;
+  const int* to_pages = nullptr;
+  const auto page_of = [&](int step) {     // of this lane's piece; -1: none
+    const int key = to_first + step * kStepKeys + piece * R;
+    if (lane >= boxes || step >= to_steps || key >= to_end) return -1;
+    const int page = __ldg(to_pages + key / ps);
+    return page < 0 ? INT_MAX : page;      // no page of the pool
+  };
+  const auto issue_from = [&](const int4& rec, int indptr) {
+    to_h = rec.y;
+    to_end = rec.w;
+    to_first = rec.z / kStepKeys * kStepKeys;
+    to_steps = (to_end - to_first + kStepKeys - 1) / kStepKeys;
+    to_step = 0;
+    to_pages = a.kv_indices + indptr;
+    ahead = page_of(0);
+  };
+  const auto issue = [&] {                 // the next step of that item
+    const int page = ahead, slot = issued % kTailStages;
+    ahead = page_of(to_step + 1);
+    const bool in = page >= 0 && page < a.num_pages;
+    if (page >= a.num_pages) report_error(a.status, kErrMetadata);
+    const uint32_t live = __popc(__ballot_sync(0xffffffffu, in));
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], live * R * 128u);
+    __syncwarp();
+    if (in) {
+      const int key = to_first + to_step * kStepKeys + piece * R;
+      const int row = page * a.page_rows + to_h * ps + key % ps + (is_v ? a.v_head_off : 0);
+      tma_load_2d(ring + slot * kStepBytes + (2 * is_v + half) * kStepHalf + piece * R * 128,
+                  is_v ? &vmap : &kmap, &full[slot], half * 64, row);
+    }
+    ++issued;
+    ++to_step;
+  };
   int item = claim();
   int4 it = make_int4(0, 0, 0, 0);
-  if (item < items) it = __ldcg(reinterpret_cast<const int4*>(a.items + item));
+  if (item < items) {
+    it = __ldcg(reinterpret_cast<const int4*>(a.items + item));
+    issue_from(it, a.kv_indptr[it.x]);
+    while (issued < kTailStages && to_step < to_steps) issue();
+  }
   bool ok = true;
   while (ok && item < items) {
     const int b = it.x, h = it.y, begin = it.z, end = it.w;
-    const int* pages = a.kv_indices + a.kv_indptr[b];
     const int L = kRowMask ? a.lens[b] : 0;
     const int first = begin / kStepKeys * kStepKeys;
     const int steps = (end - first + kStepKeys - 1) / kStepKeys;
-    const auto page_of = [&](int step) {   // of this lane's piece; -1: none
-      const int key = first + step * kStepKeys + piece * R;
-      if (lane >= boxes || step >= steps || key >= end) return -1;
-      const int page = __ldg(pages + key / ps);
-      return page < 0 ? INT_MAX : page;    // no page of the pool
-    };
-    const auto issue = [&](int step, int page) {
-      const int slot = issued % kTailStages;
-      const bool in = page >= 0 && page < a.num_pages;
-      if (page >= a.num_pages) report_error(a.status, kErrMetadata);
-      const uint32_t live = __popc(__ballot_sync(0xffffffffu, in));
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], live * R * 128u);
-      __syncwarp();
-      if (in) {
-        const int key = first + step * kStepKeys + piece * R;
-        const int row = page * a.page_rows + h * ps + key % ps + (is_v ? a.v_head_off : 0);
-        tma_load_2d(ring + slot * kStepBytes + (2 * is_v + half) * kStepHalf + piece * R * 128,
-                    is_v ? &vmap : &kmap, &full[slot], half * 64, row);
-      }
-      ++issued;
-    };
-    // the first steps' pages together, then their copies
-    int page[kTailStages];
-#pragma unroll
-    for (int s = 0; s < kTailStages; ++s) page[s] = page_of(s);
-#pragma unroll
-    for (int s = 0; s < kTailStages; ++s)
-      if (s < steps) issue(s, page[s]);
-    int ahead = page_of(kTailStages);
-    const int next = claim();
+    int next = items, next_indptr = 0, claimed = 0;
     int4 next_it = make_int4(0, 0, 0, 0);
+    bool onward = false;                   // the steps being issued are the next item's
+    if (lane == 0) claimed = atomicAdd(a.work_counter, 1);
     // rows gr and gr + 8 of Q, and how far they see
     uint4 qa[4], qb[4];
     int high[2];
@@ -398,8 +420,12 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
       const int slot = used % kTailStages;
       ok = mbar_wait_fast_warp(&full[slot], (used / kTailStages) & 1, a.status, abort_flag);
       if (!ok) break;
-      if (step == 0 && next < items)
-        next_it = __ldcg(reinterpret_cast<const int4*>(a.items + next));
+      if (step == 0) {
+        next = __shfl_sync(0xffffffffu, claimed, 0);
+        if (next < items) next_it = __ldcg(reinterpret_cast<const int4*>(a.items + next));
+      } else if (step == 1 && next < items) {
+        next_indptr = a.kv_indptr[next_it.x];
+      }
       const uint8_t* st = ring + slot * kStepBytes;
       const int key0 = first + step * kStepKeys;
       // scores of rows gr, gr + 8 and keys 8 n + 2 tq, + 1
@@ -498,9 +524,14 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         }
       }
       __syncwarp();                        // every lane has read the step
-      if (step + kTailStages < steps) {
-        issue(step + kTailStages, ahead);
-        ahead = page_of(step + kTailStages + 1);
+      // the ring is full again, with steps of the next item where this one's are all issued
+      const int most = used + 1 + kTailStages;
+      while (issued < most && to_step < to_steps) issue();
+      if (!onward && to_step >= to_steps && next < items) {
+        if (step == 0) next_indptr = a.kv_indptr[next_it.x];
+        issue_from(next_it, next_indptr);
+        onward = true;
+        while (issued < most && to_step < to_steps) issue();
       }
     }
     if (!ok) break;
@@ -536,7 +567,8 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 }
 
 // A warp per (query row, head), a lane per 4 columns: weights of the partials from their
-// log-sum-exps, a lane per partial, then their sum.
+// log-sum-exps, a lane per partial, then their sum.  (Four rows per warp, for more loads in flight,
+// took half as many warps per SM and 3 us longer.)
 constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads)
 shared_merge_kernel(const __grid_constant__ SharedLaunch a) {
@@ -632,9 +664,11 @@ int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
   const int threads = a.B * a.Hkv <= 2 * kFewThreads && a.groups < kFewThreads
                           ? kFewThreads
                           : kThreads;
-  const size_t smem = a.B <= kHeld ? 2 * sizeof(int) * static_cast<size_t>(a.B) : 0;
+  const size_t smem = sizeof(int) * ((a.B <= kHeld ? 3 * static_cast<size_t>(a.B) + 1 : 0) +
+                                     (a.groups <= kOrdered ? a.groups + 1 : 0));
   static std::atomic<uint64_t> ready{0};
-  if (smem > 47 * 1024 && !kernel_smem_ready(shared_plan_kernel, 8 * kHeld, ready)) return -1;
+  constexpr int most = 4 * (3 * kHeld + 1 + kOrdered + 1);
+  if (smem > 38 * 1024 && !kernel_smem_ready(shared_plan_kernel, most, ready)) return -1;
   return launch_after_previous(shared_plan_kernel, dim3(1), dim3(threads), smem, st, a) ==
                  cudaSuccess
              ? 0

@@ -55,8 +55,15 @@ def test_c_refusals(lib):
 
 def test_binding_refusals(lib, monkeypatch):
     monkeypatch.setattr(K, "_device", lambda: -1)
+    monkeypatch.setattr(K, "_stream", lambda stream, dev: 0)
     seen = []
-    monkeypatch.setattr(pkb, "paged_decode_shared_run", lambda *a: seen.append(a))
+
+    class Recorder:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return lambda *a: 64
+            return lambda *a: seen.append(a) or 0
+    monkeypatch.setattr(K, "_call", Recorder())
     i32 = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
     bf16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     good = dict(query=bf16(4, 8, 128), kv_cache=bf16(9, 2, 2, 16, 128), workspace_buffer=None,
@@ -64,7 +71,7 @@ def test_binding_refusals(lib, monkeypatch):
                 group_indptr=i32(3), prefix_lens=i32(2))
     out, lse = pkb.batch_decode_with_shared_prefix(**good)
     assert out.shape == (4, 8, 128) and lse is None and len(seen) == 1
-    params = seen[0][0]
+    params = seen[0][0]._obj
     assert (params.batch, params.seq_len_q, params.window_left, params.split_chunk) == (4, 1, -1, 0)
     for bad in (dict(query=bf16(4, 8, 64)), dict(query=torch.zeros(4, 8, 128)),
                 dict(kv_cache=bf16(9, 3, 2, 16, 128)), dict(kv_cache=torch.zeros(9, 2, 2, 16, 128)),
@@ -73,7 +80,19 @@ def test_binding_refusals(lib, monkeypatch):
                 dict(seq_len_q=2), dict(out=bf16(4, 8, 64)), dict(out_dtype=torch.float64),
                 dict(out=bf16(4, 8, 128), out_dtype=torch.float32), dict(lse=torch.zeros(4, 4)),
                 dict(lse=torch.zeros(4, 8).double()), dict(mask_type="window"),
-                dict(seq_lens=torch.zeros(4, dtype=torch.int64)), dict(group_indptr=i32(6)[::2])):
+                dict(seq_lens=torch.zeros(4, dtype=torch.int64)), dict(group_indptr=i32(6)[::2]),
+                dict(query=bf16(4, 128, 8).transpose(1, 2)),
+                dict(out=bf16(4, 128, 8).transpose(1, 2)),
+                dict(workspace_buffer=torch.zeros(99, 2)[:, 0])):
         with pytest.raises((ValueError, KeyError)):
             pkb.batch_decode_with_shared_prefix(**{**good, **bad})
     assert len(seen) == 1
+    lse, out = torch.zeros(4, 8), bf16(4, 8, 128)
+    versions = lse._version, out._version
+    pkb.batch_decode_with_shared_prefix(**good, out=out, lse=lse)
+    assert lse._version > versions[0] and out._version > versions[1]
+    four = {**good, "query": bf16(4, 3, 8, 128)}
+    pkb.batch_decode_with_shared_prefix(**four, seq_len_q=3, mask_type="causal", bmm2_scale=0.5,
+                                        out_dtype=torch.float32)
+    p = seen[-1][0]._obj
+    assert (p.seq_len_q, p.mask_type, p.bmm2_scale, p.out_dtype) == (3, 1, 0.5, 2)
