@@ -970,10 +970,9 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
       !encode_rows_map(&t.vmap, vp, pool_rows, D, page_piece_rows(ps, kKvTile)))
     return PAGED_ATTN_ERR_CUDA;
   const bool narrow = G * SQ <= kTailRows;
-  const int step = narrow ? 16 : 64;       // keys of a step of the tails' kernel
-  if (!encode_rows_map(&kmap, k, pool_rows, D, page_piece_rows(ps, step)) ||
-      !encode_rows_map(&vmap, vp, pool_rows, D, page_piece_rows(ps, step)) ||
-      (!narrow && !encode_q_map(&qmap, query, q_rows, Hq, D, G, SQ)))
+  if (!narrow && (!encode_rows_map(&kmap, k, pool_rows, D, page_piece_rows(ps, 64)) ||
+                  !encode_rows_map(&vmap, vp, pool_rows, D, page_piece_rows(ps, 64)) ||
+                  !encode_q_map(&qmap, query, q_rows, Hq, D, G, SQ)))
     return PAGED_ATTN_ERR_CUDA;
   SharedLaunch m{};
   m.lens = seq_lens;
@@ -990,6 +989,8 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   m.item_unit = narrow ? 16 : kKvTile;
   m.items_per_sm = narrow ? kTailWarps : kTailSplits;
   m.q = static_cast<const __nv_bfloat16*>(query);
+  m.k = static_cast<const __nv_bfloat16*>(k);
+  m.v = static_cast<const __nv_bfloat16*>(vp);
   m.kv_indptr = kv_indptr;
   m.kv_indices = kv_indices;
   m.ps = ps;
@@ -1051,7 +1052,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
     if (rc != 0) return PAGED_ATTN_ERR_CUDA;
   }
   if (narrow) {
-    if (launch_shared_tail(kmap, vmap, m, st) != 0) return PAGED_ATTN_ERR_CUDA;
+    if (launch_shared_tail(m, st) != 0) return PAGED_ATTN_ERR_CUDA;
     return launch_shared_merge(m, st) == 0 ? PAGED_ATTN_OK : PAGED_ATTN_ERR_CUDA;
   }
   DecodeLaunch d{};

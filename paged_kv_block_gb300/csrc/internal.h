@@ -231,14 +231,13 @@ struct SharedLaunch {
   float* lse;
   float out_scale;
   // tails of up to kTailRows rows
-  const __nv_bfloat16* q;
+  const __nv_bfloat16 *q, *k, *v;  // query; K and V pools, or the combined cache twice
   const int *kv_indptr, *kv_indices;
   int ps, num_pages, page_rows, v_head_off;
   float scale_log2;
   int behind_prefix;         // the launch before this one is the prefixes'
 };
-int launch_shared_tail(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedLaunch& a,
-                       cudaStream_t st);
+int launch_shared_tail(const SharedLaunch& a, cudaStream_t st);
 int launch_shared_plan(const SharedLaunch& a, cudaStream_t st);
 int launch_shared_merge(const SharedLaunch& a, cudaStream_t st);
 

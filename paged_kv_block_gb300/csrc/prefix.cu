@@ -293,42 +293,26 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
 // keys at a time through warp MMAs, S = Q K^T and O += P V.  Tails are short, so what CTA barriers
 // and a combine of warps cost per item counts (16,000 cycles for an item of 170 keys on the decode
 // kernel, a third of them its keys); here every warp has a ring of its own, three steps deep, that
-// its lanes fill by TMA, into the next item where there is one, and the warps of an SM (eight)
-// share nothing.  Operands come from shared memory 16 bytes a lane:
+// its lanes fill by asynchronous copies, with the next item's steps where its own are all under
+// way, and the warps of an SM (eight) share nothing.  Rows that are no key of the item are zeros in
+// the ring.  Operands come from shared memory 16 bytes a lane, 16-byte words swapped by row:
 //   K   the contraction runs over columns in any order, so a lane takes 16 bytes of its key's row
 //       as its operands of two MMAs;
 //   V   a lane takes 16 bytes, columns 8 g .. 8 g + 7, of the four keys of its operand; a register
 //       pairs two keys at one column, and column 8 n + j is column n of output tile j.
-// 160 MB of tails of 170 keys, 16 rows: 42 us before the ring went on into the next item, 58 us on
-// the decode kernel, 66 us with loads from HBM straight into the operands (too few in flight).
+// 160 MB of tails of 170 keys, 16 rows: XX us, 58 us on the decode kernel, 66 us with loads from HBM
+// straight into the operands (too few in flight), 43 us with a box of TMA per lane (300 cycles
+// each to issue).
 constexpr int kTailThreads = 128, kTailStages = 3;
 constexpr int kStepKeys = 16, kStepHalf = kStepKeys * 128, kStepBytes = 4 * kStepHalf;
-struct TailCtrl {
-  uint64_t full[kTailThreads / 32][kTailStages];
-  int abort_flag;
-};
-constexpr int kTailSmem =
-    kTailThreads / 32 * kTailStages * kStepBytes + static_cast<int>(sizeof(TailCtrl)) + 1024;
+constexpr int kTailSmem = kTailThreads / 32 * kTailStages * kStepBytes + 1024;
 
 template <bool kRowMask>
 __global__ void __launch_bounds__(kTailThreads, 2)
-tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-            const __grid_constant__ SharedLaunch a) {
+tail_kernel(const __grid_constant__ SharedLaunch a) {
   extern __shared__ uint8_t raw[];
-  uint8_t* base = smem_align<1024>(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, tq = lane & 3;
-  uint8_t* ring = base + warp * kTailStages * kStepBytes;
-  TailCtrl* ctl = reinterpret_cast<TailCtrl*>(base + kTailThreads / 32 * kTailStages * kStepBytes);
-  uint64_t* full = ctl->full[warp];
-  if (lane == 0) {
-    for (int s = 0; s < kTailStages; ++s) mbar_init(&full[s], 1);
-    if (warp == 0) ctl->abort_flag = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
-  }
-  __syncthreads();
-  volatile int* abort_flag = &ctl->abort_flag;
+  const int lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
+  uint8_t* ring = smem_align<1024>(raw) + (threadIdx.x >> 5) * kTailStages * kStepBytes;
   // (__ldcg: behind the prefixes, whose kernel has waited for the plan, this one has not)
   if (!a.behind_prefix) grid_dependency_wait();
   const int items = launch_aborted(a.status) ? 0 : a.Hkv * __ldcg(a.split_offset + a.B);
@@ -338,46 +322,66 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     return __shfl_sync(0xffffffffu, x, 0);
   };
   const int M = a.SQ * a.G, ps = a.ps;
-  const int R = page_piece_rows(ps, kStepKeys), boxes = 4 * (kStepKeys / R);
-  // box `lane` of a step: piece, K or V, 64-column half
-  const int piece = lane >> 2, is_v = lane >> 1 & 1, half = lane & 1;
+  const unsigned long long by_ps = ~0ull / static_cast<unsigned>(ps) + 1;    // ceil(2^64 / ps)
+  // Copies of a step: 8 times two rows of K, and of V, 16 bytes a lane.
+  const int copy_row = lane >> 4, copy_chunk = lane & 15;
+  const uint32_t copy_to = smem_u32(ring) + (copy_chunk >> 3) * kStepHalf + copy_row * 128;
   int issued = 0, used = 0;                // steps, over all items
   // The item whose steps are being issued, which may be the one after the one that is computed: its
   // id is claimed, its record and the place of its pages are read in the steps before, so that no
   // item starts with those round trips (5 us).
-  int to_h = 0, to_first = 0, to_end = 0, to_step = 0, to_steps = 0, ahead = -1;
+  int to_h = 0, to_first = 0, to_begin = 0, to_end = 0, to_step = 0, to_steps = 0;
+  int ahead[2] = {-1, -1};                 // pages of the next step's keys 0 .. 7 and 8 .. 15
   const int* to_pages = nullptr;
-  const auto page_of = [&](int step) {     // of this lane's piece; -1: none
-    const int key = to_first + step * kStepKeys + piece * R;
-    if (lane >= boxes || step >= to_steps || key >= to_end) return -1;
-    const int page = __ldg(to_pages + key / ps);
-    return page < 0 ? INT_MAX : page;      // no page of the pool
+  const auto look_ahead = [&] {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int key = to_first + to_step * kStepKeys + 8 * p;
+      ahead[p] = -1;
+      if (to_step < to_steps && key < to_end && key + 8 > to_begin) {
+        ahead[p] = __ldg(to_pages + static_cast<int>(__umul64hi(static_cast<unsigned>(key), by_ps)));
+        if (ahead[p] < 0) ahead[p] = INT_MAX;                // no page of the pool
+      }
+    }
   };
   const auto issue_from = [&](const int4& rec, int indptr) {
     to_h = rec.y;
+    to_begin = rec.z;
     to_end = rec.w;
-    to_first = rec.z / kStepKeys * kStepKeys;
+    to_first = to_begin / kStepKeys * kStepKeys;
     to_steps = (to_end - to_first + kStepKeys - 1) / kStepKeys;
     to_step = 0;
     to_pages = a.kv_indices + indptr;
-    ahead = page_of(0);
+    look_ahead();
   };
   const auto issue = [&] {                 // the next step of that item
-    const int page = ahead, slot = issued % kTailStages;
-    ahead = page_of(to_step + 1);
-    const bool in = page >= 0 && page < a.num_pages;
-    if (page >= a.num_pages) report_error(a.status, kErrMetadata);
-    const uint32_t live = __popc(__ballot_sync(0xffffffffu, in));
-    if (lane == 0) mbar_arrive_expect_tx(&full[slot], live * R * 128u);
-    __syncwarp();
-    if (in) {
-      const int key = to_first + to_step * kStepKeys + piece * R;
-      const int row = page * a.page_rows + to_h * ps + key % ps + (is_v ? a.v_head_off : 0);
-      tma_load_2d(ring + slot * kStepBytes + (2 * is_v + half) * kStepHalf + piece * R * 128,
-                  is_v ? &vmap : &kmap, &full[slot], half * 64, row);
+    const int key0 = to_first + to_step * kStepKeys;
+    const uint32_t to = copy_to + issued % kTailStages * kStepBytes;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int key8 = key0 + 8 * p, page = ahead[p];
+      const bool in = page >= 0 && page < a.num_pages;
+      if (page >= a.num_pages) report_error(a.status, kErrMetadata);
+      const int slot =
+          key8 - static_cast<int>(__umul64hi(static_cast<unsigned>(key8), by_ps)) * ps;
+      // (in bounds also where nothing is copied)
+      const long long row = in ? static_cast<long long>(page) * a.page_rows + to_h * ps + slot : 0;
+      const __nv_bfloat16* k = a.k + row * kD + copy_row * kD + copy_chunk * 8;
+      const __nv_bfloat16* v = a.v + (in ? a.v_head_off * static_cast<long long>(kD) : 0) +
+                               row * kD + copy_row * kD + copy_chunk * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * p + 2 * i + copy_row, key = key0 + r;
+        const uint32_t bytes = in && key >= to_begin && key < to_end ? 16u : 0u;
+        const uint32_t at = to + (8 * p + 2 * i) * 128 + (((copy_chunk & 7) ^ (r & 7)) << 4);
+        cp_async16(at, k + (bytes ? i * 2 * kD : 0), bytes);
+        cp_async16(at + 2 * kStepHalf, v + (bytes ? i * 2 * kD : 0), bytes);
+      }
     }
+    cp_async_commit();
     ++issued;
     ++to_step;
+    look_ahead();
   };
   int item = claim();
   int4 it = make_int4(0, 0, 0, 0);
@@ -386,8 +390,7 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     issue_from(it, a.kv_indptr[it.x]);
     while (issued < kTailStages && to_step < to_steps) issue();
   }
-  bool ok = true;
-  while (ok && item < items) {
+  while (item < items) {
     const int b = it.x, h = it.y, begin = it.z, end = it.w;
     const int L = kRowMask ? a.lens[b] : 0;
     const int first = begin / kStepKeys * kStepKeys;
@@ -418,8 +421,12 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
     for (int step = 0; step < steps; ++step, ++used) {
       const int slot = used % kTailStages;
-      ok = mbar_wait_fast_warp(&full[slot], (used / kTailStages) & 1, a.status, abort_flag);
-      if (!ok) break;
+      // this step's group has landed when at most the later ones are pending
+      const int later = issued - used - 1;
+      if (later >= 2) cp_async_wait<2>();
+      else if (later == 1) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      __syncwarp();
       if (step == 0) {
         next = __shfl_sync(0xffffffffu, claimed, 0);
         if (next < items) next_it = __ldcg(reinterpret_cast<const int4*>(a.items + next));
@@ -493,16 +500,6 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
           o[j][3] *= fade[1];
         }
       }
-      // what is no key of the item may be anything: zeroed, key by key of a pair
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-      if (key0 < begin || key0 + kStepKeys > end) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = key0 + 8 * n + 2 * tq;
-          keep[n] = (key >= begin && key < end ? 0x0000ffffu : 0u) |
-                    (key + 1 >= begin && key + 1 < end ? 0xffff0000u : 0u);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint4 v[4];                        // keys 2 tq, + 1, + 8, + 9; columns 64 i + 8 gr ..
@@ -519,8 +516,8 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         for (int j = 0; j < 8; ++j) {
           const int sel = j & 1 ? 0x7632 : 0x5410;
           mma_16816(o[8 * i + j], p,
-                    __byte_perm(word(v[0], j / 2), word(v[1], j / 2), sel) & keep[0],
-                    __byte_perm(word(v[2], j / 2), word(v[3], j / 2), sel) & keep[1]);
+                    __byte_perm(word(v[0], j / 2), word(v[1], j / 2), sel),
+                    __byte_perm(word(v[2], j / 2), word(v[3], j / 2), sel));
         }
       }
       __syncwarp();                        // every lane has read the step
@@ -534,7 +531,6 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         while (issued < most && to_step < to_steps) issue();
       }
     }
-    if (!ok) break;
     // this lane's columns 64 i + 16 tq .. + 15 of rows gr and gr + 8
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -560,9 +556,6 @@ tail_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     item = next;
     it = next_it;
   }
-  if (!ok)                                 // no copy may land after the CTA has ended
-    for (int s = used; s < issued; ++s) drain_wait(&full[s % kTailStages], (s / kTailStages) & 1);
-  __syncthreads();
   if (a.behind_prefix) grid_dependency_wait();
 }
 
@@ -675,8 +668,7 @@ int launch_shared_plan(const SharedLaunch& a, cudaStream_t st) {
              : -1;
 }
 
-int launch_shared_tail(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedLaunch& a,
-                       cudaStream_t st) {
+int launch_shared_tail(const SharedLaunch& a, cudaStream_t st) {
   const bool rowmask = a.causal && a.SQ > 1;
   const auto kernel = rowmask ? tail_kernel<true> : tail_kernel<false>;
   static std::atomic<uint64_t> ready[2];
@@ -685,7 +677,7 @@ int launch_shared_tail(const CUtensorMap& kmap, const CUtensorMap& vmap, const S
   const int most = ceil_div(a.item_capacity, kTailThreads / 32);
   count_launches(1);
   return launch_after_previous(kernel, dim3(most < 2 * sms ? most : 2 * sms), dim3(kTailThreads),
-                               kTailSmem, st, kmap, vmap, a) == cudaSuccess
+                               kTailSmem, st, a) == cudaSuccess
              ? 0
              : -1;
 }
