@@ -22,6 +22,7 @@ struct WeightsArgs {
   float* w;                                // [B, Hkv, W]
   uint32_t* status;
   int B, Hq, Hkv, G, W, C, SQ, total, last, causal, ps, P;
+  int chunk;                               // narrow: keys of a unit
   unsigned long long by_ps;                // ceil(2^64 / ps)
   long long page_rows;                     // rows of D columns per page
   float scale_log2, decay;
@@ -77,11 +78,13 @@ __device__ __forceinline__ int over(int x, unsigned long long by_ps) {
 // K comes from HBM straight into registers, without shared memory or barriers, and the loads of
 // all the SM's warps are in flight together.  The scores of a key then lie in the four lanes of a
 // quad.
+// A unit is a.chunk keys of a request and KV head, 128 at a time (32 per warp); the pages of the
+// next 128 are looked up while the present ones are on their way.
 constexpr int kNarrowThreads = 128;
-constexpr int kNarrowChunk = 128;          // keys of a unit: 32 per warp
+constexpr int kNarrowKeys = 128;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kNarrowThreads)
+__global__ void __launch_bounds__(kNarrowThreads, NT == 1 && D == 128 ? 6 : 1)
 narrow_kernel(const __grid_constant__ WeightsArgs a) {
   constexpr int kBlocks = D / 32;          // 32 columns: two MMAs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -89,30 +92,32 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int pairs = a.B * a.Hkv;
-  const int chunks = (a.W + kNarrowChunk - 1) / kNarrowChunk;
+  const int chunks = (a.W + a.chunk - 1) / a.chunk;
   for (long long u = blockIdx.x; u < static_cast<long long>(pairs) * chunks; u += gridDim.x) {
     const int c = static_cast<int>(u / pairs);
     const int bh = static_cast<int>(u - static_cast<long long>(c) * pairs);
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
     const Request r = request_of(a, b);
     if (r.bad && c == 0 && h == 0 && threadIdx.x == 0) report_error(a.status, kErrMetadata);
-    const int key0 = c * kNarrowChunk + warp * 32;
-    if (key0 >= r.keys) continue;
+    const int begin = c * a.chunk + warp * 32;
+    if (begin >= r.keys) continue;
+    const int end = min(r.keys, (c + 1) * a.chunk);
     float* w = a.w + static_cast<long long>(bh) * a.W;
-    // this lane's rows of the two 16-key steps: keys key0 + 16 s + gr and + 8
-    const __nv_bfloat16* row[4];
+    // this lane's rows of the two 16-key steps from key0 on, keys gr and gr + 8 of each; -1: none
+    const auto find = [&](int key0, int (&row)[4]) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int key = key0 + 8 * x + gr;
-      row[x] = nullptr;
-      if (key < r.keys) {
-        const int p = over(key, a.by_ps), page = __ldg(r.pages + p);
-        if (page >= 0 && page < a.P)
-          row[x] = a.k + (page * a.page_rows + h * a.ps + (key - p * a.ps)) * D + tq * 8;
-        else
-          report_error(a.status, kErrMetadata);
+      for (int x = 0; x < 4; ++x) {
+        const int key = key0 + 8 * x + gr;
+        row[x] = -1;
+        if (key < end) {
+          const int p = over(key, a.by_ps), page = __ldg(r.pages + p);
+          if (page >= 0 && page < a.P)
+            row[x] = static_cast<int>(page * a.page_rows) + h * a.ps + (key - p * a.ps);
+          else
+            report_error(a.status, kErrMetadata);
+        }
       }
-    }
+    };
     const int rows = r.n * a.G;
     for (int r0 = 0; r0 < rows; r0 += 8 * NT) {
       // columns of this lane in the scores: rows r0 + 8 nt + 2 tq and + 1
@@ -139,50 +144,58 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
         for (int i = 0; i < kBlocks; ++i)
           q[nt][i] = x < rows ? __ldg(src + i * 4) : make_uint4(0u, 0u, 0u, 0u);
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      int next[4];
+      find(begin, next);
+      for (int key0 = begin; key0 < end; key0 += kNarrowKeys) {
+        int row[4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint4 ka[kBlocks], kb[kBlocks];
+        for (int x = 0; x < 4; ++x) row[x] = next[x];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          ka[i] = kb[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row[2 * s]) ka[i] = ld_stream(reinterpret_cast<const uint4*>(row[2 * s] + i * 32));
-          if (row[2 * s + 1])
-            kb[i] = ld_stream(reinterpret_cast<const uint4*>(row[2 * s + 1] + i * 32));
-        }
-        const int key = key0 + 16 * s + gr;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < 2; ++s) {
+          uint4 ka[kBlocks], kb[kBlocks];
+          const __nv_bfloat16* pa = a.k + static_cast<long long>(row[2 * s]) * D + tq * 8;
+          const __nv_bfloat16* pb = a.k + static_cast<long long>(row[2 * s + 1]) * D + tq * 8;
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
-            const uint32_t a0[4] = {ka[i].x, kb[i].x, ka[i].y, kb[i].y};
-            const uint32_t a1[4] = {ka[i].z, kb[i].z, ka[i].w, kb[i].w};
-            mma_16816(d, a0, q[nt][i].x, q[nt][i].y);
-            mma_16816(d, a1, q[nt][i].z, q[nt][i].w);
+            ka[i] = kb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row[2 * s] >= 0) ka[i] = ld_stream(reinterpret_cast<const uint4*>(pa + i * 32));
+            if (row[2 * s + 1] >= 0) kb[i] = ld_stream(reinterpret_cast<const uint4*>(pb + i * 32));
           }
+          if (s == 0) find(key0 + kNarrowKeys, next);
+          const int key = key0 + 16 * s + gr;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = fast_exp2(fmaf(d[e], a.scale_log2, shift[nt][e & 1]));
-            if (key + 8 * (e >> 1) <= limit[nt][e & 1]) sum[2 * s + (e >> 1)] += p;
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+              const uint32_t a0[4] = {ka[i].x, kb[i].x, ka[i].y, kb[i].y};
+              const uint32_t a1[4] = {ka[i].z, kb[i].z, ka[i].w, kb[i].w};
+              mma_16816(d, a0, q[nt][i].x, q[nt][i].y);
+              mma_16816(d, a1, q[nt][i].z, q[nt][i].w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = fast_exp2(fmaf(d[e], a.scale_log2, shift[nt][e & 1]));
+              if (key + 8 * (e >> 1) <= limit[nt][e & 1]) sum[2 * s + (e >> 1)] += p;
+            }
           }
         }
-      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-      }
-      // lane tq of the quad writes key key0 + 8 tq + gr
-      const float mine = tq == 0 ? sum[0] : (tq == 1 ? sum[1] : (tq == 2 ? sum[2] : sum[3]));
-      const __nv_bfloat16* live =
-          tq == 0 ? row[0] : (tq == 1 ? row[1] : (tq == 2 ? row[2] : row[3]));
-      const int key = key0 + 8 * tq + gr;
-      if (live) {
-        float before = 0.f;
-        if (r0 > 0) before = w[key];
-        else if (key < r.old && a.decay != 0.f) before = a.decay * w[key];
-        w[key] = before + mine;
+        for (int x = 0; x < 4; ++x) {
+          sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+          sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+        }
+        // lane tq of the quad writes key key0 + 8 tq + gr
+        const float mine = tq == 0 ? sum[0] : (tq == 1 ? sum[1] : (tq == 2 ? sum[2] : sum[3]));
+        const int live = tq == 0 ? row[0] : (tq == 1 ? row[1] : (tq == 2 ? row[2] : row[3]));
+        const int key = key0 + 8 * tq + gr;
+        if (live >= 0) {
+          float before = 0.f;
+          if (r0 > 0) before = w[key];
+          else if (key < r.old && a.decay != 0.f) before = a.decay * w[key];
+          w[key] = before + mine;
+        }
       }
     }
   }
@@ -644,8 +657,6 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   }
 }
 
-constexpr int kPairRows = 1024;
-
 template <int D, bool kPair>
 int launch_wide(const WeightsArgs& a, cudaStream_t st) {
   constexpr int smem = wide_smem<D, kPair>();
@@ -666,11 +677,14 @@ int launch_wide(const WeightsArgs& a, cudaStream_t st) {
 }
 
 template <int D, int NT>
-cudaError_t launch_narrow(const WeightsArgs& a, cudaStream_t st) {
+cudaError_t launch_narrow(WeightsArgs a, cudaStream_t st) {
   const int sms = current_sm_count();
   if (sms <= 0) return cudaErrorUnknown;
-  const long long units = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, kNarrowChunk);
+  // long units where there are many: what a unit reads of its request counts once per unit
+  const long long steps = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, kNarrowKeys);
   const long long most = 16LL * sms;
+  a.chunk = kNarrowKeys * (steps >= 8 * most ? 4 : (steps >= 4 * most ? 2 : 1));
+  const long long units = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, a.chunk);
   count_launches(1);
   return launch_after_previous(narrow_kernel<D, NT>, static_cast<int>(units < most ? units : most),
                                kNarrowThreads, 0, st, a);
@@ -735,9 +749,11 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
   if (rows > 16) {
-    const bool pair = rows >= kPairRows &&
-                      static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, 256) >=
-                          current_sm_count();
+    // Tiles of 256 keys wherever they make a unit per SM (else 128: two prompts' 512 queries of 2
+    // heads, D = 128, 46 us against 62).  16 prompts' last 32 queries of 2 KV heads, D = 256: 40 us
+    // against 47, their last 8 23 against 27, 128 85 against 121.
+    const bool pair = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, 256) >=
+                      current_sm_count();
     if (p->head_dim == 128)
       return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
