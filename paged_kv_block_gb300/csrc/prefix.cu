@@ -300,9 +300,9 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
 //       as its operands of two MMAs;
 //   V   a lane takes 16 bytes, columns 8 g .. 8 g + 7, of the four keys of its operand; a register
 //       pairs two keys at one column, and column 8 n + j is column n of output tile j.
-// 160 MB of tails of 170 keys, 16 rows: XX us, 58 us on the decode kernel, 66 us with loads from HBM
-// straight into the operands (too few in flight), 43 us with a box of TMA per lane (300 cycles
-// each to issue).
+// 160 MB of tails of 170 keys, 16 rows, take 42 us cold and by themselves; 58 us on the decode
+// kernel, 66 us with loads from HBM straight into the operands (too few in flight), 43 us with TMA
+// boxes of 16 rows.
 constexpr int kTailThreads = 128, kTailStages = 3;
 constexpr int kStepKeys = 16, kStepHalf = kStepKeys * 128, kStepBytes = 4 * kStepHalf;
 constexpr int kTailSmem = kTailThreads / 32 * kTailStages * kStepBytes + 1024;
@@ -339,7 +339,7 @@ tail_kernel(const __grid_constant__ SharedLaunch a) {
       const int key = to_first + to_step * kStepKeys + 8 * p;
       ahead[p] = -1;
       if (to_step < to_steps && key < to_end && key + 8 > to_begin) {
-        ahead[p] = __ldg(to_pages + static_cast<int>(__umul64hi(static_cast<unsigned>(key), by_ps)));
+        ahead[p] = __ldg(to_pages + __umul64hi(static_cast<unsigned>(key), by_ps));
         if (ahead[p] < 0) ahead[p] = INT_MAX;                // no page of the pool
       }
     }
