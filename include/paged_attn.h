@@ -281,10 +281,10 @@ int paged_decode_run(const paged_decode_params* params, const void* query_dev,
  *     break this set the metadata status bit, and then nothing is shared (the outputs hold);
  *   - prefix_lens_dev [num_groups]: the first prefix_lens[g] keys and values of group g's
  *     requests are the same, wherever their pages lie; they are read from the pages of the
- *     group's first request.  Any length: what some member's queries do not all see (past its
- *     own length, or under the causal mask past its first query) is left to the requests
- *     themselves.
- * A length of 0 is allowed (0 / -inf).  The outputs differ from paged_decode_run's by the
+ *     group's first request that is not empty.  Any length: what some member's queries do not all
+ *     see (past its own length, or under the causal mask past its first query) is left to the
+ *     requests themselves.
+ * A length of 0 is allowed (0 / -inf), in a group too: it takes no part.  The outputs differ from paged_decode_run's by the
  * rounding of the fp32 merge and of the probabilities alone. */
 size_t paged_decode_shared_workspace_size(const paged_decode_params* params, int num_groups);
 int paged_decode_shared_run(const paged_decode_params* params, int num_groups,

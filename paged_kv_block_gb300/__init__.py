@@ -527,8 +527,8 @@ def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_
     same tokens; returns (out, lse).  Group g is the requests group_indptr[g] ..
     group_indptr[g + 1], whose first prefix_lens[g] keys and values are equal: they are read
     once, from the pages of the group's first request.  group_indptr [groups + 1] and prefix_lens
-    [groups] are int32; requests outside every group share nothing.  query is [B, Hq, D] or [B, SQ,
-    Hq, D]."""
+    [groups] are int32; requests outside every group share nothing, and those of length 0 (rows that
+    pad a batch) take no part in theirs.  query is [B, Hq, D] or [B, SQ, Hq, D]."""
     dev = _cache._device()
     if kv_layout != "HND":
         raise ValueError("only the HND layout is supported")

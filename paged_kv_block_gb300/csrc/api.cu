@@ -984,6 +984,7 @@ int paged_decode_shared_run(const paged_decode_params* p, int num_groups, const 
   m.G = G;
   m.SQ = SQ;
   m.groups = num_groups;
+  m.max_len = p->max_seq_len;
   m.causal = p->mask_type == PAGED_ATTN_MASK_CAUSAL;
   m.sms = num_sms();
   m.item_unit = narrow ? 16 : kKvTile;

@@ -210,6 +210,7 @@ struct SharedLaunch {
   const int* group_indptr;   // [groups + 1]
   const int* prefix_lens;    // [groups]
   int B, Hq, Hkv, G, SQ, groups, causal, sms;
+  int max_len;               // bound on lens
   // plan
   int* prefix_of;            // [B] shared keys of the request, 0 none
   PrefixRef* refs;           // [B]

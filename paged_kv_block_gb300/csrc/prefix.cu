@@ -53,7 +53,8 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 __device__ __forceinline__ int ceil_tiles(int keys) { return (keys + kKvTile - 1) / kKvTile; }
 
 // One CTA.  Groups: the prefix that may be shared (no longer than what every query of every member
-// sees, so that no mask is needed in it), tiles of up to 256 rows, and equal key parts.  Requests:
+// sees, so that no mask is needed in it; members of length 0, such as a batch is padded with, see
+// nothing and have no say), tiles of up to 256 rows, and equal key parts.  Requests:
 // what is left, split as decode splits it.  The kernels of the two run side by side, a prefix CTA
 // or two tail CTAs on an SM, so the prefixes are cut into parts for their share of the SMs: 64
 // requests with tails of some 300 keys behind 8,192 common ones took 64 us with parts for all SMs,
@@ -79,6 +80,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
   grid_launch_dependents();
   if (tid < 4) a.status[tid] = 0;
   if (tid == 0) *a.work_counter = 0;
+  const auto length_of = [&](int b) { return min(max(a.lens[b], 0), a.max_len); };
   bool bad = false;
   for (int g = tid; g <= a.groups; g += threads) {
     const int at = a.group_indptr[g];
@@ -86,29 +88,33 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     if (hold_groups) first_of[g] = at;
   }
   for (int b = tid; b < a.B; b += threads) {
-    if (hold) held[b] = max(a.lens[b], 0);
+    if (hold) held[b] = length_of(b);
     prefix[b] = 0;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) report_error(a.status, kErrMetadata);
   const int groups = bad ? 0 : a.groups;
   const auto start = [&](int g) { return hold_groups ? first_of[g] : a.group_indptr[g]; };
-  const auto length = [&](int b) { return hold ? held[b] : max(a.lens[b], 0); };
+  const auto length = [&](int b) { return hold ? held[b] : length_of(b); };
   // the first item of a tail starts at the prefix, the others at multiples of their unit from here
   const auto tail_base = [&](int p) { return p / a.item_unit * a.item_unit; };
   const auto tail_units = [&](int b) {
-    return (length(b) - tail_base(prefix[b]) + a.item_unit - 1) / a.item_unit;
+    const int keys = length(b) - tail_base(prefix[b]);
+    return keys > 0 ? (keys + a.item_unit - 1) / a.item_unit : 0;
   };
   // a warp per group
   const int tile_tokens = 2 * (kMTileRows / a.G);
   for (int g = warp; g < groups; g += warps) {
     const int first = start(g), last = start(g + 1);
-    int n = a.prefix_lens[g];
+    int n = a.prefix_lens[g], members = 0;
     if (last - first < 2) continue;
-    for (int b = first + lane; b < last; b += 32)          // what all queries of b see
-      n = min(n, a.causal ? length(b) - a.SQ + 1 : length(b));
+    for (int b = first + lane; b < last; b += 32) {
+      if (length(b) == 0) continue;
+      n = min(n, a.causal ? length(b) - a.SQ + 1 : length(b));     // what all queries of b see
+      ++members;
+    }
     n = __reduce_min_sync(0xffffffffu, n);
-    if (n <= 0) continue;
+    if (n <= 0 || __reduce_add_sync(0xffffffffu, members) < 2) continue;
     for (int b = first + lane; b < last; b += 32) prefix[b] = n;
   }
   __syncthreads();
@@ -122,8 +128,7 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     const int tokens = (start(g + 1) - start(g)) * a.SQ;
     return 2 * tokens <= tile_tokens ? kHalfStepCost : kStepCost;
   };
-  float steps = 0.f, cost = 0.f;           // of the tiles
-  int tails = 0;
+  float steps = 0.f, cost = 0.f, tails = 0.f;    // of the tiles; units of the tails
   for (int g = tid; g < groups; g += threads) {
     const int rows = row_tiles(g);
     if (rows == 0) continue;
@@ -131,17 +136,17 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     steps += n;
     cost += n * step_cost(g);
   }
-  for (int b = tid; b < a.B; b += threads) tails += tail_units(b);
+  for (int b = tid; b < a.B; b += threads) tails += static_cast<float>(tail_units(b));
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     steps += __shfl_xor_sync(0xffffffffu, steps, d);
     cost += __shfl_xor_sync(0xffffffffu, cost, d);
+    tails += __shfl_xor_sync(0xffffffffu, tails, d);
   }
-  tails = __reduce_add_sync(0xffffffffu, tails);
   if (lane == 0) {
     costs[0][warp] = steps;
     costs[1][warp] = cost;
-    costs[2][warp] = static_cast<float>(tails);
+    costs[2][warp] = tails;
   }
   if (tid < kPartChoices) items_at[tid] = 0.f;
   __syncthreads();
@@ -252,17 +257,20 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     if (rows == 0) continue;
     const int first = start(g), last = start(g + 1);
     const int keys = ceil_tiles(prefix[first]);
-    PrefixRef ref = a.refs[first];
+    const PrefixRef ref = a.refs[first];
     __syncwarp();
+    int reader = last;                     // the first member that has the prefix
     for (int b = first + lane; b < last; b += 32) {
-      ref.token = (b - first) * a.SQ;
-      a.refs[b] = ref;
+      const bool empty = length(b) == 0;
+      if (!empty) reader = min(reader, b);
+      a.refs[b] = {ref.base, empty ? 0 : ref.splits, ref.row_tiles, (b - first) * a.SQ};
     }
+    reader = __reduce_min_sync(0xffffffffu, reader);
     const int tokens = (last - first) * a.SQ, count = rows * ref.splits * a.Hkv;
     for (int k = lane; k < count; k += 32) {
       const int s = k % ref.splits, r = k / ref.splits % rows, h = k / ref.splits / rows;
       TileRec t;
-      t.b = first;
+      t.b = reader;
       t.g = h;
       t.tok0 = r * tile_tokens;
       t.ntok = min(tile_tokens, tokens - t.tok0);

@@ -255,3 +255,91 @@ def test_an_empty_batch():
     out, _ = pkb.batch_decode_with_shared_prefix(q, cache, None, i32([0]), i32([]), i32([]), 16,
                                                  i32([0]), i32([]))
     assert out.shape == q.shape
+
+
+class Padded(Problem):
+    """A problem whose requests `empty` have ended: length 0 and a page table of what nobody may
+    read."""
+
+    def __init__(self, empty, *args, **kw):
+        super().__init__(*args, **kw)
+        for b in empty:
+            self.lens[b], self.rows[b] = 0, self.rows[b][:, :0]
+            self.tables[b] = [10 ** 6] * len(self.tables[b])
+
+
+@pytest.mark.parametrize("Hq,SQ", [(8, 1), (8, 3), (16, 4)])
+def test_empty_members_of_a_group(Hq, SQ):
+    """They change nothing for the others, which still share: beside a member without pages of its
+    own for the prefix."""
+    groups = [(500, [9, 12, 30, 4]), (200, [7, 9]), (150, [5, 6, 7])]
+    p = Padded([0, 2, 5, 6, 7, 8], 17, groups, Hq, 2, SQ)
+    tables = [list(r) for r in p.tables]
+    tables[3][:384 // 16] = [10 ** 6] * (384 // 16)
+    for causal in (True, False):
+        out, lse = p.check(causal, tables=tables)
+        for b in (0, 2, 5):
+            assert not out[b].any() and torch.isneginf(lse[b]).all()
+
+
+@pytest.mark.parametrize("Hq,SQ", [(4, 1), (16, 2)])
+def test_batches_that_exceed_the_plan_s_shared_memory(Hq, SQ):
+    """Over 8,192 requests and over 1,024 groups."""
+    p = Problem(18, [(40, [2 + i % 3, 2, 2 + i % 5]) for i in range(2900)], Hq, 1, SQ, ps=8)
+    out, lse = p.run()
+    tables, C = p.tables, len(p.tables[0])
+    other = torch.empty_like(lse)
+    plain, _ = pkb.batch_decode_with_paged_kv_cache(
+        p.q.to(DEV), p.cache, None, i32([C * b for b in range(len(tables) + 1)]),
+        i32(sum(tables, [])), i32(p.lens), max(p.lens), lse=other, seq_len_q=SQ,
+        mask_type="causal")
+    check_out(out, plain.double().cpu().numpy())
+    check_lse(lse, other.double().cpu().numpy(), 1e-4)
+
+
+@pytest.mark.parametrize("Hq,SQ", [(8, 1), (16, 3)])
+def test_pages_past_32_bits(Hq, SQ):
+    """A cache of 2.5e9 elements, its last pages in use."""
+    p = Problem(19, [(300, [9, 30, 4]), (64, [100, 5])], Hq, 1, SQ)
+    small, P = p.cache, 600_000
+    p.cache = torch.empty(P, 2, 1, 16, 128, dtype=torch.bfloat16, device=DEV)
+    p.cache[P - small.shape[0]:] = small
+    p.tables = [[t + P - small.shape[0] if t >= 0 else t for t in r] for r in p.tables]
+    p.check()
+
+
+def test_graphs_that_share_a_workspace_and_streams_that_do_not():
+    """Two captured steps of different sizes replayed in turn on one workspace; calls on two streams
+    at once."""
+    problems = [Problem(20, [(900, [9, 30, 4]), (64, [100, 1])], 8, 2),
+                Problem(21, [(333, [40] * 9)], 32, 2, 2, ps=32)]
+    calls, graphs, need = [], [], 0
+    for p in problems:
+        C = len(p.tables[0])
+        rest = (i32([C * b for b in range(len(p.tables) + 1)]), i32(sum(p.tables, [])),
+                i32(p.lens), max(p.lens), i32(p.first), i32(p.prefixes))
+        calls.append((p.q.to(DEV), p.cache, rest, torch.empty_like(p.q, device=DEV), p.SQ))
+        need = max(need, pkb.shared_prefix_workspace_size(
+            calls[-1][0], p.cache, max(p.lens), len(p.prefixes), seq_len_q=p.SQ))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def call(c, ws=None, out=None, stream=None):
+        return pkb.batch_decode_with_shared_prefix(*c[:2], ws, *c[2], seq_len_q=c[4], out=out,
+                                                   mask_type="causal", stream=stream)[0]
+    want = [call(c) for c in calls]
+    for p, w in zip(problems, want):
+        check_out(w, p.reference()[0])
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c, ws, c[3])
+    for i in (0, 1, 1, 0, 1, 0):
+        calls[i][3].zero_()
+        graphs[i].replay()
+        assert torch.equal(calls[i][3], want[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[call(c, stream=s) for c, s in zip(calls, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(a, b) for a, b in zip(pair, want))
