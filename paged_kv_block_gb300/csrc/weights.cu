@@ -59,8 +59,8 @@ __device__ __forceinline__ Request request_of(const WeightsArgs& a, int b) {
   const long long room = static_cast<long long>(entries) * a.ps;
   r.keys = min(max(L, 0), a.W);
   if (r.keys > room) r.keys = static_cast<int>(room);
-  r.bad |= r.keys < L;
   if (nq == 0) r.keys = 0;                 // nothing is asked of the request
+  else r.bad |= r.keys < L;
   return r;
 }
 // Row of a head of KV head h in lse, and of D columns in q.
@@ -759,9 +759,7 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
   }
   if (p->head_dim == 128)
-    return cuda_status(rows <= 8 ? launch_narrow<128, 1>(a, st)
-                                 : (rows <= 16 ? launch_narrow<128, 2>(a, st)
-                                               : launch_narrow<128, 4>(a, st)));
+    return cuda_status(rows <= 8 ? launch_narrow<128, 1>(a, st) : launch_narrow<128, 2>(a, st));
   return cuda_status(rows <= 8 ? launch_narrow<256, 1>(a, st) : launch_narrow<256, 2>(a, st));
 }
 

@@ -253,3 +253,32 @@ def test_weights_of_a_step_sum_to_its_queries():
     w = p.run(fixed=True)
     total = w.nan_to_num(0).sum(-1).cpu()
     assert torch.allclose(total, torch.full_like(total, 4.0), rtol=1e-4)
+
+
+@pytest.mark.parametrize("busy", [1, 150])
+def test_requests_without_queries_are_left_alone(busy):
+    """Whatever their length: rows of a batch that sit a call out."""
+    p = Problem(13, [200, 190, 64], [busy, 0, 2], 8, 2, 128, 16)
+    w, status = p.w.to(DEV), i32([0])
+    pkb.accumulate_attention_weights(p.q.to(DEV), p.lse.to(DEV), p.cache, i32([200, 10 ** 6, 64]),
+                                     w, block_tables=i32(p.tables), qo_indptr=i32(p.starts),
+                                     status=status)
+    assert status.item() == 0
+    p.check(w)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_pages_past_32_bits(new):
+    """A cache of 2.5e9 elements, its last pages in use."""
+    p = Problem(14, [400, 333], [new, new], 8, 1, 128, 16)
+    small, P = p.cache, 600_000
+    p.cache = torch.empty(P, 2, 1, 16, 128, dtype=torch.bfloat16, device=DEV)
+    p.cache[P - small.shape[0]:] = small
+    p.tables = [[t + P - small.shape[0] if t >= 0 else t for t in r] for r in p.tables]
+    p.run()
+
+
+def test_prompts_beside_single_tokens():
+    """One request with many queries in a batch of few on average, and the other way round."""
+    Problem(15, [300] + [40 + b for b in range(20)], [90] + [1] * 20, 4, 2, 128, 16).run()
+    Problem(16, [700, 50, 20, 90], [300, 1, 0, 1], 8, 2, 256, 16).run(csr=True)
