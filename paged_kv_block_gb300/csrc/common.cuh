@@ -471,15 +471,6 @@ __device__ __forceinline__ void ffma2_bcast(float& d0, float& d1, float a0, floa
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(s), "f"(t));
 }
-// (d0, d1) = (a0, a1) * s + (t0, t1) as one packed fp32x2 FMA.
-__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float s, float t0,
-                                      float t1) {
-  asm("{\n\t.reg .b64 ra, rs, rt, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%4, %4};\n\tmov.b64 rt, {%5, %6};\n\t"
-      "fma.rn.f32x2 rd, ra, rs, rt;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(s), "f"(t0), "f"(t1));
-}
 // (a0, a1) += (b0, b1) as one packed fp32x2 add.
 __device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) {
   asm("{\n\t.reg .b64 ra, rb;\n\t"
