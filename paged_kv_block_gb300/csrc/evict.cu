@@ -10,18 +10,20 @@ namespace {
 // A list is the weights of one (layer, row, KV head).  Its tokens get 32-bit keys whose unsigned
 // order is the order of preference.  The smallest key that is kept, T, is bracketed between keys of
 // which at least and fewer than the wanted number of tokens follow.  The first bracket comes from a
-// sample of 32 keys of every warp; it is cut at pivots by interpolation between its counts, until
-// exactly the wanted number of tokens follow or few enough keys are left in it to be ranked one by
-// one.  Keys stay in registers, kOwn a thread (32; 8 where there are CTAs to spare and time is
-// latency): a step costs two instructions a key and a barrier.  A last pass writes the indices in
-// order, those of key T until their number is reached.
-// Instructions bound it: for 2,048 lists of 8,192 tokens histograms of the keys' digits took 143
-// us (half of the tokens may have the same weight, and then shared-memory atomics queue up), plain
-// bisection 112 us, interpolation between the least and the greatest key 64 us.
+// sample of 32 keys of every warp; it is cut at pivots by interpolation between its counts until
+// exactly the wanted number of tokens follow or one key is left.  Keys stay in registers, kOwn a
+// thread (32; 8 where there are CTAs to spare and time is latency): a step costs two instructions a
+// key and a barrier.  What a bracket of few keys holds goes to shared memory, where a step is cheap.
+// A last pass writes the indices in order, those of key T until their number is reached.
+// Instructions and barriers bound it: for 2,048 lists of 8,192 tokens histograms of the keys' digits
+// took 143 us (half of the tokens may have the same weight, and then shared-memory atomics queue
+// up), plain bisection 112 us, interpolation between the least and the greatest key 64 us, with
+// the sample but on the registers to the end 56 us, this 54 us; one warp alone in the last steps 58
+// us, four pivots at a time there 60 us (what every warp does beside the counting doubles).
 constexpr uint32_t kMustKeep = 0xffffffffu;
 constexpr int kSelectCluster = 8;
 constexpr int kSelectThreads = 1024;
-constexpr int kFewLeft = 64;               // keys that are ranked one by one
+constexpr int kLeft = 2048;                // keys of the bracket that go to shared memory
 
 struct SelectArgs {
   const int* rows;
@@ -44,7 +46,8 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 struct SelectShared {
   uint32_t warps[2][2][32];
   uint32_t cta[2][2][kSelectCluster];
-  uint32_t left[kFewLeft], lefts, found[3];    // the last keys of the bracket; T, its counts
+  alignas(16) uint32_t left[kLeft];        // the last keys of the bracket, and how many
+  uint32_t lefts;
 };
 
 // The tokens [begin, begin + count) of a list, this CTA's share of it.
@@ -81,32 +84,20 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
   }
   const auto load_key = [&](int t) { return t < last ? make_key(t, w[begin + t]) : 0u; };
   int turn = 0;
-  // Both values over all threads of the list: op(x, y) of two lanes, zero for none.
-  const auto exchange = [&](uint32_t& x, uint32_t& y, const auto& warp_op_x,
-                            const auto& warp_op_y, uint32_t zero_x, uint32_t zero_y) {
-    x = warp_op_x(x);
-    y = warp_op_y(y);
-    if (lane == 0) {
-      sh.warps[turn][0][warp] = x;
-      sh.warps[turn][1][warp] = y;
-    }
-    __syncthreads();
-    x = warp_op_x(lane < warps ? sh.warps[turn][0][lane] : zero_x);
-    y = warp_op_y(lane < warps ? sh.warps[turn][1][lane] : zero_y);
-    if (size > 1) {
-      if (warp == 0 && lane < size) {
-        *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = x;
-        *cl.map_shared_rank(&sh.cta[turn][1][rank], lane) = y;
-      }
-      cl.sync();
-      x = warp_op_x(lane < size ? sh.cta[turn][0][lane] : zero_x);
-      y = warp_op_y(lane < size ? sh.cta[turn][1][lane] : zero_y);
-    }
-    turn ^= 1;
-  };
   const auto min_of = [](uint32_t v) { return __reduce_min_sync(0xffffffffu, v); };
   const auto max_of = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
   const auto sum = [](uint32_t v) { return __reduce_add_sync(0xffffffffu, v); };
+  // Both values, which the CTA's threads agree on, over the CTAs of the list.
+  const auto over_cluster = [&](uint32_t& x, uint32_t& y, const auto& op_x, const auto& op_y,
+                                uint32_t zero_x, uint32_t zero_y) {
+    if (warp == 0 && lane < size) {
+      *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = x;
+      *cl.map_shared_rank(&sh.cta[turn][1][rank], lane) = y;
+    }
+    cl.sync();
+    x = op_x(lane < size ? sh.cta[turn][0][lane] : zero_x);
+    y = op_y(lane < size ? sh.cta[turn][1][lane] : zero_y);
+  };
   const auto own_count = [&](uint32_t pivot) {               // of this thread; pivot > 0
     uint32_t p[4] = {0, 0, 0, 0};
     if (kHeld) {
@@ -121,18 +112,32 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
     }
     return (p[0] + p[1]) + (p[2] + p[3]);
   };
-  const auto count_from = [&](uint32_t pivot) {
-    uint32_t c = sum(own_count(pivot));
-    if (lane == 0) sh.warps[turn][0][warp] = c;
+  // Over all threads of the list.
+  const auto sum_all = [&](uint32_t& x, uint32_t& y) {
+    x = sum(x);
+    y = sum(y);
+    if (lane == 0) {
+      sh.warps[turn][0][warp] = x;
+      sh.warps[turn][1][warp] = y;
+    }
     __syncthreads();
-    c = sum(lane < warps ? sh.warps[turn][0][lane] : 0u);
+    x = sum(lane < warps ? sh.warps[turn][0][lane] : 0u);
+    y = sum(lane < warps ? sh.warps[turn][1][lane] : 0u);
+    if (size > 1) over_cluster(x, y, sum, sum, 0u, 0u);
+    turn ^= 1;
+  };
+  const auto sum_one = [&](uint32_t x) {
+    x = sum(x);
+    if (lane == 0) sh.warps[turn][0][warp] = x;
+    __syncthreads();
+    x = sum(lane < warps ? sh.warps[turn][0][lane] : 0u);
     if (size > 1) {
-      if (warp == 0 && lane < size) *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = c;
+      if (warp == 0 && lane < size) *cl.map_shared_rank(&sh.cta[turn][0][rank], lane) = x;
       cl.sync();
-      c = sum(lane < size ? sh.cta[turn][0][lane] : 0u);
+      x = sum(lane < size ? sh.cta[turn][0][lane] : 0u);
     }
     turn ^= 1;
-    return static_cast<int>(c);
+    return static_cast<int>(x);
   };
   // from_low tokens have keys >= low, at least K; above of them keys >= high, fewer than K (K where
   // it ends early).
@@ -140,78 +145,50 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
   int from_low = L, above = a.sink + a.recent;
   bool done = above == a.K;                // nothing else is kept
   // The sample: every warp with 32 keys, all of them open, takes the one at the wanted place in their
-  // order, and the least and the greatest of those are the first two pivots (one key where many
-  // tokens have it).
+  // order; of up to 8 warps' keys the least and the greatest, of more those some two deviations
+  // about the median, are the first two pivots (one key where many tokens have it).
   uint32_t from = kMustKeep, to = 0u;
-  if (threadIdx.x == 0) sh.lefts = 0;      // (the barriers of the exchange order it)
-  if (last - first >= 32 && !ends) {
-    const uint32_t mine = kHeld ? held[0] : load_key(first + lane);
-    uint32_t not_less = 0;
+  if (threadIdx.x == 0) sh.lefts = 0;      // (the barriers below order it)
+  {
+    uint32_t place_key = 0u;
+    if (last - first >= 32 && !ends) {
+      const uint32_t mine = kHeld ? held[0] : load_key(first + lane);
+      uint32_t not_less = 0;
 #pragma unroll 8
-    for (int j = 0; j < 32; ++j) not_less += __shfl_sync(0xffffffffu, mine, j) >= mine;
-    const uint32_t place = static_cast<uint32_t>(32LL * (a.K - above) / (L - above));
-    from = to = max_of(not_less > place ? mine : 0u);
+      for (int j = 0; j < 32; ++j) not_less += __shfl_sync(0xffffffffu, mine, j) >= mine;
+      const uint32_t place = static_cast<uint32_t>(32LL * (a.K - above) / (L - above));
+      place_key = max_of(not_less > place ? mine : 0u);
+    }
+    if (lane == 0) sh.warps[turn][0][warp] = place_key;
+    __syncthreads();
+    const uint32_t x = lane < warps ? sh.warps[turn][0][lane] : 0u;
+    const int n = __popc(__ballot_sync(0xffffffffu, x != 0u));
+    if (n <= 8) {
+      from = min_of(x != 0u ? x : kMustKeep);
+      to = max_of(x);
+    } else {
+      int more = 0;                        // of the others
+      for (int j = 0; j < warps; ++j) {
+        const uint32_t y = __shfl_sync(0xffffffffu, x, j);
+        more += y > x || (y == x && j < lane);
+      }
+      const int spread = static_cast<int>(sqrtf(static_cast<float>(n))) + 1;
+      from = max_of(x != 0u && more == min(n - 1, n / 2 + spread) ? x : 0u);
+      to = max_of(x != 0u && more == max(0, (n - 1) / 2 - spread) ? x : 0u);
+    }
+    if (size > 1) over_cluster(from, to, min_of, max_of, kMustKeep, 0u);
+    turn ^= 1;
   }
-  exchange(from, to, min_of, max_of, kMustKeep, 0u);
   if (from > to) from = to = 0xbf800000u;  // no sample: some weight
   from = min(max(from, 1u), kMustKeep - 2);
   to = min(max(to, from), kMustKeep - 2) + 1;
-  uint32_t leap = max(to - from, 1u << 16);    // past the sample, where T is not inside
   // Then the root of count - K.  An end that stays while the other one moves twice in a row loses
   // half of its weight; every fourth pivot is the middle.
+  uint32_t leap = max(to - from, 1u << 16);    // past the sample, where T is not inside
   float f_low = 1.f, f_high = 1.f;
   int moved = 0;
-  for (int step = 0; !done && high - low > 1; ++step) {
-    if (kHeld && size == 1 && step >= 2 && from_low - above <= kFewLeft) {
-      // The keys in the bracket, ranked by the first warp.
-#pragma unroll
-      for (int e = 0; e < kOwn; ++e)
-        if (held[e] - low < high - low && first + e * 32 + lane < last)
-          sh.left[atomicAdd(&sh.lefts, 1)] = held[e];
-      __syncthreads();
-      if (warp == 0) {
-        const int n = from_low - above, wanted = a.K - above;
-#pragma unroll
-        for (int x0 = 0; x0 < kFewLeft; x0 += 32) {
-          const int x = x0 + lane;
-          if (x >= n) break;
-          const uint32_t mine = sh.left[x];
-          int more = 0, same = 0;
-          for (int j = 0; j < n; ++j) {
-            more += sh.left[j] > mine;
-            same += sh.left[j] == mine;
-          }
-          if (more < wanted && wanted <= more + same) {      // the same for all that are T
-            sh.found[0] = mine;
-            sh.found[1] = more;
-            sh.found[2] = same;
-          }
-        }
-      }
-      __syncthreads();
-      low = sh.found[0];
-      high = low + 1;
-      above += sh.found[1];
-      from_low = above + sh.found[2];
-      break;
-    }
-    uint32_t pivot;
-    if (step < 2) {
-      pivot = step == 0 ? from : to;
-      if (pivot <= low || pivot >= high) continue;
-    } else if (low == 0u || high == kMustKeep) {
-      pivot = low == 0u ? (high > leap ? high - leap : 1u)
-                        : (high - low > leap ? low + leap : high - 1);
-      leap = leap < 1u << 28 ? leap * 8 : 1u << 31;
-    } else {
-      const uint32_t width = high - low;
-      uint32_t d = width / 2;
-      if (step == 6 && low == from) d = 1;     // the key of many tokens?
-      else if ((step & 3) != 3)
-        d = static_cast<uint32_t>(static_cast<float>(width) * __fdividef(f_low, f_low + f_high));
-      pivot = low + min(max(d, 1u), width - 1);
-    }
-    const int c = count_from(pivot);
+  uint32_t own_low = 0, own_high = 0;      // of this thread, once the end has moved
+  const auto cut_at = [&](uint32_t pivot, int c, uint32_t own) {
     if (c == a.K) {                        // exactly the keys from here on are kept
       high = pivot;
       above = c;
@@ -219,15 +196,77 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
     } else if (c > a.K) {
       low = pivot;
       from_low = c;
+      own_low = own;
       f_low = static_cast<float>(c - a.K) + 0.5f;
       if (moved > 0) f_high *= 0.5f;
       moved = 1;
     } else {
       high = pivot;
       above = c;
+      own_high = own;
       f_high = static_cast<float>(a.K - c) - 0.5f;
       if (moved < 0) f_low *= 0.5f;
       moved = -1;
+    }
+  };
+  int step = 0;
+  const auto next_pivot = [&] {
+    ++step;
+    if (low == 0u || high == kMustKeep) {
+      const uint32_t pivot = low == 0u ? (high > leap ? high - leap : 1u)
+                                       : (high - low > leap ? low + leap : high - 1);
+      leap = leap < 1u << 28 ? leap * 8 : 1u << 31;
+      return pivot;
+    }
+    const uint32_t width = high - low;
+    uint32_t d = width / 2;
+    if (step == 5 && low == from) d = 1;   // the key of many tokens?
+    else if ((step & 3) != 0)
+      d = static_cast<uint32_t>(static_cast<float>(width) * __fdividef(f_low, f_low + f_high));
+    return low + min(max(d, 1u), width - 1);
+  };
+  if (!done) {
+    const uint32_t own_from = own_count(from), own_to = own_count(to);
+    uint32_t x = own_from, y = own_to;
+    sum_all(x, y);
+    cut_at(from, x, own_from);             // x >= y: the second one lies inside the bracket, too
+    if (!done && to < high) cut_at(to, y, own_to);
+  }
+  moved = 0;
+  bool few = false;                        // the bracket's keys are in shared memory, `left` of them
+  int left = 0, beyond = 0;                // and `beyond` tokens have greater ones
+  while (!done && high - low > 1) {
+    if (kHeld && size == 1 && !few && low > 0u && high < kMustKeep &&
+        from_low - above <= min(kLeft, 8 * static_cast<int>(blockDim.x))) {
+      // (in no order that matters)
+      const uint32_t own = own_low - own_high, width = high - low;
+      const int upto = warp_inclusive(static_cast<int>(own));
+      int base = 0;
+      if (lane == 31) base = atomicAdd(&sh.lefts, static_cast<uint32_t>(upto));
+      uint32_t* put = sh.left + __shfl_sync(0xffffffffu, base, 31) + upto - own;
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e)
+        if (held[e] - low < width) *put++ = held[e];
+      few = true;
+      left = from_low - above;
+      beyond = above;
+      for (int x = left + threadIdx.x; x < (left + 3) / 4 * 4; x += blockDim.x) sh.left[x] = 0u;
+      __syncthreads();
+    }
+    const uint32_t pivot = next_pivot();
+    if (few) {
+      uint32_t c[2] = {0, 0};
+      for (int x = threadIdx.x * 4; x < left; x += blockDim.x * 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(sh.left + x);
+        c[0] += k.x >= pivot;
+        c[1] += k.y >= pivot;
+        c[0] += k.z >= pivot;
+        c[1] += k.w >= pivot;
+      }
+      cut_at(pivot, beyond + sum_one(c[0] + c[1]), 0u);
+    } else {
+      const uint32_t own = own_count(pivot);
+      cut_at(pivot, sum_one(own), own);
     }
   }
   // Kept: the keys >= high and, while they last, the first K - above tokens with key low.  Where
