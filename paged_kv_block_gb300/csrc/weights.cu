@@ -80,6 +80,10 @@ __device__ __forceinline__ int over(int x, unsigned long long by_ps) {
 // quad.
 // A unit is a.chunk keys of a request and KV head, 128 at a time (32 per warp); the pages of the
 // next 128 are looked up while the present ones are on their way.
+// 690 MB of keys (64 requests, 8 KV heads): 128 us, 79% of the copy rate.  Rings in shared memory,
+// a warp each, took longer: filled by the lanes' asynchronous copies 212 us, by bulk copies of 16
+// rows, 12 warps per SM, 175 us, of 32 rows, 8 warps, 149 us (what a step needs beside its keys
+// then stands in the way of fewer warps).
 constexpr int kNarrowThreads = 128;
 constexpr int kNarrowKeys = 128;
 
