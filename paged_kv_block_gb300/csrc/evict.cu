@@ -13,13 +13,14 @@ namespace {
 // sample of 32 keys of every warp; it is cut at pivots by interpolation between its counts until
 // exactly the wanted number of tokens follow or one key is left.  Keys stay in registers, kOwn a
 // thread (32; 8 where there are CTAs to spare and time is latency): a step costs two instructions a
-// key and a barrier.  What a bracket of few keys holds goes to shared memory, where a step is cheap.
+// key and a barrier.  What a bracket of few keys holds goes to shared memory: steps there are cheap.
 // A last pass writes the indices in order, those of key T until their number is reached.
-// Instructions and barriers bound it: for 2,048 lists of 8,192 tokens histograms of the keys' digits
-// took 143 us (half of the tokens may have the same weight, and then shared-memory atomics queue
-// up), plain bisection 112 us, interpolation between the least and the greatest key 64 us, with
-// the sample but on the registers to the end 56 us, this 54 us; one warp alone in the last steps 58
-// us, four pivots at a time there 60 us (what every warp does beside the counting doubles).
+// Instructions bound it (the issue slots are 74% full): for 2,048 lists of up to 8,192 tokens
+// histograms of the keys' digits took 143 us (half of the tokens may have the same weight, and then
+// shared-memory atomics queue up), plain bisection 112 us, interpolation between the least and the
+// greatest key 64 us, with the sample but on the registers to the end 56 us, this 54 us; one warp
+// alone in the last steps 58 us, four pivots at a time there 60 us (what every warp does beside the
+// counting doubles).
 constexpr uint32_t kMustKeep = 0xffffffffu;
 constexpr int kSelectCluster = 8;
 constexpr int kSelectThreads = 1024;
@@ -144,8 +145,8 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
   uint32_t low = 0u, high = kMustKeep;
   int from_low = L, above = a.sink + a.recent;
   bool done = above == a.K;                // nothing else is kept
-  // The sample: every warp with 32 keys, all of them open, takes the one at the wanted place in their
-  // order; of up to 8 warps' keys the least and the greatest, of more those some two deviations
+  // The sample: every warp with 32 keys, all of them open, takes the one at the wanted place in
+  // their order; of up to 8 warps' keys the least and the greatest, of more those some two deviations
   // about the median, are the first two pivots (one key where many tokens have it).
   uint32_t from = kMustKeep, to = 0u;
   if (threadIdx.x == 0) sh.lefts = 0;      // (the barriers below order it)
@@ -233,7 +234,7 @@ __device__ __forceinline__ void select_list(const SelectArgs& a, SelectShared& s
     if (!done && to < high) cut_at(to, y, own_to);
   }
   moved = 0;
-  bool few = false;                        // the bracket's keys are in shared memory, `left` of them
+  bool few = false;                        // the bracket's keys, `left`, are in shared memory
   int left = 0, beyond = 0;                // and `beyond` tokens have greater ones
   while (!done && high - low > 1) {
     if (kHeld && size == 1 && !few && low > 0u && high < kMustKeep &&

@@ -221,3 +221,22 @@ def test_empty_calls():
     b = Rows(15, 2, 2, 4, 8)
     b.evict([], np.zeros((1, 0, 2, 5), np.int64))
     b.evict([0, 1], np.zeros((1, 2, 2, 5), np.int64))       # empty rows
+
+
+def test_pages_past_32_bits():
+    """A pool of 2.5e9 elements: the tokens of its last pages move within them."""
+    P, ps, L, K = 600_000, 16, 120, 40
+    pool = torch.empty(P, 2, 1, ps, 128, dtype=torch.bfloat16, device=DEV)
+    pages = [P - 1 - 3 * j for j in range(8)]
+    pool[pages] = torch.randn(8, 2, 1, ps, 128, device=DEV).to(torch.bfloat16)
+    held = pool[pages].transpose(0, 1).reshape(2, -1, 128).clone()
+    refs = torch.zeros(P, dtype=torch.int32, device=DEV)
+    refs[pages] = 1
+    tables, lens, word = i32([pages]), i32([L]), i32([0])
+    kept = sorted(random.Random(15).sample(range(L), K))
+    pkb.evict_cache_rows(pkb.cache_pools([pool]), i32([0]), i32([[[kept]]]), tables, lens, refs,
+                         status=word)
+    assert word.item() == 0 and lens.item() == K and tables.tolist() == [pages]
+    now = pool[pages[:3]].transpose(0, 1).reshape(2, -1, 128)[:, :K]
+    assert torch.equal(now, held[:, kept])
+    assert refs[pages].tolist() == [1, 1, 1, 0, 0, 0, 0, 0]
