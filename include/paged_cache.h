@@ -273,6 +273,7 @@ typedef struct paged_weights_params {
  * where the old weight of the tokens that the call's queries stand for, the last nq of a request
  * with nq queries, is 0: their entries are written without being read, and so is every entry with
  * decay = 0.  Entries past a request's length are left alone, and so is a request without queries.
+ * Attention calls with a window are not served: keys outside it would count.
  *   q_dev [total_q, Hq, D] bf16 and lse_dev [total_q, Hq] fp32, natural logarithm: the attention
  *   call's queries and its LSE (a row with an LSE of -inf sees nothing and adds nothing);
  *   k_cache_dev: combined cache or K pool;

@@ -81,7 +81,7 @@ def accumulate_attention_weights(query, lse, paged_kv_cache, seq_lens_kv, weight
     paged_kv_indptr with paged_kv_indices; the cache a combined one or a (K, V) pair.  Older weights
     are multiplied by `decay`; the entries of the call's own query tokens (the last of each request)
     start at 0.  last_queries = n counts only the last n queries of each request.
-    The call has no gradient.  status: an int32 word that device-side findings are OR-ed into."""
+    The attention call must have had no window; this one has no gradient.  status: an int32 word that device-side findings are OR-ed into."""
     dev = _cache._device()
     kc, _, combined, P, Hkv, ps, D = _cache._geometry(paged_kv_cache, dev)
     B = _cache._count(seq_lens_kv, "seq_lens_kv")

@@ -343,3 +343,12 @@ def test_graphs_that_share_a_workspace_and_streams_that_do_not():
     torch.cuda.synchronize()
     for pair in got:
         assert all(torch.equal(a, b) for a, b in zip(pair, want))
+
+
+@pytest.mark.parametrize("Hq", [4, 16])
+def test_queries_before_the_first_key(Hq):
+    """Requests of fewer tokens than queries: the first queries see nothing."""
+    p = Problem(22, [(0, [2, 5]), (1, [1, 40]), (3, [1])], Hq, 2, SQ=4)
+    out, lse = p.check()
+    assert not out[0, :2].any() and torch.isneginf(lse[0, :2]).all()
+    p.check(causal=False)
