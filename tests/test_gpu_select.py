@@ -110,3 +110,28 @@ def test_captured_and_on_another_stream():
     other = pkb.select_cache_tokens(rows, w, lens, 50, stream=side)
     side.synchronize()
     assert torch.equal(other, kept)
+
+
+@pytest.mark.parametrize("kind", ["uniform", "ties", "equal", "zeros", "special"])
+@pytest.mark.parametrize("L", [2, 31, 64, 255, 256, 257, 700, 3000])
+def test_all_but_one_and_only_one(kind, L):
+    """The selection's ends, for short lists and longer ones, beside tokens that are kept anyway."""
+    w = make(L, (2, 2, 3, L + 7), kind)
+    for keep, sink, recent in ((1, 0, 0), (L - 1, 0, 0), (1, 1, 0), (L // 2, L // 4, L // 4),
+                               (L // 2 + 1, 0, L // 2), (L - 1, 1, L - 2 - L // 3)):
+        if keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep:
+            check(w, [L, max(1, L - 1)], [1, 0], keep, sink, recent)
+
+
+def test_short_rows_of_wide_lists():
+    """Rows of 0 to 257 tokens where the width asks for a cluster."""
+    w = make(6, (1, 6, 1, 50000), "ties")
+    check(w, [0, 1, 40, 256, 257, 49999], [5, 4, 3, 2, 1, 0], 33, 3, 5)
+
+
+def test_one_of_many():
+    """The greatest, and the least left out, of long lists: far outside every sample."""
+    for kind in ("uniform", "signed", "special"):
+        w = make(7, (1, 3, 2, 60001), kind)
+        check(w, [60001, 59000, 300], [0, 1, 2], 5, 3, 1)
+        check(w, [60001, 59000, 300], [0, 1, 2], 58999, 3, 1)
