@@ -554,7 +554,7 @@ def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_
                             0, seq_len_q, 0, 0, DTYPE[out_dtype])
     given = out
     if out is None:
-        out = _cache._new(shape, out_dtype, query.device, stream)
+        out = _cache._empty(query, out_dtype, stream)
     op = _eviction._plain(out, out_dtype, dev, "out", shape)
     lp = None if lse is None else _eviction._plain(lse, torch.float32, dev, "lse", shape[:-1])
     if workspace_buffer is None:

@@ -15,7 +15,7 @@ namespace {
 // thread (32; 8 where there are CTAs to spare and time is latency): a step costs two instructions a
 // key and a barrier.  What a bracket of few keys holds goes to shared memory: cheap steps there.
 // A last pass writes the indices in order, those of key T until their number is reached.
-// Instructions bound it (the issue slots are 74% full): for 2,048 lists of up to 8,192 tokens
+// Instructions bound it (the issue slots are 70% full): for 2,048 lists of up to 8,192 tokens
 // histograms of the keys' digits took 143 us (half of the tokens may have the same weight, and then
 // shared-memory atomics queue up), plain bisection 112 us, interpolation between the least and the
 // greatest key 64 us, this 56 us; one warp alone in the last steps 58 us, four pivots at a time

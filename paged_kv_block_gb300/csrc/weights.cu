@@ -2,6 +2,7 @@
 // of a request the sum over its queries, and over the query heads of the key's KV head, of
 // exp(scale q.k - lse), with the log-sum-exp that the attention call returned.  No maximum and no
 // second pass are needed, and no value row is read.
+#include <climits>
 #include <cmath>
 
 #include "pages.cuh"
@@ -23,6 +24,8 @@ struct WeightsArgs {
   uint32_t* status;
   int B, Hq, Hkv, G, W, C, SQ, total, last, causal, ps, P;
   int chunk;                               // narrow: keys of a unit
+  int more_than, at_most;                  // rows (query, head) of the requests looked after
+  int beside;                              // narrow: the launch before this one is the same call's
   unsigned long long by_ps;                // ceil(2^64 / ps)
   long long page_rows;                     // rows of D columns per page
   float scale_log2, decay;
@@ -61,6 +64,8 @@ __device__ __forceinline__ Request request_of(const WeightsArgs& a, int b) {
   if (r.keys > room) r.keys = static_cast<int>(room);
   if (nq == 0) r.keys = 0;                 // nothing is asked of the request
   else r.bad |= r.keys < L;
+  const long long rows = static_cast<long long>(r.n) * a.G;
+  if (rows <= a.more_than || rows > a.at_most) r.keys = 0;     // another launch's
   return r;
 }
 // Row of a head of KV head h in lse, and of D columns in q.
@@ -84,6 +89,7 @@ __device__ __forceinline__ int over(int x, unsigned long long by_ps) {
 // a warp each, took longer: filled by the lanes' asynchronous copies 212 us, by bulk copies of 16
 // rows, 12 warps per SM, 175 us, of 32 rows, 8 warps, 149 us (what a step needs beside its keys
 // then stands in the way of fewer warps).
+constexpr int kHeavyRows = 32;             // with more, a request is taken as a prompt
 constexpr int kNarrowThreads = 128;
 constexpr int kNarrowKeys = 128;
 
@@ -93,7 +99,8 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
   constexpr int kBlocks = D / 32;          // 32 columns: two MMAs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
-  grid_dependency_wait();
+  // (beside: wide_kernel starts this one when it has waited itself, and writes other requests)
+  if (!a.beside) grid_dependency_wait();
   grid_launch_dependents();
   const int pairs = a.B * a.Hkv;
   const int chunks = (a.W + a.chunk - 1) / a.chunk;
@@ -203,6 +210,7 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
       }
     }
   }
+  if (a.beside) grid_dependency_wait();
 }
 
 // ---- many rows: prompts ------------------------------------------------------------------------
@@ -387,6 +395,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       return b < a.B ? (request_of(a, b).keys + kKeys - 1) / kKeys : 0;
     };
     int cached[kCached], most = 0;
+    uint32_t empty = 0;                    // of the first 32 such tiles, those without a unit
 #pragma unroll
     for (int g = 0; g < kCached; ++g) cached[g] = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -396,6 +405,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       for (int g = 0; g < kCached; ++g)
         if (b0 == 32 * g) cached[g] = n;
       most = max(most, n);
+      if (!__any_sync(0xffffffffu, n > 0) && b0 < 32 * 32) empty |= 1u << (b0 / 32);
     }
     most = __reduce_max_sync(0xffffffffu, most);
     int s = 0;
@@ -403,6 +413,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     bool ok = true;
     for (int left = most; ok && left > 0; --left) {
       for (int b0 = 0; ok && b0 < a.B; b0 += 32) {
+        if (b0 < 32 * 32 && (empty >> (b0 / 32) & 1u)) continue;
         int n = 0;
         if (b0 < 32 * kCached) {
 #pragma unroll
@@ -680,18 +691,36 @@ int launch_wide(const WeightsArgs& a, cudaStream_t st) {
                                            kWideThreads, smem, st, qmap, kmap, a));
 }
 
+// All of the SM's memory as L1, where the loads in flight lie: behind a kernel with much shared
+// memory (attention's) the SMs would keep its division, and narrow_kernel take 1.6 times as long.
+template <typename Kernel>
+bool all_l1(Kernel* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxL1) != cudaSuccess)
+    return false;
+  if (bit != 0) done.fetch_or(bit, std::memory_order_acq_rel);
+  return true;
+}
+
 template <int D, int NT>
-cudaError_t launch_narrow(WeightsArgs a, cudaStream_t st) {
+int launch_narrow(WeightsArgs a, cudaStream_t st) {
   const int sms = current_sm_count();
-  if (sms <= 0) return cudaErrorUnknown;
+  if (sms <= 0) return PAGED_ATTN_ERR_CUDA;
   // long units where there are many: what a unit reads of its request counts once per unit
   const long long steps = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, kNarrowKeys);
   const long long most = 16LL * sms;
   a.chunk = kNarrowKeys * (steps >= 8 * most ? 4 : (steps >= 4 * most ? 2 : 1));
   const long long units = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, a.chunk);
   count_launches(1);
-  return launch_after_previous(narrow_kernel<D, NT>, static_cast<int>(units < most ? units : most),
-                               kNarrowThreads, 0, st, a);
+  static std::atomic<uint64_t> ready{0};
+  if (!all_l1(narrow_kernel<D, NT>, ready)) return PAGED_ATTN_ERR_CUDA;
+  return cuda_status(launch_after_previous(narrow_kernel<D, NT>,
+                                           static_cast<int>(units < most ? units : most),
+                                           kNarrowThreads, 0, st, a));
 }
 
 bool params_ok(const paged_weights_params* p) {
@@ -749,6 +778,8 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   a.scale_log2 = scale * kLog2e;
   a.decay = p->decay;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.more_than = 0;
+  a.at_most = INT_MAX;
   long long rows = ceil_div(p->total_q, p->batch);         // of a request, on average
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
@@ -762,9 +793,23 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
       return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
   }
+  // Few rows on average, but some request may have many (a prompt among single tokens): a launch
+  // for each kind.  511 single tokens and a prompt of 1,000, 2,000 keys each, 8 KV heads: 510 us; 3,650
+  // as few rows, 618 as many.  63 and a prompt of 64, 4,000 keys: 104 us; 214 and 156.
+  const long long most = (a.last > 0 ? a.last : static_cast<long long>(p->total_q) - a.B + 1) * a.G;
+  const bool mixed = qo_indptr && p->total_q > a.B && most > kHeavyRows;
+  if (mixed) {
+    WeightsArgs heavy = a;
+    heavy.more_than = kHeavyRows;
+    const int rc = p->head_dim == 128 ? launch_wide<128, false>(heavy, st)
+                                      : launch_wide<256, false>(heavy, st);
+    if (rc != PAGED_ATTN_OK) return rc;
+    a.at_most = kHeavyRows;
+    a.beside = 1;
+  }
   if (p->head_dim == 128)
-    return cuda_status(rows <= 8 ? launch_narrow<128, 1>(a, st) : launch_narrow<128, 2>(a, st));
-  return cuda_status(rows <= 8 ? launch_narrow<256, 1>(a, st) : launch_narrow<256, 2>(a, st));
+    return rows <= 8 ? launch_narrow<128, 1>(a, st) : launch_narrow<128, 2>(a, st);
+  return rows <= 8 ? launch_narrow<256, 1>(a, st) : launch_narrow<256, 2>(a, st);
 }
 
 }  // extern "C"

@@ -282,3 +282,29 @@ def test_prompts_beside_single_tokens():
     """One request with many queries in a batch of few on average, and the other way round."""
     Problem(15, [300] + [40 + b for b in range(20)], [90] + [1] * 20, 4, 2, 128, 16).run()
     Problem(16, [700, 50, 20, 90], [300, 1, 0, 1], 8, 2, 256, 16).run(csr=True)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_a_prompt_in_a_large_batch_of_single_tokens(D):
+    """Both kinds in one call, beyond the requests that the schedule keeps at hand; also with an
+    invalid page in each."""
+    new = [1] * 150
+    new[140], new[7], new[60], new[61] = 70, 9, 0, 8
+    p = Problem(17, [100 + b % 13 for b in range(150)], new, 4, 1, D, 16)
+    p.run()
+    p.run(last=3)
+    p.run(csr=True, decay=0.5)
+    tables = [list(r) for r in p.tables]
+    tables[140][2] = tables[30][1] = 10 ** 6
+    w, status = p.w.to(DEV), i32([0])
+    pkb.accumulate_attention_weights(p.q.to(DEV), p.lse.to(DEV), p.cache, i32(p.lens), w,
+                                     block_tables=i32(tables), qo_indptr=i32(p.starts),
+                                     status=status)
+    assert status.item() == O.METADATA
+    clean = p.run()
+    for b in range(150):
+        skip = {140: slice(32, 48), 30: slice(16, 32)}.get(b, slice(0, 0))
+        x, y = w[b, :, :p.lens[b]].clone(), clean[b, :, :p.lens[b]].clone()
+        assert torch.equal(x[:, skip].cpu(), p.old[b][:, :p.lens[b]][:, skip])
+        x[:, skip] = y[:, skip] = 0
+        assert torch.equal(x, y)
