@@ -268,7 +268,31 @@ struct WideCtrl {
   uint64_t q_full[8], q_empty[8];
   uint32_t tmem;
   int abort_flag;
+  int tiles_begun, looked;               // beats of the MMA warp, and of the units' warp
 };
+// A wait for a ring entry of the units may last as long as another role's whole unit (0.1 s are
+// 13 million rows of queries), or its look through a large batch.  Its limit is one of progress:
+// the clock starts anew whenever the beat of the role waited for moves.
+__device__ __forceinline__ bool unit_wait_warp(uint64_t* bar, uint32_t parity,
+                                               const volatile int* beat, uint32_t* status,
+                                               volatile int* abort) {
+  bool ok = mbar_test(bar, parity);
+  if (!ok) {
+    long long t0 = clock64();
+    int seen = *beat;
+    while (!*abort && !(ok = mbar_test(bar, parity))) {
+      const int now = *beat;
+      if (now != seen) {
+        seen = now;
+        t0 = clock64();
+      } else if (clock64() - t0 > kWaitCycles) {
+        *abort = 1;
+        report_error(status, kErrTimeout);
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
 template <int D, bool kPair>
 constexpr int wide_smem() {
   using X = Wide<D, kPair>;
@@ -351,7 +375,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1);
     }
-    ctl->abort_flag = 0;
+    ctl->abort_flag = ctl->tiles_begun = ctl->looked = 0;
     fence_mbar_init();
   }
   // rows of a query tile that no box writes: zero scores
@@ -373,8 +397,12 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   volatile int* abort_flag = &ctl->abort_flag;
   // A role's view of the units: entry s of the ring, given back by release().
   const auto next_unit = [&](int s) {
-    return mbar_wait_warp<true>(&ctl->unit_full[s % kUnits], (s / kUnits) & 1, a.status,
-                                abort_flag);
+    return unit_wait_warp(&ctl->unit_full[s % kUnits], (s / kUnits) & 1, &ctl->looked, a.status,
+                          abort_flag);
+  };
+  const auto entry_free = [&](int s) {
+    return s < kUnits || unit_wait_warp(&ctl->unit_empty[s % kUnits], ((s / kUnits) - 1) & 1,
+                                        &ctl->tiles_begun, a.status, abort_flag);
   };
   const auto release = [&](int s) {
     __syncwarp();
@@ -394,12 +422,14 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     const auto count_tiles = [&](int b) {
       return b < a.B ? (request_of(a, b).keys + kKeys - 1) / kKeys : 0;
     };
-    int cached[kCached], most = 0;
+    volatile int* looked = &ctl->looked;
+    int cached[kCached], most = 0, beat = 0;
     uint32_t empty = 0;                    // of the first 32 such tiles, those without a unit
 #pragma unroll
     for (int g = 0; g < kCached; ++g) cached[g] = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane, n = count_tiles(b);
+      *looked = ++beat;
       if (blockIdx.x == 0 && b < a.B && request_of(a, b).bad) report_error(a.status, kErrMetadata);
 #pragma unroll
       for (int g = 0; g < kCached; ++g)
@@ -413,6 +443,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     bool ok = true;
     for (int left = most; ok && left > 0; --left) {
       for (int b0 = 0; ok && b0 < a.B; b0 += 32) {
+        *looked = ++beat;
         if (b0 < 32 * 32 && (empty >> (b0 / 32) & 1u)) continue;
         int n = 0;
         if (b0 < 32 * kCached) {
@@ -441,8 +472,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             }
           }
           const int slot = s % kUnits;
-          if (s >= kUnits && !mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
-                                                   a.status, abort_flag)) {
+          if (!entry_free(s)) {
             ok = false;
             break;
           }
@@ -471,12 +501,9 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       }
     }
     const int slot = s % kUnits;
-    if (ok && (s < kUnits || mbar_wait_warp<true>(&ctl->unit_empty[slot], ((s / kUnits) - 1) & 1,
-                                                  a.status, abort_flag))) {
-      if (lane == 0) {
-        ctl->units[slot].tiles = -1;
-        mbar_arrive(&ctl->unit_full[slot]);
-      }
+    if (ok && entry_free(s) && lane == 0) {
+      ctl->units[slot].tiles = -1;
+      mbar_arrive(&ctl->unit_full[slot]);
     }
   } else if (warp == kSumWarps) {
     // =============================== copies =============================================
@@ -556,6 +583,7 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
       ++units;
       for (int i = 0; ok && i < tiles; ++i, ++it) {
         const int buf = it % kSBuffers;
+        if (lane == 0) *const_cast<volatile int*>(&ctl->tiles_begun) = it;
         if (it >= kSBuffers && !mbar_wait_fast_warp(&ctl->s_empty[buf], ((it / kSBuffers) - 1) & 1,
                                                     a.status, abort_flag)) {
           ok = false;
