@@ -284,8 +284,9 @@ int paged_decode_run(const paged_decode_params* params, const void* query_dev,
  *     group's first request that is not empty.  Any length: what some member's queries do not all
  *     see (past its own length, or under the causal mask past its first query) is left to the
  *     requests themselves.
- * A length of 0 is allowed (0 / -inf), in a group too: it takes no part.  The outputs differ from paged_decode_run's by the
- * rounding of the fp32 merge and of the probabilities alone. */
+ * A length of 0 is allowed (0 / -inf), in a group too: it takes no part.  The outputs differ from
+ * paged_decode_run's by the rounding of the fp32 merge and of the probabilities alone.  Partials of
+ * the prefixes make up most of the workspace; it grows with max_seq_len from 2 million keys on. */
 size_t paged_decode_shared_workspace_size(const paged_decode_params* params, int num_groups);
 int paged_decode_shared_run(const paged_decode_params* params, int num_groups,
                             const void* query_dev, const void* k_dev, const void* v_dev,

@@ -338,6 +338,19 @@ struct SharedLayout {
   int tile_capacity, item_capacity;
 };
 
+// Tiles of the prefixes at most: a part each and two more per SM (the plan chooses parts that fit,
+// prefix.cu), or parts of the longest length.
+long long shared_tile_capacity(const paged_decode_params* p, int num_groups) {
+  const int G = p->num_qo_heads / p->num_kv_heads, B = p->batch;
+  const int pairs = num_groups < B / 2 ? num_groups : B / 2;
+  if (pairs == 0) return 0;
+  const long long tiles = static_cast<long long>(p->num_kv_heads) *
+                          (static_cast<long long>(B) * decode_q_per_item(p) / cta_tile_tokens(G) +
+                           pairs + 1);
+  const long long parts = ceil_div_ll(ceil_div_ll(p->max_seq_len, kKvTile), kPartTiles);
+  return 2 * num_sms() + tiles * parts;
+}
+
 // The decode forms with a fixed number of queries and without a window (most of a long prefix
 // lies outside a window); units of at most kDecodeMaxRows rows.
 bool shared_params_ok(const paged_decode_params* p, int num_groups) {
@@ -347,18 +360,17 @@ bool shared_params_ok(const paged_decode_params* p, int num_groups) {
   const int G = p->num_qo_heads / p->num_kv_heads;
   if (static_cast<long long>(G) * decode_q_per_item(p) > kDecodeMaxRows) return false;
   // the capacities below stay below 2^31 tiles and items
-  return static_cast<long long>(p->batch) * decode_q_per_item(p) * p->num_kv_heads < (1LL << 27);
+  return static_cast<long long>(p->batch) * decode_q_per_item(p) * p->num_kv_heads < (1LL << 27) &&
+         shared_tile_capacity(p, num_groups) <= INT_MAX;
 }
 
-// Capacities: one part per tile of a prefix and two more per SM (the plan chooses parts that fit,
-// prefix.cu); a tail's splits are one plus its share of kTailWarps or kTailSplits per SM.
+// A tail's splits are one plus its share of kTailWarps or kTailSplits per SM.
 SharedLayout shared_layout(const paged_decode_params* p, int num_groups) {
   SharedLayout s{};
   Layout l;
   const int G = p->num_qo_heads / p->num_kv_heads, SQ = decode_q_per_item(p), B = p->batch;
-  const int sms = num_sms(), pairs = num_groups < B / 2 ? num_groups : B / 2;
-  s.tile_capacity =
-      pairs == 0 ? 0 : 2 * sms + p->num_kv_heads * (B * SQ / cta_tile_tokens(G) + pairs + 1);
+  const int sms = num_sms();
+  s.tile_capacity = static_cast<int>(shared_tile_capacity(p, num_groups));
   s.item_capacity = (G * SQ <= kTailRows ? kTailWarps : kTailSplits) * sms + p->num_kv_heads * B;
   s.status = l.take(sizeof(uint32_t) * 4);
   s.n_tiles = l.take(sizeof(int));

@@ -199,6 +199,9 @@ int launch_decode(const DecodeLaunch& a, cudaStream_t st);
 // 16 keys, a warp each; longer ones on the decode kernel, in items of a multiple of 128.
 constexpr int kTailRows = 16;
 constexpr int kTailWarps = 12, kTailSplits = 8;      // items aimed at per SM, by kind
+// Key tiles of a part of a prefix at most (2 million keys): some 33 ms, since the warp that claims
+// tiles waits as long as one takes, and a wait gives up after 0.1 s.
+constexpr int kPartTiles = 1 << 14;
 // A request's prefix partials: rows 256 (base + (head * row_tiles + tile) * splits + s) of the
 // tensor-core kernel's partial output, s < splits; its queries are tokens from `token` on among
 // the group's, 256 / G of them to a tile.

@@ -180,11 +180,11 @@ shared_plan_kernel(const __grid_constant__ SharedLaunch a) {
     const int ctas = max(static_cast<int>(a.sms * share + 0.5f), 1);
     const float longest = choice * each + kTileCost;
     float time = count <= ctas ? longest : work / ctas + 0.5f * longest;
-    if (count > a.tile_capacity) time = 3.4e38f;
+    if (count > a.tile_capacity || choice > kPartTiles) time = 3.4e38f;    // (kPartTiles fits)
     const uint32_t best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));
     const int pick = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(time) == best)) - 1;
     if (lane == pick) {
-      chosen[0] = count > a.tile_capacity ? 1 << 30 : choice;
+      chosen[0] = choice;
       *a.max_ctas = ctas;
     }
     const float aim = static_cast<float>(a.items_per_sm * a.sms);
