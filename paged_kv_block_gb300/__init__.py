@@ -509,13 +509,14 @@ def batch_decode_with_paged_kv_cache(query, kv_cache, workspace_buffer, paged_kv
 
 @functools.lru_cache(maxsize=512)
 def _shared_params(*fields):
-    return C.byref(DecodeParams(*fields))
+    return _eviction._struct(DecodeParams, fields)
 
 
 def shared_prefix_workspace_size(query, kv_cache, max_seq_len, num_groups, *, seq_len_q=1) -> int:
     """Workspace bytes of batch_decode_with_shared_prefix."""
     return paged_decode_shared_workspace_size(
-        decode_params(query, kv_cache, max_seq_len, seq_len_q=seq_len_q), num_groups)
+        decode_params(query, kv_cache, _eviction._int(max_seq_len, "max_seq_len"),
+                      seq_len_q=seq_len_q), _eviction._int(num_groups, "num_groups"))
 
 
 def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_indptr,

@@ -43,14 +43,30 @@ EXPORTS = {
 }
 
 
+def _int(x, name):
+    """A whole number that the C call's int holds (ctypes would cut it off without a word)."""
+    x = operator.index(x)
+    if not -_cache._INT_MAX - 1 <= x <= _cache._INT_MAX:
+        raise ValueError(f"{name} is {x}, out of 32 bits")
+    return x
+
+
+def _struct(cls, fields):
+    """The parameter struct; its whole numbers are checked here, once per set of arguments."""
+    for (name, kind), x in zip(cls._fields_, fields):
+        if kind is C.c_int:
+            _int(x, name)
+    return C.byref(cls(*fields))
+
+
 @functools.lru_cache(maxsize=512)
 def _weights_params(*fields):
-    return C.byref(WeightsParams(*fields))
+    return _struct(WeightsParams, fields)
 
 
 @functools.lru_cache(maxsize=512)
 def _select_params(*fields):
-    return C.byref(SelectParams(*fields))
+    return _struct(SelectParams, fields)
 
 
 def _plain(t, dtype, dev, name, shape):
@@ -172,7 +188,8 @@ def select_cache_tokens(rows, weights, seq_lens, keep, *, sink=0, recent=0, kept
 
 
 def evict_cache_workspace_size(n: int, keep: int, page_size: int) -> int:
-    return int(_cache._call.paged_cache_evict_workspace_size(int(n), int(keep), int(page_size)))
+    return int(_cache._call.paged_cache_evict_workspace_size(
+        _int(n, "n"), _int(keep, "keep"), _int(page_size, "page_size")))
 
 
 def evict_cache_rows(pools, rows, kept, block_tables, seq_lens, page_refs, *, weights=None, sink=0,
@@ -194,12 +211,12 @@ def evict_cache_rows(pools, rows, kept, block_tables, seq_lens, page_refs, *, we
     shape = kept.shape
     if tuple(shape[:-1]) != (N, n, Hkv) and not (N == 1 and tuple(shape[:-1]) == (n, Hkv)):
         raise ValueError(f"kept must be [{N}, {n}, {Hkv}, keep]")
-    keep = shape[-1]
+    keep, sink = _int(shape[-1], "keep"), _int(sink, "sink")
     kp = _cache._ints(kept, dev, "kept")
     wp, W = None, 0
     if weights is not None:
         R = block_tables.shape[0]
-        W = weights.shape[-1] if weights.dim() else 0
+        W = _int(weights.shape[-1], "the width of weights") if weights.dim() else 0
         want = (R, Hkv, W) if N == 1 and weights.dim() == 3 else (N, R, Hkv, W)
         wp = _plain(weights, _F32, dev, "weights", want)
         _written(weights, "weights")
@@ -207,8 +224,8 @@ def evict_cache_rows(pools, rows, kept, block_tables, seq_lens, page_refs, *, we
     ws = _cache._workspace(workspace, lambda k: evict_cache_workspace_size(k, keep, ps), n, rows,
                            dev, stream)
     rc = _cache._call.paged_cache_evict_run(
-        p, pools.ref(dev), _cache._ints(rows, dev, "rows"), n, kp, keep, operator.index(sink), wp,
-        W, bt, sl, pr, ws.data_ptr(), ws.nbytes, _cache._stream(stream, dev))
+        p, pools.ref(dev), _cache._ints(rows, dev, "rows"), n, kp, keep, sink, wp, W, bt, sl, pr,
+        ws.data_ptr(), ws.nbytes, _cache._stream(stream, dev))
     if rc:
         _cache._check(rc, "paged_cache_evict_run")
     if weights is not None:
