@@ -558,6 +558,10 @@ def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_
         out = _cache._empty(query, out_dtype, stream)
     op = _eviction._plain(out, out_dtype, dev, "out", shape)
     lp = None if lse is None else _eviction._plain(lse, torch.float32, dev, "lse", shape[:-1])
+    if given is not None:
+        _eviction._written(given, "out")
+    if lse is not None:
+        _eviction._written(lse, "lse")
     if workspace_buffer is None:
         need = _cache._call.paged_decode_shared_workspace_size(params, groups)
         workspace_buffer = _cache._new(max(need, 256), torch.uint8, query.device, stream)
