@@ -235,6 +235,7 @@ constexpr int kWideThreads = 32 * kSumWarps + 128;
 constexpr int kRows = 128;                 // of a query tile
 constexpr int kBlockBytes = kRows * 128;   // 128 rows of 64 columns
 constexpr int kUnits = 4;                  // units described ahead
+constexpr int kListed = 512;               // requests with units that the schedule keeps at hand
 // Registers after set-up (launch: 640 x 96): 512 x 104 + 128 x 64 = 640 x 96.
 constexpr int kSumRegs = 104;
 constexpr int kControlRegs = 64;
@@ -269,6 +270,7 @@ struct WideCtrl {
   uint32_t tmem;
   int abort_flag;
   int tiles_begun, looked;               // beats of the MMA warp, and of the units' warp
+  int2 listed[kListed];                  // requests with units, their key tiles
 };
 // A wait for a ring entry of the units may last as long as another role's whole unit (0.1 s are
 // 13 million rows of queries), or its look through a large batch.  Its limit is one of progress:
@@ -358,6 +360,17 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
   WideCtrl* ctl = reinterpret_cast<WideCtrl*>(q_s + kStages * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int TM = kRows / a.G;
+  if (a.more_than > 0) {
+    // The host could not rule out requests with that many rows.  Without any (packed single tokens)
+    // the other launch, which looks at every request, must not wait for this one's set-up.
+    grid_dependency_wait();
+    bool some = false;
+    for (int b = threadIdx.x; b < a.B; b += kWideThreads) {
+      const long long n = static_cast<long long>(a.qo_indptr[b + 1]) - a.qo_indptr[b];
+      some |= (a.last > 0 && a.last < n ? a.last : n) * a.G > a.more_than;
+    }
+    if (!__syncthreads_or(some)) return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&ctl->unit_full[i], 1);
@@ -417,50 +430,56 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     // under the causal mask, so long units come first whatever the lengths.  The CTAs take them in
     // turns that reverse from round to round.  (In order of the tiles' indexes, with requests of
     // 8,192 down to 2,048 tokens, the busiest CTA had 1.25 times the mean, so 1.12.)
-    constexpr int kCached = 4;             // tiles of 32 requests each, a lane each
+    // Requests with units and their tiles are listed (batches with idle rows or single tokens, which
+    // another launch takes, have few); where the list overflows, tiles are counted anew each time.
     const int R = page_piece_rows(a.ps, kRows), pieces = kKeys / R, grid = gridDim.x;
-    const auto count_tiles = [&](int b) {
-      return b < a.B ? (request_of(a, b).keys + kKeys - 1) / kKeys : 0;
-    };
+    const auto tiles_of = [&](const Request& r) { return (r.keys + kKeys - 1) / kKeys; };
     volatile int* looked = &ctl->looked;
-    int cached[kCached], most = 0, beat = 0;
-    uint32_t empty = 0;                    // of the first 32 such tiles, those without a unit
+    int most = 0, listed = 0, beat = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 4 * 32) {
+      int n[4];
 #pragma unroll
-    for (int g = 0; g < kCached; ++g) cached[g] = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane, n = count_tiles(b);
+      for (int g = 0; g < 4; ++g) {        // (four requests' loads on their way together)
+        const int b = b0 + 32 * g + lane;
+        n[g] = 0;
+        if (b >= a.B) continue;
+        const Request r = request_of(a, b);
+        n[g] = tiles_of(r);
+        if (r.bad && blockIdx.x == 0) report_error(a.status, kErrMetadata);
+      }
       *looked = ++beat;
-      if (blockIdx.x == 0 && b < a.B && request_of(a, b).bad) report_error(a.status, kErrMetadata);
 #pragma unroll
-      for (int g = 0; g < kCached; ++g)
-        if (b0 == 32 * g) cached[g] = n;
-      most = max(most, n);
-      if (!__any_sync(0xffffffffu, n > 0) && b0 < 32 * 32) empty |= 1u << (b0 / 32);
+      for (int g = 0; g < 4; ++g) {
+        most = max(most, n[g]);
+        const uint32_t some = __ballot_sync(0xffffffffu, n[g] > 0);
+        const int at = listed + __popc(some & ((1u << lane) - 1u));
+        if (n[g] > 0 && at < kListed) ctl->listed[at] = make_int2(b0 + 32 * g + lane, n[g]);
+        listed += __popc(some);
+      }
     }
+    __syncwarp();
     most = __reduce_max_sync(0xffffffffu, most);
+    const bool complete = listed <= kListed;
+    const int candidates = complete ? listed : a.B;
     int s = 0;
     long long before = 0, round = 0, mine = blockIdx.x;      // units before; this CTA's next one
     bool ok = true;
     for (int left = most; ok && left > 0; --left) {
-      for (int b0 = 0; ok && b0 < a.B; b0 += 32) {
+      for (int x0 = 0; ok && x0 < candidates; x0 += 32) {
         *looked = ++beat;
-        if (b0 < 32 * 32 && (empty >> (b0 / 32) & 1u)) continue;
-        int n = 0;
-        if (b0 < 32 * kCached) {
-#pragma unroll
-          for (int g = 0; g < kCached; ++g)
-            if (b0 == 32 * g) n = cached[g];
-        } else {
-          n = count_tiles(b0 + lane);
-        }
-        const uint32_t live = __ballot_sync(0xffffffffu, n >= left);
+        int2 mine_of = make_int2(x0 + lane, 0);              // request and tiles
+        if (x0 + lane >= candidates) mine_of.x = 0;
+        else if (complete) mine_of = ctl->listed[x0 + lane];
+        else mine_of.y = tiles_of(request_of(a, mine_of.x));
+        const uint32_t live = __ballot_sync(0xffffffffu, mine_of.y >= left);
         const long long after = before + static_cast<long long>(__popc(live)) * a.Hkv;
         while (mine < after) {
           const int which = static_cast<int>(mine - before) / a.Hkv;
           const int h = static_cast<int>(mine - before) - which * a.Hkv;
-          const int at = __fns(live, 0, which + 1), b = b0 + at;
+          const int at = __fns(live, 0, which + 1);
+          const int b = __shfl_sync(0xffffffffu, mine_of.x, at);
           const Request r = request_of(a, b);
-          const int key0 = (__shfl_sync(0xffffffffu, n, at) - left) * kKeys;
+          const int key0 = (__shfl_sync(0xffffffffu, mine_of.y, at) - left) * kKeys;
           const int keys = min(kKeys, r.keys - key0);
           int page = -1;
           const int key = key0 + lane * R;
@@ -821,11 +840,14 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
       return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
   }
-  // Few rows on average, but some request may have many (a prompt among single tokens): a launch
-  // for each kind.  511 single tokens and a prompt of 1,000, 2,000 keys each, 8 KV heads: 510 us; 3,650
-  // as few rows, 618 as many.  63 and a prompt of 64, 4,000 keys: 104 us; 214 and 156.
-  const long long most = (a.last > 0 ? a.last : static_cast<long long>(p->total_q) - a.B + 1) * a.G;
-  const bool mixed = qo_indptr && p->total_q > a.B && most > kHeavyRows;
+  // Few rows on average, but some request may have many (a prompt among single tokens, or in a batch
+  // whose other rows sit the call out): a launch for each kind.  511 single tokens and a prompt of
+  // 1,000, 2,000 keys each, 8 KV heads: 510 us; 3,650 as few rows, 618 as many.  63 and a prompt of
+  // 64, 4,000 keys: 104 us; 214 and 156.  511 idle rows and a prompt of 512: 48 us, 1,840 as few
+  // rows; 63 and one of 9: 25 and 30.  Packed single tokens pay 2 us for the launch that finds no
+  // prompt (64 of up to 8,192 keys 136 us, 134 without it; 9 of up to 700 15.5 and 13.4).
+  const long long total = p->total_q, most = a.last > 0 && a.last < total ? a.last : total;
+  const bool mixed = qo_indptr && most * a.G > kHeavyRows;
   if (mixed) {
     WeightsArgs heavy = a;
     heavy.more_than = kHeavyRows;

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import paged_kv_block_gb300 as pkb
+from tests.test_gpu_weights import Problem
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -13,13 +14,13 @@ def i32(x):
 
 
 def test_units_longer_than_a_wait():
-    """A unit of 16.7 million rows takes longer than the 0.1 s after which a wait without progress
-    gives up; five of them for every SM.  Scores and LSEs of 0 make every weight the number of rows,
-    exactly: all partial sums are whole numbers below 2^24."""
+    """A unit of 16.7 million rows takes 0.16 s, longer than the 0.1 s after which a wait without
+    progress gives up; five of them for every SM.  Scores and LSEs of 0 make every weight the number
+    of rows, exactly: all partial sums are whole numbers below 2^24."""
     Hq, ps, T = 64, 128, 262143
     pages = 5 * torch.cuda.get_device_properties(0).multi_processor_count * 256 // ps
-    q = torch.zeros(T, Hq, 128, dtype=torch.bfloat16, device=DEV)
-    cache = torch.zeros(pages, 2, 1, ps, 128, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(T, Hq, 256, dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros(pages, 2, 1, ps, 256, dtype=torch.bfloat16, device=DEV)
     lse, status = torch.zeros(T, Hq, device=DEV), i32([0])
     w = torch.full((1, 1, pages * ps), 7.0, device=DEV)
     pkb.accumulate_attention_weights(
@@ -27,3 +28,20 @@ def test_units_longer_than_a_wait():
         block_tables=torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1), status=status)
     assert status.item() == 0
     assert (w == T * Hq).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("idle,heavy", [(1, 20), (62, 30), (200, 90), (700, 130)])
+def test_a_prompt_among_idle_requests(D, idle, heavy):
+    """No more queries than requests, most of them of one: as if that one were alone."""
+    lens = [40 + b % 23 for b in range(idle)] + [333]
+    new = [1 if b % 9 == 4 else 0 for b in range(idle)] + [heavy]
+    p = Problem(idle, lens, new, 8, 2, D, 16)
+    p.run(decay=0.5)
+    p.run(csr=True, last=7)
+
+
+def test_more_prompts_than_the_schedule_lists():
+    """600 requests with units, beside idle ones and single tokens."""
+    new = [3 + b % 12 if b % 3 else b % 2 for b in range(900)]
+    Problem(41, [20 + b % 150 for b in range(900)], new, 24, 2, 128, 16).run()
