@@ -250,31 +250,36 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
       }
       if (a.order) item = __ldcg(a.order + item);
       const SplitItem it = item_of(item);
-      const int L = a.seq_lens[it.b];
-      if (lane == 0) {
-        sm->item_id[islot] = item;
-        uint8_t* qdst = qslots + islot * 2 * qhalf;
-        // box: 64 columns x G heads x (M / G) queries; rows past the tensor read as zero
-        const int q_row0 = a.qo_indptr ? __ldg(a.qo_indptr + it.b) : it.b * a.q_len;
-        // what the consumers need, so that they start without round trips of their own
-        const int splits = __ldcg(a.split_offset + it.b + 1) - __ldcg(a.split_offset + it.b);
-        sm->item_rec[islot] = it;
-        sm->item_of[islot] = make_int4(
-            L, splits, a.qo_indptr ? __ldg(a.qo_indptr + it.b + 1) - q_row0 : a.q_len, q_row0);
-        mbar_arrive_expect_tx(&sm->item_full[islot], 2u * M * 128u);
-        tma_load_3d(qdst, &qmap, &sm->item_full[islot], 0, it.g * G, q_row0);
-        tma_load_3d(qdst + qhalf, &qmap, &sm->item_full[islot], 64, it.g * G, q_row0);
+      // All of an item's loads on their way together, then its first pages, then Q: its keys wait for
+      // the pages (with Q, and what the consumers need, before them the headline took 0.7% longer).
+      const int L = a.seq_lens[it.b], indptr = a.kv_indptr[it.b];
+      const int split0 = __ldcg(a.split_offset + it.b), split1 = __ldcg(a.split_offset + it.b + 1);
+      int q_row0 = it.b * a.q_len, nq = a.q_len;
+      if (a.qo_indptr) {
+        q_row0 = __ldg(a.qo_indptr + it.b);
+        nq = __ldg(a.qo_indptr + it.b + 1) - q_row0;
       }
       const int first_key = (it.kv_begin / kStageKeys) * kStageKeys;
       const int n_stages =
           it.kv_end > first_key ? (it.kv_end - first_key + kStageKeys - 1) / kStageKeys : 0;
-      const int* pages = a.kv_indices + a.kv_indptr[it.b];
+      const int* pages = a.kv_indices + indptr;
       auto page_of = [&](int s) -> int {      // page id of this lane's piece of stage s, or -1
         const int key = first_key + s * kStageKeys + lane * R;
         if (lane >= pieces || s >= n_stages || key >= L || key >= it.kv_end) return -1;
         return __ldg(pages + key / ps);
       };
       int page_next = page_of(0);
+      if (lane == 0) {
+        sm->item_id[islot] = item;
+        uint8_t* qdst = qslots + islot * 2 * qhalf;
+        // what the consumers need, so that they start without round trips of their own
+        sm->item_rec[islot] = it;
+        sm->item_of[islot] = make_int4(L, split1 - split0, nq, q_row0);
+        // box: 64 columns x G heads x (M / G) queries; rows past the tensor read as zero
+        mbar_arrive_expect_tx(&sm->item_full[islot], 2u * M * 128u);
+        tma_load_3d(qdst, &qmap, &sm->item_full[islot], 0, it.g * G, q_row0);
+        tma_load_3d(qdst + qhalf, &qmap, &sm->item_full[islot], 64, it.g * G, q_row0);
+      }
       bool ok = true;
       for (int s = 0; s < n_stages; ++s, ++sg) {
         const int page = page_next;
@@ -602,39 +607,21 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
         }
       }
       named_bar(1, kConsumerWarps * 32);
-      const int d = threadIdx.x;   // 0..127
       const int live_rows = nq <= 0 ? 0 : (nq * G < M ? nq * G : M);
       const bool direct = n_split == 1 && !a.parts_only;
-      // Thread m: the weights of row m's slices (in the place of their maxima), its sum (in the
-      // place of its first) and its LSE, once for all columns.
-      if (d < live_rows) {
-        float Mx = -INFINITY, Lsum = 0.f;
-        if (have_stage) {
-          for (int w = 0; w < kg; ++w) Mx = fmaxf(Mx, sm->red_m[w * M + d]);
-          const float Mu = Mx == -INFINITY ? 0.f : Mx;
-          for (int w = 0; w < kg; ++w) {
-            const float f = fast_exp2(sm->red_m[w * M + d] - Mu);
-            Lsum += f * sm->red_l[w * M + d];
-            sm->red_m[w * M + d] = f;
-          }
-          Mx = Mu;
-        }
-        sm->red_l[d] = Lsum;
-        const float lse_nat = Lsum > 0.f ? (Mx + fast_log2(Lsum)) * kLn2 : -INFINITY;
-        const int qrow = q_row0 + d / G;
-        if (!direct)
-          a.part_lse[static_cast<long long>(item) * M + d] = lse_nat;
-        else if (a.lse && qrow >= 0 && qrow < a.q_rows)
-          a.lse[static_cast<long long>(qrow) * a.Hq + g * G + d % G] = lse_nat;
-      }
-      named_bar(1, kConsumerWarps * 32);
-      // a warp per row, a lane per 4 columns
+      // A warp per row, a lane per 4 columns; every lane computes the weights of the row's slices
+      // for itself (up to four, and no further barrier).
       for (int m = warp; m < live_rows; m += kConsumerWarps) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float Mx = -INFINITY, Lsum = 0.f;
         if (have_stage) {
 #pragma unroll
+          for (int w = 0; w < kg; ++w) Mx = fmaxf(Mx, sm->red_m[w * M + m]);
+          Mx = Mx == -INFINITY ? 0.f : Mx;
+#pragma unroll
           for (int w = 0; w < kg; ++w) {
-            const float f = sm->red_m[w * M + m];
+            const float f = fast_exp2(sm->red_m[w * M + m] - Mx);
+            Lsum += f * sm->red_l[w * M + m];
             const float4 v = *reinterpret_cast<const float4*>(
                 red_o + (w * M + m) * kD + ((lane * 4) ^ ((m & 3) << 3)));
             acc.x += f * v.x;
@@ -643,7 +630,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
             acc.w += f * v.w;
           }
         }
-        const float Lsum = sm->red_l[m];
+        const float lse_nat = Lsum > 0.f ? (Mx + fast_log2(Lsum)) * kLn2 : -INFINITY;
         const float4 on = Lsum > 0.f ? make_float4(acc.x / Lsum, acc.y / Lsum, acc.z / Lsum,
                                                    acc.w / Lsum)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -655,9 +642,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                      make_float4(on.x * a.out_scale, on.y * a.out_scale, on.z * a.out_scale,
                                  on.w * a.out_scale),
                      a.out_dtype);
+          if (a.lse && lane == 0) a.lse[orow] = lse_nat;
         } else {
           const long long prow = static_cast<long long>(item) * M + m;
           reinterpret_cast<float4*>(a.part_o + prow * kD)[lane] = on;
+          if (lane == 0) a.part_lse[prow] = lse_nat;
         }
       }
       if (n_split > 1 && !a.parts_only) {
