@@ -273,6 +273,7 @@ typedef struct paged_weights_params {
  * where the old weight of the tokens that the call's queries stand for, the last nq of a request
  * with nq queries, is 0: their entries are written without being read, and so is every entry with
  * decay = 0.  Entries past a request's length are left alone, and so is a request without queries.
+ * Weights belong to a row as its page table does: whoever forks a row copies them to the child.
  * Attention calls with a window are not served: keys outside it would count.
  *   q_dev [total_q, Hq, D] bf16 and lse_dev [total_q, Hq] fp32, natural logarithm: the attention
  *   call's queries and its LSE (a row with an LSE of -inf sees nothing and adds nothing);
@@ -280,10 +281,11 @@ typedef struct paged_weights_params {
  *   qo_indptr_dev [B + 1]: packed form, or NULL: the fixed form;
  *   kv_indptr_dev [B + 1] with pages_dev (CSR), or NULL: pages_dev is block_tables [B, C];
  *   weights_dev [B, Hkv, W] fp32.
- * Scores, exponentials and sums are fp32, each sum in one order whatever the launch, so calls
- * repeat bit for bit.  Keys past W or past the request's table entries get no weight, a key whose
- * page id lies outside [0, num_pages) keeps its old one, and a request whose offsets do not lie in
- * [0, total_q] is left out (metadata bit). */
+ * Scores, exponentials and sums are fp32.  The order of a sum depends on the batch's shape, W and
+ * the device, never on timing: the same call on the same device repeats bit for bit.  Keys past W
+ * or past the request's table entries get no weight, a key whose page id lies outside
+ * [0, num_pages) keeps its old one, and a request whose offsets do not lie in [0, total_q] is left
+ * out (metadata bit). */
 int paged_weights_run(const paged_weights_params* params, const void* q_dev, const float* lse_dev,
                       const void* k_cache_dev, const int32_t* qo_indptr_dev,
                       const int32_t* kv_indptr_dev, const int32_t* pages_dev,
@@ -321,7 +323,10 @@ int paged_cache_select_run(const paged_cache_select_params* params, const int32_
  * ceil(keep / page_size) that other rows share is replaced by a fresh one (as in extend: the lowest
  * free ids, item by item, in the order of the row); pages past them, and replaced ones, lose a
  * count, and pages whose counts reach 0 this way are free after the call.  What the row's table
- * holds past its new length, and slots past it in its last page, are kept.
+ * holds past its new length is kept, and so are the slots past it in its last page, unless that
+ * page was replaced: a fresh one holds there whatever it held before.
+ * The row has no more in common with others than its first `sink` tokens: behind a shared prefix
+ * (paged_decode_shared_run) prefix_lens is to be cut to that.
  * Left out (metadata bit): rows outside [0, rows), a row listed before, rows with ids outside the
  * pool or more tokens than C pages or weights_width hold, lists whose first entry is negative or
  * whose last one is not in [keep - 1, length).  A slot whose entry breaks the order (below the

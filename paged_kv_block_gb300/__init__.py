@@ -527,9 +527,10 @@ def batch_decode_with_shared_prefix(query, kv_cache, workspace_buffer, paged_kv_
     """batch_decode_with_paged_kv_cache for groups of consecutive requests that start with the
     same tokens; returns (out, lse).  Group g is the requests group_indptr[g] ..
     group_indptr[g + 1], whose first prefix_lens[g] keys and values are equal: they are read
-    once, from the pages of the group's first request.  group_indptr [groups + 1] and prefix_lens
-    [groups] are int32; requests outside every group share nothing, and those of length 0 (rows that
-    pad a batch) take no part in theirs.  query is [B, Hq, D] or [B, SQ, Hq, D]."""
+    once, from the pages of the group's first request that is not empty.  group_indptr [groups + 1]
+    and prefix_lens [groups] are int32; requests outside every group share nothing, and those of
+    length 0 (rows that pad a batch) take no part in theirs.  query is [B, Hq, D] or [B, SQ, Hq, D].
+    Rows that were cut back (evict_cache_rows) have no more in common than their sink."""
     dev = _cache._device()
     if kv_layout != "HND":
         raise ValueError("only the HND layout is supported")

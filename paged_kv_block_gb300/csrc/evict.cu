@@ -15,13 +15,16 @@ namespace {
 // thread (32; 8 where there are CTAs to spare and time is latency): a step costs two instructions a
 // key and a barrier.  What a bracket of few keys holds goes to shared memory: cheap steps there.
 // A last pass writes the indices in order, those of key T until their number is reached.
-// Instructions bound it (the issue slots are 70% full): for 2,048 lists of up to 8,192 tokens
-// histograms of the keys' digits took 143 us (half of the tokens may have the same weight, and then
-// shared-memory atomics queue up), plain bisection 112 us, interpolation between the least and the
-// greatest key 64 us, this 56 us; one warp alone in the last steps 58 us, four pivots at a time
-// there 60 us (what every warp does beside the counting doubles).  Where no warp has 32 open keys, or
-// T lies outside the sample, a second sample and the ends of the list's range cost 2 us of them, and
-// save up to half: 384 lists of 796 tokens, 301 of them kept anyway, 18.6 us against 39.
+// Instructions bound it: the issue slots are 70% full, some 3,000 instructions a warp, of which its
+// keys ask for about 1,000; the rest is the sample and what every warp does at each step.  For
+// 2,048 lists of up to 8,192 tokens histograms of the keys' digits took 143 us (half of the tokens
+// may have the same weight, and then shared-memory atomics queue up), plain bisection 112 us,
+// interpolation between the least and the greatest key 64 us, this 56 us; one warp alone in the
+// last steps 58 us, four pivots at a time there 60 us (what every warp does beside the counting
+// doubles).  Where no warp has 32 open keys, or T lies outside the sample, a second sample and the
+// ends of the list's range cost 2 us of them, and save up to half: 384 lists of 796 tokens, 301 of
+// them kept anyway, 18.6 us against 39.  Lists of more than 32,768 tokens that get no cluster are
+// read from memory at every step.
 constexpr uint32_t kMustKeep = 0xffffffffu;
 constexpr int kSelectCluster = 8;
 constexpr int kSelectThreads = 1024;

@@ -484,7 +484,7 @@ tail_kernel(const __grid_constant__ SharedLaunch a) {
       }
       const float shift[2] = {top[0] == -INFINITY ? 0.f : top[0],
                               top[1] == -INFINITY ? 0.f : top[1]};
-      // P in bf16, as everywhere in this library: its rounding (2^-9 of each probability) is
+      // P in bf16, as everywhere in this library: its rounding (2^-8 of a probability at most) is
       // averaged over the keys; the sums are of the unrounded ones
       uint32_t p[4];
       float add[2] = {0.f, 0.f};

@@ -225,9 +225,11 @@ narrow_kernel(const __grid_constant__ WeightsArgs a) {
 //   warp  19    unit descriptions, page ids among them
 // kPair: tiles of 256 keys; the four warpgroups take every query tile, 64 keys each.  Else tiles of
 // 128 keys, and two pairs of warpgroups take query tiles in turn.
-// The queries come from L2 once per key tile: 128 keys ask for 64 bytes per cycle and SM, far above
-// what L2 gives all SMs (some 20), so prompts want the 256; tiles of 128 make more and smaller
-// units and leave room for the next unit's K at D = 256.
+// The queries come from L2 once per key tile, so tiles of 256 keys halve that traffic (3.4 GB a
+// call for four prompts of up to 8,192 tokens, 32 heads: 4.9 TB/s); tiles of 128 make more and
+// smaller units and leave room for the next unit's K at D = 256.  Those four prompts take 690 us,
+// 1.24 PFLOP/s: the tensor pipe is active 62% of the time and 60% of the issue slots are taken,
+// neither full; which of the waits between them costs the rest is not known.
 constexpr int kGroups = 4;                 // warpgroups of exponentials
 constexpr int kOwn = 64;                   // keys of a thread
 constexpr int kSumWarps = 4 * kGroups;
@@ -430,8 +432,8 @@ wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     // under the causal mask, so long units come first whatever the lengths.  The CTAs take them in
     // turns that reverse from round to round.  (In order of the tiles' indexes, with requests of
     // 8,192 down to 2,048 tokens, the busiest CTA had 1.25 times the mean, so 1.12.)
-    // Requests with units and their tiles are listed (batches with idle rows or single tokens, which
-    // another launch takes, have few); where the list overflows, tiles are counted anew each time.
+    // Requests with units and their tiles are listed (batches with idle rows or single tokens,
+    // which another launch takes, have few); where the list overflows, tiles are counted anew.
     const int R = page_piece_rows(a.ps, kRows), pieces = kKeys / R, grid = gridDim.x;
     const auto tiles_of = [&](const Request& r) { return (r.keys + kKeys - 1) / kKeys; };
     volatile int* looked = &ctl->looked;
@@ -831,17 +833,19 @@ int paged_weights_run(const paged_weights_params* p, const void* q, const float*
   if (a.last > 0 && a.last < rows) rows = a.last;
   rows *= a.G;
   if (rows > 16) {
-    // Tiles of 256 keys wherever they make a unit per SM (else 128: two prompts' 512 queries of 2
-    // heads, D = 128, 46 us against 62).  16 prompts' last 32 queries of 2 KV heads, D = 256: 40 us
-    // against 47, their last 8 23 against 27, 128 85 against 121.
+    // Tiles of 256 keys wherever they make a unit per SM by the weights' width (the lengths are on
+    // the device); else 128: two prompts' 512 queries of 2 heads, D = 128, 46 us against 62.  16
+    // prompts' last 32 queries of 2 KV heads, D = 256: 40 us against 47, their last 8 23 against
+    // 27, 128 85 against 121.  A width far above the lengths takes the 256 where 128 were better:
+    // two prompts of 512 tokens, 8 heads, 17.3 us in rows of 576 weights, 20.3 in rows of 32,768.
     const bool pair = static_cast<long long>(a.B) * a.Hkv * ceil_div(a.W, 256) >=
                       current_sm_count();
     if (p->head_dim == 128)
       return pair ? launch_wide<128, true>(a, st) : launch_wide<128, false>(a, st);
     return pair ? launch_wide<256, true>(a, st) : launch_wide<256, false>(a, st);
   }
-  // Few rows on average, but some request may have many (a prompt among single tokens, or in a batch
-  // whose other rows sit the call out): a launch for each kind.  511 single tokens and a prompt of
+  // Few rows on average, but some request may have many (a prompt among single tokens, or in a
+  // batch whose other rows sit the call out): a launch for each kind.  511 single tokens and one of
   // 1,000, 2,000 keys each, 8 KV heads: 510 us; 3,650 as few rows, 618 as many.  63 and a prompt of
   // 64, 4,000 keys: 104 us; 214 and 156.  511 idle rows and a prompt of 512: 48 us, 1,840 as few
   // rows; 63 and one of 9: 25 and 30.  Packed single tokens pay 2 us for the launch that finds no

@@ -96,8 +96,10 @@ def accumulate_attention_weights(query, lse, paged_kv_cache, seq_lens_kv, weight
     packed [total, Hq, D] with [total, Hq] and qo_indptr.  The page table is block_tables [B, C] or
     paged_kv_indptr with paged_kv_indices; the cache a combined one or a (K, V) pair.  Older weights
     are multiplied by `decay`; the entries of the call's own query tokens (the last of each request)
-    start at 0.  last_queries = n counts only the last n queries of each request.
-    The attention call must have had no window; this one has no gradient.  status: an int32 word that device-side findings are OR-ed into."""
+    start at 0, those of a forked row are the program's to copy from its parent's.  last_queries = n
+    counts only the last n queries of each request.
+    The attention call must have had no window; this one has no gradient.  status: an int32 word
+    that device-side findings are OR-ed into."""
     dev = _cache._device()
     kc, _, combined, P, Hkv, ps, D = _cache._geometry(paged_kv_cache, dev)
     B = _cache._count(seq_lens_kv, "seq_lens_kv")
@@ -198,7 +200,8 @@ def evict_cache_rows(pools, rows, kept, block_tables, seq_lens, page_refs, *, we
     select_cache_tokens; [n, Hkv, keep] with one layer): in every layer and KV head they move to
     the row's first slots, and so do their `weights` [layers, rows, Hkv, W]; pages past them are
     given back, and pages that other rows share are replaced by fresh ones before they change.
-    Rows of at most `keep` tokens stay as they are.
+    Rows of at most `keep` tokens stay as they are.  The others have no more in common with other
+    rows than their first `sink` tokens.
 
     sink: the `sink` that the lists were selected with; pages that lie wholly in it stay shared.
     Rows that the free pages do not suffice for stay as they are; `status` and the workspace tell,
