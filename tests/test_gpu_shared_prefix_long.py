@@ -3,9 +3,9 @@
 Tolerances.  |v| <= 1, so outputs are below 1.  A part of the prefix has at most 2^14 tiles of 128
 keys, 2^17 additions into an accumulator that grows evenly and that the tensor core may truncate:
 at worst 2^17 * 2^-23 / 2 = 7.8e-3.  The probabilities' rounding to bf16 is the same in every copy
-of a page, at worst 2^-8, and the output's is 2^-8 again: 1.6e-2 in all, below the parity contract's
-2e-2.  The sum of a part's 2^14 tile sums in fp32 is off by 2^14 * 2^-24 = 1e-3 at worst, sums inside
-a tile and the scores by some 1e-5 more, and so is its logarithm: 1.2e-3."""
+of a page, at worst 2^-8, and the output's is 2^-8 again: 1.6e-2 in all, below the parity
+contract's 2e-2.  The sum of a part's 2^14 tile sums in fp32 is off by 2^14 * 2^-24 = 1e-3 at
+worst, sums inside a tile and the scores by some 1e-5 more, and so is its logarithm: 1.2e-3."""
 import math
 
 import pytest

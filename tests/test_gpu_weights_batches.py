@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import paged_kv_block_gb300 as pkb
+from oracle.eviction import METADATA
 from tests.test_gpu_weights import Problem
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,39 @@ def test_more_prompts_than_the_schedule_lists():
     """600 requests with units, beside idle ones and single tokens."""
     new = [3 + b % 12 if b % 3 else b % 2 for b in range(900)]
     Problem(41, [20 + b % 150 for b in range(900)], new, 24, 2, 128, 16).run()
+
+
+def test_a_captured_call_reads_who_sits_out():
+    """Replays go by the offsets of the moment: all of 60 queries in one request, spread, one each,
+    and offsets that leave the batch."""
+    B, total = 60, 60
+    lens = [70 + b % 31 for b in range(B)]
+    spreads = [[60 if b == 17 else 0 for b in range(B)], [1] * B,
+               [20 if b % 20 == 3 else 0 for b in range(B)]]
+    problems = [Problem(50 + i, lens, new, 8, 2, 128, 16) for i, new in enumerate(spreads)]
+    p = problems[0]
+    q, lse = torch.empty_like(p.q, device=DEV), torch.empty_like(p.lse, device=DEV)
+    qo, device_lens = i32([0] * (B + 1)), i32(lens)
+    cache, w = p.cache.clone(), torch.empty_like(p.w, device=DEV)
+    tables, status = torch.empty_like(i32(p.tables)), i32([0])
+
+    def load(p):
+        assert p.starts[-1] == total and p.cache.shape == cache.shape
+        for to, x in ((q, p.q), (lse, p.lse), (qo, i32(p.starts)), (cache, p.cache), (w, p.w),
+                      (tables, i32(p.tables))):
+            to.copy_(x)
+    load(p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkb.accumulate_attention_weights(q, lse, cache, device_lens, w, qo_indptr=qo,
+                                         block_tables=tables, status=status)
+    for p in problems + problems[::-1]:
+        load(p)
+        graph.replay()
+        p.check(w)
+        assert status.item() == 0
+    load(p)
+    qo.copy_(i32([0] * 18 + [10 ** 9] * 43))
+    graph.replay()
+    assert status.item() == METADATA
+    assert torch.equal(w.nan_to_num(-1), p.w.to(DEV).nan_to_num(-1))
